@@ -6,7 +6,10 @@
  * (or relu^2) -> grouped GEMM2 + bias * routing weight -> top-k combine (moe_forward; in
  * MXFP8 with h quantised between the GEMMs, moe_mx_quantize); a single grouped GEMM over
  * given operands (moe_grouped_gemm); a per-token-scaled FP8 grouped GEMM over per-expert
- * group sizes (moe_gemm_per_token); and the per-expert weight gradient (moe_wgrad).
+ * group sizes (moe_gemm_per_token); and the per-expert weight gradient (moe_wgrad).  Around
+ * that path, for training: the router's auxiliary losses with their gradient
+ * (moe_router_loss) and the expert activation with an MXFP8 checkpoint and its backward pass
+ * (moe_act_checkpoint, moe_act_backward).
  *
  * Sources of the definitions (pull-request pages):
  *  [BUCKET] "Bound Triton MoE JIT specializations via token-dim bucketing and warmup",
@@ -362,6 +365,70 @@ moe_status moe_wgrad(const void* grad, const void* input, int32_t input_per_pair
                      const int32_t* sorted_token_ids, const int32_t* expert_ids,
                      const int32_t* num_tokens_post_padded, int32_t block_m,
                      int64_t cap_tokens, float* dW, int32_t mode, const moe_ctx* ctx);
+
+/* ------------------------------------------------------------------------------------ *
+ * Router losses (training)                                                               *
+ * ------------------------------------------------------------------------------------ */
+
+/* Workspace bytes of moe_router_loss (0 for E outside [1, 1024]). */
+size_t moe_router_loss_workspace_size(int32_t E);
+
+/* Balance loss and z loss of a top-k softmax router, per-expert counts and the gradient of
+ * the logits.  With n the tokens whose token_mask byte is not 0 (all T where it is NULL), c_e
+ * the number of their choices topk_ids that name expert e, p_t = softmax(logits_t) over the E
+ * experts and lse_t = log sum_e exp(logits_te):
+ *   balance = sum_e f_e P_e,  f_e = E c_e / (n k),  P_e = (1/n) sum_t p_te
+ *   z       = (1/n) sum_t lse_t^2
+ *   loss[0] = balance_coef * balance + z_coef * z (a part of coefficient 0 is left out);
+ *   loss[1] = balance;  loss[2] = z
+ *   d_logits_te = (balance_coef/n) p_te (f_e - sum_e' f_e' p_te') + (2 z_coef/n) lse_t p_te
+ *               + sum_{j: id_tj = e} w_tj (dw_tj - sum_i w_ti dw_ti)
+ * (the counts are constants of the gradient).  The last line, the gradient through the routing
+ * weights of moe_align, is there when d_topk_w is not NULL: w_tj = topk_w[t, j], dw_tj =
+ * d_topk_w[t, j].
+ * logits [T, E] fp32 (-inf: an expert the token may not use); topk_ids [T, k] int32, topk_w and
+ * d_topk_w [T, k] fp32 (topk_w is read only with d_topk_w); token_mask [T] bytes or NULL.  counts [E] int32,
+ * prob_mean [E] fp32 (P) and d_logits [T, E] fp32 may each be NULL; loss [3] fp32.  d_logits
+ * may be logits itself.
+ *  - A token with mask 0 counts for nothing and its row of d_logits is zeros, whatever its
+ *    logits, ids and weights hold.  With no token at all every output is 0.
+ *  - A row whose logits are all -inf adds its choices to the counts and nothing else; its row
+ *    of d_logits is zeros.
+ *  - A choice outside [0, E) of a token that counts sets MOE_ERR_INVALID_EXPERT in
+ *    ctx->dev_status and is left out (of c, and of the gradient through the weights).
+ * Sums and gradients in fp32, in a fixed order: repeated calls give identical bits.
+ * Limits: 1 <= k <= 32, k <= E <= 1024, T*k < 2^31. */
+moe_status moe_router_loss(const float* logits, const int32_t* topk_ids, const float* topk_w,
+                           const float* d_topk_w, const uint8_t* token_mask, int64_t T, int32_t k, int32_t E,
+                           float balance_coef, float z_coef, int32_t* counts, float* prob_mean, float* loss,
+                           float* d_logits, const moe_ctx* ctx);
+
+/* ------------------------------------------------------------------------------------ *
+ * Expert activation with an 8-bit checkpoint (training)                                  *
+ * ------------------------------------------------------------------------------------ */
+
+/* Forward: gu [rows, N1] bf16 pre-activations (MOE_ACT_SWIGLU: N1 = 2I, columns 0..I-1 gate,
+ * I..2I-1 up; MOE_ACT_RELU2: N1 = I) -> h [rows, I] bf16 = row_w * silu(gate) * up (or row_w *
+ * max(gu, 0)^2), computed in fp32 from gu and rounded once; and the checkpoint that the backward
+ * pass reads in place of gu: codes [rows, N1] E4M3 and scales [rows, N1/32] E8M0, the MXFP8
+ * values of gu by the rule of moe_mx_quantize.  row_w [rows] fp32 (a pair's routing weight; NULL:
+ * 1).  h may be NULL (checkpoint only).  A row of weight exactly 0 is left out: gu is not read,
+ * its h and its checkpoint are zeros.  I must be a multiple of 32. */
+moe_status moe_act_checkpoint(const void* gu, const float* row_w, int64_t rows, int32_t I, int32_t activation,
+                              void* h, uint8_t* codes, uint8_t* scales, const moe_ctx* ctx);
+
+/* Backward, from the checkpoint's values g, u (or z) and dh [rows, I] bf16, the gradient of h:
+ *   SwiGLU: d_gu = (row_w dh u s (1 + g (1 - s)) | row_w dh g s), s = sigmoid(g);
+ *   relu^2: d_gu = 2 row_w dh max(z, 0)                            [rows, N1] bf16
+ *   h = row_w a, a = silu(g) u or max(z, 0)^2                       [rows, I] bf16, or NULL: the
+ *       activations again, the operand of the next layer's weight gradient (moe_wgrad)
+ *   d_row_w = sum_i dh_i a_i                                        [rows] fp32, or NULL: the
+ *       gradient of the routing weight (moe_router_loss takes it as d_topk_w)
+ * in fp32, each rounded once; the sum runs in a fixed order.  A row of weight exactly 0 is left
+ * out: its outputs are zeros, whatever dh and the checkpoint hold. */
+moe_status moe_act_backward(const uint8_t* codes, const uint8_t* scales, const void* dh, const float* row_w,
+                            int64_t rows, int32_t I, int32_t activation, void* d_gu, void* h, float* d_row_w,
+                            const moe_ctx* ctx);
 
 /* ------------------------------------------------------------------------------------ *
  * Diagnostics: failure detection of the bounded waits                                    *

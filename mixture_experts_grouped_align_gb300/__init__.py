@@ -21,6 +21,7 @@ __all__ = [
     "moe_bucket_count", "moe_bucket_pad", "moe_forward_workspace_size", "moe_forward",
     "moe_forward_no_alloc", "moe_grouped_gemm", "moe_grouped_gemm_workspace_size", "moe_mx_quantize",
     "moe_gemm_per_token", "moe_wgrad", "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels",
+    "moe_router_loss", "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -36,7 +37,8 @@ EXPORTED_SYMBOLS = [
     "moe_last_error", "moe_align_capacity", "moe_align", "moe_bucket", "moe_bucket_count",
     "moe_bucket_pad", "moe_forward_workspace_size", "moe_forward", "moe_forward_no_alloc",
     "moe_grouped_gemm", "moe_grouped_gemm_workspace_size", "moe_mx_quantize", "moe_gemm_per_token", "moe_wgrad",
-    "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels",
+    "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels", "moe_router_loss",
+    "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward",
 ]
 
 
@@ -73,6 +75,7 @@ def load(path: str | None = None):
                            "(mixture_experts_grouped_align_gb300.build.build())")
     lib = ctypes.CDLL(path)
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    F32 = ctypes.c_float
     sig = {
         "moe_last_error": (ctypes.c_char_p, []),
         "moe_align_capacity": (I32, [I64, I32, I32, P, P]),
@@ -91,6 +94,10 @@ def load(path: str | None = None):
         "moe_wgrad": (I32, [P, P, I32, I64, I32, I32, I32, I32, P, P, P, I32, I64, P, I32, P]),
         "moe_wgrad_workspace_size": (SZ, [I32, I32, I32, I32, I64, I32]),
         "moe_debug_stall_tensor_kernels": (None, [I64]),
+        "moe_router_loss_workspace_size": (SZ, [I32]),
+        "moe_router_loss": (I32, [P, P, P, P, P, I64, I32, I32, F32, F32, P, P, P, P, P]),
+        "moe_act_checkpoint": (I32, [P, P, I64, I32, I32, P, P, P, P]),
+        "moe_act_backward": (I32, [P, P, P, P, I64, I32, I32, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -251,6 +258,59 @@ def moe_wgrad(grad, input, input_per_pair, T, k, E, N, Kin, sorted_token_ids, ex
 
 def moe_wgrad_workspace_size(E, N, Kin, block_m, cap_tokens, mode=0) -> int:
     return load().moe_wgrad_workspace_size(E, N, Kin, block_m, cap_tokens, int(mode))
+
+
+def _tensor(t, what, dtype, numel):
+    """The device pointer of a tensor argument, after the checks the C ABI cannot make: a torch
+    tensor must be dense, of the stated type and of at least ``numel`` elements."""
+    if t is None or isinstance(t, int):
+        return t
+    if str(t.dtype) != dtype or not t.is_contiguous() or t.numel() < numel or not t.is_cuda:
+        raise MoeError(-1, f"{what}: need a contiguous {dtype} device tensor of {numel} elements, got "
+                           f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    return t.data_ptr()
+
+
+def moe_router_loss_workspace_size(E) -> int:
+    return load().moe_router_loss_workspace_size(E)
+
+
+def moe_router_loss(logits, topk_ids, topk_w, d_topk_w, token_mask, T, k, E, balance_coef, z_coef, counts,
+                    prob_mean, loss, d_logits, ctx):
+    """Balance and z losses, per-expert counts and d_logits [T, E] (with the gradient d_topk_w of
+    the routing weights, if given).  loss [3] = total, balance, z."""
+    f32, i32 = "torch.float32", "torch.int32"
+    return _check(load().moe_router_loss(
+        _tensor(logits, "logits", f32, T * E), _tensor(topk_ids, "topk_ids", i32, T * k),
+        _tensor(topk_w, "topk_w", f32, T * k), _tensor(d_topk_w, "d_topk_w", f32, T * k),
+        _tensor(token_mask, "token_mask", "torch.uint8", T), T, k, E, balance_coef, z_coef,
+        _tensor(counts, "counts", i32, E), _tensor(prob_mean, "prob_mean", f32, E), _tensor(loss, "loss", f32, 3),
+        _tensor(d_logits, "d_logits", f32, T * E), _ctx(ctx)))
+
+
+def moe_act_checkpoint(gu, row_w, rows, I, activation, h, codes, scales, ctx=None):
+    """gu [rows, N1] bf16 -> h [rows, I] bf16 and the MXFP8 checkpoint of gu (N1 = 2I for
+    "swiglu", I for "relu2")."""
+    a = _act(activation)
+    n1 = I if a == 1 else 2 * I
+    bf, u8 = "torch.bfloat16", "torch.uint8"
+    return _check(load().moe_act_checkpoint(
+        _tensor(gu, "gu", bf, rows * n1), _tensor(row_w, "row_w", "torch.float32", rows), rows, I, a,
+        _tensor(h, "h", bf, rows * I), _tensor(codes, "codes", u8, rows * n1),
+        _tensor(scales, "scales", u8, rows * n1 // 32), _ctx(ctx)))
+
+
+def moe_act_backward(codes, scales, dh, row_w, rows, I, activation, d_gu, h=None, d_row_w=None, ctx=None):
+    """The checkpoint and dh [rows, I] bf16 -> d_gu [rows, N1] bf16, the activations h again and
+    the row weights' gradient d_row_w [rows] fp32."""
+    a = _act(activation)
+    n1 = I if a == 1 else 2 * I
+    bf, u8, f32 = "torch.bfloat16", "torch.uint8", "torch.float32"
+    return _check(load().moe_act_backward(
+        _tensor(codes, "codes", u8, rows * n1), _tensor(scales, "scales", u8, rows * n1 // 32),
+        _tensor(dh, "dh", bf, rows * I), _tensor(row_w, "row_w", f32, rows), rows, I, a,
+        _tensor(d_gu, "d_gu", bf, rows * n1), _tensor(h, "h", bf, rows * I),
+        _tensor(d_row_w, "d_row_w", f32, rows), _ctx(ctx)))
 
 
 def moe_debug_stall_tensor_kernels(stall_ns: int) -> None:

@@ -1,0 +1,256 @@
+// The expert activation with an MXFP8 checkpoint, and its backward pass from the checkpoint.
+//
+// Forward, per row of pre-activations z (SwiGLU: gate | up, 2I values; relu^2: I values) with
+// an optional row weight w:
+//   h = w * silu(g) * u   or   h = w * max(z, 0)^2           (fp32, rounded once to bf16)
+//   checkpoint = MXFP8(z): E4M3 codes and one E8M0 scale per 32 values (mx_quant.cuh)
+// Backward, with z~ the checkpoint's values, s = sigmoid(g~) and a the activation of z~:
+//   d g = w dh u~ s (1 + g~ (1 - s)),  d u = w dh g~ s   or   d z = 2 w dh max(z~, 0)
+//   d w = sum_i dh_i a_i,  h~ = w a (the operand of the weight gradient, recomputed)
+// The checkpoint keeps 33/64 of the bytes of bf16 pre-activations between the passes.
+//
+// Both are streams: the forward reads 2 N1 and writes 2 I + 33/32 N1 bytes per row, the
+// backward reads 33/32 N1 + 2 I and writes 2 N1 + 2 I (N1 = 2I or I), and nothing is read
+// twice.  A thread owns eight consecutive columns (16 bytes of bf16, 8 of codes), so the four
+// lanes of a quad own one 32-value block of each half: its maximum takes two shuffles.  A
+// row's columns belong to one warp (LANES < 32 lanes of it for narrow rows), or with few rows
+// to one block, and d w is a shuffle reduction over them in a fixed order.
+#include <cuda_fp8.h>
+
+#include "moe_common.cuh"
+#include "moe_launch.h"
+#include "mx_quant.cuh"
+
+namespace {
+
+using moe_launch::ActBackward;
+using moe_launch::ActCheckpoint;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr unsigned kAll = 0xffffffffu;
+
+MOE_DEV void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+MOE_DEV uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// MXFP8 of a 32-value block held eight values a lane by four neighbouring lanes (all of which
+// call): this lane's codes, and the block's scale byte.  The rule of mxq::quant32.
+MOE_DEV uint2 quant8(const float (&v)[8], uint32_t& scale) {
+  float amax = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    nan |= v[i] != v[i];
+    amax = fmaxf(amax, fabsf(v[i]));
+  }
+  if (nan) amax = __uint_as_float(0x7fffffffu);  // above infinity as an integer
+  uint32_t b = __float_as_uint(amax);
+  b = max(b, __shfl_xor_sync(kAll, b, 1));
+  b = max(b, __shfl_xor_sync(kAll, b, 2));
+  if (b > 0x7f800000u) {
+    scale = 255u;
+    return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+  const int e = mxq::block_exponent(__uint_as_float(b));
+  scale = (uint32_t)(e + 127);
+  const float inv = e >= 127 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(127 - e) << 23);
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// Eight E4M3 codes under one E8M0 scale -> their values (exact).
+MOE_DEV void dequant8(uint2 c, uint32_t scale, float (&v)[8]) {
+  const float s = moe::e8m0_to_f32(scale);
+  uint32_t h[4];
+  moe::e4m3x4_to_f16x2(c.x, h[0], h[1]);
+  moe::e4m3x4_to_f16x2(c.y, h[2], h[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    v[2 * i] = f.x * s;
+    v[2 * i + 1] = f.y * s;
+  }
+}
+
+MOE_DEV float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+// The rows of a block: WIDE = the whole block on one row, otherwise 32 / LANES rows a warp.
+template <int LANES, bool WIDE>
+struct Map {
+  static constexpr int kRowsPerBlock = WIDE ? 1 : kWarps * (32 / LANES);
+  static constexpr int kStep = WIDE ? kThreads : LANES;  // columns of eight per turn
+  MOE_DEV static int64_t row() {
+    if (WIDE) return blockIdx.x;
+    return (int64_t)blockIdx.x * kRowsPerBlock + threadIdx.x / LANES;
+  }
+  MOE_DEV static int col() { return WIDE ? threadIdx.x : threadIdx.x % LANES; }
+};
+
+template <bool GATED, int LANES, bool WIDE>
+__global__ void __launch_bounds__(kThreads) act_checkpoint_kernel(ActCheckpoint a) {
+  using M = Map<LANES, WIDE>;
+  const int64_t row = M::row();
+  const bool in = row < a.rows;
+  const int units = a.I / 8;
+  const int64_t N1 = GATED ? 2 * (int64_t)a.I : a.I;
+  const float w = !in ? 0.f : (a.row_w ? a.row_w[row] : 1.f);
+  const uint4* zg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.gu) + row * N1);
+  uint4* h = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.h) + row * a.I);
+  uint2* codes = reinterpret_cast<uint2*>(a.codes + row * N1);
+  uint8_t* scales = a.scales + row * (N1 / 32);
+  // every lane makes every turn: the shuffles of a quad need its four lanes
+  for (int c0 = 0; c0 < units; c0 += M::kStep) {
+    const int c = c0 + M::col();
+    const bool live = in && c < units;
+    float g[8], u[8], o[8];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    // a row of weight 0 is left out: nothing of it is read, its outputs are zeros
+    unpack8(live && w != 0.f ? __ldcs(zg + c) : zero, g);
+    if (GATED) unpack8(live && w != 0.f ? __ldcs(zg + units + c) : zero, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = w == 0.f ? 0.f : w * (GATED ? moe::silu(g[i]) * u[i] : moe::relu2(g[i]));
+    uint32_t sg, su = 0;
+    const uint2 cg = quant8(g, sg);
+    uint2 cu = make_uint2(0, 0);
+    if (GATED) cu = quant8(u, su);
+    if (live) {
+      if (a.h) __stcs(h + c, pack8(o));
+      codes[c] = cg;
+      if (GATED) codes[units + c] = cu;
+      if ((c & 3) == 0) {
+        scales[c >> 2] = (uint8_t)sg;
+        if (GATED) scales[(units + c) >> 2] = (uint8_t)su;
+      }
+    }
+  }
+}
+
+template <bool GATED, int LANES, bool WIDE>
+__global__ void __launch_bounds__(kThreads) act_backward_kernel(ActBackward a) {
+  using M = Map<LANES, WIDE>;
+  const int64_t row = M::row();
+  const bool in = row < a.rows;
+  const int units = a.I / 8;
+  const int64_t N1 = GATED ? 2 * (int64_t)a.I : a.I;
+  const float w = !in ? 0.f : (a.row_w ? a.row_w[row] : 1.f);
+  const uint2* codes = reinterpret_cast<const uint2*>(a.codes + row * N1);
+  const uint8_t* scales = a.scales + row * (N1 / 32);
+  const uint4* dh = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dh) + row * a.I);
+  uint4* dz = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d_gu) + row * N1);
+  uint4* h = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.h) + row * a.I);
+  float dot = 0.f;
+  for (int c = M::col(); c < units; c += M::kStep) {
+    if (!in) break;
+    float dg[8], du[8], o[8];
+    if (w == 0.f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dg[i] = du[i] = o[i] = 0.f;
+    } else {
+      float g[8], u[8], d[8];
+      unpack8(__ldcs(dh + c), d);
+      dequant8(__ldcs(codes + c), scales[c >> 2], g);
+      if (GATED) dequant8(__ldcs(codes + units + c), scales[(units + c) >> 2], u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = w * d[i];
+        if (GATED) {
+          const float s = sigmoid(g[i]), gs = g[i] * s;
+          dot += d[i] * (gs * u[i]);
+          o[i] = w * (gs * u[i]);
+          du[i] = t * gs;
+          dg[i] = t * u[i] * (s + gs * (1.f - s));
+        } else {
+          const float r = g[i] < 0.f ? 0.f : g[i];
+          dot += d[i] * (r * r);
+          o[i] = w * (r * r);
+          dg[i] = 2.f * t * r;
+        }
+      }
+    }
+    __stcs(dz + c, pack8(dg));
+    if (GATED) __stcs(dz + units + c, pack8(du));
+    if (a.h) __stcs(h + c, pack8(o));
+  }
+  if (a.d_row_w == nullptr) return;
+#pragma unroll
+  for (int o = (WIDE ? 32 : LANES) / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(kAll, dot, o);
+  if (WIDE) {
+    __shared__ float red[kWarps];
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
+    __syncthreads();
+    dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) dot += red[i];
+    if (threadIdx.x == 0) a.d_row_w[row] = dot;
+  } else if (in && threadIdx.x % LANES == 0) {
+    a.d_row_w[row] = dot;
+  }
+}
+
+// A block per row below this many rows (a warp per row would leave SMs empty), otherwise
+// 32, 16, 8 or 4 lanes per row: the fewest that hold it in one turn, at most a warp.
+constexpr int64_t kWideBelow = 1024;
+
+template <bool GATED, typename Args, typename F>
+cudaError_t pick(const Args& a, F launch) {
+  const int units = a.I / 8;
+  if (a.rows < kWideBelow && units > 32) return launch(std::integral_constant<int, 32>{}, std::true_type{});
+  if (units <= 4) return launch(std::integral_constant<int, 4>{}, std::false_type{});
+  if (units <= 8) return launch(std::integral_constant<int, 8>{}, std::false_type{});
+  if (units <= 16) return launch(std::integral_constant<int, 16>{}, std::false_type{});
+  return launch(std::integral_constant<int, 32>{}, std::false_type{});
+}
+
+template <bool GATED>
+cudaError_t checkpoint(const ActCheckpoint& a, cudaStream_t s) {
+  return pick<GATED>(a, [&](auto lanes, auto wide) {
+    using M = Map<decltype(lanes)::value, decltype(wide)::value>;
+    const int64_t blocks = (a.rows + M::kRowsPerBlock - 1) / M::kRowsPerBlock;
+    act_checkpoint_kernel<GATED, decltype(lanes)::value, decltype(wide)::value><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+template <bool GATED>
+cudaError_t backward(const ActBackward& a, cudaStream_t s) {
+  return pick<GATED>(a, [&](auto lanes, auto wide) {
+    using M = Map<decltype(lanes)::value, decltype(wide)::value>;
+    const int64_t blocks = (a.rows + M::kRowsPerBlock - 1) / M::kRowsPerBlock;
+    act_backward_kernel<GATED, decltype(lanes)::value, decltype(wide)::value><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace
+
+namespace moe_launch {
+
+cudaError_t act_checkpoint(const ActCheckpoint& a, cudaStream_t stream) {
+  if (a.rows == 0) return cudaSuccess;
+  return a.gated ? checkpoint<true>(a, stream) : checkpoint<false>(a, stream);
+}
+
+cudaError_t act_backward(const ActBackward& a, cudaStream_t stream) {
+  if (a.rows == 0) return cudaSuccess;
+  return a.gated ? backward<true>(a, stream) : backward<false>(a, stream);
+}
+
+}  // namespace moe_launch

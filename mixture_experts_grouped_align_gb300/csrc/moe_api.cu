@@ -635,6 +635,83 @@ moe_status moe_wgrad(const void* grad, const void* input, int32_t input_per_pair
   return st;
 }
 
+size_t moe_router_loss_workspace_size(int32_t E) {
+  return E >= 1 && E <= 1024 ? moe_launch::router_loss_workspace_bytes(E) : 0;
+}
+
+moe_status moe_router_loss(const float* logits, const int32_t* topk_ids, const float* topk_w, const float* d_topk_w,
+                           const uint8_t* token_mask, int64_t T, int32_t k, int32_t E, float balance_coef,
+                           float z_coef, int32_t* counts, float* prob_mean, float* loss, float* d_logits,
+                           const moe_ctx* ctx) {
+  MOE_REQUIRE(k >= 1 && k <= 32 && E >= k && E <= 1024, MOE_ERR_UNSUPPORTED,
+              "need 1 <= k <= 32 and k <= E <= 1024 (k=%d, E=%d)", k, E);
+  MOE_REQUIRE(T >= 0, MOE_ERR_INVALID_ARG, "T must be >= 0");
+  MOE_REQUIRE(pairs_fit(T, k), MOE_ERR_UNSUPPORTED, "T*k must be < 2^31");
+  MOE_REQUIRE((logits && topk_ids) || T == 0, MOE_ERR_INVALID_ARG, "null logits or topk_ids");
+  MOE_REQUIRE(loss, MOE_ERR_INVALID_ARG, "null loss");
+  MOE_REQUIRE(topk_w || !d_topk_w, MOE_ERR_INVALID_ARG, "d_topk_w needs topk_w");
+  MOE_REQUIRE(aligned16(logits) && aligned16(topk_ids) && aligned16(topk_w) && aligned16(d_topk_w) &&
+                  aligned16(token_mask) && aligned16(counts) && aligned16(prob_mean) && aligned16(loss) &&
+                  aligned16(d_logits),
+              MOE_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+  const size_t need = moe_router_loss_workspace_size(E);
+  MOE_REQUIRE(ctx && ctx->workspace && ctx->workspace_bytes >= need && aligned16(ctx->workspace), MOE_ERR_CAPACITY,
+              "workspace of %zu bytes needed", need);
+  moe_launch::RouterLoss a{};
+  a.logits = logits; a.ids = topk_ids; a.w = topk_w; a.dw = d_topk_w; a.mask = token_mask;
+  a.T = T; a.k = k; a.E = E; a.balance_coef = balance_coef; a.z_coef = z_coef;
+  a.counts = counts; a.prob_mean = prob_mean; a.loss = loss; a.d_logits = d_logits;
+  a.ws = ctx->workspace; a.status = status_of(ctx);
+  rec(ctx, 0, 2);
+  const moe_status st = cuda_status(moe_launch::router_loss(a, stream_of(ctx)), "moe_router_loss");
+  rec(ctx, 1, 2);
+  return st;
+}
+
+static moe_status check_act(int64_t rows, int32_t I, int32_t activation) {
+  MOE_REQUIRE(activation == MOE_ACT_SWIGLU || activation == MOE_ACT_RELU2, MOE_ERR_INVALID_ARG,
+              "unknown activation");
+  MOE_REQUIRE(rows >= 0 && rows < ((int64_t)1 << 31), MOE_ERR_INVALID_ARG, "rows must be in [0, 2^31)");
+  MOE_REQUIRE(I >= 32 && I % 32 == 0 && I <= (1 << 29), MOE_ERR_UNSUPPORTED, "I must be a positive multiple of 32");
+  return MOE_OK;
+}
+
+moe_status moe_act_checkpoint(const void* gu, const float* row_w, int64_t rows, int32_t I, int32_t activation,
+                              void* h, uint8_t* codes, uint8_t* scales, const moe_ctx* ctx) {
+  moe_status st = check_act(rows, I, activation);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(gu && codes && scales, MOE_ERR_INVALID_ARG, "null tensor pointer");
+  MOE_REQUIRE(aligned16(gu) && aligned16(row_w) && aligned16(h) && aligned16(codes) && aligned16(scales),
+              MOE_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+  moe_launch::ActCheckpoint a{};
+  a.gu = gu; a.row_w = row_w; a.rows = rows; a.I = I; a.gated = activation == MOE_ACT_SWIGLU;
+  a.h = h; a.codes = codes; a.scales = scales;
+  rec(ctx, 0, 2);
+  st = cuda_status(moe_launch::act_checkpoint(a, stream_of(ctx)), "moe_act_checkpoint");
+  rec(ctx, 1, 2);
+  return st;
+}
+
+moe_status moe_act_backward(const uint8_t* codes, const uint8_t* scales, const void* dh, const float* row_w,
+                            int64_t rows, int32_t I, int32_t activation, void* d_gu, void* h, float* d_row_w,
+                            const moe_ctx* ctx) {
+  moe_status st = check_act(rows, I, activation);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  MOE_REQUIRE(codes && scales && dh && d_gu, MOE_ERR_INVALID_ARG, "null tensor pointer");
+  MOE_REQUIRE(aligned16(codes) && aligned16(scales) && aligned16(dh) && aligned16(row_w) && aligned16(d_gu) &&
+                  aligned16(h) && aligned16(d_row_w),
+              MOE_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+  moe_launch::ActBackward a{};
+  a.codes = codes; a.scales = scales; a.dh = dh; a.row_w = row_w; a.rows = rows; a.I = I;
+  a.gated = activation == MOE_ACT_SWIGLU; a.d_gu = d_gu; a.h = h; a.d_row_w = d_row_w;
+  rec(ctx, 0, 2);
+  st = cuda_status(moe_launch::act_backward(a, stream_of(ctx)), "moe_act_backward");
+  rec(ctx, 1, 2);
+  return st;
+}
+
 void moe_debug_stall_tensor_kernels(int64_t stall_ns) {
   moe_launch::g_debug_stall_ns.store(stall_ns > 0 ? stall_ns : 0, std::memory_order_relaxed);
 }

@@ -185,4 +185,49 @@ int wgrad_tc_tile(const Wgrad& g);
 bool wgrad_tc_slot_feed(const Wgrad& g);
 cudaError_t wgrad_tc(const Wgrad& g, cudaStream_t stream);
 
+// ---- router losses (router_loss.cu)
+struct RouterLoss {
+  const float* logits;   // [T, E]
+  const int32_t* ids;    // [T, k]
+  const float* w;        // [T, k] routing weights (with dw)
+  const float* dw;       // [T, k] their gradient, or null
+  const uint8_t* mask;   // [T] or null
+  int64_t T;
+  int k, E;
+  float balance_coef, z_coef;
+  int32_t* counts;       // [E] or null
+  float* prob_mean;      // [E] or null
+  float* loss;           // [3]
+  float* d_logits;       // [T, E] or null
+  void* ws;
+  int32_t* status;
+  int count_blocks;      // set by the launcher
+};
+size_t router_loss_workspace_bytes(int E);
+cudaError_t router_loss(RouterLoss a, cudaStream_t stream);
+
+// ---- expert activation with an MXFP8 checkpoint (act_checkpoint.cu)
+struct ActCheckpoint {
+  const void* gu;        // [rows, N1] bf16, N1 = 2I (gated) or I
+  const float* row_w;    // [rows] or null
+  int64_t rows;
+  int I, gated;
+  void* h;               // [rows, I] bf16 or null
+  uint8_t* codes;        // [rows, N1]
+  uint8_t* scales;       // [rows, N1 / 32]
+};
+struct ActBackward {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const void* dh;        // [rows, I] bf16
+  const float* row_w;
+  int64_t rows;
+  int I, gated;
+  void* d_gu;            // [rows, N1] bf16
+  void* h;               // [rows, I] bf16 or null
+  float* d_row_w;        // [rows] or null
+};
+cudaError_t act_checkpoint(const ActCheckpoint& a, cudaStream_t stream);
+cudaError_t act_backward(const ActBackward& a, cudaStream_t stream);
+
 }  // namespace moe_launch

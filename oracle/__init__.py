@@ -19,7 +19,9 @@ import this package.  It shares no code with the CUDA library and never imports 
 
 Modules: ``formats`` (E2M1 / E4M3 / E8M0 / bf16 decoding), ``route`` (top-k routing),
 ``align`` (token-to-expert alignment), ``bucket`` (token-dimension buckets and padding),
-``layer`` (grouped GEMMs, SwiGLU, combine), ``wgrad`` (per-expert weight gradient).
+``layer`` (grouped GEMMs, SwiGLU, combine), ``wgrad`` (per-expert weight gradient),
+``router_loss`` (balance and z losses with the logits' gradient), ``activation`` (the expert
+activation from an MXFP8 checkpoint, forward and backward).
 Every function is pinned by ``tests/test_oracle_*.py`` against closed forms, library
 routines, brute force on tiny inputs or properties the pages state.
 """
