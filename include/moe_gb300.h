@@ -9,7 +9,9 @@
  * group sizes (moe_gemm_per_token); and the per-expert weight gradient (moe_wgrad).  Around
  * that path, for training: the router's auxiliary losses with their gradient
  * (moe_router_loss) and the expert activation with an MXFP8 checkpoint and its backward pass
- * (moe_act_checkpoint, moe_act_backward).
+ * (moe_act_checkpoint, moe_act_backward); and, for the dense layers beside the experts (a
+ * shared expert, the router's projection), a matrix product with bias, activation and residual
+ * in its epilogue and its backward products (moe_dense_gemm, moe_dense_bias_grad).
  *
  * Sources of the definitions (pull-request pages):
  *  [BUCKET] "Bound Triton MoE JIT specializations via token-dim bucketing and warmup",
@@ -157,7 +159,8 @@ moe_status moe_bucket_pad(int64_t T, moe_quant quant, int64_t* T_pad,
  * (the Nemotron recipe in its table of added files: GEMM1 N = 1856 = I, no gate product). */
 typedef enum {
   MOE_ACT_SWIGLU = 0,     /* h = silu(gate) * up; GEMM1 has 2I rows (gate | up)           */
-  MOE_ACT_RELU2 = 1       /* h = max(a, 0)^2;     GEMM1 has I rows                        */
+  MOE_ACT_RELU2 = 1,      /* h = max(a, 0)^2;     GEMM1 has I rows                        */
+  MOE_ACT_NONE = 2        /* moe_dense_gemm only: no activation                           */
 } moe_activation;
 
 /* N1 = 2I for MOE_ACT_SWIGLU, I for MOE_ACT_RELU2. */
@@ -431,13 +434,41 @@ moe_status moe_act_backward(const uint8_t* codes, const uint8_t* scales, const v
                             const moe_ctx* ctx);
 
 /* ------------------------------------------------------------------------------------ *
+ * Dense matrix product with bias, activation and residual                                *
+ * ------------------------------------------------------------------------------------ */
+
+#define MOE_W_NK 0 /* w [N1, K]: a layer's forward weight                                  */
+#define MOE_W_KN 1 /* w [K, N1]: contracted over its rows, e.g. dx = dz . W with the forward
+                      weight of a layer of K outputs and N inputs                          */
+
+/* out = act(x . W^T + bias) + residual_scale * residual
+ * x [M, K] bf16; w bf16 in layout w_layout; bias [N1] bf16 or NULL; residual [M, N] in out's
+ * type or NULL; out [M, N] bf16 (out_f32 == 0) or fp32.  activation: MOE_ACT_NONE or
+ * MOE_ACT_RELU2 (N1 = N), or MOE_ACT_SWIGLU (N1 = 2N: gate features 0..N-1, up N..2N-1;
+ * silu(gate) * up).  Everything after the products is in fp32 and rounded once.  residual may be
+ * out itself (accumulation in place); out must not overlap x or w.
+ * Limits: K a multiple of 8; w_layout MOE_W_KN: N a multiple of 8; M, N1, K < 2^30.  Any M
+ * (0: nothing is done) and, for MOE_W_NK, any N.  An output depends on its own row of x only
+ * and is summed in one fixed order for given M, N, K (which choose the kernel): repeated calls
+ * give identical bits.  Needs no workspace.
+ * Backward: dx = moe_dense_gemm(dz, w, the other layout), with the residual path's gradient as
+ * residual; dW = moe_wgrad with E = 1 and k = 1; the bias's gradient: moe_dense_bias_grad. */
+moe_status moe_dense_gemm(const void* x, const void* w, int32_t w_layout, const void* bias, const void* residual,
+                          float residual_scale, int64_t M, int32_t N, int32_t K, int32_t activation, void* out,
+                          int32_t out_f32, const moe_ctx* ctx);
+
+/* d_bias[n] = sum_m dz[m, n]: dz [M, N] bf16, d_bias [N] fp32, summed in fp32 in a fixed order.
+ * M = 0 gives zeros.  Needs no workspace. */
+moe_status moe_dense_bias_grad(const void* dz, int64_t M, int32_t N, float* d_bias, const moe_ctx* ctx);
+
+/* ------------------------------------------------------------------------------------ *
  * Diagnostics: failure detection of the bounded waits                                    *
  * ------------------------------------------------------------------------------------ */
 
 /* Self-test switch of the tensor-memory kernels' failure detection (their waits on
  * mbarriers are bounded and report MOE_ERR_TIMEOUT instead of hanging).  With stall_ns > 0,
  * every later launch of the W4A16 and MXFP8 tensor-memory grouped GEMMs in this process
- * (moe_forward above 256 rows, moe_grouped_gemm in MXFP8) runs with its copy and MMA roles
+ * (moe_forward above 256 rows, moe_grouped_gemm in MXFP8) and of moe_dense_gemm runs with its copy and MMA roles
  * switched off: the other roles wait on barriers that nothing arrives on, give up after
  * stall_ns nanoseconds, write MOE_ERR_TIMEOUT to ctx->dev_status, free their tensor memory
  * and return; no copy or MMA is in flight when they give up, and the context stays usable.

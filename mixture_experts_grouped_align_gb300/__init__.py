@@ -22,7 +22,7 @@ __all__ = [
     "moe_forward_no_alloc", "moe_grouped_gemm", "moe_grouped_gemm_workspace_size", "moe_mx_quantize",
     "moe_gemm_per_token", "moe_wgrad", "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels",
     "moe_router_loss", "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward",
-    "EXPORTED_SYMBOLS",
+    "moe_dense_gemm", "moe_dense_bias_grad", "W_LAYOUT", "EXPORTED_SYMBOLS",
 ]
 
 MOE_OK = 0
@@ -31,14 +31,16 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_WARN_PAD_IGNORED", -1: "MOE_ERR_INVALID_ARG
                 -2: "MOE_ERR_UNSUPPORTED", -3: "MOE_ERR_CAPACITY", -4: "MOE_ERR_CUDA",
                 -5: "MOE_ERR_INVALID_EXPERT", -6: "MOE_ERR_RANGE", -7: "MOE_ERR_TIMEOUT"}
 QUANT = {"bf16": 0, "mxfp4": 1, "mxfp8": 2}
-ACTIVATION = {"swiglu": 0, "relu2": 1}
+ACTIVATION = {"swiglu": 0, "relu2": 1, "none": 2}
+W_LAYOUT = {"nk": 0, "kn": 1}
 
 EXPORTED_SYMBOLS = [
     "moe_last_error", "moe_align_capacity", "moe_align", "moe_bucket", "moe_bucket_count",
     "moe_bucket_pad", "moe_forward_workspace_size", "moe_forward", "moe_forward_no_alloc",
     "moe_grouped_gemm", "moe_grouped_gemm_workspace_size", "moe_mx_quantize", "moe_gemm_per_token", "moe_wgrad",
     "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels", "moe_router_loss",
-    "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward",
+    "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward", "moe_dense_gemm",
+    "moe_dense_bias_grad",
 ]
 
 
@@ -98,6 +100,8 @@ def load(path: str | None = None):
         "moe_router_loss": (I32, [P, P, P, P, P, I64, I32, I32, F32, F32, P, P, P, P, P]),
         "moe_act_checkpoint": (I32, [P, P, I64, I32, I32, P, P, P, P]),
         "moe_act_backward": (I32, [P, P, P, P, I64, I32, I32, P, P, P, P]),
+        "moe_dense_gemm": (I32, [P, P, I32, P, P, F32, I64, I32, I32, I32, P, I32, P]),
+        "moe_dense_bias_grad": (I32, [P, I64, I32, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -311,6 +315,30 @@ def moe_act_backward(codes, scales, dh, row_w, rows, I, activation, d_gu, h=None
         _tensor(dh, "dh", bf, rows * I), _tensor(row_w, "row_w", f32, rows), rows, I, a,
         _tensor(d_gu, "d_gu", bf, rows * n1), _tensor(h, "h", bf, rows * I),
         _tensor(d_row_w, "d_row_w", f32, rows), _ctx(ctx)))
+
+
+def moe_dense_gemm(x, w, w_layout, bias, residual, residual_scale, M, N, K, activation, out, ctx=None,
+                   out_f32=None):
+    """out [M, N] = act(x [M, K] . W^T + bias) + residual_scale * residual.  w_layout "nk" (w [N1, K])
+    or "kn" (w [K, N1]); activation "none", "relu2" or "swiglu" (N1 = 2N).  out is bf16 or fp32
+    (``out_f32`` says which for a raw pointer), residual of the same type."""
+    a = _act(activation)
+    n1 = 2 * N if a == 0 else N
+    lay = W_LAYOUT[w_layout] if isinstance(w_layout, str) else int(w_layout)
+    bf = "torch.bfloat16"
+    if out_f32 is None:
+        out_f32 = not isinstance(out, int) and out is not None and str(out.dtype) == "torch.float32"
+    ot = "torch.float32" if out_f32 else bf
+    return _check(load().moe_dense_gemm(
+        _tensor(x, "x", bf, M * K), _tensor(w, "w", bf, n1 * K), lay, _tensor(bias, "bias", bf, n1),
+        _tensor(residual, "residual", ot, M * N), residual_scale, M, N, K, a, _tensor(out, "out", ot, M * N),
+        int(out_f32), _ctx(ctx)))
+
+
+def moe_dense_bias_grad(dz, M, N, d_bias, ctx=None):
+    """d_bias [N] fp32 = the column sums of dz [M, N] bf16."""
+    return _check(load().moe_dense_bias_grad(_tensor(dz, "dz", "torch.bfloat16", M * N), M, N,
+                                             _tensor(d_bias, "d_bias", "torch.float32", N), _ctx(ctx)))
 
 
 def moe_debug_stall_tensor_kernels(stall_ns: int) -> None:

@@ -1,0 +1,379 @@
+// Dense matrix product with its bias, activation and residual in the epilogue, on tcgen05.
+//
+//   z = x . W^T + b;   out = act(z) + residual_scale * residual
+// x [M, K] bf16; W stored [N1, K] or (contracted over its rows, as an input gradient needs the
+// forward weight) [K, N1]; act = none, relu^2 or SwiGLU (N1 = 2N: gate features, then up).
+// fp32 accumulation, one rounding to the output type.
+//
+// Bound: 2 M N1 K operations on the tensor cores (the operands are read about once through L2:
+// a 128 x 256 tile does 85 operations per operand byte it loads).  Persistent blocks, one per
+// SM, over 128 x 256 tiles (SwiGLU: 128 gate and 128 up columns, so both lie in the same TMEM
+// lane and thread), two fp32 accumulators of 256 TMEM columns so that a tile's epilogue runs
+// under the next tile's products:
+//   warp 0  loads a stage (64 of K: 128 rows of x and 256 of W, 48 KB) by TMA, four stages;
+//   warp 1  issues the MMAs (M 128, N 256, K 16) from one lane;
+//   warps 4..11  drain the accumulator, two per TMEM lane quarter with half of the columns
+//           each: bias, activation, residual (a TMA box loaded into the staging box the result
+//           then replaces), rounding, and a TMA store of 32 rows x 128 bytes, which drops what
+//           lies past M or N.  Rows of out that are no multiple of 16 bytes are stored by
+//           plain stores instead.
+// Tiles are taken sixteen row tiles at a time, the column tile slower, so that the blocks
+// running at once share their operands in L2.
+// Every wait is bounded; one that runs out sets MOE_ERR_TIMEOUT, all roles leave their loops,
+// and the loads in flight are waited for before the block ends.
+#include "dense_common.cuh"
+
+namespace {
+
+using namespace dense;
+
+constexpr int kThreads = 384;
+constexpr int kBM = 128, kBN = 256;
+constexpr int kStages = 4;
+constexpr int kA = 0, kB = kBM * 128, kSlot = (kBM + kBN) * 128;
+constexpr int kStg = kStages * kSlot;           // staging boxes, 4 KB per epilogue warp
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kBars = kStg + kEpiWarps * 4096;
+constexpr int kSmem = kBars + 256 + 1024;
+constexpr int kGroupM = 16;
+
+struct Tiles {
+  int64_t m, n, total;
+};
+
+__device__ __forceinline__ void tile_of(const Tiles& ts, int64_t t, int64_t& mt, int64_t& nt) {
+  const int64_t per = kGroupM * ts.n, g = t / per, r = t - g * per;
+  const int64_t rows = ts.m - g * kGroupM < kGroupM ? ts.m - g * kGroupM : kGroupM;
+  nt = r / rows;
+  mt = g * kGroupM + (r - nt * rows);
+}
+
+// Bias of the 8 features n .. n + 7 (zeros past N); `base` is the first feature's index.
+__device__ __forceinline__ void bias8(const void* bias, int64_t base, int64_t n, int64_t N, bool vec, float (&b)[8]) {
+  if (vec && n + 8 <= N) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(bias) + base + n));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      b[2 * i] = __uint_as_float(w[i] << 16);
+      b[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = n + i < N ? bias_at(bias, base + n + i) : 0.f;
+  }
+}
+
+template <bool GATED, bool F32>
+__global__ void __launch_bounds__(kThreads, 1)
+    dense_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_r, Dense d,
+                      Tiles ts) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBars);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;   // [2]
+  uint64_t* tempty = tfull + 2;        // [2]
+  uint64_t* drain = tempty + 2;
+  uint64_t* rfull = drain + 1;         // [kEpiWarps] residual box landed
+  uint32_t* taddr_s = reinterpret_cast<uint32_t*>(rfull + kEpiWarps);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(taddr_s + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&tfull[i], 1);
+      tc::mbar_init(&tempty[i], kEpiWarps);
+    }
+    tc::mbar_init(drain, 1);
+    for (int i = 0; i < kEpiWarps; ++i) tc::mbar_init(&rfull[i], 1);
+    *abort_flag = 0;
+    tc::mbar_fence_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(taddr_s, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t taddr = *taddr_s, smem_s = tc::smem_addr(smem);
+  const int nk = (d.K + kBK - 1) / kBK;
+  const bool kn = d.w_kn != 0;
+  const uint64_t wb = d.wait_ns > 0 ? (uint64_t)d.wait_ns : tc::kWaitNs;
+  constexpr int kOutN = GATED ? 128 : kBN;  // output columns of a tile
+
+  if (warp == 0 && !d.stall) {
+    // ------------------------------------------------------------------ loads
+    if (lane == 0) {
+      tma::prefetch_map(&tm_x);
+      tma::prefetch_map(&tm_w);
+      uint32_t it = 0;
+      for (int64_t t = blockIdx.x; t < ts.total && !*abort_flag; t += gridDim.x) {
+        int64_t mt, nt;
+        tile_of(ts, t, mt, nt);
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!tc::mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, wb)) {
+            moe::set_status(d.status, MOE_ERR_TIMEOUT);
+            *abort_flag = 1;
+            break;
+          }
+          const uint32_t sl = smem_s + s * kSlot;
+          tma::mbar_arrive_expect_tx(&full[s], kSlot);
+          tma::load_2d(sl + kA, &tm_x, kb * 128, (int32_t)(mt * kBM), &full[s]);
+          if (GATED) {
+            load_w(sl + kB, &tm_w, kn, nt * 128, 128, kb, &full[s]);
+            load_w(sl + kB + 128 * 128, &tm_w, kn, d.N + nt * 128, 128, kb, &full[s]);
+          } else {
+            load_w(sl + kB, &tm_w, kn, nt * kBN, kBN, kb, &full[s]);
+          }
+        }
+      }
+      // every load lands before the block may end, also when another role has given up
+      for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
+        if (!tc::mbar_wait(&full[j % kStages], (j / kStages) & 1, wb)) moe::set_status(d.status, MOE_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp == 1 && !d.stall) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc = tc::idesc_f16(kBM, kBN, 1) | (kn ? 1u << 16 : 0u);
+      uint32_t it = 0, acc_it = 0;
+      for (int64_t t = blockIdx.x; t < ts.total && !*abort_flag; t += gridDim.x, ++acc_it) {
+        const uint32_t acc = acc_it & 1;
+        if (!tc::mbar_wait(&tempty[acc], ((acc_it >> 1) & 1) ^ 1, wb)) {
+          moe::set_status(d.status, MOE_ERR_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        tc::tc_fence_after();
+        bool ok = true;
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!tc::mbar_wait(&full[s], (it / kStages) & 1, wb)) {
+            moe::set_status(d.status, MOE_ERR_TIMEOUT);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t sl = smem_s + s * kSlot;
+#pragma unroll
+          for (int j = 0; j < kBK / 16; ++j)
+            tc::mma_f16_ss(taddr + acc * kBN, tc::sdesc_sw128(sl + kA + j * 32), w_desc(sl + kB, kn, j), idesc,
+                           (kb | j) != 0);
+          tc::mma_commit(&empty[s]);
+        }
+        if (!ok) break;
+        tc::mma_commit(&tfull[acc]);
+      }
+      tc::mma_commit(drain);
+      if (!tc::mbar_wait(drain, 0, wb)) moe::set_status(d.status, MOE_ERR_TIMEOUT);
+    }
+    __syncwarp();
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------------ epilogue
+    const int ew = warp - kEpiWarp0, quarter = warp & 3, half = ew >> 2;
+    constexpr int kCols = F32 ? 32 : 64;         // columns of a 128-byte staging row
+    const uint32_t box = smem_s + kStg + ew * 4096;
+    const bool vec = d.N % 8 == 0;
+    const bool res_box = d.residual != nullptr && d.tma_out;
+    uint32_t acc_it = 0, rph = 0;
+    for (int64_t t = blockIdx.x; t < ts.total && !*abort_flag; t += gridDim.x, ++acc_it) {
+      int64_t mt, nt;
+      tile_of(ts, t, mt, nt);
+      const uint32_t acc = acc_it & 1;
+      if (!tc::mbar_wait(&tfull[acc], (acc_it >> 1) & 1, wb)) {
+        moe::set_status(d.status, MOE_ERR_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
+      tc::tc_fence_after();
+      const uint32_t tb = taddr + acc * kBN + ((uint32_t)(quarter * 32) << 16);
+      const int64_t m0 = mt * kBM + quarter * 32, m = m0 + lane;
+      for (int c0 = half * (kOutN / 2); c0 < (half + 1) * (kOutN / 2); c0 += kCols) {
+        const int64_t n0 = nt * kOutN + c0;
+        if (n0 >= d.N || m0 >= d.M) continue;  // the same for the whole warp
+        if (lane == 0 && d.tma_out) {
+          tma::bulk_wait_read_all();  // the last store has read the box
+          if (res_box) {
+            tma::mbar_arrive_expect_tx(&rfull[ew], 4096);
+            tma::load_2d(box, &tm_r, (int32_t)(n0 * (F32 ? 4 : 2)), (int32_t)m0, &rfull[ew]);
+          }
+        }
+        __syncwarp();
+        bool have = !res_box;
+#pragma unroll
+        for (int b = 0; b < kCols; b += 32) {
+          uint32_t v[32], u[32];
+          tc::tmem_ld32(tb + c0 + b, v);
+          if (GATED) tc::tmem_ld32(tb + 128 + c0 + b, u);
+          tc::tmem_ld_wait();
+          if (!have) {
+            if (!tc::mbar_wait(&rfull[ew], rph, wb)) {
+              moe::set_status(d.status, MOE_ERR_TIMEOUT);
+              *abort_flag = 1;
+            }
+            have = true;
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {  // eight columns
+            const int64_t n = n0 + b + 8 * q;
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(v[8 * q + i]);
+            if (d.bias) {
+              float bb[8];
+              bias8(d.bias, 0, n, d.N, vec, bb);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] += bb[i];
+            }
+            if (GATED) {
+              float up[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) up[i] = __uint_as_float(u[8 * q + i]);
+              if (d.bias) {
+                float bb[8];
+                bias8(d.bias, d.N, n, d.N, vec, bb);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) up[i] += bb[i];
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = moe::silu(o[i]) * up[i];
+            } else if (d.relu2) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = moe::relu2(o[i]);
+            }
+            if (d.residual && !res_box) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (m < d.M && n + i < d.N) o[i] += d.residual_scale * residual_at(d, m * d.N + n + i);
+            }
+            if (F32) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t at = box + lane * 128 + (((2 * q + j) ^ (lane & 7)) << 4);
+                if (res_box) {
+                  float r[4];
+                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
+                               : "r"(at)
+                               : "memory");
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[4 * j + i] += d.residual_scale * r[i];
+                }
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(o[4 * j]), "f"(o[4 * j + 1]),
+                             "f"(o[4 * j + 2]), "f"(o[4 * j + 3])
+                             : "memory");
+              }
+            } else {
+              const uint32_t at = box + lane * 128 + (((b / 8 + q) ^ (lane & 7)) << 4);
+              if (res_box) {
+                uint32_t r[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                             : "r"(at)
+                             : "memory");
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  o[2 * i] += d.residual_scale * __uint_as_float(r[i] << 16);
+                  o[2 * i + 1] += d.residual_scale * __uint_as_float(r[i] & 0xffff0000u);
+                }
+              }
+              uint32_t pk[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+                pk[i] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pk[0]), "r"(pk[1]), "r"(pk[2]),
+                           "r"(pk[3])
+                           : "memory");
+            }
+          }
+        }
+        if (res_box) rph ^= 1;
+        if (d.tma_out) {
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma::store_2d(&tm_o, (int32_t)(n0 * (F32 ? 4 : 2)), (int32_t)m0, box);
+            tma::bulk_commit();
+          }
+        } else {  // rows of out not a multiple of 16 bytes: a row's columns by the lanes
+          __syncwarp();
+          const int rows = d.M - m0 < 32 ? (int)(d.M - m0) : 32;
+          const int cols = d.N - n0 < kCols ? (int)(d.N - n0) : kCols;
+          for (int r = 0; r < rows; ++r)
+            for (int c = lane; c < cols; c += 32) {
+              if (F32) {
+                uint32_t w;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(box + r * 128 + (((c >> 2) ^ (r & 7)) << 4) + (c & 3) * 4) : "memory");
+                static_cast<uint32_t*>(d.out)[(m0 + r) * d.N + n0 + c] = w;
+              } else {
+                uint16_t w;
+                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(box + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2) : "memory");
+                static_cast<uint16_t*>(d.out)[(m0 + r) * d.N + n0 + c] = w;
+              }
+            }
+          __syncwarp();
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&tempty[acc]);
+    }
+    if (lane == 0) tma::bulk_wait_all();
+    __syncwarp();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(taddr, 512);
+  }
+}
+
+template <bool GATED, bool F32>
+cudaError_t launch(const Dense& d, cudaStream_t stream) {
+  Tiles ts;
+  ts.m = (d.M + kBM - 1) / kBM;
+  ts.n = (d.N + (GATED ? 127 : kBN - 1)) / (GATED ? 128 : kBN);
+  ts.total = ts.m * ts.n;
+  const uint64_t K2 = (uint64_t)d.K * 2, N1 = GATED ? 2 * (uint64_t)d.N : (uint64_t)d.N;
+  CUtensorMap mx{}, mw{}, mo{}, mr{};
+  if (!tma::encode_2d_u8(&mx, d.x, K2, (uint64_t)d.M, K2, 128, kBM, true)) return cudaErrorInvalidValue;
+  const bool okw = d.w_kn ? tma::encode_2d_u8(&mw, d.w, N1 * 2, (uint64_t)d.K, N1 * 2, 128, kBK, true)
+                          : tma::encode_2d_u8(&mw, d.w, K2, N1, K2, 128, GATED ? 128 : kBN, true);
+  if (!okw) return cudaErrorInvalidValue;
+  if (d.tma_out) {
+    const uint64_t row = (uint64_t)d.N * (F32 ? 4 : 2);
+    if (!tma::encode_2d_u8(&mo, d.out, row, (uint64_t)d.M, row, 128, 32, true)) return cudaErrorInvalidValue;
+    if (d.residual && !tma::encode_2d_u8(&mr, d.residual, row, (uint64_t)d.M, row, 128, 32, true))
+      return cudaErrorInvalidValue;
+  }
+  cudaError_t err = cudaFuncSetAttribute(dense_gemm_kernel<GATED, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (err != cudaSuccess) return err;
+  const int64_t sms = moe_launch::sm_count_current();
+  dense_gemm_kernel<GATED, F32><<<(unsigned)(ts.total < sms ? ts.total : sms), kThreads, kSmem, stream>>>(mx, mw, mo, mr, d, ts);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace moe_launch {
+
+cudaError_t dense_gemm(Dense d, cudaStream_t stream) {
+  if (d.M == 0) return cudaSuccess;
+  if (dense_split_takes(d)) return dense_split(d, stream);
+  d.tma_out = ((int64_t)d.N * (d.out_f32 ? 4 : 2)) % 16 == 0;
+  if (d.gated) return d.out_f32 ? launch<true, true>(d, stream) : launch<true, false>(d, stream);
+  return d.out_f32 ? launch<false, true>(d, stream) : launch<false, false>(d, stream);
+}
+
+}  // namespace moe_launch

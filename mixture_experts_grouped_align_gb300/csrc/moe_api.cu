@@ -40,6 +40,11 @@ void apply_debug_stall(Wgrad& g) {
   g.wait_ns = ns > 0 ? ns : 0;
   g.stall = ns > 0 ? 1 : 0;
 }
+void apply_debug_stall(Dense& d) {
+  const int64_t ns = debug_stall_ns();
+  d.wait_ns = ns > 0 ? ns : 0;
+  d.stall = ns > 0 ? 1 : 0;
+}
 
 int sm_count_current() {
   constexpr int kMaxDev = 64;
@@ -708,6 +713,43 @@ moe_status moe_act_backward(const uint8_t* codes, const uint8_t* scales, const v
   a.gated = activation == MOE_ACT_SWIGLU; a.d_gu = d_gu; a.h = h; a.d_row_w = d_row_w;
   rec(ctx, 0, 2);
   st = cuda_status(moe_launch::act_backward(a, stream_of(ctx)), "moe_act_backward");
+  rec(ctx, 1, 2);
+  return st;
+}
+
+moe_status moe_dense_gemm(const void* x, const void* w, int32_t w_layout, const void* bias, const void* residual,
+                          float residual_scale, int64_t M, int32_t N, int32_t K, int32_t activation, void* out,
+                          int32_t out_f32, const moe_ctx* ctx) {
+  MOE_REQUIRE(activation == MOE_ACT_SWIGLU || activation == MOE_ACT_RELU2 || activation == MOE_ACT_NONE,
+              MOE_ERR_INVALID_ARG, "unknown activation");
+  MOE_REQUIRE(w_layout == MOE_W_NK || w_layout == MOE_W_KN, MOE_ERR_INVALID_ARG, "unknown weight layout");
+  MOE_REQUIRE(M >= 0 && N >= 1 && K >= 1, MOE_ERR_INVALID_ARG, "need M >= 0, N >= 1, K >= 1");
+  const int64_t most = (int64_t)1 << 30;
+  MOE_REQUIRE(M < most && N < most / 2 && K < most, MOE_ERR_UNSUPPORTED, "M, N1 and K must be < 2^30");
+  MOE_REQUIRE(K % 8 == 0, MOE_ERR_UNSUPPORTED, "K must be a multiple of 8");
+  MOE_REQUIRE(w_layout == MOE_W_NK || N % 8 == 0, MOE_ERR_UNSUPPORTED, "N must be a multiple of 8 for [K, N] weights");
+  if (M == 0) return MOE_OK;
+  MOE_REQUIRE(x && w && out, MOE_ERR_INVALID_ARG, "null tensor pointer");
+  MOE_REQUIRE(aligned16(x) && aligned16(w) && aligned16(bias) && aligned16(residual) && aligned16(out),
+              MOE_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+  moe_launch::Dense d{};
+  d.x = x; d.w = w; d.bias = bias; d.residual = residual; d.out = out; d.residual_scale = residual_scale;
+  d.M = M; d.N = N; d.K = K; d.w_kn = w_layout == MOE_W_KN; d.gated = activation == MOE_ACT_SWIGLU;
+  d.relu2 = activation == MOE_ACT_RELU2; d.out_f32 = out_f32 ? 1 : 0; d.status = status_of(ctx);
+  moe_launch::apply_debug_stall(d);
+  rec(ctx, 0, 2);
+  const moe_status st = cuda_status(moe_launch::dense_gemm(d, stream_of(ctx)), "moe_dense_gemm");
+  rec(ctx, 1, 2);
+  return st;
+}
+
+moe_status moe_dense_bias_grad(const void* dz, int64_t M, int32_t N, float* d_bias, const moe_ctx* ctx) {
+  MOE_REQUIRE(M >= 0 && N >= 1, MOE_ERR_INVALID_ARG, "need M >= 0 and N >= 1");
+  MOE_REQUIRE((dz || M == 0) && d_bias, MOE_ERR_INVALID_ARG, "null tensor pointer");
+  MOE_REQUIRE(aligned16(dz) && aligned16(d_bias), MOE_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+  MOE_REQUIRE(M < ((int64_t)1 << 40) && N < (1 << 30), MOE_ERR_UNSUPPORTED, "M must be < 2^40 and N < 2^30");
+  rec(ctx, 0, 2);
+  const moe_status st = cuda_status(moe_launch::column_sum(dz, M, N, d_bias, stream_of(ctx)), "moe_dense_bias_grad");
   rec(ctx, 1, 2);
   return st;
 }

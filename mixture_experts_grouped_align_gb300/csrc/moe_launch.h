@@ -230,4 +230,27 @@ struct ActBackward {
 cudaError_t act_checkpoint(const ActCheckpoint& a, cudaStream_t stream);
 cudaError_t act_backward(const ActBackward& a, cudaStream_t stream);
 
+// ---- dense product with a fused epilogue (dense_gemm.cu; few tiles: dense_split.cu)
+struct Dense {
+  const void* x;         // [M, K] bf16
+  const void* w;         // [N1, K] or (w_kn) [K, N1] bf16, N1 = 2N (gated) or N
+  const void* bias;      // [N1] bf16 or null
+  const void* residual;  // [M, N] in out's type, or null
+  void* out;             // [M, N] bf16 or fp32
+  float residual_scale;
+  int64_t M, N;
+  int K;
+  int w_kn, gated, relu2, out_f32;
+  int tma_out;           // rows of out are whole 16-byte units (set by the launcher)
+  int32_t* status;
+  int64_t wait_ns;       // limit of every wait (0: the 2 s default)
+  int stall;             // failure-detection self-test: the copy and MMA roles off
+};
+void apply_debug_stall(Dense& d);
+cudaError_t dense_gemm(Dense d, cudaStream_t stream);
+bool dense_split_takes(const Dense& d);
+cudaError_t dense_split(const Dense& d, cudaStream_t stream);
+// out[n] = sum_m x[m, n], x [M, N] bf16 (column_sum.cu)
+cudaError_t column_sum(const void* x, int64_t M, int64_t N, float* out, cudaStream_t stream);
+
 }  // namespace moe_launch

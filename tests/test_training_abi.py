@@ -75,3 +75,30 @@ def test_binding_refuses_what_the_abi_cannot_see():
     refused(-1, forward, gu=torch.zeros((128, 4), dtype=torch.bfloat16).t())  # strides
     refused(-1, backward, dh=torch.zeros((3, 64), dtype=torch.bfloat16))      # short
     refused(-1, router, logits=torch.zeros((4, 8)))
+
+
+def dense(x=P, w=P, lay="nk", bias=None, residual=None, scale=1.0, M=4, N=64, K=64, act="none", out=P, f32=False):
+    return moe.moe_dense_gemm(x, w, lay, bias, residual, scale, M, N, K, act, out, moe.Ctx(stream=0), out_f32=f32)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (-1, dict(act=3)), (-1, dict(lay=2)), (-1, dict(M=-1)), (-1, dict(N=0)), (-1, dict(K=0)), (-2, dict(K=12)),
+    (-2, dict(K=1 << 30)), (-2, dict(M=1 << 30)), (-2, dict(N=1 << 29)), (-2, dict(lay="kn", N=60)),
+    (-1, dict(x=None)), (-1, dict(w=None)), (-1, dict(out=None)), (-1, dict(x=P + 2)), (-1, dict(w=P + 8)),
+    (-1, dict(bias=P + 2)), (-1, dict(residual=P + 4)), (-1, dict(out=P + 8)),
+])
+def test_dense_gemm_refusals(status, kw):
+    refused(status, dense, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(dz=None), dict(d=None), dict(M=-1), dict(N=0), dict(dz=P + 2), dict(d=P + 4)])
+def test_bias_grad_refusals(kw):
+    a = {"dz": P, "M": 4, "N": 64, "d": P} | kw
+    refused(-1, moe.moe_dense_bias_grad, a["dz"], a["M"], a["N"], a["d"], moe.Ctx(stream=0))
+
+
+def test_dense_binding_refusals():
+    assert dense(x=None, w=None, out=None, M=0) == 0
+    refused(-1, dense, x=torch.zeros((4, 64), dtype=torch.bfloat16))
+    # a residual in another type than the output
+    refused(-1, dense, residual=torch.zeros((4, 64), dtype=torch.bfloat16), f32=True)
