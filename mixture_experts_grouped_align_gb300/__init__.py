@@ -66,6 +66,18 @@ class _Weights(ctypes.Structure):
 _lib = None
 
 
+class _Dtypes(dict):
+    """The torch types of tensor arguments (torch is imported with the first one)."""
+
+    def __missing__(self, name):
+        import torch
+        self.update(f32=torch.float32, i32=torch.int32, bf16=torch.bfloat16, u8=torch.uint8)
+        return self[name]
+
+
+_DTYPES = _Dtypes()
+
+
 def load(path: str | None = None):
     """Loads the library once.  Raises if it has not been built."""
     global _lib
@@ -267,12 +279,12 @@ def moe_wgrad_workspace_size(E, N, Kin, block_m, cap_tokens, mode=0) -> int:
 def _tensor(t, what, dtype, numel):
     """The device pointer of a tensor argument, after the checks the C ABI cannot make: a torch
     tensor must be dense, of the stated type and of at least ``numel`` elements."""
-    if t is None or isinstance(t, int):
+    if t is None or t.__class__ is int:
         return t
-    if str(t.dtype) != dtype or not t.is_contiguous() or t.numel() < numel or not t.is_cuda:
-        raise MoeError(-1, f"{what}: need a contiguous {dtype} device tensor of {numel} elements, got "
-                           f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.is_contiguous() and t.is_cuda and t.numel() >= numel:
+        return t.data_ptr()
+    raise MoeError(-1, f"{what}: need a contiguous {dtype} device tensor of {numel} elements, got "
+                       f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
 
 def moe_router_loss_workspace_size(E) -> int:
@@ -283,11 +295,11 @@ def moe_router_loss(logits, topk_ids, topk_w, d_topk_w, token_mask, T, k, E, bal
                     prob_mean, loss, d_logits, ctx):
     """Balance and z losses, per-expert counts and d_logits [T, E] (with the gradient d_topk_w of
     the routing weights, if given).  loss [3] = total, balance, z."""
-    f32, i32 = "torch.float32", "torch.int32"
+    f32, i32 = _DTYPES["f32"], _DTYPES["i32"]
     return _check(load().moe_router_loss(
         _tensor(logits, "logits", f32, T * E), _tensor(topk_ids, "topk_ids", i32, T * k),
         _tensor(topk_w, "topk_w", f32, T * k), _tensor(d_topk_w, "d_topk_w", f32, T * k),
-        _tensor(token_mask, "token_mask", "torch.uint8", T), T, k, E, balance_coef, z_coef,
+        _tensor(token_mask, "token_mask", _DTYPES["u8"], T), T, k, E, balance_coef, z_coef,
         _tensor(counts, "counts", i32, E), _tensor(prob_mean, "prob_mean", f32, E), _tensor(loss, "loss", f32, 3),
         _tensor(d_logits, "d_logits", f32, T * E), _ctx(ctx)))
 
@@ -297,9 +309,9 @@ def moe_act_checkpoint(gu, row_w, rows, I, activation, h, codes, scales, ctx=Non
     "swiglu", I for "relu2")."""
     a = _act(activation)
     n1 = I if a == 1 else 2 * I
-    bf, u8 = "torch.bfloat16", "torch.uint8"
+    bf, u8 = _DTYPES["bf16"], _DTYPES["u8"]
     return _check(load().moe_act_checkpoint(
-        _tensor(gu, "gu", bf, rows * n1), _tensor(row_w, "row_w", "torch.float32", rows), rows, I, a,
+        _tensor(gu, "gu", bf, rows * n1), _tensor(row_w, "row_w", _DTYPES["f32"], rows), rows, I, a,
         _tensor(h, "h", bf, rows * I), _tensor(codes, "codes", u8, rows * n1),
         _tensor(scales, "scales", u8, rows * n1 // 32), _ctx(ctx)))
 
@@ -309,7 +321,7 @@ def moe_act_backward(codes, scales, dh, row_w, rows, I, activation, d_gu, h=None
     the row weights' gradient d_row_w [rows] fp32."""
     a = _act(activation)
     n1 = I if a == 1 else 2 * I
-    bf, u8, f32 = "torch.bfloat16", "torch.uint8", "torch.float32"
+    bf, u8, f32 = _DTYPES["bf16"], _DTYPES["u8"], _DTYPES["f32"]
     return _check(load().moe_act_backward(
         _tensor(codes, "codes", u8, rows * n1), _tensor(scales, "scales", u8, rows * n1 // 32),
         _tensor(dh, "dh", bf, rows * I), _tensor(row_w, "row_w", f32, rows), rows, I, a,
@@ -325,10 +337,10 @@ def moe_dense_gemm(x, w, w_layout, bias, residual, residual_scale, M, N, K, acti
     a = _act(activation)
     n1 = 2 * N if a == 0 else N
     lay = W_LAYOUT[w_layout] if isinstance(w_layout, str) else int(w_layout)
-    bf = "torch.bfloat16"
+    bf, f32 = _DTYPES["bf16"], _DTYPES["f32"]
     if out_f32 is None:
-        out_f32 = not isinstance(out, int) and out is not None and str(out.dtype) == "torch.float32"
-    ot = "torch.float32" if out_f32 else bf
+        out_f32 = out is not None and out.__class__ is not int and out.dtype is f32
+    ot = f32 if out_f32 else bf
     return _check(load().moe_dense_gemm(
         _tensor(x, "x", bf, M * K), _tensor(w, "w", bf, n1 * K), lay, _tensor(bias, "bias", bf, n1),
         _tensor(residual, "residual", ot, M * N), residual_scale, M, N, K, a, _tensor(out, "out", ot, M * N),
@@ -337,8 +349,8 @@ def moe_dense_gemm(x, w, w_layout, bias, residual, residual_scale, M, N, K, acti
 
 def moe_dense_bias_grad(dz, M, N, d_bias, ctx=None):
     """d_bias [N] fp32 = the column sums of dz [M, N] bf16."""
-    return _check(load().moe_dense_bias_grad(_tensor(dz, "dz", "torch.bfloat16", M * N), M, N,
-                                             _tensor(d_bias, "d_bias", "torch.float32", N), _ctx(ctx)))
+    return _check(load().moe_dense_bias_grad(_tensor(dz, "dz", _DTYPES["bf16"], M * N), M, N,
+                                             _tensor(d_bias, "d_bias", _DTYPES["f32"], N), _ctx(ctx)))
 
 
 def moe_debug_stall_tensor_kernels(stall_ns: int) -> None:

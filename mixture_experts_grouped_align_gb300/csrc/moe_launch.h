@@ -204,7 +204,7 @@ struct RouterLoss {
   int count_blocks;      // set by the launcher
 };
 size_t router_loss_workspace_bytes(int E);
-cudaError_t router_loss(RouterLoss a, cudaStream_t stream);
+cudaError_t router_loss(const RouterLoss& a, cudaStream_t stream);
 
 // ---- expert activation with an MXFP8 checkpoint (act_checkpoint.cu)
 struct ActCheckpoint {

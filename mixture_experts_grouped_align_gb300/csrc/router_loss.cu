@@ -13,29 +13,32 @@
 //
 // The counts f are no function of the logits' values, so one pass over the logits gives both
 // the sums of p and the gradient: T E floats read once and written once, which is the floor.
-// Two launches: the counts (T k ids), then the pass; a batch of at most kOneBlockElems logits
-// is one launch of one block, which counts for itself.
+// Two launches: the counts (T k ids), then the pass; a small batch is one launch of one cluster,
+// which counts for itself.
 //
-// The pass gives a row to LANES lanes (8, 16 or 32: the fewest that hold it at four values a
-// lane, then NV vectors of four a lane) and keeps it in registers from the load to the store.
+// The pass gives a row to LANES lanes (4 to 32, NV vectors of four values each) and keeps it in
+// registers from the load to the store.
 // Every lane keeps the column sums of its own columns over its rows; blocks add theirs in a
 // fixed order into one row of partial sums each, and the last block to finish adds those rows
 // in order, so that repeated calls give the same bits (no floating-point atomics).
 #include "moe_common.cuh"
 #include "moe_launch.h"
+#include "tcgen05.cuh"
 
 namespace {
 
 using moe_launch::RouterLoss;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kCountThreads = 512;
 constexpr int kMaxCountBlocks = 64;
-constexpr int64_t kOneBlockElems = 16384;
+constexpr int kMaxPassBlocks = 256;       // one block per SM
+constexpr int kClusterBlocks = 8;
 constexpr unsigned kAll = 0xffffffffu;
 
 // Workspace: ticket (256 bytes) | counts of the count blocks [kMaxCountBlocks][E + 1] (the last
-// word: its real tokens) | partial sums of the pass [blocks][E + 1] (the last word: sum lse^2).
+// word: its real tokens) | column sums of the pass's blocks [kMaxPassBlocks][part_pitch(E)] | their
+// sums of lse^2 [kMaxPassBlocks].
+__host__ __device__ inline int part_pitch(int E) { return (E + 3) / 4 * 4; }
 struct Ws {
   unsigned* ticket;
   int* counts;
@@ -46,43 +49,81 @@ __host__ __device__ inline Ws carve(void* ws, int E) {
   Ws w;
   w.ticket = reinterpret_cast<unsigned*>(p);
   w.counts = reinterpret_cast<int*>(p + 256);
-  w.part = reinterpret_cast<float*>(p + 256 + (size_t)kMaxCountBlocks * (E + 1) * 4);
+  w.part = reinterpret_cast<float*>(p + 256 + ((size_t)kMaxCountBlocks * (E + 1) * 4 + 255) / 256 * 256);
   return w;
 }
 
-// Counts of tokens [t0, t1) into hist[E] (shared) and their real tokens into *n_real (shared).
+// Counts of tokens [t0, t1) (t0 a multiple of 4) into hist[E] (shared) and their real tokens into
+// *n_real (shared).  Four ids a load, four loads in flight per thread.
+template <int kThreads>
 __device__ void count_tokens(const RouterLoss& a, int64_t t0, int64_t t1, int* hist, int* n_real) {
   for (int e = threadIdx.x; e < a.E; e += kThreads) hist[e] = 0;
   if (threadIdx.x == 0) *n_real = 0;
   __syncthreads();
-  const int64_t p1 = t1 * a.k;
-  for (int64_t p = t0 * a.k + threadIdx.x; p < p1; p += kThreads) {
-    const int64_t t = p / a.k;
-    if (a.mask && a.mask[t] == 0) continue;
-    const int id = a.ids[p];
-    if (id < 0 || id >= a.E) moe::set_status(a.status, MOE_ERR_INVALID_EXPERT);
-    else atomicAdd(&hist[id], 1);
+  const uint32_t p0 = (uint32_t)(t0 * a.k), n = (uint32_t)((t1 - t0) * a.k), k = (uint32_t)a.k;
+  bool bad = false;
+  auto add = [&](int id) {
+    if ((uint32_t)id < (uint32_t)a.E) atomicAdd(&hist[id], 1);
+    else bad = true;
+  };
+  const int4* v = reinterpret_cast<const int4*>(a.ids + p0);
+  const uint32_t n4 = n / 4;
+  for (uint32_t i = threadIdx.x; i < n4; i += 4 * kThreads) {
+    int4 q[4];
+    bool live[16];  // all loads before the first count
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t j = i + u * kThreads, p = p0 + 4 * j;
+      if (j < n4) q[u] = __ldg(v + j);
+      const bool in = j < n4;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) live[4 * u + c] = in;
+      if (a.mask && in) {
+        const uint32_t t = p / k, r = p - t * k;  // four ids: of tokens t and t + 1 at most where k >= 4
+        if (k >= 4) {
+          const bool m0 = a.mask[t] != 0, m1 = r + 3 < k ? m0 : a.mask[t + 1] != 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) live[4 * u + c] = r + c < k ? m0 : m1;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) live[4 * u + c] = a.mask[(p + c) / k] != 0;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (live[4 * u]) add(q[u].x);
+      if (live[4 * u + 1]) add(q[u].y);
+      if (live[4 * u + 2]) add(q[u].z);
+      if (live[4 * u + 3]) add(q[u].w);
+    }
   }
+  if (threadIdx.x < n - 4 * n4) {
+    const uint32_t p = p0 + 4 * n4 + threadIdx.x;
+    if (!a.mask || a.mask[p / k] != 0) add(a.ids[p]);
+  }
+  if (bad) moe::set_status(a.status, MOE_ERR_INVALID_EXPERT);
   if (a.mask) {
-    int n = 0;
-    for (int64_t t = t0 + threadIdx.x; t < t1; t += kThreads) n += a.mask[t] != 0;
-    n = __reduce_add_sync(kAll, n);
-    if ((threadIdx.x & 31) == 0 && n) atomicAdd(n_real, n);
+    int c = 0;
+    for (int64_t t = t0 + threadIdx.x; t < t1; t += kThreads) c += a.mask[t] != 0;
+    c = __reduce_add_sync(kAll, c);
+    if ((threadIdx.x & 31) == 0 && c) atomicAdd(n_real, c);
   } else if (threadIdx.x == 0) {
     *n_real = (int)(t1 - t0);
   }
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads) router_count_kernel(RouterLoss a, int64_t per_block) {
+__global__ void __launch_bounds__(kCountThreads) router_count_kernel(RouterLoss a, int64_t per_block) {
   extern __shared__ int sm_count[];
   __shared__ int n_real;
+  asm volatile("griddepcontrol.launch_dependents;");
   const Ws w = carve(a.ws, a.E);
   const int64_t t0 = blockIdx.x * per_block;
   const int64_t t1 = t0 + per_block < a.T ? t0 + per_block : a.T;
-  count_tokens(a, t0, t1 > t0 ? t1 : t0, sm_count, &n_real);
+  count_tokens<kCountThreads>(a, t0, t1 > t0 ? t1 : t0, sm_count, &n_real);
   int* out = w.counts + (size_t)blockIdx.x * (a.E + 1);
-  for (int e = threadIdx.x; e < a.E; e += kThreads) out[e] = sm_count[e];
+  for (int e = threadIdx.x; e < a.E; e += kCountThreads) out[e] = sm_count[e];
   if (threadIdx.x == 0) {
     out[a.E] = n_real;
     if (blockIdx.x == 0) *w.ticket = 0;
@@ -92,10 +133,7 @@ __global__ void __launch_bounds__(kThreads) router_count_kernel(RouterLoss a, in
 template <int LANES>
 __device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) {
-    const float x = __shfl_xor_sync(kAll, v, o);
-    v = (v != v || x != x) ? __int_as_float(0x7fc00000) : fmaxf(v, x);
-  }
+  for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
   return v;
 }
 template <int LANES>
@@ -105,234 +143,423 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Column of value i (0 .. 4 NV - 1) of lane `sub` of a row's LANES lanes.
-template <int LANES, int VEC>
-__device__ __forceinline__ int col_of(int sub, int i) {
-  return VEC == 4 ? (i >> 2) * 4 * LANES + sub * 4 + (i & 3) : i * LANES + sub;
+// 2^x with the hardware's exponential and 1/x with its reciprocal (1 to 2 ulp), results below the
+// normal range flushed to 0: probabilities that small add nothing in fp32.
+MOE_DEV float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+MOE_DEV float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-template <int LANES, int NV, int VEC>
-__device__ __forceinline__ void load_row(const float* row, int E, int sub, float (&x)[4 * NV]) {
-  if (VEC == 4) {
+// Two fp32 values in a register pair, and the instructions that work on both at once: the pass
+// is bound by the instructions it issues, not by its loads, where every value takes its own.
+typedef unsigned long long f2;
+MOE_DEV f2 pack2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+MOE_DEV float lo2(f2 v) { return __uint_as_float((uint32_t)v); }
+MOE_DEV float hi2(f2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+MOE_DEV f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MOE_DEV f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MOE_DEV f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A row's LANES lanes hold 2 NV pairs each.  Column of the pair's two values: adjacent where rows
+// are whole 16-byte vectors (VEC), LANES apart otherwise.
+template <int LANES, bool VEC>
+__device__ __forceinline__ int col_of(int sub, int pair, int half) {
+  return VEC ? (pair >> 1) * 4 * LANES + sub * 4 + (pair & 1) * 2 + half : (2 * pair + half) * LANES + sub;
+}
+
+// Reads a row of E values (or, WHOLE, of as many as the lanes hold): -inf past E.
+template <int LANES, int NV, bool VEC, bool WHOLE>
+__device__ __forceinline__ void load_row(const float* row, int E, int sub, f2 (&x)[2 * NV]) {
+  const f2 none = pack2(-INFINITY, -INFINITY);
+  if (VEC) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = v * 4 * LANES + sub * 4;
-      float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (c < E) f = __ldcs(reinterpret_cast<const float4*>(row + c));
-      x[4 * v] = f.x; x[4 * v + 1] = f.y; x[4 * v + 2] = f.z; x[4 * v + 3] = f.w;
+      if (WHOLE || c < E) {
+        const longlong2 f = *reinterpret_cast<const longlong2*>(row + c);
+        x[2 * v] = (f2)f.x;
+        x[2 * v + 1] = (f2)f.y;
+      } else {
+        x[2 * v] = x[2 * v + 1] = none;
+      }
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) {
-      const int c = i * LANES + sub;
-      x[i] = c < E ? __ldcs(row + c) : -INFINITY;
+    for (int p = 0; p < 2 * NV; ++p) {
+      const int c0 = col_of<LANES, VEC>(sub, p, 0), c1 = col_of<LANES, VEC>(sub, p, 1);
+      x[p] = pack2(c0 < E ? row[c0] : -INFINITY, c1 < E ? row[c1] : -INFINITY);
     }
   }
 }
 
-template <int LANES, int NV, int VEC>
-__device__ __forceinline__ void store_row(float* row, int E, int sub, const float (&d)[4 * NV]) {
-  if (VEC == 4) {
+template <int LANES, int NV, bool VEC, bool WHOLE>
+__device__ __forceinline__ void store_row(float* row, int E, int sub, const f2 (&d)[2 * NV]) {
+  if (VEC) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = v * 4 * LANES + sub * 4;
-      if (c < E) __stcs(reinterpret_cast<float4*>(row + c), make_float4(d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]));
+      if (WHOLE || c < E)
+        __stcs(reinterpret_cast<longlong2*>(row + c), make_longlong2((long long)d[2 * v], (long long)d[2 * v + 1]));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) {
-      const int c = i * LANES + sub;
-      if (c < E) __stcs(row + c, d[i]);
+    for (int p = 0; p < 2 * NV; ++p) {
+      const int c0 = col_of<LANES, VEC>(sub, p, 0), c1 = col_of<LANES, VEC>(sub, p, 1);
+      if (c0 < E) __stcs(row + c0, lo2(d[p]));
+      if (c1 < E) __stcs(row + c1, hi2(d[p]));
     }
   }
 }
 
-// Sum over the block's threads of v (every thread gets it; `red` holds kWarps floats).
+// The lanes' columns of a shared row of kCols values.
+template <int LANES, int NV, bool VEC>
+__device__ __forceinline__ void shared_row(const float* r, int sub, f2 (&v)[2 * NV]) {
+  if (VEC) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(r + i * 4 * LANES + sub * 4);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < 2 * NV; ++p) v[p] = pack2(r[col_of<LANES, VEC>(sub, p, 0)], r[col_of<LANES, VEC>(sub, p, 1)]);
+  }
+}
+
+// Sum over the block's threads of v (every thread gets it; `red` holds a float per warp).
+template <int kThreads>
 __device__ float block_sum(float v, float* red) {
   v = group_sum<32>(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   float s = 0.f;
-  for (int i = 0; i < kWarps; ++i) s += red[i];
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) s += red[i];
   return s;
 }
 
-// ONE: the grid is one block, which counts the choices itself.
-// Shared memory: g [E] | the routing weights' gradient of one row per group [groups][E] (the
-// column sums of one warp each at the end, [kWarps][4 NV 32]).
-template <int LANES, int NV, int VEC, bool ONE>
-__global__ void __launch_bounds__(kThreads) router_pass_kernel(RouterLoss a) {
+// Threads of the pass: what the register file holds of a row, the next row, the columns' sums and
+// their g at sixteen or at 32 values a lane.
+__host__ __device__ constexpr int pass_threads(int nv) { return nv <= 4 ? 640 : 384; }
+
+MOE_DEV uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_addr(p)), "r"(rank));
+  return a;
+}
+MOE_DEV int ld_cluster_s32(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+MOE_DEV float ld_cluster_f32(const float* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+
+// CLUSTER: the grid is one cluster, whose blocks count a share of the choices each and exchange
+// counts and column sums through distributed shared memory.  Otherwise the counts come from
+// router_count_kernel, and the last block to finish adds the blocks' column sums.
+// Shared memory: g [kCols] | this block's counts, later its column sums [kCols] | at the end the
+// column sums of its warps [kWarps][kCols], or four of other blocks a thread.
+template <int LANES, int NV, bool VEC, bool WHOLE, bool CLUSTER>
+__global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(RouterLoss a) {
+  constexpr int kThreads = pass_threads(NV), kWarps = kThreads / 32;
   constexpr int kGroups = 32 / LANES;       // rows of a warp
   constexpr int kCols = 4 * NV * LANES;     // columns the lanes can hold, >= E
-  constexpr int kRows = NV == 1 ? 2 : 1;    // rows in flight per group
+  constexpr int kWide = kCols < 32 ? 32 : (kCols < 256 ? kCols : 256);  // threads across columns
   extern __shared__ float sm[];
   __shared__ int n_sh;
   __shared__ unsigned last;
-  __shared__ float red[kWarps];
+  __shared__ float red[kThreads];
+  __shared__ float z_sh;
   const int E = a.E, k = a.k;
   float* gs = sm;
-  float* up_all = sm + kCols;
+  float* mine = sm + kCols;
+  float* sums = sm + 2 * kCols;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % LANES, grp = lane / LANES;
-  float* up = up_all + (size_t)(warp * kGroups + grp) * kCols;
   const Ws ws = carve(a.ws, E);
+  const int pitch = part_pitch(E);
 
-  int* cs = reinterpret_cast<int*>(gs);
-  if (ONE) {
-    count_tokens(a, 0, a.T, cs, &n_sh);
-  } else {
-    for (int e = tid; e <= E; e += kThreads) {
-      int s = 0;
-      for (int b = 0; b < a.count_blocks; ++b) s += ws.counts[(size_t)b * (E + 1) + e];
-      if (e == E) n_sh = s;
-      else cs[e] = s;
+  const bool with_dw = a.dw != nullptr && a.d_logits != nullptr;
+  const uint32_t T = (uint32_t)a.T, step = gridDim.x * kWarps * kGroups;  // T k < 2^31
+  uint32_t t = (blockIdx.x * kWarps + warp) * kGroups + grp;              // this group's row
+  // What a row needs is under way a turn ahead: its logits, its mask byte and this lane's choice
+  // (and, once that is there, the choice's own logit).  Rows that the mask leaves out are read
+  // like the others, so that no load waits for the mask.
+  f2 next[2 * NV];
+  int id_n = -1;
+  float w_n = 0.f, dw_n = 0.f;
+  bool real_n = false;
+  auto load = [&](uint32_t tr) {
+    real_n = tr < T;
+    if (!real_n) return;
+    load_row<LANES, NV, VEC, WHOLE>(a.logits + (size_t)tr * E, E, sub, next);
+    if (a.mask) real_n = a.mask[tr] != 0;
+    if (with_dw && sub < k) {
+      id_n = a.ids[tr * k + sub];
+      w_n = a.w[tr * k + sub];
+      dw_n = a.dw[tr * k + sub];
     }
+  };
+  auto chosen = [&](uint32_t tr) { return (uint32_t)id_n < (uint32_t)E ? a.logits[(size_t)tr * E + id_n] : 0.f; };
+  load(t);  // before the counts are waited for
+  float l0 = chosen(t);
+  int* cs = reinterpret_cast<int*>(gs);
+  if (CLUSTER) {
+    int* hist = reinterpret_cast<int*>(mine);
+    const uint32_t share = ((T + gridDim.x - 1) / gridDim.x + 3) / 4 * 4;
+    const uint32_t t0 = blockIdx.x * share < T ? blockIdx.x * share : T, t1 = t0 + share < T ? t0 + share : T;
+    count_tokens<kThreads>(a, t0, t1, hist, &n_sh);
+    if (gridDim.x > 1) tc::cluster_sync();
+    int n = 0;
+    for (uint32_t r = 0; r < gridDim.x; ++r) n += ld_cluster_s32(&n_sh, r);
+    for (int e = tid; e < E; e += kThreads) {
+      int s = 0;
+      for (uint32_t r = 0; r < gridDim.x; ++r) s += ld_cluster_s32(hist + e, r);
+      cs[e] = s;
+    }
+    if (gridDim.x > 1) tc::cluster_sync();  // every block has read the others' counts
+    else __syncthreads();
+    if (tid == 0) n_sh = n;
     __syncthreads();
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // kThreads / kWide threads share a column's count blocks
+    int* redi = reinterpret_cast<int*>(red);
+    if (warp == 0) {
+      int c = 0;
+      for (int b = lane; b < a.count_blocks; b += 32) c += __ldcg(ws.counts + (size_t)b * (E + 1) + E);
+      c = __reduce_add_sync(kAll, c);
+      if (lane == 0) n_sh = c;
+    }
+    for (int e0 = 0; e0 < E; e0 += kWide) {
+      const int e = e0 + tid % kWide;
+      int s = 0;
+      if (e < E) {
+#pragma unroll 8
+        for (int b = tid / kWide; b < a.count_blocks; b += kThreads / kWide) s += __ldcg(ws.counts + (size_t)b * (E + 1) + e);
+      }
+      redi[tid] = s;
+      __syncthreads();
+      if (tid < kWide && e < E) {
+#pragma unroll
+        for (int i = 1; i < kThreads / kWide; ++i) s += redi[i * kWide + tid];
+        cs[e] = s;
+      }
+      __syncthreads();
+    }
   }
   const int n = n_sh;
   const float inv_n = n > 0 ? 1.f / (float)n : 0.f;
+  const float ca = a.balance_coef * inv_n, cz = 2.f * a.z_coef * inv_n;
   for (int e = tid; e < kCols; e += kThreads) {
     float g = 0.f;
     if (e < E) {
       const int c = cs[e];
       if (blockIdx.x == 0 && a.counts) a.counts[e] = c;
-      if (n > 0) g = (float)((double)((int64_t)E * c - (int64_t)n * k) / (double)((int64_t)n * k));
+      const int64_t nk = (int64_t)n * k;
+      if (n > 0) g = (float)((int64_t)E * c - nk) / (float)nk;  // the numerator from integers
     }
     gs[e] = g;  // the same word cs[e] was read from, by the same thread
   }
-  for (int i = tid; i < kWarps * kGroups * kCols; i += kThreads) up_all[i] = 0.f;
   __syncthreads();
 
-  float acc[4 * NV], zacc = 0.f;
+  f2 acc[2 * NV], g[2 * NV];
+  float zacc = 0.f;
+  shared_row<LANES, NV, VEC>(gs, sub, g);
 #pragma unroll
-  for (int i = 0; i < 4 * NV; ++i) acc[i] = 0.f;
-  const float ca = a.balance_coef * inv_n, cz = 2.f * a.z_coef * inv_n;
-  const int64_t per = (int64_t)kGroups * kRows;  // rows of a warp per turn
-  const int64_t step = (int64_t)gridDim.x * kWarps * per;
-  // every lane of a warp makes the same number of turns (the shuffles need them all)
-  for (int64_t base = ((int64_t)blockIdx.x * kWarps + warp) * per; base < a.T; base += step) {
-    float x[kRows][4 * NV];
-    bool in[kRows], real[kRows];
-    int id[kRows];
-    float w[kRows], dw[kRows];
+  for (int p = 0; p < 2 * NV; ++p) acc[p] = 0ull;
+  while (t - grp < T) {  // the same turns for every lane of a warp: the shuffles need them all
+    f2 x[2 * NV];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int64_t t = base + (int64_t)r * kGroups + grp;
-      in[r] = t < a.T;
-      real[r] = in[r] && (!a.mask || a.mask[t] != 0);
-      if (real[r]) {
-        load_row<LANES, NV, VEC>(a.logits + t * E, E, sub, x[r]);
-      } else {
+    for (int p = 0; p < 2 * NV; ++p) x[p] = next[p];
+    const bool real = real_n;
+    const int id0 = id_n;
+    const float w0 = w_n, dw0 = dw_n;
+    if (t - grp + step < T) load(t + step);
+    if (!__all_sync(kAll, real)) {  // pad rows and rows past the end look like rows with nothing left
+      if (!real)
 #pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) x[r][i] = -INFINITY;
+        for (int p = 0; p < 2 * NV; ++p) x[p] = pack2(-INFINITY, -INFINITY);
+    }
+    float m = fmaxf(lo2(x[0]), hi2(x[0]));
+#pragma unroll
+    for (int p = 1; p < 2 * NV; ++p) m = fmaxf(m, fmaxf(lo2(x[p]), hi2(x[p])));
+    m = group_max<LANES>(m);
+    // a row with nothing left by its mask (all -inf), a pad row or a row past the end: p = 0.
+    // fmaxf passes over NaN, so a row of -inf and NaN looks the same and is told apart here.
+    bool some = m > -INFINITY;
+    if (__any_sync(kAll, !some && real)) {
+      bool nan = false;
+#pragma unroll
+      for (int p = 0; p < 2 * NV; ++p) nan |= lo2(x[p]) != lo2(x[p]) || hi2(x[p]) != hi2(x[p]);
+      const unsigned lanes = __ballot_sync(kAll, nan) >> (grp * LANES);
+      some |= (LANES == 32 ? lanes : lanes & ((1u << (LANES & 31)) - 1u)) != 0;
+    }
+    const float m0 = m > -INFINITY ? m : 0.f;
+    const f2 minus = pack2(-m0, -m0), log2e = pack2(1.44269504f, 1.44269504f);
+    f2 tot2 = 0ull, s2 = 0ull;
+#pragma unroll
+    for (int p = 0; p < 2 * NV; ++p) {
+      const f2 y = mul2(add2(x[p], minus), log2e);  // -inf stays -inf, the largest becomes 0
+      x[p] = pack2(exp2_fast(lo2(y)), exp2_fast(hi2(y)));
+      tot2 = add2(tot2, x[p]);
+      s2 = fma2(x[p], g[p], s2);
+    }
+    const float tot = group_sum<LANES>(lo2(tot2) + hi2(tot2));
+    const float s = group_sum<LANES>(lo2(s2) + hi2(s2));
+    const float inv = some ? rcp_fast(tot) : 0.f;
+    const float lse = some ? m + logf(tot) : 0.f;
+    if (sub == 0) zacc += lse * lse;
+    const float caz = ca * inv, lin = (cz * lse - caz * s) * inv;
+    const f2 inv2 = pack2(inv, inv), caz2 = pack2(caz, caz), lin2 = pack2(lin, lin);
+#pragma unroll
+    for (int p = 0; p < 2 * NV; ++p) {
+      acc[p] = fma2(x[p], inv2, acc[p]);
+      x[p] = mul2(x[p], fma2(caz2, g[p], lin2));
+    }
+    if (a.d_logits && t < T) store_row<LANES, NV, VEC, WHOLE>(a.d_logits + (size_t)t * E, E, sub, x);
+    if (with_dw) {
+      // The chosen columns are stored once more with the routing weights' share, by the lane
+      // that holds the choice, from the choice's own logit.  Choices that repeat an expert, or
+      // more of them than lanes, are added to the stored row by one lane in order instead.
+      const bool live = real && some, mine = live && (uint32_t)id0 < (uint32_t)E;
+      const uint32_t c0 = t * k;
+      float wd = mine ? w0 * dw0 : 0.f;
+      if (k > LANES && live)
+        for (int j = sub + LANES; j < k; j += LANES)
+          if ((uint32_t)a.ids[c0 + j] < (uint32_t)E) wd += a.w[c0 + j] * a.dw[c0 + j];
+      wd = group_sum<LANES>(wd);
+      const unsigned same = __match_any_sync(kAll, mine ? (grp << 16) + id0 : (int)(0x80000000u + lane));
+      const bool one_by_one = __any_sync(kAll, k > LANES || (same & (same - 1)) != 0);
+      __syncwarp();  // the row's stores come before these
+      if (!one_by_one) {
+        if (mine)
+          a.d_logits[(size_t)t * E + id0] =
+              exp2_fast((l0 - m0) * 1.44269504f) * (caz * gs[id0] + lin) + w0 * (dw0 - wd);
+      } else if (live && sub == 0) {
+        float* d = a.d_logits + (size_t)t * E;
+        for (int j = 0; j < k; ++j) {
+          const int e = a.ids[c0 + j];
+          if ((uint32_t)e < (uint32_t)E) d[e] += a.w[c0 + j] * (a.dw[c0 + j] - wd);
+        }
       }
     }
-    const bool with_dw = a.dw != nullptr && a.d_logits != nullptr;
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int64_t t = base + (int64_t)r * kGroups + grp;
-      float m = x[r][0];
-#pragma unroll
-      for (int i = 1; i < 4 * NV; ++i) m = (m != m || x[r][i] != x[r][i]) ? __int_as_float(0x7fc00000) : fmaxf(m, x[r][i]);
-      m = group_max<LANES>(m);
-      // a row with nothing left by its mask (all -inf), a pad row or a row past the end: p = 0
-      const bool some = m != -INFINITY;
-      float p[4 * NV], tot = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) {
-        p[i] = some ? __expf(x[r][i] - m) : 0.f;
-        tot += p[i];
-      }
-      tot = group_sum<LANES>(tot);
-      const float inv = some ? 1.f / tot : 0.f;
-      const float lse = some ? m + logf(tot) : 0.f;
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) {
-        p[i] *= inv;
-        acc[i] += p[i];
-        s += p[i] * gs[col_of<LANES, VEC>(sub, i)];
-      }
-      s = group_sum<LANES>(s);
-      if (sub == 0) zacc += lse * lse;
-      if (a.d_logits == nullptr) continue;
-      float d[4 * NV];
-      const float lin = cz * lse - ca * s;
-#pragma unroll
-      for (int i = 0; i < 4 * NV; ++i) d[i] = p[i] * (ca * gs[col_of<LANES, VEC>(sub, i)] + lin);
-      if (with_dw) {
-        // the k choices, one after another (k may exceed the group's lanes); ids of a token may
-        // repeat, so each choice's share is added by one lane in the order of j
-        float wd = 0.f;
-        if (real[r] && some)
-          for (int j = sub; j < k; j += LANES) {
-            const int e = a.ids[t * k + j];
-            if (e >= 0 && e < E) wd += a.w[t * k + j] * a.dw[t * k + j];
-          }
-        wd = group_sum<LANES>(wd);
-        if (real[r] && some && sub == 0)
-          for (int j = 0; j < k; ++j) {
-            const int e = a.ids[t * k + j];
-            if (e >= 0 && e < E) up[e] += a.w[t * k + j] * (a.dw[t * k + j] - wd);
-          }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4 * NV; ++i) d[i] += up[col_of<LANES, VEC>(sub, i)];
-        __syncwarp();
-        if (real[r] && some && sub == 0)
-          for (int j = 0; j < k; ++j) {
-            const int e = a.ids[t * k + j];
-            if (e >= 0 && e < E) up[e] = 0.f;
-          }
-        __syncwarp();
-      }
-      if (in[r]) store_row<LANES, NV, VEC>(a.d_logits + t * E, E, sub, d);
-    }
+    t += step;
+    if (t < T) l0 = chosen(t);
   }
 
   // column sums of the block: groups of a warp by shuffles, warps through shared memory
-#pragma unroll
-  for (int i = 0; i < 4 * NV; ++i)
-#pragma unroll
-    for (int o = LANES; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(kAll, acc[i], o);
   __syncthreads();
-  if (grp == 0)
 #pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) up_all[(size_t)warp * kCols + col_of<LANES, VEC>(sub, i)] = acc[i];
-  const float z = block_sum(zacc, red);
-  __syncthreads();
-  float* part = ws.part + (size_t)blockIdx.x * (E + 1);
-  for (int e = tid; e < E; e += kThreads) {
+  for (int p = 0; p < 2 * NV; ++p)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float v = half ? hi2(acc[p]) : lo2(acc[p]);
+#pragma unroll
+      for (int o = LANES; o < 32; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+      if (grp == 0) sums[(size_t)warp * kCols + col_of<LANES, VEC>(sub, p, half)] = v;
+    }
+  const float z = block_sum<kThreads>(zacc, red);  // its barriers also publish the warps' sums
+  float* part = ws.part + (size_t)blockIdx.x * pitch;  // rows of partial sums, their pad words zero
+  float* zpart = ws.part + (size_t)kMaxPassBlocks * pitch;
+  for (int e = tid; e < (CLUSTER ? E : pitch); e += kThreads) {
     float s = 0.f;
-    for (int i = 0; i < kWarps; ++i) s += up_all[(size_t)i * kCols + e];
-    part[e] = s;
+    if (e < E)
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) s += sums[(size_t)i * kCols + e];
+    if (CLUSTER) mine[e] = s;
+    else part[e] = s;
   }
-  if (tid == 0) part[E] = z;
-  if (!ONE) {
+  float bal = 0.f, zs = 0.f;
+  if (CLUSTER) {
+    if (tid == 0) z_sh = z;
+    if (gridDim.x > 1) tc::cluster_sync();
+    else __syncthreads();
+    if (blockIdx.x == 0) {
+      for (int e = tid; e < E; e += kThreads) {
+        float s = 0.f;
+        for (uint32_t r = 0; r < gridDim.x; ++r) s += ld_cluster_f32(mine + e, r);
+        s *= inv_n;
+        if (a.prob_mean) a.prob_mean[e] = s;
+        bal += (gs[e] + 1.f) * s;
+      }
+      for (uint32_t r = 0; r < gridDim.x; ++r) zs += ld_cluster_f32(&z_sh, r);
+      zs *= inv_n;
+    }
+    if (gridDim.x > 1) tc::cluster_sync();  // no block leaves before its sums are read
+    if (blockIdx.x != 0) return;
+  } else {
+    if (tid == 0) zpart[blockIdx.x] = z;
     __threadfence();
     __syncthreads();
     if (tid == 0) last = atomicAdd(ws.ticket, 1u) == gridDim.x - 1;
     __syncthreads();
     if (!last) return;
     __threadfence();
-  } else {
+    // the last block: four columns a thread, kRowsAt threads sharing a column's blocks, eight
+    // blocks in flight
+    constexpr int kAcross = kCols / 4, kRowsAt = kThreads / kAcross, kBatch = 8;
+    const int c = (tid % kAcross) * 4, r0 = tid / kAcross;
+    float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < E)
+      for (unsigned b0 = r0; b0 < gridDim.x; b0 += kRowsAt * kBatch) {
+        float4 v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const unsigned b = b0 + i * kRowsAt;
+          v[i] = b < gridDim.x ? __ldcg(reinterpret_cast<const float4*>(ws.part + (size_t)b * pitch + c))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          s4.x += v[i].x;
+          s4.y += v[i].y;
+          s4.z += v[i].z;
+          s4.w += v[i].w;
+        }
+      }
+    zs = tid < gridDim.x ? __ldcg(zpart + tid) : 0.f;
+    zs = block_sum<kThreads>(zs, red) * inv_n;
+    *reinterpret_cast<float4*>(sums + (size_t)r0 * kCols + c) = s4;
     __syncthreads();
+    for (int e = tid; e < E; e += kThreads) {
+      float s = 0.f;
+#pragma unroll 8
+      for (int i = 0; i < kRowsAt; ++i) s += sums[(size_t)i * kCols + e];
+      s *= inv_n;
+      if (a.prob_mean) a.prob_mean[e] = s;
+      bal += (gs[e] + 1.f) * s;
+    }
   }
-  // the last block: P, and the three losses
-  float bal = 0.f;
-  for (int e = tid; e < E; e += kThreads) {
-    float s = 0.f;
-    for (unsigned b = 0; b < gridDim.x; ++b) s += __ldcg(ws.part + (size_t)b * (E + 1) + e);
-    s *= inv_n;
-    if (a.prob_mean) a.prob_mean[e] = s;
-    bal += (gs[e] + 1.f) * s;
-  }
-  float zs = 0.f;
-  for (unsigned b = tid; b < gridDim.x; b += kThreads) zs += __ldcg(ws.part + (size_t)b * (E + 1) + E);
-  bal = block_sum(bal, red);
-  zs = block_sum(zs, red) * inv_n;
+  bal = block_sum<kThreads>(bal, red);
   if (tid == 0) {
-    if (n == 0) bal = zs = 0.f;
     // a part whose coefficient is 0 is off, also where its value is infinite
     a.loss[0] = (a.balance_coef != 0.f ? a.balance_coef * bal : 0.f) + (a.z_coef != 0.f ? a.z_coef * zs : 0.f);
     a.loss[1] = bal;
@@ -340,33 +567,67 @@ __global__ void __launch_bounds__(kThreads) router_pass_kernel(RouterLoss a) {
   }
 }
 
-template <int LANES, int NV, int VEC>
-cudaError_t launch_pass(const RouterLoss& a, int blocks, bool one, cudaStream_t stream) {
-  constexpr int kCols = 4 * NV * LANES;
-  const size_t smem = (size_t)kCols * 4 * (1 + kWarps * (32 / LANES));
-  auto kern = one ? router_pass_kernel<LANES, NV, VEC, true> : router_pass_kernel<LANES, NV, VEC, false>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (err != cudaSuccess) return err;
-  kern<<<blocks, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+template <int LANES, int NV, bool VEC, bool WHOLE>
+cudaError_t launch_pass(RouterLoss a, cudaStream_t stream) {
+  constexpr int kCols = 4 * NV * LANES, kThreads = pass_threads(NV), kWarps = kThreads / 32;
+  constexpr int kRows = kWarps * (32 / LANES);  // rows of a block per turn
+  constexpr size_t kSmem = 4 * (2 * kCols + (kWarps * kCols > 4 * kThreads ? kWarps * kCols : 4 * kThreads));
+  const int64_t turns = (a.T + kRows - 1) / kRows;  // of one block alone
+  const bool cluster = turns <= kClusterBlocks;
+  auto kern = cluster ? router_pass_kernel<LANES, NV, VEC, WHOLE, true> : router_pass_kernel<LANES, NV, VEC, WHOLE, false>;
+  if (kSmem > 48 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (err != cudaSuccess) return err;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cluster) {
+    const unsigned c = (unsigned)(turns < 1 ? 1 : (turns < kClusterBlocks ? turns : kClusterBlocks));
+    cfg.gridDim = dim3(c);
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = c;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  } else {
+    int64_t blocks = (a.T * a.k + 4095) / 4096;
+    if (blocks > kMaxCountBlocks) blocks = kMaxCountBlocks;
+    const int64_t per = ((a.T + blocks - 1) / blocks + 3) / 4 * 4;  // ids of a block start on 16 bytes
+    a.count_blocks = (int)((a.T + per - 1) / per);
+    router_count_kernel<<<(unsigned)a.count_blocks, kCountThreads, (size_t)a.E * 4, stream>>>(a, per);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    int64_t cap = moe_launch::sm_count_current();
+    if (cap > kMaxPassBlocks) cap = kMaxPassBlocks;
+    cfg.gridDim = dim3((unsigned)(turns < cap ? turns : cap));
+    // programmatic launch: the pass's first loads run under the counts, which it then waits for
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+  }
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a);
+  return err == cudaSuccess ? cudaGetLastError() : err;
 }
 
-template <int VEC>
-cudaError_t launch_width(const RouterLoss& a, int blocks, bool one, cudaStream_t s) {
+template <int LANES, int NV>
+cudaError_t launch_rows(const RouterLoss& a, cudaStream_t s) {
+  if (a.E % 4) return launch_pass<LANES, NV, false, false>(a, s);
+  return a.E == 4 * NV * LANES ? launch_pass<LANES, NV, true, true>(a, s) : launch_pass<LANES, NV, true, false>(a, s);
+}
+
+// The fewest lanes that hold a row at sixteen values each (fewer for narrow rows, 32 above 512
+// experts): fewer lanes mean fewer shuffle steps per row and more rows in flight per warp.
+cudaError_t launch(const RouterLoss& a, cudaStream_t s) {
   const int E = a.E;
-  if (E <= 32) return launch_pass<8, 1, VEC>(a, blocks, one, s);
-  if (E <= 64) return launch_pass<16, 1, VEC>(a, blocks, one, s);
-  if (E <= 128) return launch_pass<32, 1, VEC>(a, blocks, one, s);
-  if (E <= 256) return launch_pass<32, 2, VEC>(a, blocks, one, s);
-  if (E <= 512) return launch_pass<32, 4, VEC>(a, blocks, one, s);
-  return launch_pass<32, 8, VEC>(a, blocks, one, s);
-}
-
-int pass_blocks(int64_t T, int E) {
-  const int lanes = E <= 32 ? 8 : (E <= 64 ? 16 : 32);
-  const int64_t rows = (int64_t)kWarps * (32 / lanes) * (E <= 128 ? 2 : 1);
-  const int64_t need = (T + rows - 1) / rows, cap = (int64_t)moe_launch::sm_count_current() * 2;
-  return (int)(need < 1 ? 1 : (need < cap ? need : cap));
+  if (E <= 16) return launch_rows<4, 1>(a, s);
+  if (E <= 32) return launch_rows<4, 2>(a, s);
+  if (E <= 64) return launch_rows<4, 4>(a, s);
+  if (E <= 128) return launch_rows<8, 4>(a, s);
+  if (E <= 256) return launch_rows<16, 4>(a, s);
+  if (E <= 512) return launch_rows<32, 4>(a, s);
+  return launch_rows<32, 8>(a, s);
 }
 
 }  // namespace
@@ -374,24 +635,11 @@ int pass_blocks(int64_t T, int E) {
 namespace moe_launch {
 
 size_t router_loss_workspace_bytes(int E) {
-  // the partial sums of at most two blocks per SM (up to 256 SMs)
-  return 256 + (size_t)kMaxCountBlocks * (E + 1) * 4 + (size_t)512 * (E + 1) * 4;
+  return 512 + (size_t)kMaxCountBlocks * (E + 1) * 4 + (size_t)kMaxPassBlocks * (part_pitch(E) + 1) * 4;
 }
 
-cudaError_t router_loss(RouterLoss a, cudaStream_t stream) {
-  const bool one = a.T * a.E <= kOneBlockElems;
-  if (!one) {
-    int64_t blocks = (a.T * a.k + 4095) / 4096;
-    if (blocks > kMaxCountBlocks) blocks = kMaxCountBlocks;
-    const int64_t per = (a.T + blocks - 1) / blocks;
-    a.count_blocks = (int)blocks;
-    router_count_kernel<<<(unsigned)blocks, kThreads, (size_t)a.E * 4, stream>>>(a, per);
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-  }
-  int blocks = one ? 1 : pass_blocks(a.T, a.E);
-  if (blocks > 512) blocks = 512;
-  return a.E % 4 == 0 ? launch_width<4>(a, blocks, one, stream) : launch_width<1>(a, blocks, one, stream);
+cudaError_t router_loss(const RouterLoss& a, cudaStream_t stream) {
+  return launch(a, stream);
 }
 
 }  // namespace moe_launch
