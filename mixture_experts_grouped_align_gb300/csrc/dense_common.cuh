@@ -31,6 +31,22 @@ MOE_DEV uint64_t w_desc(uint32_t tile, bool kn, int j) {
   return kn ? tc::sdesc_sw128_mn(tile + j * 2 * 1024, kAtomCol, 1024) : tc::sdesc_sw128(tile + j * 32);
 }
 
+// The warp's elected lane: true in exactly one lane, in warp-uniform code.
+MOE_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Descriptor steps, in the descriptor's units of 16 bytes: a K step of 16 elements of the weight
+// tile (w_desc's j) and of a K-major tile.
+MOE_DEV uint32_t w_step(bool kn) { return kn ? 2 * 1024 / 16 : 2; }
+constexpr uint32_t kXStep = 2;
+
 MOE_DEV float bias_at(const void* bias, int64_t i) {
   return moe::bf16_bits_to_f32(static_cast<const uint16_t*>(bias)[i]);
 }

@@ -3,7 +3,7 @@
 //   z = x . W^T + b;   out = act(z) + residual_scale * residual
 // x [M, K] bf16; W stored [N1, K] or (contracted over its rows, as an input gradient needs the
 // forward weight) [K, N1]; act = none, relu^2 or SwiGLU (N1 = 2N: gate features, then up).
-// fp32 accumulation, one rounding to the output type.
+// fp32 accumulation, one rounding to bf16 (fp32 outputs, and shapes of few tiles: dense_split.cu).
 //
 // Bound: 2 M N1 K operations on the tensor cores (the operands are read about once through L2:
 // a 128 x 256 tile does 85 operations per operand byte it loads).  Persistent blocks, one per
@@ -64,7 +64,7 @@ __device__ __forceinline__ void bias8(const void* bias, int64_t base, int64_t n,
   }
 }
 
-template <bool GATED, bool F32>
+template <bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_r, Dense d,
@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* rfull = drain + 1;         // [kEpiWarps] residual box landed
   uint32_t* taddr_s = reinterpret_cast<uint32_t*>(rfull + kEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(taddr_s + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // from lane 0: values the compiler can keep in uniform registers
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&full[s], 1);
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t taddr = *taddr_s, smem_s = tc::smem_addr(smem);
+  const uint32_t taddr = __shfl_sync(0xffffffffu, *taddr_s, 0), smem_s = tc::smem_addr(smem);
   const int nk = (d.K + kBK - 1) / kBK;
   const bool kn = d.w_kn != 0;
   const uint64_t wb = d.wait_ns > 0 ? (uint64_t)d.wait_ns : tc::kWaitNs;
@@ -141,45 +142,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1 && !d.stall) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc = tc::idesc_f16(kBM, kBN, 1) | (kn ? 1u << 16 : 0u);
-      uint32_t it = 0, acc_it = 0;
-      for (int64_t t = blockIdx.x; t < ts.total && !*abort_flag; t += gridDim.x, ++acc_it) {
-        const uint32_t acc = acc_it & 1;
-        if (!tc::mbar_wait(&tempty[acc], ((acc_it >> 1) & 1) ^ 1, wb)) {
-          moe::set_status(d.status, MOE_ERR_TIMEOUT);
-          *abort_flag = 1;
+    // The whole warp runs the loop and one lane issues: descriptors and addresses are the same in
+    // every lane, so they stay in uniform registers and a stage's issue takes few instructions.
+    const bool leader = elect_one();
+    const uint32_t idesc = tc::idesc_f16(kBM, kBN, 1) | (kn ? 1u << 16 : 0u);
+    const uint32_t wstep = w_step(kn);
+    const uint64_t a0 = tc::sdesc_sw128(smem_s + kA), b0 = w_desc(smem_s + kB, kn, 0);
+    uint32_t s = 0, ph = 0, acc = 0, acc_ph = 1;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < ts.total && ok && !*abort_flag; t += gridDim.x) {
+      if (!tc::mbar_wait(&tempty[acc], acc_ph, wb)) {
+        ok = false;
+        break;
+      }
+      tc::tc_fence_after();
+      const uint32_t d_tmem = taddr + acc * kBN;
+      for (int kb = 0; kb < nk; ++kb) {
+        if (!tc::mbar_wait(&full[s], ph, wb)) {
+          ok = false;
           break;
         }
         tc::tc_fence_after();
-        bool ok = true;
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!tc::mbar_wait(&full[s], (it / kStages) & 1, wb)) {
-            moe::set_status(d.status, MOE_ERR_TIMEOUT);
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const uint32_t sl = smem_s + s * kSlot;
+        if (leader) {
+          const uint64_t ad = a0 + s * (kSlot / 16), bd = b0 + s * (kSlot / 16);
 #pragma unroll
           for (int j = 0; j < kBK / 16; ++j)
-            tc::mma_f16_ss(taddr + acc * kBN, tc::sdesc_sw128(sl + kA + j * 32), w_desc(sl + kB, kn, j), idesc,
-                           (kb | j) != 0);
+            tc::mma_f16_ss(d_tmem, ad + j * kXStep, bd + j * wstep, idesc, (kb | j) != 0);
           tc::mma_commit(&empty[s]);
         }
-        if (!ok) break;
-        tc::mma_commit(&tfull[acc]);
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      tc::mma_commit(drain);
-      if (!tc::mbar_wait(drain, 0, wb)) moe::set_status(d.status, MOE_ERR_TIMEOUT);
+      if (!ok) break;
+      if (leader) tc::mma_commit(&tfull[acc]);
+      __syncwarp();
+      acc ^= 1;
+      if (acc == 0) acc_ph ^= 1;
     }
+    if (!ok) {
+      moe::set_status(d.status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    if (leader) tc::mma_commit(drain);
+    if (!tc::mbar_wait(drain, 0, wb)) moe::set_status(d.status, MOE_ERR_TIMEOUT);
     __syncwarp();
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------------ epilogue
     const int ew = warp - kEpiWarp0, quarter = warp & 3, half = ew >> 2;
-    constexpr int kCols = F32 ? 32 : 64;         // columns of a 128-byte staging row
+    constexpr int kCols = 64;                    // columns of a 128-byte staging row
     const uint32_t box = smem_s + kStg + ew * 4096;
     const bool vec = d.N % 8 == 0;
     const bool res_box = d.residual != nullptr && d.tma_out;
@@ -203,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma::bulk_wait_read_all();  // the last store has read the box
           if (res_box) {
             tma::mbar_arrive_expect_tx(&rfull[ew], 4096);
-            tma::load_2d(box, &tm_r, (int32_t)(n0 * (F32 ? 4 : 2)), (int32_t)m0, &rfull[ew]);
+            tma::load_2d(box, &tm_r, (int32_t)(n0 * 2), (int32_t)m0, &rfull[ew]);
           }
         }
         __syncwarp();
@@ -254,24 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 8; ++i)
                 if (m < d.M && n + i < d.N) o[i] += d.residual_scale * residual_at(d, m * d.N + n + i);
             }
-            if (F32) {
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t at = box + lane * 128 + (((2 * q + j) ^ (lane & 7)) << 4);
-                if (res_box) {
-                  float r[4];
-                  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
-                               : "r"(at)
-                               : "memory");
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) o[4 * j + i] += d.residual_scale * r[i];
-                }
-                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(o[4 * j]), "f"(o[4 * j + 1]),
-                             "f"(o[4 * j + 2]), "f"(o[4 * j + 3])
-                             : "memory");
-              }
-            } else {
+            {
               const uint32_t at = box + lane * 128 + (((b / 8 + q) ^ (lane & 7)) << 4);
               if (res_box) {
                 uint32_t r[4];
@@ -302,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma::store_2d(&tm_o, (int32_t)(n0 * (F32 ? 4 : 2)), (int32_t)m0, box);
+            tma::store_2d(&tm_o, (int32_t)(n0 * 2), (int32_t)m0, box);
             tma::bulk_commit();
           }
         } else {  // rows of out not a multiple of 16 bytes: a row's columns by the lanes
@@ -311,11 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int cols = d.N - n0 < kCols ? (int)(d.N - n0) : kCols;
           for (int r = 0; r < rows; ++r)
             for (int c = lane; c < cols; c += 32) {
-              if (F32) {
-                uint32_t w;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(box + r * 128 + (((c >> 2) ^ (r & 7)) << 4) + (c & 3) * 4) : "memory");
-                static_cast<uint32_t*>(d.out)[(m0 + r) * d.N + n0 + c] = w;
-              } else {
+              {
                 uint16_t w;
                 asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(box + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2) : "memory");
                 static_cast<uint16_t*>(d.out)[(m0 + r) * d.N + n0 + c] = w;
@@ -339,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool GATED, bool F32>
+template <bool GATED>
 cudaError_t launch(const Dense& d, cudaStream_t stream) {
   Tiles ts;
   ts.m = (d.M + kBM - 1) / kBM;
@@ -352,15 +344,15 @@ cudaError_t launch(const Dense& d, cudaStream_t stream) {
                           : tma::encode_2d_u8(&mw, d.w, K2, N1, K2, 128, GATED ? 128 : kBN, true);
   if (!okw) return cudaErrorInvalidValue;
   if (d.tma_out) {
-    const uint64_t row = (uint64_t)d.N * (F32 ? 4 : 2);
+    const uint64_t row = (uint64_t)d.N * 2;
     if (!tma::encode_2d_u8(&mo, d.out, row, (uint64_t)d.M, row, 128, 32, true)) return cudaErrorInvalidValue;
     if (d.residual && !tma::encode_2d_u8(&mr, d.residual, row, (uint64_t)d.M, row, 128, 32, true))
       return cudaErrorInvalidValue;
   }
-  cudaError_t err = cudaFuncSetAttribute(dense_gemm_kernel<GATED, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t err = cudaFuncSetAttribute(dense_gemm_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (err != cudaSuccess) return err;
   const int64_t sms = moe_launch::sm_count_current();
-  dense_gemm_kernel<GATED, F32><<<(unsigned)(ts.total < sms ? ts.total : sms), kThreads, kSmem, stream>>>(mx, mw, mo, mr, d, ts);
+  dense_gemm_kernel<GATED><<<(unsigned)(ts.total < sms ? ts.total : sms), kThreads, kSmem, stream>>>(mx, mw, mo, mr, d, ts);
   return cudaGetLastError();
 }
 
@@ -370,10 +362,10 @@ namespace moe_launch {
 
 cudaError_t dense_gemm(Dense d, cudaStream_t stream) {
   if (d.M == 0) return cudaSuccess;
-  if (dense_split_takes(d)) return dense_split(d, stream);
-  d.tma_out = ((int64_t)d.N * (d.out_f32 ? 4 : 2)) % 16 == 0;
-  if (d.gated) return d.out_f32 ? launch<true, true>(d, stream) : launch<true, false>(d, stream);
-  return d.out_f32 ? launch<false, true>(d, stream) : launch<false, false>(d, stream);
+  cudaError_t err;
+  if (dense_split(d, stream, &err)) return err;
+  d.tma_out = d.N % 8 == 0;
+  return d.gated ? launch<true>(d, stream) : launch<false>(d, stream);
 }
 
 }  // namespace moe_launch

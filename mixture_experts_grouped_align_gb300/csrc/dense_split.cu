@@ -1,30 +1,45 @@
-// The dense product (dense_gemm.cu) where its 128 x 256 tiles would leave SMs idle: few rows,
-// or few columns.
+// The dense product (dense_gemm.cu) where its 128 x 256 tiles would leave SMs idle (few rows, or
+// few columns), and all of its fp32 outputs.
 //
-// Bound with few rows: reading W once.  A tile is 128 features x BN rows of x with the roles of
-// the operands exchanged (A = the 128 weight rows, B = the rows of x), so that one row of x
-// costs an MMA of N = 16 and not of M = 128.  K is split over the C CTAs of a cluster, which
-// makes tiles x C CTAs pull on W at once; each accumulates its share in TMEM, leaves it in its
-// shared memory as fp32 (token-major, so that lanes are consecutive features), and the C shares
-// are added in rank order through distributed shared memory by the CTA that stores the row: no
-// workspace, no second launch, the same bits every time.  SwiGLU keeps two accumulators (gate
-// and up features in the same lane).
-//   warp 0 loads stages (64 of K: the weight tile(s), BN rows of x) by TMA, as many stages as
-//   fit; warp 1 issues the MMAs; then all eight warps drain, add and store.
+// Bound with few rows: reading W once.  A tile is 128 NA features x BN rows of x with the roles
+// of the operands exchanged (A = 128 weight rows, B = the rows of x), so that one row of x costs
+// an MMA of N = 16 and not of M = 128.  K is split over the C CTAs of a cluster, which makes
+// tiles x C CTAs pull on W at once; each accumulates its share in TMEM, leaves it in its shared
+// memory as fp32 (token-major, so that lanes are consecutive features), and the C shares are
+// added in rank order through distributed shared memory by the CTA that stores the row: no
+// workspace, no second launch, the same bits every time.  A SwiGLU weight tile is 64 gate rows
+// and the 64 up rows of the same features, which meet in that sum.  NA = 2 keeps two accumulators
+// that share one load of x.
+//
+// The tensor core's accumulator loses up to one unit in the last place with every MMA, always
+// towards zero, which a bf16 output hides and an fp32 output does not.  For fp32 outputs K is
+// therefore also split over G accumulators in TMEM, of at most kGroupBlocks stages each where
+// the columns suffice, and those are added in fp32 registers.
+//   warp 0 loads stages (64 of K: the weight tiles, BN rows of x) by TMA, as many stages as fit,
+//   from before the block's other roles are ready;
+//   warp 1 issues the MMAs; then all sixteen warps drain, add and store.
+#include <atomic>
+
 #include "dense_common.cuh"
 
 namespace {
 
 using namespace dense;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kFeat = 128;
 constexpr int kMaxStages = 12;
+constexpr int kAlone = 116 * 1024;  // more than half of an SM's shared memory
 constexpr int kRing = 208 * 1024;  // shared memory of the stages, at most
 
+constexpr int kGroupBlocks = 14;   // stages (64 of K) an accumulator takes for fp32 outputs
+
 struct Split {
-  int BN;        // rows of x per tile: 16, 32, 64, 128 or (not SwiGLU) 256
+  int BN;        // rows of x per tile: 16, 32, 64, 128 or 256
+  int NA;        // weight tiles (128 features) per tile
   int C;         // CTAs of a cluster: the shares of K
+  int G;         // accumulators a share is split over
+  int phase;     // rows of x that leave through shared memory at a time
   int stages;
   int slot;      // bytes of a stage
   int smem;
@@ -32,15 +47,77 @@ struct Split {
   int64_t n_tiles, m_tiles;
 };
 
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr, uint32_t rank) {
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr, uint32_t rank) {
   uint32_t a;
-  float2 v;
+  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
 
+// 32 lanes x 16 columns of TMEM -> 16 registers a thread.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+
+// The epilogue of four neighbouring features of a row: z (SwiGLU: the gate) and u (the up part).
 template <bool GATED>
+__device__ __forceinline__ void store4(const Dense& d, int64_t m, int64_t n, float4 z4, float4 u4) {
+  if (n >= d.N) return;
+  float z[4] = {z4.x, z4.y, z4.z, z4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
+  const int some = d.N - n < 4 ? (int)(d.N - n) : 4;
+  if (d.bias)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < some) {
+        z[i] += bias_at(d.bias, n + i);
+        if (GATED) u[i] += bias_at(d.bias, d.N + n + i);
+      }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (GATED) z[i] = moe::silu(z[i]) * u[i];
+    else if (d.relu2) z[i] = moe::relu2(z[i]);
+  }
+  const int64_t at = m * d.N + n;
+  if (some == 4 && d.N % 4 == 0) {
+    if (d.out_f32) {
+      if (d.residual) {
+        const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(d.residual) + at);
+        z[0] += d.residual_scale * r.x;
+        z[1] += d.residual_scale * r.y;
+        z[2] += d.residual_scale * r.z;
+        z[3] += d.residual_scale * r.w;
+      }
+      *reinterpret_cast<float4*>(static_cast<float*>(d.out) + at) = make_float4(z[0], z[1], z[2], z[3]);
+    } else {
+      if (d.residual) {
+        const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(d.residual) + at);
+        z[0] += d.residual_scale * __uint_as_float(r.x << 16);
+        z[1] += d.residual_scale * __uint_as_float(r.x & 0xffff0000u);
+        z[2] += d.residual_scale * __uint_as_float(r.y << 16);
+        z[3] += d.residual_scale * __uint_as_float(r.y & 0xffff0000u);
+      }
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(z[0], z[1]), hi = __floats2bfloat162_rn(z[2], z[3]);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(d.out) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < some) {
+        const float o = z[i] + (d.residual ? d.residual_scale * residual_at(d, at + i) : 0.f);
+        if (d.out_f32) static_cast<float*>(d.out)[at + i] = o;
+        else static_cast<uint16_t*>(d.out)[at + i] = moe::f32_to_bf16_bits(o);
+      }
+  }
+}
+
+template <int NA, bool GATED>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_split_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, Dense d,
                        Split sp) {
@@ -49,9 +126,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
   __shared__ uint32_t taddr_s;
   __shared__ volatile int abort_flag;
-  constexpr int kNA = GATED ? 2 : 1;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = sp.C > 1 ? (int)tc::cluster_ctarank() : 0;
+  constexpr int kOut = GATED ? kFeat / 2 : kFeat;  // output features of a weight tile
+  // from lane 0: values the compiler can keep in uniform registers
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int rank = sp.C > 1 ? __shfl_sync(0xffffffffu, (int)tc::cluster_ctarank(), 0) : 0;
+  const uint32_t smem_s = tc::smem_addr(smem);
+  const bool kn = d.w_kn != 0;
+  const uint64_t wb = d.wait_ns > 0 ? (uint64_t)d.wait_ns : tc::kWaitNs;
+  const uint32_t tile = blockIdx.x / (uint32_t)sp.C, mt = tile / (uint32_t)sp.n_tiles, nt = tile - mt * (uint32_t)sp.n_tiles;
+  const int64_t n0 = (int64_t)nt * NA * kOut;  // the tile's first output feature
+  const int nk = (d.K + kBK - 1) / kBK;
+  const int k0 = (int)((int64_t)nk * rank / sp.C), share = (int)((int64_t)nk * (rank + 1) / sp.C) - k0;
+  const int kx = NA * kFeat * 128;  // x rows of a stage, behind the weight tiles
+  auto load_stage = [&](int it, int s) {
+    const uint32_t sl = smem_s + s * sp.slot;
+    const int kb = k0 + it;
+    tma::mbar_arrive_expect_tx(&full[s], (uint32_t)(kx + sp.BN * 128));
+#pragma unroll
+    for (int a = 0; a < NA; ++a) {
+      const uint32_t w = sl + a * kFeat * 128;
+      if (GATED) {
+        load_w(w, &tm_w, kn, n0 + a * kOut, kOut, kb, &full[s]);
+        load_w(w + kOut * 128, &tm_w, kn, d.N + n0 + a * kOut, kOut, kb, &full[s]);
+      } else {
+        load_w(w, &tm_w, kn, n0 + a * kOut, kOut, kb, &full[s]);
+      }
+    }
+    tma::load_2d(sl + kx, &tm_x, kb * 128, (int32_t)(mt * sp.BN), &full[s]);
+  };
+  // two stages are under way before the block's other warps are ready
+  const int first = share < 2 ? share : (sp.stages < 2 ? sp.stages : 2);
   if (tid == 0) {
     for (int s = 0; s < sp.stages; ++s) {
       tc::mbar_init(&full[s], 1);
@@ -60,6 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(&done, 1);
     abort_flag = 0;
     tc::mbar_fence_init();
+    tc::fence_proxy_async_smem();
+    if (!d.stall)
+      for (int it = 0; it < first; ++it) load_stage(it, it);
   }
   if (warp == 1) {
     tc::tmem_alloc(&taddr_s, sp.cols);
@@ -68,30 +175,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t taddr = taddr_s, smem_s = tc::smem_addr(smem);
-  const bool kn = d.w_kn != 0;
-  const uint64_t wb = d.wait_ns > 0 ? (uint64_t)d.wait_ns : tc::kWaitNs;
-  const int64_t tile = blockIdx.x / sp.C;
-  const int64_t nt = tile % sp.n_tiles, mt = tile / sp.n_tiles;
-  const int nk = (d.K + kBK - 1) / kBK;
-  const int k0 = (int)((int64_t)nk * rank / sp.C), k1 = (int)((int64_t)nk * (rank + 1) / sp.C);
-  const int kx = kNA * kFeat * 128;  // x rows of a stage, behind the weight tiles
+  const uint32_t taddr = __shfl_sync(0xffffffffu, taddr_s, 0);
 
-  if (warp == 0 && lane == 0 && !d.stall) {
-    int issued = 0;
-    for (int kb = k0; kb < k1; ++kb) {
-      const int it = kb - k0, s = it % sp.stages;
-      if (!tc::mbar_wait(&empty[s], ((it / sp.stages) & 1) ^ 1, wb)) {
+  if (warp == 0 && !d.stall) {
+    const bool leader = elect_one();
+    int s = first == sp.stages ? 0 : first, issued = first;
+    uint32_t ph = first == sp.stages ? 0 : 1;  // a slot's first use waits for nothing
+    for (int it = first; it < share; ++it) {
+      if (!tc::mbar_wait(&empty[s], ph, wb)) {
         moe::set_status(d.status, MOE_ERR_TIMEOUT);
         abort_flag = 1;
         break;
       }
+      if (leader) load_stage(it, s);
+      __syncwarp();
       issued = it + 1;
-      const uint32_t sl = smem_s + s * sp.slot;
-      tma::mbar_arrive_expect_tx(&full[s], (uint32_t)(kx + sp.BN * 128));
-      load_w(sl, &tm_w, kn, nt * kFeat, kFeat, kb, &full[s]);
-      if (GATED) load_w(sl + kFeat * 128, &tm_w, kn, d.N + nt * kFeat, kFeat, kb, &full[s]);
-      tma::load_2d(sl + kx, &tm_x, kb * 128, (int32_t)(mt * sp.BN), &full[s]);
+      if (++s == sp.stages) {
+        s = 0;
+        ph ^= 1;
+      }
     }
     // every load lands before the block may end, also when another role has given up
     for (int j = issued > sp.stages ? issued - sp.stages : 0; j < issued; ++j)
@@ -99,171 +201,252 @@ __global__ void __launch_bounds__(kThreads, 1)
         moe::set_status(d.status, MOE_ERR_TIMEOUT);
         abort_flag = 1;
       }
-  } else if (warp == 1 && lane == 0 && !d.stall) {
+  } else if (warp == 1 && !d.stall) {
+    // The whole warp runs the loop and one lane issues: descriptors and addresses are the same in
+    // every lane, so they stay in uniform registers and a stage's issue takes few instructions.
+    const bool leader = elect_one();
     const uint32_t idesc = tc::idesc_f16(kFeat, sp.BN, 1) | (kn ? 1u << 15 : 0u);
-    for (int kb = k0; kb < k1; ++kb) {
-      const int it = kb - k0, s = it % sp.stages;
-      if (!tc::mbar_wait(&full[s], (it / sp.stages) & 1, wb)) {
+    const uint32_t wstep = w_step(kn), slot16 = (uint32_t)sp.slot / 16;
+    const uint64_t w0 = w_desc(smem_s, kn, 0), x0 = tc::sdesc_sw128(smem_s + kx);
+    // accumulator group g takes the stages up to (g + 1) share / G
+    int s = 0, g = 0, last_of_g = share / sp.G;
+    uint32_t ph = 0, d_tmem = taddr, fresh = 1;
+    uint64_t wd = w0, xd = x0;
+    for (int it = 0; it < share; ++it) {
+      if (it == last_of_g) {
+        ++g;
+        last_of_g = (int)((int64_t)share * (g + 1) / sp.G);
+        d_tmem += NA * sp.BN;
+        fresh = 1;
+      }
+      if (!tc::mbar_wait(&full[s], ph, wb)) {
         moe::set_status(d.status, MOE_ERR_TIMEOUT);
         abort_flag = 1;
         break;
       }
       tc::tc_fence_after();
-      const uint32_t sl = smem_s + s * sp.slot;
+      if (leader) {
 #pragma unroll
-      for (int a = 0; a < kNA; ++a)
+        for (int a = 0; a < NA; ++a)
 #pragma unroll
-        for (int j = 0; j < kBK / 16; ++j)
-          tc::mma_f16_ss(taddr + a * sp.BN, w_desc(sl + a * kFeat * 128, kn, j), tc::sdesc_sw128(sl + kx + j * 32), idesc,
-                         it > 0 || j > 0);
-      tc::mma_commit(&empty[s]);
-    }
-    tc::mma_commit(&done);
-  }
-  __syncwarp();
-  bool ok = true;
-  // every thread waits for the last product (the loader's lane too: a timeout ends its loop)
-  if (!tc::mbar_wait(&done, 0, wb)) {
-    moe::set_status(d.status, MOE_ERR_TIMEOUT);
-    ok = false;
-  }
-  if (abort_flag) ok = false;
-  tc::tc_fence_after();
-  // the accumulators -> this CTA's shared memory, [accumulator][token][feature] fp32 (the ring
-  // is free: every load has landed and every product has read it)
-  float* part = reinterpret_cast<float*>(smem);
-  const int feat = (warp & 3) * 32 + lane;
-  const int64_t m0 = mt * sp.BN;
-  const int rows = d.M - m0 < sp.BN ? (int)(d.M - m0) : sp.BN;
-  if (ok) {
-    const uint32_t tb = taddr + ((uint32_t)((warp & 3) * 32) << 16);
-    // warps 0-3 take the even groups of 16 columns, warps 4-7 the odd ones
-    for (int a = 0; a < kNA; ++a)
-      for (int c = (warp >> 2) * 16; c < sp.BN; c += 32) {
-        if (c >= rows) break;  // tokens past M: nothing is read of them
-        uint32_t v[16];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-              "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-            : "r"(tb + a * sp.BN + c));
-        tc::tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) part[((size_t)a * sp.BN + c + j) * kFeat + feat] = __uint_as_float(v[j]);
+          for (int j = 0; j < kBK / 16; ++j)
+            tc::mma_f16_ss(d_tmem + a * sp.BN, wd + a * (kFeat * 128 / 16) + j * wstep, xd + j * kXStep, idesc, j > 0 || !fresh);
+        tc::mma_commit(&empty[s]);
       }
+      __syncwarp();
+      fresh = 0;
+      wd += slot16;
+      xd += slot16;
+      if (++s == sp.stages) {
+        s = 0;
+        ph ^= 1;
+        wd = w0;
+        xd = x0;
+      }
+    }
+    if (leader) tc::mma_commit(&done);
+  }
+  // One warp watches for the last product; the others sleep at the block's barrier and leave the
+  // issue slots to it.
+  if (warp == 1 && !tc::mbar_wait(&done, 0, wb)) {
+    moe::set_status(d.status, MOE_ERR_TIMEOUT);
+    abort_flag = 1;
+  }
+  __syncthreads();
+  const bool ok = !abort_flag;
+  tc::tc_fence_after();
+  const int64_t m0 = (int64_t)mt * sp.BN;
+  const int rows = d.M - m0 < sp.BN ? (int)(d.M - m0) : sp.BN;
+  const int phase = sp.phase;
+  // `phase` rows at a time: accumulators -> this CTA's shared memory, [weight tile][row][feature]
+  // fp32 (the ring is free: every load has landed and every product has read it), then the sum
+  // over the cluster.  The same turns for every CTA of the cluster: they share the tile's rows.
+  float* part = reinterpret_cast<float*>(smem);
+  const uint32_t base = tc::smem_addr(part);
+  for (int p0 = 0; p0 < rows; p0 += phase) {
+    const int prow = rows - p0 < phase ? rows - p0 : phase;
+    if (ok) {
+      const uint32_t tb = taddr + ((uint32_t)((warp & 3) * 32) << 16) + p0;
+      // a warp takes its 32 lanes of every fourth group of 16 rows
+#pragma unroll
+      for (int a = 0; a < NA; ++a)
+        for (int c = (warp >> 2) * 16; c < prow; c += 64) {
+          float* dst = part + (a * phase + c) * kFeat + (warp & 3) * 32 + lane;
+          uint32_t v[16];
+          tmem_ld16(tb + a * sp.BN + c, v);
+          tc::tmem_ld_wait();
+          for (int g = 1; g < sp.G; ++g) {
+            uint32_t r[16];
+            tmem_ld16(tb + (g * NA + a) * sp.BN + c, r);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(r[j]));
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) dst[j * kFeat] = __uint_as_float(v[j]);
+        }
+    }
+    if (sp.C > 1) tc::cluster_sync();
+    else __syncthreads();
+    // rows rank, rank + C, ... of the phase: four features a lane, kOut / 4 lanes a row
+    constexpr int kLanes = kOut / 4, kRows = kThreads / kLanes;
+    const int f = (tid % kLanes) * 4, t0 = rank + sp.C * (tid / kLanes);
+    if (ok && sp.C == 1) {
+      for (int t = t0; t < prow; t += kRows)
+#pragma unroll
+        for (int a = 0; a < NA; ++a) {
+          const float* at = part + (a * phase + t) * kFeat + f;
+          const float4 v = *reinterpret_cast<const float4*>(at);
+          store4<GATED>(d, m0 + p0 + t, n0 + a * kOut + f, v, GATED ? *reinterpret_cast<const float4*>(at + kOut) : v);
+        }
+    } else if (ok) {
+      for (int t = t0; t < prow; t += sp.C * kRows)
+#pragma unroll
+        for (int a = 0; a < NA; ++a) {
+          const uint32_t at = base + (uint32_t)((a * phase + t) * kFeat + f) * 4;
+          float4 v[8], u[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            v[r] = r < sp.C ? ld_cluster_f4(at, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (GATED) u[r] = r < sp.C ? ld_cluster_f4(at + kOut * 4, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+#pragma unroll
+          for (int r = 1; r < 8; ++r) {
+            v[0].x += v[r].x;
+            v[0].y += v[r].y;
+            v[0].z += v[r].z;
+            v[0].w += v[r].w;
+            if (GATED) {
+              u[0].x += u[r].x;
+              u[0].y += u[r].y;
+              u[0].z += u[r].z;
+              u[0].w += u[r].w;
+            }
+          }
+          store4<GATED>(d, m0 + p0 + t, n0 + a * kOut + f, v[0], GATED ? u[0] : v[0]);
+        }
+    }
+    // before the next phase overwrites, or the CTA leaves, every CTA has read its share
+    if (sp.C > 1) tc::cluster_sync();
+    else __syncthreads();
   }
   tc::tc_fence_before();
-  if (sp.C > 1) tc::cluster_sync();
-  else __syncthreads();
+  __syncthreads();
   if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_dealloc(taddr, sp.cols);
   }
-  // rows rank, rank + C, ... of the tile: four rows at a time, two features a thread
-  if (ok) {
-    const int f = (tid & 63) * 2;
-    const int64_t n = nt * kFeat + f;
-    const uint32_t base = tc::smem_addr(part);
-    float b0 = 0.f, b1 = 0.f, u0 = 0.f, u1 = 0.f;
-    if (d.bias) {
-      if (n < d.N) b0 = bias_at(d.bias, n);
-      if (n + 1 < d.N) b1 = bias_at(d.bias, n + 1);
-      if (GATED && n < d.N) u0 = bias_at(d.bias, d.N + n);
-      if (GATED && n + 1 < d.N) u1 = bias_at(d.bias, d.N + n + 1);
+}
+
+// CTAs of clusters of C that the device holds at once with one CTA per SM (queried once).
+int resident_ctas(int C) {
+  static std::atomic<int> seen[9];
+  int n = seen[C].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  const int sms = moe_launch::sm_count_current();
+  n = sms;
+  if (C > 1) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(C * sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kRing + 1024;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaFuncSetAttribute(dense_split_kernel<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&clusters, dense_split_kernel<1, false>, &cfg) != cudaSuccess || clusters < 1) {
+      (void)cudaGetLastError();
+      clusters = 1;
     }
-    for (int t = rank + sp.C * (tid >> 6); t < rows; t += sp.C * 4) {
-      float2 z = make_float2(0.f, 0.f), u = make_float2(0.f, 0.f);
-      const uint32_t at = base + (uint32_t)(t * kFeat + f) * 4;
-      for (int r = 0; r < sp.C; ++r) {
-        const float2 v = ld_cluster_f2(at, r);
-        z.x += v.x;
-        z.y += v.y;
-        if (GATED) {
-          const float2 w = ld_cluster_f2(at + (uint32_t)(sp.BN * kFeat * 4), r);
-          u.x += w.x;
-          u.y += w.y;
-        }
-      }
-      z.x += b0;
-      z.y += b1;
-      if (GATED) {
-        z.x = moe::silu(z.x) * (u.x + u0);
-        z.y = moe::silu(z.y) * (u.y + u1);
-      } else if (d.relu2) {
-        z.x = moe::relu2(z.x);
-        z.y = moe::relu2(z.y);
-      }
-      const int64_t at_o = (m0 + t) * d.N + n;
-      if (n + 1 < d.N && d.N % 2 == 0) {
-        if (d.out_f32) {
-          if (d.residual) {
-            const float2 r = *reinterpret_cast<const float2*>(static_cast<const float*>(d.residual) + at_o);
-            z.x += d.residual_scale * r.x;
-            z.y += d.residual_scale * r.y;
-          }
-          *reinterpret_cast<float2*>(static_cast<float*>(d.out) + at_o) = z;
-        } else {
-          if (d.residual) {
-            const uint32_t r = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(d.residual) + at_o);
-            z.x += d.residual_scale * __uint_as_float(r << 16);
-            z.y += d.residual_scale * __uint_as_float(r & 0xffff0000u);
-          }
-          *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(d.out) + at_o) = __floats2bfloat162_rn(z.x, z.y);
-        }
-      } else {
-        const float zz[2] = {z.x, z.y};
-        for (int i = 0; i < 2; ++i)
-          if (n + i < d.N) {
-            const float o = zz[i] + (d.residual ? d.residual_scale * residual_at(d, at_o + i) : 0.f);
-            if (d.out_f32) static_cast<float*>(d.out)[at_o + i] = o;
-            else static_cast<uint16_t*>(d.out)[at_o + i] = moe::f32_to_bf16_bits(o);
-          }
-      }
-    }
+    n = clusters * C;
   }
-  if (sp.C > 1) tc::cluster_sync();  // no CTA leaves while another still reads its share
+  seen[C].store(n, std::memory_order_relaxed);
+  return n;
 }
 
-int tile_rows(const Dense& d) {
-  const int most = d.gated ? 128 : 256;
-  int bn = 16;
-  while (bn < most && bn < d.M) bn *= 2;
-  return bn;
+// The variant with the least estimated time in clocks.  Per CTA a stage costs what its operands
+// take from L2 (about 60 bytes a clock and SM) or its MMAs on the tensor core (BN / 2 clocks
+// each), whichever is more; a wave of CTAs is as long as its longest share; the sum over the
+// cluster moves about 20 bytes a clock into an SM.
+Split plan(const Dense& d, double* clocks) {
+  const uint32_t nk = (uint32_t)(d.K + kBK - 1) / kBK;
+  const int kOut = d.gated ? kFeat / 2 : kFeat;
+  Split best{};
+  double least = 0;
+  for (int NA = 1; NA <= 2; ++NA)
+    for (int BN = 16; BN <= 256; BN *= 2) {
+      Split s{};
+      s.NA = NA;
+      s.BN = BN;
+      s.n_tiles = (d.N + NA * kOut - 1) / (NA * kOut);
+      s.m_tiles = (d.M + BN - 1) / BN;
+      const int64_t tiles = s.n_tiles * s.m_tiles;
+      if (tiles < (1 << 27)) {
+        const double load = (NA * kFeat + BN) * (128 / 60.0), mma = BN * 2.0 * NA, stage = mma > load ? mma : load;
+        for (uint32_t C = 1; C <= 8 && C <= nk; ++C) {
+          const uint32_t at_once = (uint32_t)resident_ctas((int)C);
+          // more shares than fill a wave only shorten fp32 sums
+          if (C > 1 && (uint32_t)tiles * (C - 1) >= at_once && !d.out_f32) break;
+          const uint32_t share = (nk + C - 1) / C, waves = ((uint32_t)tiles * C + at_once - 1) / at_once;
+          uint32_t G = 1;
+          if (d.out_f32) {
+            G = (share + kGroupBlocks - 1) / kGroupBlocks;
+            if (G > (uint32_t)(512 / (NA * BN))) continue;  // too long a sum in one accumulator
+          }
+          // each wave: its stages, about 3000 clocks to start, the drain and the cluster's sum
+          const double bytes = NA * BN * kFeat * 4.0;
+          const double t = waves * (share * stage + 3000 + bytes * G / 100 + (C > 1 ? 1000 + bytes / 20 * (C - 1) / C : 0));
+          if (best.BN == 0 || t < least) {
+            least = t;
+            best = s;
+            best.C = (int)C;
+            best.G = (int)G;
+          }
+        }
+      }
+      if (BN >= d.M) break;
+    }
+  if (best.BN == 0) {  // K beyond what the accumulators hold apart: as many sums as fit
+    best.NA = 1;
+    best.BN = 32;
+    best.C = nk < 8 ? (int)nk : 8;
+    best.G = 512 / (best.NA * best.BN);
+    best.n_tiles = (d.N + kOut - 1) / kOut;
+    best.m_tiles = (d.M + best.BN - 1) / best.BN;
+  }
+  const int share = (int)((nk + best.C - 1) / best.C);
+  if (best.G > share) best.G = share;
+  best.slot = (best.NA * kFeat + best.BN) * 128;
+  best.stages = kRing / best.slot;
+  if (best.stages > kMaxStages) best.stages = kMaxStages;
+  if (best.stages > share) best.stages = share;
+  best.phase = best.BN;
+  while (best.NA * best.phase * kFeat * 4 > kRing) best.phase /= 2;
+  const int part = best.NA * best.phase * kFeat * 4;
+  best.smem = (best.stages * best.slot > part ? best.stages * best.slot : part) + 1024;
+  // Never two CTAs of this kernel on an SM: one could wait for tensor memory that the other holds
+  // until its cluster has met, while the clusters' other CTAs wait the other way round.
+  if (best.smem < kAlone) best.smem = kAlone;
+  best.cols = 32;
+  while (best.cols < best.NA * best.BN * best.G) best.cols *= 2;
+  *clocks = least;
+  return best;
 }
 
-Split plan(const Dense& d) {
-  Split s{};
-  const int64_t sms = moe_launch::sm_count_current();
-  s.BN = tile_rows(d);
-  s.n_tiles = (d.N + kFeat - 1) / kFeat;
-  s.m_tiles = (d.M + s.BN - 1) / s.BN;
-  const int64_t tiles = s.n_tiles * s.m_tiles, nk = (d.K + kBK - 1) / kBK;
-  int64_t c = sms / tiles;
-  if (c > 8) c = 8;
-  if (c > nk) c = nk;
-  s.C = c < 1 ? 1 : (int)c;
-  s.slot = ((d.gated ? 2 : 1) * kFeat + s.BN) * 128;
-  s.stages = kRing / s.slot;
-  if (s.stages > kMaxStages) s.stages = kMaxStages;
-  const int share = (int)((nk + s.C - 1) / s.C);
-  if (s.stages > share) s.stages = share;
-  const int part = (d.gated ? 2 : 1) * s.BN * kFeat * 4;
-  s.smem = (s.stages * s.slot > part ? s.stages * s.slot : part) + 1024;
-  s.cols = 32;
-  while (s.cols < (d.gated ? 2 : 1) * s.BN) s.cols *= 2;
-  return s;
-}
-
-template <bool GATED>
+template <int NA, bool GATED>
 cudaError_t launch(const Dense& d, const Split& s, cudaStream_t stream) {
   const uint64_t K2 = (uint64_t)d.K * 2, N1 = GATED ? 2 * (uint64_t)d.N : (uint64_t)d.N;
   CUtensorMap mx{}, mw{};
   if (!tma::encode_2d_u8(&mx, d.x, K2, (uint64_t)d.M, K2, 128, (uint32_t)s.BN, true)) return cudaErrorInvalidValue;
   const bool okw = d.w_kn ? tma::encode_2d_u8(&mw, d.w, N1 * 2, (uint64_t)d.K, N1 * 2, 128, kBK, true)
-                          : tma::encode_2d_u8(&mw, d.w, K2, N1, K2, 128, kFeat, true);
+                          : tma::encode_2d_u8(&mw, d.w, K2, N1, K2, 128, GATED ? kFeat / 2 : kFeat, true);
   if (!okw) return cudaErrorInvalidValue;
-  auto kern = dense_split_kernel<GATED>;
+  auto kern = dense_split_kernel<NA, GATED>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
@@ -285,21 +468,20 @@ cudaError_t launch(const Dense& d, const Split& s, cudaStream_t stream) {
 
 namespace moe_launch {
 
-bool dense_split_takes(const Dense& d) {
-  const Split s = plan(d);
-  const int64_t sms = sm_count_current(), nk = (d.K + kBK - 1) / kBK;
-  const int64_t ctas = s.n_tiles * s.m_tiles * s.C;
-  if (ctas >= ((int64_t)1 << 31)) return false;
-  // tensor-core time of both kernels in units of one 128 x 256 stage
-  const int64_t tiles = ((d.M + 127) / 128) * ((d.N + (d.gated ? 127 : 255)) / (d.gated ? 128 : 256));
-  const int64_t big = (tiles + sms - 1) / sms * nk * 256;
-  const int64_t small = (ctas + sms - 1) / sms * ((nk + s.C - 1) / s.C) * (d.gated ? 2 : 1) * s.BN;
-  return small < big;
-}
-
-cudaError_t dense_split(const Dense& d, cudaStream_t stream) {
-  const Split s = plan(d);
-  return d.gated ? launch<true>(d, s, stream) : launch<false>(d, s, stream);
+bool dense_split(const Dense& d, cudaStream_t stream, cudaError_t* err) {
+  double split = 0;
+  const Split s = plan(d, &split);
+  const bool fits = s.n_tiles * s.m_tiles * s.C < ((int64_t)1 << 31);
+  if (!d.out_f32) {
+    // the tiled kernel: 512 clocks a stage, its start and the last tile's epilogue
+    const int64_t sms = sm_count_current(), nk = (d.K + kBK - 1) / kBK;
+    const int64_t tiles = ((d.M + 127) / 128) * ((d.N + (d.gated ? 127 : 255)) / (d.gated ? 128 : 256));
+    if (!fits || split >= (double)((tiles + sms - 1) / sms) * nk * 512 + 6000) return false;
+  }
+  if (!fits) *err = cudaErrorInvalidValue;
+  else if (d.gated) *err = s.NA == 2 ? launch<2, true>(d, s, stream) : launch<1, true>(d, s, stream);
+  else *err = s.NA == 2 ? launch<2, false>(d, s, stream) : launch<1, false>(d, s, stream);
+  return true;
 }
 
 }  // namespace moe_launch
