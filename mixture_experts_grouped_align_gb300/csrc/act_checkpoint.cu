@@ -48,18 +48,15 @@ MOE_DEV uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// MXFP8 of a 32-value block held eight values a lane by four neighbouring lanes (all of which
-// call): this lane's codes, and the block's scale byte.  The rule of mxq::quant32.
-MOE_DEV uint2 quant8(const float (&v)[8], uint32_t& scale) {
-  float amax = 0.f;
-  bool nan = false;
+// MXFP8 of a 32-value block held eight values (bf16 pairs `raw`, fp32 `v`) a lane by four
+// neighbouring lanes, all of which call: this lane's codes, and the block's scale byte.  The rule
+// of mxq::quant32; the largest magnitude is found on the bf16 pairs, where NaN is the largest.
+MOE_DEV uint2 quant8(const uint4& raw, const float (&v)[8], uint32_t& scale) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t m = 0;  // magnitudes are ordered like their bits
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    nan |= v[i] != v[i];
-    amax = fmaxf(amax, fabsf(v[i]));
-  }
-  if (nan) amax = __uint_as_float(0x7fffffffu);  // above infinity as an integer
-  uint32_t b = __float_as_uint(amax);
+  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  uint32_t b = max(m << 16, m & 0xffff0000u);
   b = max(b, __shfl_xor_sync(kAll, b, 1));
   b = max(b, __shfl_xor_sync(kAll, b, 2));
   if (b > 0x7f800000u) {
@@ -90,13 +87,23 @@ MOE_DEV void dequant8(uint2 c, uint32_t scale, float (&v)[8]) {
   }
 }
 
-MOE_DEV float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// 1 / (1 + 2^(-g log2 e)) with the hardware's exponential and reciprocal (2 ulp and 1 ulp).
+MOE_DEV float sigmoid(float g) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
 
 // The rows of a block: WIDE = the whole block on one row, otherwise 32 / LANES rows a warp.
-template <int LANES, bool WIDE>
+// A warp on a row of its own takes kTurns turns of 256 columns at a time, all loads first: that
+// many bytes in flight are what the stream needs, and the 32 scale bytes of the turns are one
+// sector, moved by one byte per lane.
+template <int LANES, bool WIDE, int TURNS>
 struct Map {
   static constexpr int kRowsPerBlock = WIDE ? 1 : kWarps * (32 / LANES);
   static constexpr int kStep = WIDE ? kThreads : LANES;  // columns of eight per turn
+  static constexpr int kTurns = TURNS;
   MOE_DEV static int64_t row() {
     if (WIDE) return blockIdx.x;
     return (int64_t)blockIdx.x * kRowsPerBlock + threadIdx.x / LANES;
@@ -104,51 +111,73 @@ struct Map {
   MOE_DEV static int col() { return WIDE ? threadIdx.x : threadIdx.x % LANES; }
 };
 
-template <bool GATED, int LANES, bool WIDE>
-__global__ void __launch_bounds__(kThreads) act_checkpoint_kernel(ActCheckpoint a) {
-  using M = Map<LANES, WIDE>;
+template <bool GATED, int LANES, bool WIDE, int TURNS>
+__global__ void __launch_bounds__(kThreads, TURNS > 1 ? 3 : 4) act_checkpoint_kernel(ActCheckpoint a) {
+  using M = Map<LANES, WIDE, TURNS>;
+  constexpr int kT = M::kTurns, kH = GATED ? 2 : 1;
   const int64_t row = M::row();
   const bool in = row < a.rows;
-  const int units = a.I / 8;
+  const int units = a.I / 8, lane = threadIdx.x & 31;
   const int64_t N1 = GATED ? 2 * (int64_t)a.I : a.I;
   const float w = !in ? 0.f : (a.row_w ? a.row_w[row] : 1.f);
-  const uint4* zg = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.gu) + row * N1);
+  const uint4* z = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.gu) + row * N1);
   uint4* h = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.h) + row * a.I);
   uint2* codes = reinterpret_cast<uint2*>(a.codes + row * N1);
   uint8_t* scales = a.scales + row * (N1 / 32);
   // every lane makes every turn: the shuffles of a quad need its four lanes
-  for (int c0 = 0; c0 < units; c0 += M::kStep) {
-    const int c = c0 + M::col();
-    const bool live = in && c < units;
-    float g[8], u[8], o[8];
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    // a row of weight 0 is left out: nothing of it is read, its outputs are zeros
-    unpack8(live && w != 0.f ? __ldcs(zg + c) : zero, g);
-    if (GATED) unpack8(live && w != 0.f ? __ldcs(zg + units + c) : zero, u);
+  for (int c0 = 0; c0 < units; c0 += kT * M::kStep) {
+    uint4 raw[kT][kH];
+    uint32_t packed[kH] = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = w == 0.f ? 0.f : w * (GATED ? moe::silu(g[i]) * u[i] : moe::relu2(g[i]));
-    uint32_t sg, su = 0;
-    const uint2 cg = quant8(g, sg);
-    uint2 cu = make_uint2(0, 0);
-    if (GATED) cu = quant8(u, su);
-    if (live) {
-      if (a.h) __stcs(h + c, pack8(o));
-      codes[c] = cg;
-      if (GATED) codes[units + c] = cu;
-      if ((c & 3) == 0) {
-        scales[c >> 2] = (uint8_t)sg;
-        if (GATED) scales[(units + c) >> 2] = (uint8_t)su;
+    for (int t = 0; t < kT; ++t) {
+      const int c = c0 + t * M::kStep + M::col();
+#pragma unroll
+      for (int p = 0; p < kH; ++p)  // a row of weight 0 is left out: nothing of it is read, its outputs are zeros
+        raw[t][p] = in && c < units && w != 0.f ? __ldcs(z + p * units + c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      const int c = c0 + t * M::kStep + M::col();
+      const bool live = in && c < units;
+      float g[8], u[8], o[8];
+      unpack8(raw[t][0], g);
+      if (GATED) unpack8(raw[t][kH - 1], u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = w == 0.f ? 0.f : w * (GATED ? g[i] * sigmoid(g[i]) * u[i] : moe::relu2(g[i]));
+      uint32_t sg, su = 0;
+      const uint2 cg = quant8(raw[t][0], g, sg);
+      uint2 cu = make_uint2(0, 0);
+      if (GATED) cu = quant8(raw[t][kH - 1], u, su);
+      if (live) {
+        if (a.h) __stcs(h + c, pack8(o));
+        __stcs(codes + c, cg);
+        if (GATED) __stcs(codes + units + c, cu);
+        if (kT == 1 && (c & 3) == 0) {
+          scales[c >> 2] = (uint8_t)sg;
+          if (GATED) scales[(units + c) >> 2] = (uint8_t)su;
+        }
+      }
+      packed[0] |= sg << (8 * t);
+      if (GATED) packed[kH - 1] |= su << (8 * t);
+    }
+    if (kT > 1) {  // lane 8 t + q stores the scale of turn t's quad q
+      const int b = c0 / 4 + lane;
+#pragma unroll
+      for (int p = 0; p < kH; ++p) {
+        const uint32_t v = __shfl_sync(kAll, packed[p], (lane & 7) * 4);
+        if (in && lane < 8 * kT && b * 4 < units) scales[p * (units / 4) + b] = (uint8_t)(v >> (8 * (lane >> 3)));
       }
     }
   }
 }
 
-template <bool GATED, int LANES, bool WIDE>
-__global__ void __launch_bounds__(kThreads) act_backward_kernel(ActBackward a) {
-  using M = Map<LANES, WIDE>;
+template <bool GATED, int LANES, bool WIDE, int TURNS>
+__global__ void __launch_bounds__(kThreads, TURNS > 1 ? 3 : 4) act_backward_kernel(ActBackward a) {
+  using M = Map<LANES, WIDE, TURNS>;
+  constexpr int kT = M::kTurns, kH = GATED ? 2 : 1;
   const int64_t row = M::row();
   const bool in = row < a.rows;
-  const int units = a.I / 8;
+  const int units = a.I / 8, lane = threadIdx.x & 31;
   const int64_t N1 = GATED ? 2 * (int64_t)a.I : a.I;
   const float w = !in ? 0.f : (a.row_w ? a.row_w[row] : 1.f);
   const uint2* codes = reinterpret_cast<const uint2*>(a.codes + row * N1);
@@ -157,37 +186,60 @@ __global__ void __launch_bounds__(kThreads) act_backward_kernel(ActBackward a) {
   uint4* dz = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.d_gu) + row * N1);
   uint4* h = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.h) + row * a.I);
   float dot = 0.f;
-  for (int c = M::col(); c < units; c += M::kStep) {
-    if (!in) break;
-    float dg[8], du[8], o[8];
-    if (w == 0.f) {
+  for (int c0 = 0; c0 < units; c0 += kT * M::kStep) {
+    uint4 rd[kT];
+    uint2 rc[kT][kH];
+    uint32_t rs[kT][kH], turns[kH] = {};
+    // a row of weight 0 is left out: nothing of it is read, its outputs are zeros
+    const bool read = in && w != 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dg[i] = du[i] = o[i] = 0.f;
-    } else {
-      float g[8], u[8], d[8];
-      unpack8(__ldcs(dh + c), d);
-      dequant8(__ldcs(codes + c), scales[c >> 2], g);
-      if (GATED) dequant8(__ldcs(codes + units + c), scales[(units + c) >> 2], u);
+    for (int t = 0; t < kT; ++t) {
+      const int c = c0 + t * M::kStep + M::col();
+      const bool live = read && c < units;
+      rd[t] = live ? __ldcs(dh + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int p = 0; p < kH; ++p) {
+        rc[t][p] = live ? __ldcs(codes + p * units + c) : make_uint2(0, 0);
+        if (kT == 1) rs[t][p] = live ? scales[(p * units + c) >> 2] : 0;
+      }
+    }
+    if (kT > 1) {  // lane 8 t + q holds the scale of turn t's quad q
+      const int b = c0 / 4 + lane;
+#pragma unroll
+      for (int p = 0; p < kH; ++p) {
+        turns[p] = read && lane < 8 * kT && b * 4 < units ? scales[p * (units / 4) + b] : 0;
+#pragma unroll
+        for (int t = 0; t < kT; ++t) rs[t][p] = __shfl_sync(kAll, turns[p], 8 * t + (lane >> 2));
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      const int c = c0 + t * M::kStep + M::col();
+      if (!in || c >= units) continue;
+      float g[8], u[8], d[8], dg[8], du[8], o[8];
+      unpack8(rd[t], d);
+      dequant8(rc[t][0], rs[t][0], g);
+      if (GATED) dequant8(rc[t][kH - 1], rs[t][kH - 1], u);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float t = w * d[i];
+        const float wt = w * d[i];
         if (GATED) {
           const float s = sigmoid(g[i]), gs = g[i] * s;
           dot += d[i] * (gs * u[i]);
           o[i] = w * (gs * u[i]);
-          du[i] = t * gs;
-          dg[i] = t * u[i] * (s + gs * (1.f - s));
+          du[i] = wt * gs;
+          dg[i] = wt * u[i] * (s + gs * (1.f - s));
         } else {
           const float r = g[i] < 0.f ? 0.f : g[i];
           dot += d[i] * (r * r);
           o[i] = w * (r * r);
-          dg[i] = 2.f * t * r;
+          dg[i] = 2.f * wt * r;
         }
       }
+      __stcs(dz + c, pack8(dg));
+      if (GATED) __stcs(dz + units + c, pack8(du));
+      if (a.h) __stcs(h + c, pack8(o));
     }
-    __stcs(dz + c, pack8(dg));
-    if (GATED) __stcs(dz + units + c, pack8(du));
-    if (a.h) __stcs(h + c, pack8(o));
   }
   if (a.d_row_w == nullptr) return;
 #pragma unroll
@@ -205,36 +257,47 @@ __global__ void __launch_bounds__(kThreads) act_backward_kernel(ActBackward a) {
   }
 }
 
-// A block per row below this many rows (a warp per row would leave SMs empty), otherwise
-// 32, 16, 8 or 4 lanes per row: the fewest that hold it in one turn, at most a warp.
-constexpr int64_t kWideBelow = 1024;
+// A block per row while the rows are few (a warp per row would leave SMs empty: 1500 rows of
+// I = 2048, forward 7.1 us as blocks and 9.7 as warps; 20000 rows, 71 and 60 us), otherwise 32,
+// 16, 8 or 4 lanes per row: the fewest that hold it in one turn, at most a warp, which then takes
+// two or four turns at a time.
+constexpr int64_t kWideBelow = 400000;  // eights of columns in all
 
-template <bool GATED, typename Args, typename F>
+template <int LANES, bool WIDE, int TURNS>
+struct Pick {
+  using M = Map<LANES, WIDE, TURNS>;
+  static constexpr int kLanes = LANES, kTurns = TURNS;
+  static constexpr bool kWide = WIDE;
+};
+
+template <typename Args, typename F>
 cudaError_t pick(const Args& a, F launch) {
   const int units = a.I / 8;
-  if (a.rows < kWideBelow && units > 32) return launch(std::integral_constant<int, 32>{}, std::true_type{});
-  if (units <= 4) return launch(std::integral_constant<int, 4>{}, std::false_type{});
-  if (units <= 8) return launch(std::integral_constant<int, 8>{}, std::false_type{});
-  if (units <= 16) return launch(std::integral_constant<int, 16>{}, std::false_type{});
-  return launch(std::integral_constant<int, 32>{}, std::false_type{});
+  if (units > 64 && a.rows * units < kWideBelow) return launch(Pick<32, true, 1>{});
+  if (units <= 4) return launch(Pick<4, false, 1>{});
+  if (units <= 8) return launch(Pick<8, false, 1>{});
+  if (units <= 16) return launch(Pick<16, false, 1>{});
+  if (units <= 32) return launch(Pick<32, false, 1>{});
+  if (units <= 64) return launch(Pick<32, false, 2>{});
+  return launch(Pick<32, false, 4>{});
 }
 
 template <bool GATED>
 cudaError_t checkpoint(const ActCheckpoint& a, cudaStream_t s) {
-  return pick<GATED>(a, [&](auto lanes, auto wide) {
-    using M = Map<decltype(lanes)::value, decltype(wide)::value>;
-    const int64_t blocks = (a.rows + M::kRowsPerBlock - 1) / M::kRowsPerBlock;
-    act_checkpoint_kernel<GATED, decltype(lanes)::value, decltype(wide)::value><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  return pick(a, [&](auto p) {
+    using P = decltype(p);
+    const int64_t blocks = (a.rows + P::M::kRowsPerBlock - 1) / P::M::kRowsPerBlock;
+    act_checkpoint_kernel<GATED, P::kLanes, P::kWide, P::kTurns><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return cudaGetLastError();
   });
 }
 
 template <bool GATED>
 cudaError_t backward(const ActBackward& a, cudaStream_t s) {
-  return pick<GATED>(a, [&](auto lanes, auto wide) {
-    using M = Map<decltype(lanes)::value, decltype(wide)::value>;
-    const int64_t blocks = (a.rows + M::kRowsPerBlock - 1) / M::kRowsPerBlock;
-    act_backward_kernel<GATED, decltype(lanes)::value, decltype(wide)::value><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  return pick(a, [&](auto p) {
+    using P = decltype(p);
+    const int64_t blocks = (a.rows + P::M::kRowsPerBlock - 1) / P::M::kRowsPerBlock;
+    act_backward_kernel<GATED, P::kLanes, P::kWide, P::kTurns><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     return cudaGetLastError();
   });
 }
