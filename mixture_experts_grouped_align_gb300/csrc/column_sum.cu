@@ -1,58 +1,62 @@
 // Column sums of a bf16 matrix: the gradient of a bias that every row was given,
 // d_b[n] = sum_m dz[m, n], in fp32.
 //
-// A stream of 2 M N bytes.  A cluster of eight CTAs owns 128 columns and shares the rows among
-// its CTAs; a thread adds eight columns (16 bytes a row) of every sixteenth row of its share,
-// eight rows in flight.  The sixteen row groups of a CTA and then the eight CTAs (distributed
-// shared memory) are added in order: the same bits every time, one launch, no workspace.
+// A stream of 2 M N bytes.  A cluster of eight CTAs owns 64 columns (one 128-byte line of a row)
+// and shares the rows among its CTAs; a thread adds eight columns (16 bytes a row) of every 32nd
+// row of its share, eight rows in flight.  The row groups of a CTA and then the eight CTAs
+// (distributed shared memory) are added in order: the same bits every time, one launch, no
+// workspace.
 #include "moe_common.cuh"
 #include "moe_launch.h"
 #include "tcgen05.cuh"
 
 namespace {
 
-constexpr int kThreads = 256, kCols = 128, kSplit = 8;
+constexpr int kThreads = 256, kCols = 64, kSplit = 8;
+constexpr int kLanes = kCols / 8, kGroups = kThreads / kLanes;
 
+__device__ __forceinline__ void add8(float (&acc)[8], const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[2 * i] += __uint_as_float(w[i] << 16);
+    acc[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// VEC: rows are whole 16-byte units.
 template <bool VEC>
 __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads)
     column_sum_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t N, float* __restrict__ out) {
-  __shared__ float part[16][kCols];
+  __shared__ float part[kGroups][kCols];
   __shared__ float mine[kCols];
-  const int tid = threadIdx.x, cg = tid & 15, rg = tid >> 4;
+  const int tid = threadIdx.x, cg = tid % kLanes, rg = tid / kLanes;
   const int rank = (int)tc::cluster_ctarank();
   const int64_t n0 = (int64_t)(blockIdx.x / kSplit) * kCols + cg * 8;
-  const int64_t r0 = M * rank / kSplit, r1 = M * (rank + 1) / kSplit;
+  const int64_t r1 = M * (rank + 1) / kSplit;
+  int64_t r = M * rank / kSplit + rg;
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-  constexpr int kU = 8;
-  for (int64_t r = r0 + rg; r < r1; r += 16 * kU) {
-    uint32_t v[kU][4];
+  if (VEC) {
+    constexpr int kU = 8;
+    if (n0 < N) {
+      const uint4* p = reinterpret_cast<const uint4*>(x + r * N + n0);
+      const int64_t step = kGroups * N / 8;
+      for (; r + (kU - 1) * kGroups < r1; r += kU * kGroups, p += kU * step) {
+        uint4 v[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int64_t m = r + 16 * u;
+        for (int u = 0; u < kU; ++u) v[u] = __ldcs(p + u * step);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[u][i] = 0;
-      if (m < r1) {
-        if (VEC) {
-          if (n0 < N) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(x + m * N + n0));
-            v[u][0] = w.x; v[u][1] = w.y; v[u][2] = w.z; v[u][3] = w.w;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (n0 + i < N) v[u][i >> 1] |= (uint32_t)x[m * N + n0 + i] << (16 * (i & 1));
-        }
+        for (int u = 0; u < kU; ++u) add8(acc, v[u]);
       }
+      for (; r < r1; r += kGroups, p += step) add8(acc, __ldcs(p));
     }
+  } else {
+    for (; r < r1; r += kGroups)
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[2 * i] += __uint_as_float(v[u][i] << 16);
-        acc[2 * i + 1] += __uint_as_float(v[u][i] & 0xffff0000u);
-      }
+      for (int i = 0; i < 8; ++i)
+        if (n0 + i < N) acc[i] += moe::bf16_bits_to_f32(x[r * N + n0 + i]);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) part[rg][cg * 8 + i] = acc[i];
@@ -60,21 +64,22 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads)
   if (tid < kCols) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += part[i][tid];
+    for (int i = 0; i < kGroups; ++i) s += part[i][tid];
     mine[tid] = s;
   }
   tc::cluster_sync();
   const int64_t n = (int64_t)(blockIdx.x / kSplit) * kCols + tid;
   if (rank == 0 && tid < kCols && n < N) {
-    float s = 0.f;
+    float v[kSplit];
+#pragma unroll
     for (int r = 0; r < kSplit; ++r) {
       uint32_t a;
-      float v;
       asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_addr(&mine[tid])), "r"(r));
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-      s += v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(a) : "memory");
     }
-    out[n] = s;
+#pragma unroll
+    for (int r = 1; r < kSplit; ++r) v[0] += v[r];
+    out[n] = v[0];
   }
   tc::cluster_sync();
 }
