@@ -5,22 +5,27 @@
 // forward weight) [K, N1]; act = none, relu^2 or SwiGLU (N1 = 2N: gate features, then up).
 // fp32 accumulation, one rounding to bf16 (fp32 outputs, and shapes of few tiles: dense_split.cu).
 //
-// Bound: 2 M N1 K operations on the tensor cores (the operands are read about once through L2:
-// a 128 x 256 tile does 85 operations per operand byte it loads).  Persistent blocks, one per
-// SM, over 128 x 256 tiles (SwiGLU: 128 gate and 128 up columns, so both lie in the same TMEM
-// lane and thread), two fp32 accumulators of 256 TMEM columns so that a tile's epilogue runs
-// under the next tile's products:
-//   warp 0  loads a stage (64 of K: 128 rows of x and 256 of W, 48 KB) by TMA, four stages;
-//   warp 1  issues the MMAs (M 128, N 256, K 16) from one lane;
+// Bound: 2 M N1 K operations on the tensor cores, as long as the operands arrive: an SM takes
+// about 64 bytes a clock from L2, and a 128 x 256 tile on one SM (48 KB of operands per 512 clocks
+// of MMAs) was held to 70% of the tensor cores by that.  So two CTAs, a cluster on two SMs, share
+// a 256 x 256 tile: the MMAs (cta_group::2, M 256, N 256, K 16) read 128 rows of x and 128 of W
+// from either CTA's shared memory, 32 KB per CTA and stage, and leave 128 rows of the tile in
+// each CTA's TMEM.  Persistent pairs over the tiles (SwiGLU: 128 gate columns from the first CTA
+// and 128 up columns from the second, so both lie in the same TMEM lane and thread), two fp32
+// accumulators of 256 TMEM columns so that a tile's epilogue runs under the next tile's products:
+//   warp 0  loads this CTA's half of a stage (64 of K) by TMA, completing on the first CTA's
+//           barrier, six stages;
+//   warp 1  of the first CTA issues the MMAs; their commits free the stage, and announce the
+//           accumulator, in both CTAs;
 //   warps 4..11  drain the accumulator, two per TMEM lane quarter with half of the columns
 //           each: bias, activation, residual (a TMA box loaded into the staging box the result
 //           then replaces), rounding, and a TMA store of 32 rows x 128 bytes, which drops what
 //           lies past M or N.  Rows of out that are no multiple of 16 bytes are stored by
 //           plain stores instead.
-// Tiles are taken sixteen row tiles at a time, the column tile slower, so that the blocks
-// running at once share their operands in L2.
+// Tiles are taken eight row tiles at a time, the column tile slower, so that the pairs running at
+// once share their operands in L2.
 // Every wait is bounded; one that runs out sets MOE_ERR_TIMEOUT, all roles leave their loops,
-// and the loads in flight are waited for before the block ends.
+// the loads in flight are waited for, and both CTAs meet before either ends.
 #include "dense_common.cuh"
 
 namespace {
@@ -28,18 +33,71 @@ namespace {
 using namespace dense;
 
 constexpr int kThreads = 384;
-constexpr int kBM = 128, kBN = 256;
-constexpr int kStages = 4;
-constexpr int kA = 0, kB = kBM * 128, kSlot = (kBM + kBN) * 128;
+constexpr int kBM = 128, kBN = 256;             // a CTA's rows and the pair's columns of a tile
+constexpr int kStages = 6;
+constexpr int kA = 0, kB = kBM * 128, kSlot = 2 * kBM * 128;  // x rows | this CTA's 128 W rows
 constexpr int kStg = kStages * kSlot;           // staging boxes, 4 KB per epilogue warp
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
 constexpr int kBars = kStg + kEpiWarps * 4096;
 constexpr int kSmem = kBars + 256 + 1024;
-constexpr int kGroupM = 16;
+constexpr int kGroupM = 8;
 
 struct Tiles {
   int64_t m, n, total;
 };
+
+// The tensor-core instructions of a CTA pair.
+namespace pair {
+
+// Allocation, release and deallocation are executed by a warp of each CTA of the pair.
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_addr(dst)), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D (+)= A . B^T, M = 256: rows 0..127 of A and D are the first CTA's, 128..255 the second's, and
+// so are the halves of B's rows, each at the same shared-memory offset.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this offset in both CTAs when the MMAs issued before have completed.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          tc::smem_addr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// Cluster address of a barrier of the first CTA.
+__device__ __forceinline__ uint32_t first_cta_addr(const uint64_t* bar) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(tc::smem_addr(bar)));
+  return a;
+}
+__device__ __forceinline__ void arrive_first_cta(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(first_cta_addr(bar)) : "memory");
+}
+// Loads a box into this CTA's shared memory; its bytes complete on a barrier of either CTA.
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+}  // namespace pair
 
 __device__ __forceinline__ void tile_of(const Tiles& ts, int64_t t, int64_t& mt, int64_t& nt) {
   const int64_t per = kGroupM * ts.n, g = t / per, r = t - g * per;
@@ -81,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(taddr_s + 1);
   // from lane 0: values the compiler can keep in uniform registers
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const uint32_t rank = __shfl_sync(0xffffffffu, tc::cluster_ctarank(), 0);
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&full[s], 1);
@@ -88,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&tfull[i], 1);
-      tc::mbar_init(&tempty[i], kEpiWarps);
+      tc::mbar_init(&tempty[i], 2 * kEpiWarps);
     }
     tc::mbar_init(drain, 1);
     for (int i = 0; i < kEpiWarps; ++i) tc::mbar_init(&rfull[i], 1);
@@ -96,61 +155,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_fence_init();
   }
   if (warp == 1) {
-    tc::tmem_alloc(taddr_s, 512);
-    tc::tmem_relinquish();
+    pair::tmem_alloc(taddr_s, 512);
+    pair::tmem_relinquish();
   }
   tc::tc_fence_before();
   __syncthreads();
+  tc::cluster_sync();  // both CTAs' barriers are there before either is signalled
   tc::tc_fence_after();
   const uint32_t taddr = __shfl_sync(0xffffffffu, *taddr_s, 0), smem_s = tc::smem_addr(smem);
   const int nk = (d.K + kBK - 1) / kBK;
   const bool kn = d.w_kn != 0;
   const uint64_t wb = d.wait_ns > 0 ? (uint64_t)d.wait_ns : tc::kWaitNs;
   constexpr int kOutN = GATED ? 128 : kBN;  // output columns of a tile
+  const int64_t pair0 = blockIdx.x / 2, pairs = gridDim.x / 2;
 
   if (warp == 0 && !d.stall) {
     // ------------------------------------------------------------------ loads
-    if (lane == 0) {
+    const bool leader = elect_one();
+    if (leader) {
       tma::prefetch_map(&tm_x);
       tma::prefetch_map(&tm_w);
-      uint32_t it = 0;
-      for (int64_t t = blockIdx.x; t < ts.total && !*abort_flag; t += gridDim.x) {
-        int64_t mt, nt;
-        tile_of(ts, t, mt, nt);
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!tc::mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, wb)) {
-            moe::set_status(d.status, MOE_ERR_TIMEOUT);
-            *abort_flag = 1;
-            break;
-          }
-          const uint32_t sl = smem_s + s * kSlot;
-          tma::mbar_arrive_expect_tx(&full[s], kSlot);
-          tma::load_2d(sl + kA, &tm_x, kb * 128, (int32_t)(mt * kBM), &full[s]);
-          if (GATED) {
-            load_w(sl + kB, &tm_w, kn, nt * 128, 128, kb, &full[s]);
-            load_w(sl + kB + 128 * 128, &tm_w, kn, d.N + nt * 128, 128, kb, &full[s]);
+    }
+    uint32_t s = 0, ph = 1, it = 0;
+    bool ok = true;
+    for (int64_t t = pair0; t < ts.total && ok && !*abort_flag; t += pairs) {
+      int64_t mt, nt;
+      tile_of(ts, t, mt, nt);
+      const int32_t row = (int32_t)(mt * 2 * kBM + rank * kBM);
+      const int64_t n0 = GATED ? nt * 128 + (rank ? d.N : 0) : nt * kBN + rank * 128;
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        if (!tc::mbar_wait(&empty[s], ph, wb)) {
+          ok = false;
+          break;
+        }
+        if (leader) {
+          const uint32_t sl = smem_s + s * kSlot, bar = pair::first_cta_addr(&full[s]);
+          if (rank == 0) tma::mbar_arrive_expect_tx(&full[s], 2 * kSlot);  // both CTAs' halves
+          pair::load_2d(sl + kA, &tm_x, kb * 128, row, bar);
+          if (kn) {
+            pair::load_2d(sl + kB, &tm_w, (int32_t)n0 * 2, kb * kBK, bar);
+            pair::load_2d(sl + kB + kAtomCol, &tm_w, (int32_t)(n0 + 64) * 2, kb * kBK, bar);
           } else {
-            load_w(sl + kB, &tm_w, kn, nt * kBN, kBN, kb, &full[s]);
+            pair::load_2d(sl + kB, &tm_w, kb * 128, (int32_t)n0, bar);
           }
         }
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1;
+        }
       }
-      // every load lands before the block may end, also when another role has given up
+    }
+    if (!ok) {
+      moe::set_status(d.status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    // every load lands before the pair may end, also when another role has given up (the first
+    // CTA's barriers count both CTAs' loads)
+    if (rank == 0)
       for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
         if (!tc::mbar_wait(&full[j % kStages], (j / kStages) & 1, wb)) moe::set_status(d.status, MOE_ERR_TIMEOUT);
-    }
     __syncwarp();
-  } else if (warp == 1 && !d.stall) {
+  } else if (warp == 1 && rank == 0 && !d.stall) {
     // ------------------------------------------------------------------ MMA issuer
     // The whole warp runs the loop and one lane issues: descriptors and addresses are the same in
     // every lane, so they stay in uniform registers and a stage's issue takes few instructions.
     const bool leader = elect_one();
-    const uint32_t idesc = tc::idesc_f16(kBM, kBN, 1) | (kn ? 1u << 16 : 0u);
+    const uint32_t idesc = tc::idesc_f16(2 * kBM, kBN, 1) | (kn ? 1u << 16 : 0u);
     const uint32_t wstep = w_step(kn);
     const uint64_t a0 = tc::sdesc_sw128(smem_s + kA), b0 = w_desc(smem_s + kB, kn, 0);
     uint32_t s = 0, ph = 0, acc = 0, acc_ph = 1;
     bool ok = true;
-    for (int64_t t = blockIdx.x; t < ts.total && ok && !*abort_flag; t += gridDim.x) {
+    for (int64_t t = pair0; t < ts.total && ok && !*abort_flag; t += pairs) {
       if (!tc::mbar_wait(&tempty[acc], acc_ph, wb)) {
         ok = false;
         break;
@@ -166,9 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (leader) {
           const uint64_t ad = a0 + s * (kSlot / 16), bd = b0 + s * (kSlot / 16);
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j)
-            tc::mma_f16_ss(d_tmem, ad + j * kXStep, bd + j * wstep, idesc, (kb | j) != 0);
-          tc::mma_commit(&empty[s]);
+          for (int j = 0; j < kBK / 16; ++j) pair::mma_f16_ss(d_tmem, ad + j * kXStep, bd + j * wstep, idesc, (kb | j) != 0);
+          pair::mma_commit(&empty[s]);
         }
         __syncwarp();
         if (++s == kStages) {
@@ -177,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (leader) tc::mma_commit(&tfull[acc]);
+      if (leader) pair::mma_commit(&tfull[acc]);
       __syncwarp();
       acc ^= 1;
       if (acc == 0) acc_ph ^= 1;
@@ -186,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       moe::set_status(d.status, MOE_ERR_TIMEOUT);
       *abort_flag = 1;
     }
-    if (leader) tc::mma_commit(drain);
+    if (leader) pair::mma_commit(drain);
     if (!tc::mbar_wait(drain, 0, wb)) moe::set_status(d.status, MOE_ERR_TIMEOUT);
     __syncwarp();
   } else if (warp >= kEpiWarp0) {
@@ -197,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool vec = d.N % 8 == 0;
     const bool res_box = d.residual != nullptr && d.tma_out;
     uint32_t acc_it = 0, rph = 0;
-    for (int64_t t = blockIdx.x; t < ts.total && !*abort_flag; t += gridDim.x, ++acc_it) {
+    for (int64_t t = pair0; t < ts.total && !*abort_flag; t += pairs, ++acc_it) {
       int64_t mt, nt;
       tile_of(ts, t, mt, nt);
       const uint32_t acc = acc_it & 1;
@@ -208,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::tc_fence_after();
       const uint32_t tb = taddr + acc * kBN + ((uint32_t)(quarter * 32) << 16);
-      const int64_t m0 = mt * kBM + quarter * 32, m = m0 + lane;
+      const int64_t m0 = mt * 2 * kBM + rank * kBM + quarter * 32, m = m0 + lane;
       for (int c0 = half * (kOutN / 2); c0 < (half + 1) * (kOutN / 2); c0 += kCols) {
         const int64_t n0 = nt * kOutN + c0;
         if (n0 >= d.N || m0 >= d.M) continue;  // the same for the whole warp
@@ -318,30 +393,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&tempty[acc]);
+      if (lane == 0) pair::arrive_first_cta(&tempty[acc]);
     }
     if (lane == 0) tma::bulk_wait_all();
     __syncwarp();
   }
   tc::tc_fence_before();
   __syncthreads();
+  // the last commit reaches the second CTA too: it is waited for there before the CTA may end
+  if (warp == 1 && rank == 1 && !d.stall && !tc::mbar_wait(drain, 0, wb)) moe::set_status(d.status, MOE_ERR_TIMEOUT);
+  __syncwarp();
+  tc::cluster_sync();  // neither CTA leaves while the other's products or signals may reach it
   if (warp == 1) {
     tc::tc_fence_after();
-    tc::tmem_dealloc(taddr, 512);
+    pair::tmem_dealloc(taddr, 512);
   }
 }
 
 template <bool GATED>
 cudaError_t launch(const Dense& d, cudaStream_t stream) {
   Tiles ts;
-  ts.m = (d.M + kBM - 1) / kBM;
+  ts.m = (d.M + 2 * kBM - 1) / (2 * kBM);
   ts.n = (d.N + (GATED ? 127 : kBN - 1)) / (GATED ? 128 : kBN);
   ts.total = ts.m * ts.n;
   const uint64_t K2 = (uint64_t)d.K * 2, N1 = GATED ? 2 * (uint64_t)d.N : (uint64_t)d.N;
   CUtensorMap mx{}, mw{}, mo{}, mr{};
   if (!tma::encode_2d_u8(&mx, d.x, K2, (uint64_t)d.M, K2, 128, kBM, true)) return cudaErrorInvalidValue;
   const bool okw = d.w_kn ? tma::encode_2d_u8(&mw, d.w, N1 * 2, (uint64_t)d.K, N1 * 2, 128, kBK, true)
-                          : tma::encode_2d_u8(&mw, d.w, K2, N1, K2, 128, GATED ? 128 : kBN, true);
+                          : tma::encode_2d_u8(&mw, d.w, K2, N1, K2, 128, 128, true);
   if (!okw) return cudaErrorInvalidValue;
   if (d.tma_out) {
     const uint64_t row = (uint64_t)d.N * 2;
@@ -351,9 +430,20 @@ cudaError_t launch(const Dense& d, cudaStream_t stream) {
   }
   cudaError_t err = cudaFuncSetAttribute(dense_gemm_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (err != cudaSuccess) return err;
-  const int64_t sms = moe_launch::sm_count_current();
-  dense_gemm_kernel<GATED><<<(unsigned)(ts.total < sms ? ts.total : sms), kThreads, kSmem, stream>>>(mx, mw, mo, mr, d, ts);
-  return cudaGetLastError();
+  const int64_t most = moe_launch::sm_count_current() / 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(2 * (ts.total < most ? ts.total : most)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  err = cudaLaunchKernelEx(&cfg, dense_gemm_kernel<GATED>, mx, mw, mo, mr, d, ts);
+  return err == cudaSuccess ? cudaGetLastError() : err;
 }
 
 }  // namespace

@@ -473,10 +473,10 @@ bool dense_split(const Dense& d, cudaStream_t stream, cudaError_t* err) {
   const Split s = plan(d, &split);
   const bool fits = s.n_tiles * s.m_tiles * s.C < ((int64_t)1 << 31);
   if (!d.out_f32) {
-    // the tiled kernel: 512 clocks a stage, its start and the last tile's epilogue
-    const int64_t sms = sm_count_current(), nk = (d.K + kBK - 1) / kBK;
-    const int64_t tiles = ((d.M + 127) / 128) * ((d.N + (d.gated ? 127 : 255)) / (d.gated ? 128 : 256));
-    if (!fits || split >= (double)((tiles + sms - 1) / sms) * nk * 512 + 6000) return false;
+    // the pairs' kernel: 512 clocks a stage of a 256 x 256 tile, its start and its last epilogue
+    const int64_t pairs = sm_count_current() / 2, nk = (d.K + kBK - 1) / kBK;
+    const int64_t tiles = ((d.M + 255) / 256) * ((d.N + (d.gated ? 127 : 255)) / (d.gated ? 128 : 256));
+    if (!fits || split >= (double)((tiles + pairs - 1) / pairs) * nk * 512 + 7000) return false;
   }
   if (!fits) *err = cudaErrorInvalidValue;
   else if (d.gated) *err = s.NA == 2 ? launch<2, true>(d, s, stream) : launch<1, true>(d, s, stream);
