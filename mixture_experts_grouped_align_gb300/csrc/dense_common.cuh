@@ -47,6 +47,16 @@ MOE_DEV bool elect_one() {
 MOE_DEV uint32_t w_step(bool kn) { return kn ? 2 * 1024 / 16 : 2; }
 constexpr uint32_t kXStep = 2;
 
+// 32 lanes x 16 columns of TMEM -> 16 registers a thread.
+MOE_DEV void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+
 MOE_DEV float bias_at(const void* bias, int64_t i) {
   return moe::bf16_bits_to_f32(static_cast<const uint16_t*>(bias)[i]);
 }

@@ -3,7 +3,7 @@
 //   z = x . W^T + b;   out = act(z) + residual_scale * residual
 // x [M, K] bf16; W stored [N1, K] or (contracted over its rows, as an input gradient needs the
 // forward weight) [K, N1]; act = none, relu^2 or SwiGLU (N1 = 2N: gate features, then up).
-// fp32 accumulation, one rounding to bf16 (fp32 outputs, and shapes of few tiles: dense_split.cu).
+// fp32 accumulation, one rounding to the output type (shapes of few tiles: dense_split.cu).
 //
 // Bound: 2 M N1 K operations on the tensor cores, as long as the operands arrive: an SM takes
 // about 64 bytes a clock from L2, and a 128 x 256 tile on one SM (48 KB of operands per 512 clocks
@@ -14,14 +14,16 @@
 // and 128 up columns from the second, so both lie in the same TMEM lane and thread), two fp32
 // accumulators of 256 TMEM columns so that a tile's epilogue runs under the next tile's products:
 //   warp 0  loads this CTA's half of a stage (64 of K) by TMA, completing on the first CTA's
-//           barrier, six stages;
+//           barrier, five stages;
 //   warp 1  of the first CTA issues the MMAs; their commits free the stage, and announce the
 //           accumulator, in both CTAs;
-//   warps 4..11  drain the accumulator, two per TMEM lane quarter with half of the columns
+//   warps 4..19  drain the accumulator, four per TMEM lane quarter with a quarter of the columns
 //           each: bias, activation, residual (a TMA box loaded into the staging box the result
-//           then replaces), rounding, and a TMA store of 32 rows x 128 bytes, which drops what
-//           lies past M or N.  Rows of out that are no multiple of 16 bytes are stored by
-//           plain stores instead.
+//           then replaces), rounding, and a TMA store of a box of 32 rows, which drops what lies
+//           past M or N.  Rows of out that are no multiple of 16 bytes are stored by plain stores.
+// The tensor core's accumulator loses up to one unit in the last place with every MMA, always
+// towards zero, which a bf16 output hides.  For fp32 outputs an accumulator therefore takes at
+// most kChunk stages, and the epilogue warps add the chunks up in registers meanwhile.
 // Tiles are taken eight row tiles at a time, the column tile slower, so that the pairs running at
 // once share their operands in L2.
 // Every wait is bounded; one that runs out sets MOE_ERR_TIMEOUT, all roles leave their loops,
@@ -32,15 +34,16 @@ namespace {
 
 using namespace dense;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kBM = 128, kBN = 256;             // a CTA's rows and the pair's columns of a tile
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kA = 0, kB = kBM * 128, kSlot = 2 * kBM * 128;  // x rows | this CTA's 128 W rows
 constexpr int kStg = kStages * kSlot;           // staging boxes, 4 KB per epilogue warp
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 16;
 constexpr int kBars = kStg + kEpiWarps * 4096;
-constexpr int kSmem = kBars + 256 + 1024;
+constexpr int kSmem = kBars + 512 + 1024;
 constexpr int kGroupM = 8;
+constexpr int kChunk = 12;                      // stages (64 of K) an accumulator takes for fp32 outputs
 
 struct Tiles {
   int64_t m, n, total;
@@ -106,6 +109,19 @@ __device__ __forceinline__ void tile_of(const Tiles& ts, int64_t t, int64_t& mt,
   mt = g * kGroupM + (r - nt * rows);
 }
 
+// Byte offset of 16-byte unit q of row r of a staging box: rows of 128 bytes in the 128-byte
+// swizzle, or of 64 bytes as they are.
+template <int BYTES>
+__device__ __forceinline__ uint32_t box_offset(int r, int q) {
+  return BYTES == 128 ? (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4)) : (uint32_t)(r * BYTES + (q << 4));
+}
+__device__ __forceinline__ void lds128(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t at, const uint32_t (&r)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+
 // Bias of the 8 features n .. n + 7 (zeros past N); `base` is the first feature's index.
 __device__ __forceinline__ void bias8(const void* bias, int64_t base, int64_t n, int64_t N, bool vec, float (&b)[8]) {
   if (vec && n + 8 <= N) {
@@ -122,7 +138,7 @@ __device__ __forceinline__ void bias8(const void* bias, int64_t base, int64_t n,
   }
 }
 
-template <bool GATED>
+template <bool GATED, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_r, Dense d,
@@ -227,35 +243,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s = 0, ph = 0, acc = 0, acc_ph = 1;
     bool ok = true;
     for (int64_t t = pair0; t < ts.total && ok && !*abort_flag; t += pairs) {
-      if (!tc::mbar_wait(&tempty[acc], acc_ph, wb)) {
-        ok = false;
-        break;
-      }
-      tc::tc_fence_after();
-      const uint32_t d_tmem = taddr + acc * kBN;
-      for (int kb = 0; kb < nk; ++kb) {
-        if (!tc::mbar_wait(&full[s], ph, wb)) {
+      // fp32 outputs: kChunk stages an accumulator, which the epilogue adds up in registers
+      for (int k0 = 0; k0 < nk && ok; k0 += F32 ? kChunk : nk) {
+        const int k1 = F32 && k0 + kChunk < nk ? k0 + kChunk : nk;
+        if (!tc::mbar_wait(&tempty[acc], acc_ph, wb)) {
           ok = false;
           break;
         }
         tc::tc_fence_after();
-        if (leader) {
-          const uint64_t ad = a0 + s * (kSlot / 16), bd = b0 + s * (kSlot / 16);
+        const uint32_t d_tmem = taddr + acc * kBN;
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!tc::mbar_wait(&full[s], ph, wb)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          if (leader) {
+            const uint64_t ad = a0 + s * (kSlot / 16), bd = b0 + s * (kSlot / 16);
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j) pair::mma_f16_ss(d_tmem, ad + j * kXStep, bd + j * wstep, idesc, (kb | j) != 0);
-          pair::mma_commit(&empty[s]);
+            for (int j = 0; j < kBK / 16; ++j) pair::mma_f16_ss(d_tmem, ad + j * kXStep, bd + j * wstep, idesc, kb > k0 || j > 0);
+            pair::mma_commit(&empty[s]);
+          }
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
+        if (!ok) break;
+        if (leader) pair::mma_commit(&tfull[acc]);
         __syncwarp();
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1;
-        }
+        acc ^= 1;
+        if (acc == 0) acc_ph ^= 1;
       }
-      if (!ok) break;
-      if (leader) pair::mma_commit(&tfull[acc]);
-      __syncwarp();
-      acc ^= 1;
-      if (acc == 0) acc_ph ^= 1;
     }
     if (!ok) {
       moe::set_status(d.status, MOE_ERR_TIMEOUT);
@@ -266,52 +286,87 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------------ epilogue
-    const int ew = warp - kEpiWarp0, quarter = warp & 3, half = ew >> 2;
-    constexpr int kCols = 64;                    // columns of a 128-byte staging row
+    const int ew = warp - kEpiWarp0, quarter = warp & 3;
+    constexpr int kPer = kOutN / (kEpiWarps / 4);     // output columns of a warp
+    constexpr int kCols = F32 ? 32 : 64;              // columns of a 128-byte staging row
+    constexpr int kBoxes = kPer < kCols ? 1 : kPer / kCols, kBlocks = (kPer < kCols ? kPer : kCols) / 32;
+    const int col0 = (ew >> 2) * kPer;
     const uint32_t box = smem_s + kStg + ew * 4096;
     const bool vec = d.N % 8 == 0;
     const bool res_box = d.residual != nullptr && d.tma_out;
-    uint32_t acc_it = 0, rph = 0;
-    for (int64_t t = pair0; t < ts.total && !*abort_flag; t += pairs, ++acc_it) {
+    uint32_t acc = 0, acc_ph = 0, rph = 0;
+    float sum[F32 ? kPer : 1], sum_u[F32 && GATED ? kPer : 1];  // fp32 outputs: the chunks' sums
+    bool ok = true;
+    for (int64_t t = pair0; t < ts.total && ok && !*abort_flag; t += pairs) {
       int64_t mt, nt;
       tile_of(ts, t, mt, nt);
-      const uint32_t acc = acc_it & 1;
-      if (!tc::mbar_wait(&tfull[acc], (acc_it >> 1) & 1, wb)) {
-        moe::set_status(d.status, MOE_ERR_TIMEOUT);
-        *abort_flag = 1;
-        break;
+      const uint32_t lane_quarter = (uint32_t)(quarter * 32) << 16;
+      for (int k0 = 0; k0 < nk; k0 += F32 ? kChunk : nk) {
+        if (!tc::mbar_wait(&tfull[acc], acc_ph, wb)) {
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        if (!F32) break;
+        const uint32_t tb = taddr + acc * kBN + lane_quarter + col0;
+#pragma unroll
+        for (int c = 0; c < kPer; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(tb + c, v);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[F32 ? c + i : 0] = (k0 ? sum[F32 ? c + i : 0] : 0.f) + __uint_as_float(v[i]);
+          if (GATED) {
+            tmem_ld16(tb + 128 + c, v);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              sum_u[F32 && GATED ? c + i : 0] = (k0 ? sum_u[F32 && GATED ? c + i : 0] : 0.f) + __uint_as_float(v[i]);
+          }
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pair::arrive_first_cta(&tempty[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_ph ^= 1;
       }
-      tc::tc_fence_after();
-      const uint32_t tb = taddr + acc * kBN + ((uint32_t)(quarter * 32) << 16);
+      if (!ok) break;
+      const uint32_t tb = taddr + acc * kBN + lane_quarter + col0;
       const int64_t m0 = mt * 2 * kBM + rank * kBM + quarter * 32, m = m0 + lane;
-      for (int c0 = half * (kOutN / 2); c0 < (half + 1) * (kOutN / 2); c0 += kCols) {
-        const int64_t n0 = nt * kOutN + c0;
+#pragma unroll
+      for (int bx = 0; bx < kBoxes; ++bx) {
+        const int64_t n0 = nt * kOutN + col0 + bx * kCols;
         if (n0 >= d.N || m0 >= d.M) continue;  // the same for the whole warp
         if (lane == 0 && d.tma_out) {
           tma::bulk_wait_read_all();  // the last store has read the box
           if (res_box) {
-            tma::mbar_arrive_expect_tx(&rfull[ew], 4096);
-            tma::load_2d(box, &tm_r, (int32_t)(n0 * 2), (int32_t)m0, &rfull[ew]);
+            tma::mbar_arrive_expect_tx(&rfull[ew], 32 * kBlocks * 32 * (F32 ? 4 : 2));
+            tma::load_2d(box, &tm_r, (int32_t)(n0 * (F32 ? 4 : 2)), (int32_t)m0, &rfull[ew]);
           }
         }
         __syncwarp();
         bool have = !res_box;
 #pragma unroll
-        for (int b = 0; b < kCols; b += 32) {
+        for (int b = 0; b < kBlocks; ++b) {
           uint32_t v[32], u[32];
-          tc::tmem_ld32(tb + c0 + b, v);
-          if (GATED) tc::tmem_ld32(tb + 128 + c0 + b, u);
-          tc::tmem_ld_wait();
-          if (!have) {
-            if (!tc::mbar_wait(&rfull[ew], rph, wb)) {
-              moe::set_status(d.status, MOE_ERR_TIMEOUT);
-              *abort_flag = 1;
+          if (F32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              v[i] = __float_as_uint(sum[F32 ? bx * kCols + 32 * b + i : 0]);
+              if (GATED) u[i] = __float_as_uint(sum_u[F32 && GATED ? bx * kCols + 32 * b + i : 0]);
             }
+          } else {
+            tc::tmem_ld32(tb + bx * kCols + 32 * b, v);
+            if (GATED) tc::tmem_ld32(tb + 128 + bx * kCols + 32 * b, u);
+            tc::tmem_ld_wait();
+          }
+          if (!have) {
+            if (!tc::mbar_wait(&rfull[ew], rph, wb)) ok = false;
             have = true;
           }
 #pragma unroll
           for (int q = 0; q < 4; ++q) {  // eight columns
-            const int64_t n = n0 + b + 8 * q;
+            const int64_t n = n0 + 32 * b + 8 * q;
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(v[8 * q + i]);
@@ -342,14 +397,25 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 8; ++i)
                 if (m < d.M && n + i < d.N) o[i] += d.residual_scale * residual_at(d, m * d.N + n + i);
             }
-            {
-              const uint32_t at = box + lane * 128 + (((b / 8 + q) ^ (lane & 7)) << 4);
+            if (F32) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t at = box + box_offset<4 * kBlocks * 32>(lane, 2 * q + j);
+                if (res_box) {
+                  uint32_t r[4];
+                  lds128(at, r);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[4 * j + i] += d.residual_scale * __uint_as_float(r[i]);
+                }
+                const uint32_t w[4] = {__float_as_uint(o[4 * j]), __float_as_uint(o[4 * j + 1]), __float_as_uint(o[4 * j + 2]),
+                                       __float_as_uint(o[4 * j + 3])};
+                sts128(at, w);
+              }
+            } else {
+              const uint32_t at = box + box_offset<2 * kBlocks * 32>(lane, 4 * b + q);
               if (res_box) {
                 uint32_t r[4];
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                             : "r"(at)
-                             : "memory");
+                lds128(at, r);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   o[2 * i] += d.residual_scale * __uint_as_float(r[i] << 16);
@@ -362,9 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
                 pk[i] = *reinterpret_cast<const uint32_t*>(&h);
               }
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pk[0]), "r"(pk[1]), "r"(pk[2]),
-                           "r"(pk[3])
-                           : "memory");
+              sts128(at, pk);
             }
           }
         }
@@ -373,27 +437,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma::store_2d(&tm_o, (int32_t)(n0 * 2), (int32_t)m0, box);
+            tma::store_2d(&tm_o, (int32_t)(n0 * (F32 ? 4 : 2)), (int32_t)m0, box);
             tma::bulk_commit();
           }
         } else {  // rows of out not a multiple of 16 bytes: a row's columns by the lanes
           __syncwarp();
+          constexpr int kBoxCols = 32 * kBlocks;
           const int rows = d.M - m0 < 32 ? (int)(d.M - m0) : 32;
-          const int cols = d.N - n0 < kCols ? (int)(d.N - n0) : kCols;
+          const int cols = d.N - n0 < kBoxCols ? (int)(d.N - n0) : kBoxCols;
           for (int r = 0; r < rows; ++r)
             for (int c = lane; c < cols; c += 32) {
-              {
+              if (F32) {
+                uint32_t w;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(box + box_offset<4 * kBoxCols>(r, c >> 2) + (c & 3) * 4) : "memory");
+                static_cast<uint32_t*>(d.out)[(m0 + r) * d.N + n0 + c] = w;
+              } else {
                 uint16_t w;
-                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(box + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2) : "memory");
+                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(box + box_offset<2 * kBoxCols>(r, c >> 3) + (c & 7) * 2) : "memory");
                 static_cast<uint16_t*>(d.out)[(m0 + r) * d.N + n0 + c] = w;
               }
             }
           __syncwarp();
         }
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) pair::arrive_first_cta(&tempty[acc]);
+      if (!F32) {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) pair::arrive_first_cta(&tempty[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_ph ^= 1;
+      }
+    }
+    if (!ok) {
+      moe::set_status(d.status, MOE_ERR_TIMEOUT);
+      *abort_flag = 1;
     }
     if (lane == 0) tma::bulk_wait_all();
     __syncwarp();
@@ -410,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool GATED>
+template <bool GATED, bool F32>
 cudaError_t launch(const Dense& d, cudaStream_t stream) {
   Tiles ts;
   ts.m = (d.M + 2 * kBM - 1) / (2 * kBM);
@@ -423,12 +500,13 @@ cudaError_t launch(const Dense& d, cudaStream_t stream) {
                           : tma::encode_2d_u8(&mw, d.w, K2, N1, K2, 128, 128, true);
   if (!okw) return cudaErrorInvalidValue;
   if (d.tma_out) {
-    const uint64_t row = (uint64_t)d.N * 2;
-    if (!tma::encode_2d_u8(&mo, d.out, row, (uint64_t)d.M, row, 128, 32, true)) return cudaErrorInvalidValue;
-    if (d.residual && !tma::encode_2d_u8(&mr, d.residual, row, (uint64_t)d.M, row, 128, 32, true))
+    const uint64_t row = (uint64_t)d.N * (F32 ? 4 : 2);
+    constexpr uint32_t kBox = GATED && !F32 ? 64 : 128;  // bytes of a staging row
+    if (!tma::encode_2d_u8(&mo, d.out, row, (uint64_t)d.M, row, kBox, 32, kBox == 128)) return cudaErrorInvalidValue;
+    if (d.residual && !tma::encode_2d_u8(&mr, d.residual, row, (uint64_t)d.M, row, kBox, 32, kBox == 128))
       return cudaErrorInvalidValue;
   }
-  cudaError_t err = cudaFuncSetAttribute(dense_gemm_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t err = cudaFuncSetAttribute(dense_gemm_kernel<GATED, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (err != cudaSuccess) return err;
   const int64_t most = moe_launch::sm_count_current() / 2;
   cudaLaunchConfig_t cfg{};
@@ -442,7 +520,7 @@ cudaError_t launch(const Dense& d, cudaStream_t stream) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, dense_gemm_kernel<GATED>, mx, mw, mo, mr, d, ts);
+  err = cudaLaunchKernelEx(&cfg, dense_gemm_kernel<GATED, F32>, mx, mw, mo, mr, d, ts);
   return err == cudaSuccess ? cudaGetLastError() : err;
 }
 
@@ -454,8 +532,9 @@ cudaError_t dense_gemm(Dense d, cudaStream_t stream) {
   if (d.M == 0) return cudaSuccess;
   cudaError_t err;
   if (dense_split(d, stream, &err)) return err;
-  d.tma_out = d.N % 8 == 0;
-  return d.gated ? launch<true>(d, stream) : launch<false>(d, stream);
+  d.tma_out = ((int64_t)d.N * (d.out_f32 ? 4 : 2)) % 16 == 0;
+  if (d.gated) return d.out_f32 ? launch<true, true>(d, stream) : launch<true, false>(d, stream);
+  return d.out_f32 ? launch<false, true>(d, stream) : launch<false, false>(d, stream);
 }
 
 }  // namespace moe_launch

@@ -254,3 +254,25 @@ def test_waits_that_run_out_are_reported(moe, M, N, K):
     assert int(status[0]) == 0
     ref, err = reference(x, w, None, "none", None, 1.0)
     near(out, ref, err, False)
+
+
+@pytest.mark.parametrize("act,residual", [("none", True), ("swiglu", False), ("swiglu", True), ("relu2", False)])
+@pytest.mark.parametrize("M,N,K", [(2500, 2056, 1600), (2049, 1999, 904), (3000, 2052, 776)])
+def test_fp32_outputs_of_several_accumulators(moe, M, N, K, act, residual):
+    """Long sums on the pairs' kernel: chunks of K added up by the epilogue, a ragged last one."""
+    run(moe, M, N, K, act, "nk", True, residual, True, seed=K)
+
+
+@pytest.mark.parametrize("M,N,layout", [(500, 128, "nk"), (4099, 256, "nk"), (4096, 4096, "nk"), (4096, 4096, "kn"), (33, 264, "kn")])
+def test_fp32_outputs_keep_their_precision(moe, M, N, layout):
+    """An accumulator takes at most 14 stages of 64, each of which costs it 6e-8 of its value at the
+    most; the sums over accumulators round to nearest: below 1e-6 in all, whatever K is."""
+    K = 7168
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    x = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn((N, K) if layout == "nk" else (K, N), generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.empty((M, N), device="cuda")
+    moe.moe_dense_gemm(x, w, layout, None, None, 1.0, M, N, K, "none", out)
+    torch.cuda.synchronize()
+    ref = x.double() @ (w.double().t() if layout == "nk" else w.double())
+    assert float((out.double() - ref).norm() / ref.norm()) < 1e-6
