@@ -163,14 +163,15 @@ class Ctx:
         self._c = _Ctx(s, _ptr(workspace), nbytes, _ptr(dev_status),
                        ctypes.cast(ev_arr, ctypes.POINTER(ctypes.c_void_p)) if ev_arr else None, n_ev)
         self._keep = (workspace, dev_status, events, ev_arr)
+        self._ref = ctypes.byref(self._c)
 
     @property
     def ref(self):
-        return ctypes.byref(self._c)
+        return self._ref
 
 
 def _ctx(ctx):
-    return (ctx or Ctx()).ref
+    return (ctx or Ctx())._ref
 
 
 def moe_align_capacity(num_pairs: int, E: int, block_m: int):
@@ -334,9 +335,9 @@ def moe_dense_gemm(x, w, w_layout, bias, residual, residual_scale, M, N, K, acti
     """out [M, N] = act(x [M, K] . W^T + bias) + residual_scale * residual.  w_layout "nk" (w [N1, K])
     or "kn" (w [K, N1]); activation "none", "relu2" or "swiglu" (N1 = 2N).  out is bf16 or fp32
     (``out_f32`` says which for a raw pointer), residual of the same type."""
-    a = _act(activation)
+    a = ACTIVATION[activation] if activation.__class__ is str else int(activation)
     n1 = 2 * N if a == 0 else N
-    lay = W_LAYOUT[w_layout] if isinstance(w_layout, str) else int(w_layout)
+    lay = W_LAYOUT[w_layout] if w_layout.__class__ is str else int(w_layout)
     bf, f32 = _DTYPES["bf16"], _DTYPES["f32"]
     if out_f32 is None:
         out_f32 = out is not None and out.__class__ is not int and out.dtype is f32

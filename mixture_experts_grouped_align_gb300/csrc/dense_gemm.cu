@@ -506,7 +506,8 @@ cudaError_t launch(const Dense& d, cudaStream_t stream) {
     if (d.residual && !tma::encode_2d_u8(&mr, d.residual, row, (uint64_t)d.M, row, kBox, 32, kBox == 128))
       return cudaErrorInvalidValue;
   }
-  cudaError_t err = cudaFuncSetAttribute(dense_gemm_kernel<GATED, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> sized{0};
+  cudaError_t err = moe_launch::allow_smem(reinterpret_cast<const void*>(&dense_gemm_kernel<GATED, F32>), kSmem, sized);
   if (err != cudaSuccess) return err;
   const int64_t most = moe_launch::sm_count_current() / 2;
   cudaLaunchConfig_t cfg{};

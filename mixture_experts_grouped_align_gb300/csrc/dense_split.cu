@@ -434,7 +434,8 @@ cudaError_t launch(const Dense& d, const Split& s, cudaStream_t stream) {
                           : tma::encode_2d_u8(&mw, d.w, K2, N1, K2, 128, GATED ? kFeat / 2 : kFeat, true);
   if (!okw) return cudaErrorInvalidValue;
   auto kern = dense_split_kernel<NA, GATED>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024);
+  static std::atomic<uint64_t> sized{0};
+  cudaError_t err = moe_launch::allow_smem(reinterpret_cast<const void*>(kern), kRing + 1024, sized);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(s.n_tiles * s.m_tiles * s.C));

@@ -46,6 +46,15 @@ void apply_debug_stall(Dense& d) {
   d.stall = ns > 0 ? 1 : 0;
 }
 
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = -1;
+  const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
+  if (known && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess && known) done.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
+  return err;
+}
+
 int sm_count_current() {
   constexpr int kMaxDev = 64;
   static std::atomic<int> cache[kMaxDev];

@@ -4,11 +4,17 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace moe_launch {
 
 // Streaming multiprocessors of the current device (cached per device index; 1 if the
 // query fails).
 int sm_count_current();
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device; `done` holds a bit per
+// device on which that has been said already (one static per kernel).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 // ---- route + align (route_align.cu)
 size_t align_smem_bytes(int E);

@@ -576,7 +576,8 @@ cudaError_t launch_pass(RouterLoss a, cudaStream_t stream) {
   const bool cluster = turns <= kClusterBlocks;
   auto kern = cluster ? router_pass_kernel<LANES, NV, VEC, WHOLE, true> : router_pass_kernel<LANES, NV, VEC, WHOLE, false>;
   if (kSmem > 48 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    static std::atomic<uint64_t> sized[2] = {};
+    const cudaError_t err = moe_launch::allow_smem(reinterpret_cast<const void*>(kern), (int)kSmem, sized[cluster]);
     if (err != cudaSuccess) return err;
   }
   cudaLaunchConfig_t cfg{};
