@@ -11,7 +11,8 @@
  * (moe_router_loss) and the expert activation with an MXFP8 checkpoint and its backward pass
  * (moe_act_checkpoint, moe_act_backward); and, for the dense layers beside the experts (a
  * shared expert, the router's projection), a matrix product with bias, activation and residual
- * in its epilogue and its backward products (moe_dense_gemm, moe_dense_bias_grad).
+ * in its epilogue and its backward products (moe_dense_gemm, moe_dense_bias_grad), and the sum
+ * of a token's pair rows (moe_pair_sum).
  *
  * Sources of the definitions (pull-request pages):
  *  [BUCKET] "Bound Triton MoE JIT specializations via token-dim bucketing and warmup",
@@ -460,6 +461,18 @@ moe_status moe_dense_gemm(const void* x, const void* w, int32_t w_layout, const 
 /* d_bias[n] = sum_m dz[m, n]: dz [M, N] bf16, d_bias [N] fp32, summed in fp32 in a fixed order.
  * M = 0 gives zeros.  Needs no workspace. */
 moe_status moe_dense_bias_grad(const void* dz, int64_t M, int32_t N, float* d_bias, const moe_ctx* ctx);
+
+/* ------------------------------------------------------------------------------------ *
+ * Sum of a token's pair rows                                                             *
+ * ------------------------------------------------------------------------------------ */
+
+/* y[t] = sum_{j<k} o[t*k + j] (+ residual[t]): o [T*k, K] bf16 pair rows as moe_grouped_gemm
+ * writes them, residual [T, K] bf16 or NULL, y [T, K] bf16; summed in fp32 in the order of j, the
+ * residual last, rounded once.  The training counterpart of moe_forward's combine: outputs whose
+ * pairs carry their routing weight already (moe_act_checkpoint's row_w), and input gradients.
+ * y may be residual.  K a multiple of 8, 1 <= k <= 1024, T*k < 2^31. */
+moe_status moe_pair_sum(const void* o, const void* residual, int64_t T, int32_t k, int32_t K, void* y,
+                        const moe_ctx* ctx);
 
 /* ------------------------------------------------------------------------------------ *
  * Diagnostics: failure detection of the bounded waits                                    *

@@ -22,7 +22,7 @@ __all__ = [
     "moe_forward_no_alloc", "moe_grouped_gemm", "moe_grouped_gemm_workspace_size", "moe_mx_quantize",
     "moe_gemm_per_token", "moe_wgrad", "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels",
     "moe_router_loss", "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward",
-    "moe_dense_gemm", "moe_dense_bias_grad", "W_LAYOUT", "EXPORTED_SYMBOLS",
+    "moe_dense_gemm", "moe_dense_bias_grad", "moe_pair_sum", "W_LAYOUT", "EXPORTED_SYMBOLS",
 ]
 
 MOE_OK = 0
@@ -40,7 +40,7 @@ EXPORTED_SYMBOLS = [
     "moe_grouped_gemm", "moe_grouped_gemm_workspace_size", "moe_mx_quantize", "moe_gemm_per_token", "moe_wgrad",
     "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels", "moe_router_loss",
     "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward", "moe_dense_gemm",
-    "moe_dense_bias_grad",
+    "moe_dense_bias_grad", "moe_pair_sum",
 ]
 
 
@@ -114,6 +114,7 @@ def load(path: str | None = None):
         "moe_act_backward": (I32, [P, P, P, P, I64, I32, I32, P, P, P, P]),
         "moe_dense_gemm": (I32, [P, P, I32, P, P, F32, I64, I32, I32, I32, P, I32, P]),
         "moe_dense_bias_grad": (I32, [P, I64, I32, P, P]),
+        "moe_pair_sum": (I32, [P, P, I64, I32, I32, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -352,6 +353,13 @@ def moe_dense_bias_grad(dz, M, N, d_bias, ctx=None):
     """d_bias [N] fp32 = the column sums of dz [M, N] bf16."""
     return _check(load().moe_dense_bias_grad(_tensor(dz, "dz", _DTYPES["bf16"], M * N), M, N,
                                              _tensor(d_bias, "d_bias", _DTYPES["f32"], N), _ctx(ctx)))
+
+
+def moe_pair_sum(o, residual, T, k, K, y, ctx=None):
+    """y [T, K] bf16 = the sums of o [T*k, K]'s rows of each token (+ residual [T, K])."""
+    bf = _DTYPES["bf16"]
+    return _check(load().moe_pair_sum(_tensor(o, "o", bf, T * k * K), _tensor(residual, "residual", bf, T * K), T, k, K,
+                                      _tensor(y, "y", bf, T * K), _ctx(ctx)))
 
 
 def moe_debug_stall_tensor_kernels(stall_ns: int) -> None:

@@ -763,6 +763,21 @@ moe_status moe_dense_bias_grad(const void* dz, int64_t M, int32_t N, float* d_bi
   return st;
 }
 
+moe_status moe_pair_sum(const void* o, const void* residual, int64_t T, int32_t k, int32_t K, void* y,
+                        const moe_ctx* ctx) {
+  MOE_REQUIRE(T >= 0 && k >= 1 && k <= 1024 && K >= 1, MOE_ERR_INVALID_ARG, "need T >= 0, 1 <= k <= 1024, K >= 1");
+  MOE_REQUIRE(K % 8 == 0, MOE_ERR_UNSUPPORTED, "K must be a multiple of 8");
+  MOE_REQUIRE(pairs_fit(T, k), MOE_ERR_UNSUPPORTED, "T*k must be < 2^31");
+  if (T == 0) return MOE_OK;
+  MOE_REQUIRE(o && y, MOE_ERR_INVALID_ARG, "null tensor pointer");
+  MOE_REQUIRE(aligned16(o) && aligned16(residual) && aligned16(y), MOE_ERR_INVALID_ARG,
+              "all pointers must be 16-byte aligned");
+  rec(ctx, 0, 2);
+  const moe_status st = cuda_status(moe_launch::pair_sum(o, residual, T, k, K, y, stream_of(ctx)), "moe_pair_sum");
+  rec(ctx, 1, 2);
+  return st;
+}
+
 void moe_debug_stall_tensor_kernels(int64_t stall_ns) {
   moe_launch::g_debug_stall_ns.store(stall_ns > 0 ? stall_ns : 0, std::memory_order_relaxed);
 }

@@ -259,4 +259,7 @@ bool dense_split(const Dense& d, cudaStream_t stream, cudaError_t* err);
 // out[n] = sum_m x[m, n], x [M, N] bf16 (column_sum.cu)
 cudaError_t column_sum(const void* x, int64_t M, int64_t N, float* out, cudaStream_t stream);
 
+// ---- sum of a token's pair rows (pair_sum.cu)
+cudaError_t pair_sum(const void* o, const void* residual, int64_t T, int k, int K, void* y, cudaStream_t stream);
+
 }  // namespace moe_launch

@@ -1,0 +1,64 @@
+// The sum of a token's pair rows: y[t] = sum_{j < k} o[t k + j] (+ residual[t]), bf16 rows summed
+// in fp32 in the order of j, the residual last, and rounded once.
+//
+// A stream: k + 1 (+ 1) rows of 2 K bytes per token, each read or written once.  A thread owns
+// eight columns of a token and has four pair rows in flight.
+#include "moe_common.cuh"
+#include "moe_launch.h"
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ void add8(float (&acc)[8], const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc[2 * i] += __uint_as_float(w[i] << 16);
+    acc[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) pair_sum_kernel(const uint4* __restrict__ o, const uint4* residual, int64_t T,
+                                                            int k, int per, uint4* y) {
+  const int64_t n = T * per;
+  for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t t = i / per;
+    const uint4* src = o + t * k * per + (i - t * per);
+    float acc[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+    for (int j0 = 0; j0 < k; j0 += 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = j0 + j < k ? __ldcs(src + (int64_t)(j0 + j) * per) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j0 + j < k) add8(acc, v[j]);
+    }
+    if (residual) add8(acc, residual[i]);
+    uint32_t w[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * c], acc[2 * c + 1]);
+      w[c] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    y[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+}  // namespace
+
+namespace moe_launch {
+
+cudaError_t pair_sum(const void* o, const void* residual, int64_t T, int k, int K, void* y, cudaStream_t stream) {
+  const int64_t n = T * (K / 8);
+  if (n == 0) return cudaSuccess;
+  int64_t blocks = (n + kThreads - 1) / kThreads;
+  const int64_t cap = (int64_t)sm_count_current() * 32;
+  pair_sum_kernel<<<(unsigned)(blocks < cap ? blocks : cap), kThreads, 0, stream>>>(
+      static_cast<const uint4*>(o), static_cast<const uint4*>(residual), T, k, K / 8, static_cast<uint4*>(y));
+  return cudaGetLastError();
+}
+
+}  // namespace moe_launch

@@ -1,0 +1,121 @@
+"""One training step of a bf16 MoE layer: routed experts, a dense shared expert beside them, and
+the router's auxiliary losses.
+
+Forward, for x [T, K]:
+    logits = x Wr^T (fp32);  ids, w = top-k routing (moe_align)
+    gu = x W1[e]^T per pair;  h = w * silu(g) u, gu kept as an MXFP8 checkpoint;  o = h W2[e]^T
+    gs = x Ws1^T + bs1;       hs = silu(g) u,   gs kept as an MXFP8 checkpoint
+    y = hs Ws2^T + bs2 + sum_j o_tj
+Backward, from dy [T, K]: the activations' gradients come from the checkpoints, which also give
+the activations again for the weight gradients; the routing weights' gradients join the
+balance and z losses' in d_logits.
+
+Marshalling only: every step runs in the library's kernels.  ``TrainLayer`` holds the weights,
+the buffers that live from a forward to its backward, and the workspaces.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import (Ctx, moe_act_backward, moe_act_checkpoint, moe_align, moe_align_capacity, moe_dense_bias_grad,
+               moe_dense_gemm, moe_grouped_gemm, moe_pair_sum, moe_router_loss, moe_router_loss_workspace_size,
+               moe_wgrad, moe_wgrad_workspace_size)
+
+BLOCK_M = 128
+
+
+class TrainLayer:
+    """wr [E, K], w1 [E, 2I, K], w2 [E, K, I], ws1 [2Is, K], ws2 [K, Is], bs1 [2Is], bs2 [K]: bf16
+    device tensors; E, K, I and Is multiples of 64.  Batches of up to ``max_rows`` tokens."""
+
+    def __init__(self, wr, w1, w2, ws1, bs1, ws2, bs2, k, max_rows, balance_coef=0.01, z_coef=0.001):
+        self.wr, self.w1, self.w2, self.ws1, self.bs1, self.ws2, self.bs2 = wr, w1, w2, ws1, bs1, ws2, bs2
+        self.E, self.K, self.k = wr.shape[0], wr.shape[1], k
+        self.I, self.Is = w2.shape[2], ws2.shape[1]
+        if any(n % 64 for n in (self.E, self.K, self.I, self.Is)):
+            raise ValueError("E, K, I and Is must be multiples of 64 (moe_wgrad)")
+        self.coef = (balance_coef, z_coef)
+        dev, bf = wr.device, torch.bfloat16
+        T, P, E, K, I, Is = max_rows, max_rows * k, self.E, self.K, self.I, self.Is
+        self.max_rows = T
+        # the experts' input gradients contract over their outputs: transposed copies of the weights
+        self.w1t, self.w2t = w1.transpose(1, 2).contiguous(), w2.transpose(1, 2).contiguous()
+        new = lambda *shape, dtype=bf: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+        i32, u8, f32 = torch.int32, torch.uint8, torch.float32
+        self.logits, self.ids, self.w = new(T, E, dtype=f32), new(T, k, dtype=i32), new(T, k, dtype=f32)
+        self.cap, blocks = moe_align_capacity(P, E, BLOCK_M)
+        self.sorted, self.expert_ids, self.ntpp = new(self.cap, dtype=i32), new(blocks, dtype=i32), new(4, dtype=i32)
+        self.gu, self.h, self.o = new(P, 2 * I), new(P, I), new(P, K)
+        self.codes, self.scales = new(P, 2 * I, dtype=u8), new(P, 2 * I // 32, dtype=u8)
+        self.gs, self.hs, self.routed = new(T, 2 * Is), new(T, Is), new(T, K)
+        self.codes_s, self.scales_s = new(T, 2 * Is, dtype=u8), new(T, 2 * Is // 32, dtype=u8)
+        # every token once, for the dense layers' weight gradients (one expert)
+        self.cap1, blocks1 = moe_align_capacity(T, 1, BLOCK_M)
+        self.sorted1, self.expert_ids1, self.ntpp1 = new(self.cap1, dtype=i32), new(blocks1, dtype=i32), new(4, dtype=i32)
+        self.zeros = torch.zeros((T, 1), dtype=i32, device=dev)
+        self.dh, self.dgu, self.dw, self.dx_pairs = new(P, I), new(P, 2 * I), new(T, k, dtype=f32), new(P, K)
+        self.dhs, self.dgs = new(T, Is), new(T, 2 * Is)
+        self.d_logits, self.d_logits16, self.dx_router = new(T, E, dtype=f32), new(T, E), new(T, K)
+        self.counts, self.prob_mean, self.loss = new(E, dtype=i32), new(E, dtype=f32), new(3, dtype=f32)
+        self.status = torch.zeros(4, dtype=i32, device=dev)
+        self.grads = {"wr": new(E, K, dtype=f32), "w1": new(E, 2 * I, K, dtype=f32), "w2t": new(E, I, K, dtype=f32),
+                      "ws1": new(2 * Is, K, dtype=f32), "ws2": new(K, Is, dtype=f32), "bs1": new(2 * Is, dtype=f32),
+                      "bs2": new(K, dtype=f32)}
+        need = max(moe_router_loss_workspace_size(E), 256,
+                   *(moe_wgrad_workspace_size(e, n, kin, BLOCK_M, c) for e, n, kin, c in
+                     [(E, 2 * I, K, self.cap), (E, I, K, self.cap), (1, 2 * Is, K, self.cap1), (1, K, Is, self.cap1)]))
+        self.workspace = torch.empty(need, dtype=u8, device=dev)
+
+    def _ctx(self):
+        return Ctx(workspace=self.workspace, dev_status=self.status)
+
+    def forward(self, x, y):
+        """x [T, K] bf16 -> y [T, K] bf16.  x is needed again by ``backward``."""
+        T, k, E, K, I, Is, c = x.shape[0], self.k, self.E, self.K, self.I, self.Is, self._ctx()
+        self.T, self.x = T, x
+        moe_dense_gemm(x, self.wr, "nk", None, None, 1.0, T, E, K, "none", self.logits, c)
+        cap, _ = moe_align_capacity(T * k, E, BLOCK_M)
+        moe_align(self.logits, self.ids, self.w, T, k, E, BLOCK_M, self.sorted, cap, self.expert_ids, self.ntpp, None, c)
+        args = (T, k, self.sorted, self.expert_ids, self.ntpp, BLOCK_M, cap)
+        moe_grouped_gemm("bf16", E, 2 * I, K, x, None, 0, self.w1, None, None, *args, self.gu, c)
+        moe_act_checkpoint(self.gu, self.w, T * k, I, "swiglu", self.h, self.codes, self.scales, c)
+        moe_grouped_gemm("bf16", E, K, I, self.h, None, 1, self.w2, None, None, *args, self.o, c)
+        moe_pair_sum(self.o, None, T, k, K, self.routed, c)
+        moe_dense_gemm(x, self.ws1, "nk", self.bs1, None, 1.0, T, 2 * Is, K, "none", self.gs, c)
+        moe_act_checkpoint(self.gs, None, T, Is, "swiglu", self.hs, self.codes_s, self.scales_s, c)
+        moe_dense_gemm(self.hs, self.ws2, "nk", self.bs2, self.routed, 1.0, T, K, Is, "none", y, c)
+        return y
+
+    def backward(self, dy, dx, token_mask=None):
+        """dy [T, K] bf16, the gradient of y -> dx [T, K] bf16, the weights' gradients in
+        ``grads`` (fp32; "w2t" is [E, I, K]), the losses in ``loss`` (total, balance, z) and the
+        experts' counts in ``counts``.  token_mask [T]: 0 for tokens the losses leave out."""
+        T, k, E, K, I, Is, c, g = self.T, self.k, self.E, self.K, self.I, self.Is, self._ctx(), self.grads
+        x = self.x
+        cap, _ = moe_align_capacity(T * k, E, BLOCK_M)
+        args = (T, k, self.sorted, self.expert_ids, self.ntpp, BLOCK_M, cap)
+        # routed experts: dh, then the activation from its checkpoint (h is w h again)
+        moe_grouped_gemm("bf16", E, I, K, dy, None, 0, self.w2t, None, None, *args, self.dh, c)
+        moe_act_backward(self.codes, self.scales, self.dh, self.w, T * k, I, "swiglu", self.dgu, self.h, self.dw, c)
+        moe_wgrad(self.h, dy, 0, T, k, E, I, K, *args[2:], g["w2t"], 0, c)
+        moe_wgrad(self.dgu, x, 0, T, k, E, 2 * I, K, *args[2:], g["w1"], 0, c)
+        moe_grouped_gemm("bf16", E, K, 2 * I, self.dgu, None, 1, self.w1t, None, None, *args, self.dx_pairs, c)
+        # router: the routing weights' gradient joins the auxiliary losses'
+        moe_router_loss(self.logits, self.ids, self.w, self.dw, token_mask, T, k, E, *self.coef, self.counts,
+                        self.prob_mean, self.loss, self.d_logits, c)
+        self.d_logits16[:T].copy_(self.d_logits[:T])
+        moe_dense_gemm(self.d_logits16, self.wr, "kn", None, None, 1.0, T, K, E, "none", self.dx_router, c)
+        moe_pair_sum(self.dx_pairs, self.dx_router, T, k, K, dx, c)
+        # shared expert
+        cap1, _ = moe_align_capacity(T, 1, BLOCK_M)
+        moe_align(None, self.zeros, None, T, 1, 1, BLOCK_M, self.sorted1, cap1, self.expert_ids1, self.ntpp1, None, c)
+        one = (self.sorted1, self.expert_ids1, self.ntpp1, BLOCK_M, cap1)
+        moe_dense_gemm(dy, self.ws2, "kn", None, None, 1.0, T, Is, K, "none", self.dhs, c)
+        moe_act_backward(self.codes_s, self.scales_s, self.dhs, None, T, Is, "swiglu", self.dgs, self.hs, None, c)
+        moe_wgrad(dy, self.hs, 0, T, 1, 1, K, Is, *one, g["ws2"], 0, c)
+        moe_wgrad(self.dgs, x, 0, T, 1, 1, 2 * Is, K, *one, g["ws1"], 0, c)
+        moe_dense_bias_grad(dy, T, K, g["bs2"], c)
+        moe_dense_bias_grad(self.dgs, T, 2 * Is, g["bs1"], c)
+        moe_wgrad(self.d_logits16, x, 0, T, 1, 1, E, K, *one, g["wr"], 0, c)
+        moe_dense_gemm(self.dgs, self.ws1, "kn", None, dx, 1.0, T, K, 2 * Is, "none", dx, c)
+        return dx

@@ -102,3 +102,11 @@ def test_dense_binding_refusals():
     refused(-1, dense, x=torch.zeros((4, 64), dtype=torch.bfloat16))
     # a residual in another type than the output
     refused(-1, dense, residual=torch.zeros((4, 64), dtype=torch.bfloat16), f32=True)
+
+
+@pytest.mark.parametrize("status,kw", [(-1, dict(T=-1)), (-1, dict(k=0)), (-1, dict(k=1025)), (-2, dict(K=12)),
+                                       (-2, dict(T=1 << 30, k=4)), (-1, dict(o=None)), (-1, dict(y=None)), (-1, dict(o=P + 2)),
+                                       (-1, dict(r=P + 8))])
+def test_pair_sum_refusals(status, kw):
+    a = {"o": P, "r": None, "T": 4, "k": 2, "K": 64, "y": P} | kw
+    refused(status, moe.moe_pair_sum, a["o"], a["r"], a["T"], a["k"], a["K"], a["y"], moe.Ctx(stream=0))
