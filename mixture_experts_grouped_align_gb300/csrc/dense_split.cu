@@ -6,15 +6,15 @@
 // an MMA of N = 16 and not of M = 128.  K is split over the C CTAs of a cluster, which makes
 // tiles x C CTAs pull on W at once; each accumulates its share in TMEM, leaves it in its shared
 // memory as fp32 (token-major, so that lanes are consecutive features), and the C shares are
-// added in rank order through distributed shared memory by the CTA that stores the row: no
-// workspace, no second launch, the same bits every time.  A SwiGLU weight tile is 64 gate rows
-// and the 64 up rows of the same features, which meet in that sum.  NA = 2 keeps two accumulators
-// that share one load of x.
+// added through distributed shared memory by the CTA that stores the row, from its own share on
+// in rank order: no workspace, no second launch, the same bits every time.  A SwiGLU weight tile
+// is 64 gate rows and the 64 up rows of the same features, which meet in that sum.  NA = 2 keeps
+// two accumulators that share one load of x.
 //
 // The tensor core's accumulator loses up to one unit in the last place with every MMA, always
 // towards zero, which a bf16 output hides and an fp32 output does not (relative error 6e-8 for
-// every 64 of K, measured).  For fp32 outputs K is therefore also split over G accumulators in TMEM, of at most kGroupBlocks stages each where
-// the columns suffice, and those are added in fp32 registers.
+// every 64 of K, measured).  For fp32 outputs K is therefore also split over G accumulators in
+// TMEM of at most kGroupBlocks stages each, which are added in fp32 registers.
 //   warp 0 loads stages (64 of K: the weight tiles, BN rows of x) by TMA, as many stages as fit,
 //   from before the block's other roles are ready;
 //   warp 1 issues the MMAs; then all sixteen warps drain, add and store.
@@ -299,8 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           float4 v[8], u[8];
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
-            v[r] = r < sp.C ? ld_cluster_f4(at, r) : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (GATED) u[r] = r < sp.C ? ld_cluster_f4(at + kOut * 4, r) : make_float4(0.f, 0.f, 0.f, 0.f);
+            // from this CTA's own share on, so that the CTAs do not all read the same one at once
+            const int from = rank + r < sp.C ? rank + r : rank + r - sp.C;
+            v[r] = r < sp.C ? ld_cluster_f4(at, from) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (GATED) u[r] = r < sp.C ? ld_cluster_f4(at + kOut * 4, from) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
 #pragma unroll
           for (int r = 1; r < 8; ++r) {
