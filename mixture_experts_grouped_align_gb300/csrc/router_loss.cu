@@ -618,13 +618,14 @@ cudaError_t launch_rows(const RouterLoss& a, cudaStream_t s) {
   return a.E == 4 * NV * LANES ? launch_pass<LANES, NV, true, true>(a, s) : launch_pass<LANES, NV, true, false>(a, s);
 }
 
-// The fewest lanes that hold a row at sixteen values each (fewer for narrow rows, 32 above 512
-// experts): fewer lanes mean fewer shuffle steps per row and more rows in flight per warp.
+// The fewest lanes that hold a row at sixteen values each (32 above 512 experts): fewer lanes mean
+// fewer shuffle steps per row and more rows in flight per warp.  Above 16 experts at least eight,
+// so that each of up to eight choices has a lane of its own.
 cudaError_t launch(const RouterLoss& a, cudaStream_t s) {
   const int E = a.E;
   if (E <= 16) return launch_rows<4, 1>(a, s);
-  if (E <= 32) return launch_rows<4, 2>(a, s);
-  if (E <= 64) return launch_rows<4, 4>(a, s);
+  if (E <= 32) return launch_rows<8, 1>(a, s);
+  if (E <= 64) return launch_rows<8, 2>(a, s);
   if (E <= 128) return launch_rows<8, 4>(a, s);
   if (E <= 256) return launch_rows<16, 4>(a, s);
   if (E <= 512) return launch_rows<32, 4>(a, s);

@@ -177,3 +177,41 @@ def test_gradient_is_the_difference_quotient(moe):
         assert np.all(np.abs(got[:, c] - q) <= 2.0 ** -8 * np.abs(q) + 1e-4 * 2.0 ** -8 + 1e-8)
     q = (f(v, w + 1e-3) - f(v, w - 1e-3)) / 2e-3
     assert np.allclose(dw.cpu().numpy(), q, rtol=1e-4, atol=1e-4)
+
+
+def test_offsets_past_32_bits(moe):
+    """More than 2^31 pre-activations: rows on both sides of the wrap against the oracle."""
+    R, I = 400_000, 2880
+    g = torch.Generator(device="cuda").manual_seed(26)
+    z = torch.randn((R, 2 * I), generator=g, device="cuda", dtype=torch.bfloat16)
+    dh = torch.randn((R, I), generator=g, device="cuda", dtype=torch.bfloat16)
+    h, dz, codes = torch.empty_like(dh), torch.empty_like(z), torch.empty((R, 2 * I), dtype=torch.uint8, device="cuda")
+    scales, dw = torch.empty((R, 2 * I // 32), dtype=torch.uint8, device="cuda"), torch.empty(R, device="cuda")
+    moe.moe_act_checkpoint(z, None, R, I, "swiglu", h, codes, scales)
+    moe.moe_act_backward(codes, scales, dh, None, R, I, "swiglu", dz, None, dw)
+    torch.cuda.synchronize()
+    wrap = 2 ** 31 // (2 * I)
+    rows = torch.tensor([0, 1, wrap - 1, wrap, wrap + 1, 2 ** 32 // (2 * I) % R, R - 1], device="cuda")
+    zv, dv = bf16_to_np(z[rows].contiguous()), bf16_to_np(dh[rows].contiguous())
+    oc, os_, v = activation.held(zv)
+    assert np.array_equal(codes[rows].cpu().numpy(), oc) and np.array_equal(scales[rows].cpu().numpy(), os_)
+    ref = activation.forward(zv, None, True)
+    assert np.all(near_bf16(bf16_to_np(h[rows].contiguous()), ref, np.abs(ref)))
+    rz, _, rw = activation.backward(v, dv, None, True)
+    gate, u = v[:, :I], v[:, I:]
+    mag = np.abs(rz)
+    mag[:, :I] = np.abs(dv * u) * activation._sigmoid(gate) * (1 + np.abs(gate))
+    assert np.all(near_bf16(bf16_to_np(dz[rows].contiguous()), rz, mag))
+    a = np.abs(gate * activation._sigmoid(gate) * u)
+    assert np.all(np.abs(dw[rows].cpu().numpy() - rw) <= 2.0 ** -16 * (np.abs(dv) * a).sum(axis=1))
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("R,I", [(2000, 512), (5000, 544), (1700, 2048), (20000, 352), (3000, 1056)])
+def test_rows_of_several_turns(moe, R, I, gated):
+    """A warp per row with two or four turns of columns, whole and ragged."""
+    rng = np.random.default_rng(I)
+    z = rng.standard_normal((R, 2 * I if gated else I)) * 2
+    w = rng.uniform(0.01, 1, R)
+    w[::7] = 0.0
+    check(moe, z, rng.standard_normal((R, I)) * 0.05, w, gated)

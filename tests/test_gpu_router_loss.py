@@ -207,3 +207,33 @@ def test_gradient_is_the_loss_difference(moe):
     lm = orl.router_loss(x - h * d.astype(np.float64), ids, None, None, None, 1.0, 1.0)[2][0]
     # the quotient's own error is of second order in the step's length 1e-2
     assert abs((lp - lm) / (2 * h) - gg) <= 1e-3 * gg
+
+
+def test_offsets_past_32_bits(moe):
+    """More than 2^31 logits: rows on both sides of the wrap, against torch in float64."""
+    T, E, k = 2_200_000, 1000, 4
+    g = torch.Generator(device="cuda").manual_seed(16)
+    x = torch.randn((T, E), generator=g, device="cuda")
+    val, ids = x.topk(k, dim=1)
+    w, dw = torch.softmax(val, 1), torch.randn((T, k), generator=g, device="cuda")
+    ids = ids.to(torch.int32)
+    counts, loss, d = torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(3, device="cuda"), torch.empty_like(x)
+    ws = torch.empty(moe.moe_router_loss_workspace_size(E), dtype=torch.uint8, device="cuda")
+    moe.moe_router_loss(x, ids, w, dw, None, T, k, E, 1.0, 0.0, counts, None, loss, d, moe.Ctx(workspace=ws))
+    torch.cuda.synchronize()
+    assert torch.equal(counts.long(), torch.bincount(ids.long().reshape(-1), minlength=E))
+    rows = torch.tensor([0, 1, 2147483, 2147484, T // 2, T - 1], device="cuda")
+    p = torch.softmax(x[rows].double(), 1)
+    f = counts.double() * E / (T * k)
+    ref = p / T * (f - (p @ f)[:, None])
+    wr, dr = w[rows].double(), dw[rows].double()
+    ref.scatter_add_(1, ids[rows].long(), wr * (dr - (wr * dr).sum(1, keepdim=True)))
+    # the terms are of order 1 and within a few ulp each
+    assert float((d[rows].double() - ref).abs().max()) < 2.0 ** -20
+
+
+@pytest.mark.parametrize("E,k", [(12, 5), (16, 8), (31, 7), (60, 12), (200, 20), (700, 32)])
+def test_more_choices_than_lanes(moe, E, k):
+    x, ids, w, dw = make(900, E, k, 17)
+    ids[3, 0] = ids[3, 1]
+    check(call(moe, x, ids, w, dw), x, ids, w, dw, None)
