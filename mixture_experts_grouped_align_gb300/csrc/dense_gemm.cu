@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       moe::set_status(d.status, MOE_ERR_TIMEOUT);
       *abort_flag = 1;
     }
-    if (lane == 0) tma::bulk_wait_all();
+    if (lane == 0) tma::bulk_wait_read_all();  // the stores need the boxes no more; they end with the grid
     __syncwarp();
   }
   tc::tc_fence_before();
