@@ -115,6 +115,8 @@ template <bool GATED, int LANES, bool WIDE, int TURNS>
 __global__ void __launch_bounds__(kThreads, TURNS > 1 ? 3 : 4) act_checkpoint_kernel(ActCheckpoint a) {
   using M = Map<LANES, WIDE, TURNS>;
   constexpr int kT = M::kTurns, kH = GATED ? 2 : 1;
+  moe::wait_for_stream();
+  moe::let_next_start();
   const int64_t row = M::row();
   const bool in = row < a.rows;
   const int units = a.I / 8, lane = threadIdx.x & 31;
@@ -175,6 +177,8 @@ template <bool GATED, int LANES, bool WIDE, int TURNS>
 __global__ void __launch_bounds__(kThreads, TURNS > 1 ? 3 : 4) act_backward_kernel(ActBackward a) {
   using M = Map<LANES, WIDE, TURNS>;
   constexpr int kT = M::kTurns, kH = GATED ? 2 : 1;
+  moe::wait_for_stream();
+  moe::let_next_start();
   const int64_t row = M::row();
   const bool in = row < a.rows;
   const int units = a.I / 8, lane = threadIdx.x & 31;
@@ -287,8 +291,8 @@ cudaError_t checkpoint(const ActCheckpoint& a, cudaStream_t s) {
   return pick(a, [&](auto p) {
     using P = decltype(p);
     const int64_t blocks = (a.rows + P::M::kRowsPerBlock - 1) / P::M::kRowsPerBlock;
-    act_checkpoint_kernel<GATED, P::kLanes, P::kWide, P::kTurns><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return moe_launch::launch_staged(act_checkpoint_kernel<GATED, P::kLanes, P::kWide, P::kTurns>, dim3((unsigned)blocks),
+                                     dim3(kThreads), 0, s, 1, a);
   });
 }
 
@@ -297,8 +301,8 @@ cudaError_t backward(const ActBackward& a, cudaStream_t s) {
   return pick(a, [&](auto p) {
     using P = decltype(p);
     const int64_t blocks = (a.rows + P::M::kRowsPerBlock - 1) / P::M::kRowsPerBlock;
-    act_backward_kernel<GATED, P::kLanes, P::kWide, P::kTurns><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return moe_launch::launch_staged(act_backward_kernel<GATED, P::kLanes, P::kWide, P::kTurns>, dim3((unsigned)blocks),
+                                     dim3(kThreads), 0, s, 1, a);
   });
 }
 

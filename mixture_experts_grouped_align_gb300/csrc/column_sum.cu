@@ -26,8 +26,10 @@ __device__ __forceinline__ void add8(float (&acc)[8], const uint4& v) {
 
 // VEC: rows are whole 16-byte units.
 template <bool VEC>
-__global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
     column_sum_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t N, float* __restrict__ out) {
+  moe::wait_for_stream();
+  moe::let_next_start();
   __shared__ float part[kGroups][kCols];
   __shared__ float mine[kCols];
   const int tid = threadIdx.x, cg = tid % kLanes, rg = tid / kLanes;
@@ -90,11 +92,8 @@ namespace moe_launch {
 
 cudaError_t column_sum(const void* x, int64_t M, int64_t N, float* out, cudaStream_t stream) {
   const int64_t blocks = (N + kCols - 1) / kCols * kSplit;
-  if (N % 8 == 0)
-    column_sum_kernel<true><<<(unsigned)blocks, kThreads, 0, stream>>>(static_cast<const uint16_t*>(x), M, N, out);
-  else
-    column_sum_kernel<false><<<(unsigned)blocks, kThreads, 0, stream>>>(static_cast<const uint16_t*>(x), M, N, out);
-  return cudaGetLastError();
+  return launch_staged(N % 8 == 0 ? column_sum_kernel<true> : column_sum_kernel<false>, dim3((unsigned)blocks),
+                       dim3(kThreads), 0, stream, kSplit, static_cast<const uint16_t*>(x), M, N, out);
 }
 
 }  // namespace moe_launch

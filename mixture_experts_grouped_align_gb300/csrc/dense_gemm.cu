@@ -179,6 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::cluster_sync();  // both CTAs' barriers are there before either is signalled
   tc::tc_fence_after();
+  moe::wait_for_stream();
+  moe::let_next_start();
   const uint32_t taddr = __shfl_sync(0xffffffffu, *taddr_s, 0), smem_s = tc::smem_addr(smem);
   const int nk = (d.K + kBK - 1) / kBK;
   const bool kn = d.w_kn != 0;
@@ -511,19 +513,8 @@ cudaError_t launch(const Dense& d, cudaStream_t stream) {
   cudaError_t err = moe_launch::allow_smem(reinterpret_cast<const void*>(&dense_gemm_kernel<GATED, F32>), kSmem, sized);
   if (err != cudaSuccess) return err;
   const int64_t most = moe_launch::sm_count_current() / 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(2 * (ts.total < most ? ts.total : most)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 2;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, dense_gemm_kernel<GATED, F32>, mx, mw, mo, mr, d, ts);
-  return err == cudaSuccess ? cudaGetLastError() : err;
+  return moe_launch::launch_staged(dense_gemm_kernel<GATED, F32>, dim3((unsigned)(2 * (ts.total < most ? ts.total : most))),
+                                   dim3(kThreads), kSmem, stream, 2, mx, mw, mo, mr, d, ts);
 }
 
 }  // namespace

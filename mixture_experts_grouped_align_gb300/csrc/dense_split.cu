@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     tc::mbar_fence_init();
     tc::fence_proxy_async_smem();
+    moe::wait_for_stream();
     if (!d.stall)
       for (int it = 0; it < first; ++it) load_stage(it, it);
   }
@@ -168,6 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t taddr = __shfl_sync(0xffffffffu, taddr_s, 0);
+  moe::wait_for_stream();
+  moe::let_next_start();
 
   if (warp == 0 && !d.stall) {
     const bool leader = elect_one();
@@ -442,19 +445,8 @@ cudaError_t launch(const Dense& d, const Split& s, cudaStream_t stream) {
   static std::atomic<uint64_t> sized{0};
   cudaError_t err = moe_launch::allow_smem(reinterpret_cast<const void*>(kern), kRing + 1024, sized);
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(s.n_tiles * s.m_tiles * s.C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = s.smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = s.C;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  err = cudaLaunchKernelEx(&cfg, kern, mx, mw, d, s);
-  return err == cudaSuccess ? cudaGetLastError() : err;
+  return moe_launch::launch_staged(kern, dim3((unsigned)(s.n_tiles * s.m_tiles * s.C)), dim3(kThreads), (size_t)s.smem, stream,
+                                   s.C, mx, mw, d, s);
 }
 
 }  // namespace

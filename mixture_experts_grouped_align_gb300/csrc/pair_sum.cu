@@ -21,6 +21,8 @@ __device__ __forceinline__ void add8(float (&acc)[8], const uint4& v) {
 
 __global__ void __launch_bounds__(kThreads) pair_sum_kernel(const uint4* __restrict__ o, const uint4* residual, int64_t T,
                                                             int k, int per, uint4* y) {
+  moe::wait_for_stream();
+  moe::let_next_start();
   const int64_t n = T * per;
   for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kThreads) {
     const int64_t t = i / per;
@@ -56,9 +58,8 @@ cudaError_t pair_sum(const void* o, const void* residual, int64_t T, int k, int 
   if (n == 0) return cudaSuccess;
   int64_t blocks = (n + kThreads - 1) / kThreads;
   const int64_t cap = (int64_t)sm_count_current() * 32;
-  pair_sum_kernel<<<(unsigned)(blocks < cap ? blocks : cap), kThreads, 0, stream>>>(
-      static_cast<const uint4*>(o), static_cast<const uint4*>(residual), T, k, K / 8, static_cast<uint4*>(y));
-  return cudaGetLastError();
+  return launch_staged(pair_sum_kernel, dim3((unsigned)(blocks < cap ? blocks : cap)), dim3(kThreads), 0, stream, 1,
+                       static_cast<const uint4*>(o), static_cast<const uint4*>(residual), T, k, K / 8, static_cast<uint4*>(y));
 }
 
 }  // namespace moe_launch

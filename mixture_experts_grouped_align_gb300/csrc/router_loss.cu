@@ -117,7 +117,8 @@ __device__ void count_tokens(const RouterLoss& a, int64_t t0, int64_t t1, int* h
 __global__ void __launch_bounds__(kCountThreads) router_count_kernel(RouterLoss a, int64_t per_block) {
   extern __shared__ int sm_count[];
   __shared__ int n_real;
-  asm volatile("griddepcontrol.launch_dependents;");
+  moe::wait_for_stream();
+  moe::let_next_start();  // the pass: what its first loads read is complete by now
   const Ws w = carve(a.ws, a.E);
   const int64_t t0 = blockIdx.x * per_block;
   const int64_t t1 = t0 + per_block < a.T ? t0 + per_block : a.T;
@@ -328,6 +329,10 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
     }
   };
   auto chosen = [&](uint32_t tr) { return (uint32_t)id_n < (uint32_t)E ? a.logits[(size_t)tr * E + id_n] : 0.f; };
+  if (CLUSTER) {
+    moe::wait_for_stream();
+    moe::let_next_start();
+  }
   load(t);  // before the counts are waited for
   float l0 = chosen(t);
   int* cs = reinterpret_cast<int*>(gs);
@@ -349,7 +354,8 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
     if (tid == 0) n_sh = n;
     __syncthreads();
   } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    moe::wait_for_stream();
+    moe::let_next_start();
     // kThreads / kWide threads share a column's count blocks
     int* redi = reinterpret_cast<int*>(red);
     if (warp == 0) {
@@ -580,36 +586,21 @@ cudaError_t launch_pass(RouterLoss a, cudaStream_t stream) {
     const cudaError_t err = moe_launch::allow_smem(reinterpret_cast<const void*>(kern), (int)kSmem, sized[cluster]);
     if (err != cudaSuccess) return err;
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   if (cluster) {
-    const unsigned c = (unsigned)(turns < 1 ? 1 : (turns < kClusterBlocks ? turns : kClusterBlocks));
-    cfg.gridDim = dim3(c);
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = c;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  } else {
-    int64_t blocks = (a.T * a.k + 4095) / 4096;
-    if (blocks > kMaxCountBlocks) blocks = kMaxCountBlocks;
-    const int64_t per = ((a.T + blocks - 1) / blocks + 3) / 4 * 4;  // ids of a block start on 16 bytes
-    a.count_blocks = (int)((a.T + per - 1) / per);
-    router_count_kernel<<<(unsigned)a.count_blocks, kCountThreads, (size_t)a.E * 4, stream>>>(a, per);
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    int64_t cap = moe_launch::sm_count_current();
-    if (cap > kMaxPassBlocks) cap = kMaxPassBlocks;
-    cfg.gridDim = dim3((unsigned)(turns < cap ? turns : cap));
-    // programmatic launch: the pass's first loads run under the counts, which it then waits for
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    const int c = (int)(turns < 1 ? 1 : turns);
+    return moe_launch::launch_staged(kern, dim3((unsigned)c), dim3(kThreads), kSmem, stream, c, a);
   }
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a);
-  return err == cudaSuccess ? cudaGetLastError() : err;
+  int64_t blocks = (a.T * a.k + 4095) / 4096;
+  if (blocks > kMaxCountBlocks) blocks = kMaxCountBlocks;
+  const int64_t per = ((a.T + blocks - 1) / blocks + 3) / 4 * 4;  // ids of a block start on 16 bytes
+  a.count_blocks = (int)((a.T + per - 1) / per);
+  const cudaError_t err = moe_launch::launch_staged(router_count_kernel, dim3((unsigned)a.count_blocks), dim3(kCountThreads),
+                                                    (size_t)a.E * 4, stream, 1, a, per);
+  if (err != cudaSuccess) return err;
+  int64_t cap = moe_launch::sm_count_current();
+  if (cap > kMaxPassBlocks) cap = kMaxPassBlocks;
+  // the pass's first loads run under the counts, which it then waits for
+  return moe_launch::launch_staged(kern, dim3((unsigned)(turns < cap ? turns : cap)), dim3(kThreads), kSmem, stream, 1, a);
 }
 
 template <int LANES, int NV>
