@@ -1,9 +1,9 @@
 """Python binding of the GB300 MoE expert-layer library (libmoe_gb300.so).
 
-Argument marshalling only: every step of the path runs in the library's CUDA kernels.
-Functions carry the C ABI's names (include/moe_gb300.h).  Tensor arguments may be torch
-tensors (their device pointer is passed) or plain integers (raw device pointers) or None
-(NULL).  PyTorch is used only for device memory and streams.
+Argument marshalling only (ctypes; for the training and dense calls csrc/binding.c): every step
+of the path runs in the library's CUDA kernels.  Functions carry the C ABI's names
+(include/moe_gb300.h).  Tensor arguments may be torch tensors (their device pointer is passed)
+or plain integers (raw device pointers) or None (NULL).  PyTorch is used only for device memory and streams.
 
 The library must have been built (``build()`` or ``python -m
 mixture_experts_grouped_align_gb300.build``); loading fails loudly otherwise -- there is
@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-from .build import LIB, build  # noqa: F401
+from .build import BINDING, LIB, build  # noqa: F401
 
 __all__ = [
     "MoeError", "load", "Ctx", "QUANT", "ACTIVATION", "moe_align_capacity", "moe_align", "moe_bucket",
@@ -64,18 +64,26 @@ class _Weights(ctypes.Structure):
 
 
 _lib = None
+_native = None  # csrc/binding.c, with the library's addresses
 
 
-class _Dtypes(dict):
-    """The torch types of tensor arguments (torch is imported with the first one)."""
+def _load_native():
+    """The marshalling of the training and dense calls (imports torch, whose types it checks)."""
+    global _native
+    import importlib.machinery
+    import importlib.util
 
-    def __missing__(self, name):
-        import torch
-        self.update(f32=torch.float32, i32=torch.int32, bf16=torch.bfloat16, u8=torch.uint8)
-        return self[name]
-
-
-_DTYPES = _Dtypes()
+    import torch
+    loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+    loader.exec_module(mod)
+    lib = load()
+    names = ("moe_router_loss", "moe_act_checkpoint", "moe_act_backward", "moe_dense_gemm", "moe_dense_bias_grad",
+             "moe_pair_sum")
+    mod.setup(_refuse, torch.float32, torch.int32, torch.bfloat16, torch.uint8,
+              tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+    _native = mod
+    return mod
 
 
 def load(path: str | None = None):
@@ -165,6 +173,7 @@ class Ctx:
                        ctypes.cast(ev_arr, ctypes.POINTER(ctypes.c_void_p)) if ev_arr else None, n_ev)
         self._keep = (workspace, dev_status, events, ev_arr)
         self._ref = ctypes.byref(self._c)
+        self.address = ctypes.addressof(self._c)
 
     @property
     def ref(self):
@@ -211,7 +220,7 @@ def moe_forward_workspace_size(T_rows, k, K, I, cap_tokens) -> int:
 
 
 def _act(activation):
-    return ACTIVATION[activation] if isinstance(activation, str) else int(activation)
+    return ACTIVATION[activation] if activation.__class__ is str else int(activation)
 
 
 def moe_forward(quant, E, K, I, w1, w1_scale, b1, w2, w2_scale, b2, x, x_scale, T_rows, T_real, k,
@@ -278,15 +287,14 @@ def moe_wgrad_workspace_size(E, N, Kin, block_m, cap_tokens, mode=0) -> int:
     return load().moe_wgrad_workspace_size(E, N, Kin, block_m, cap_tokens, int(mode))
 
 
-def _tensor(t, what, dtype, numel):
-    """The device pointer of a tensor argument, after the checks the C ABI cannot make: a torch
-    tensor must be dense, of the stated type and of at least ``numel`` elements."""
-    if t is None or t.__class__ is int:
-        return t
-    if t.dtype is dtype and t.is_contiguous() and t.is_cuda and t.numel() >= numel:
-        return t.data_ptr()
+def _refuse(t, what, dtype, numel):
     raise MoeError(-1, f"{what}: need a contiguous {dtype} device tensor of {numel} elements, got "
                        f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+
+
+# Tensor arguments of the calls below are checked: contiguous, of the stated type, on a device,
+# of at least the elements the call reads or writes; otherwise MoeError.  Raw pointers (ints) are
+# taken as they are.
 
 
 def moe_router_loss_workspace_size(E) -> int:
@@ -297,38 +305,26 @@ def moe_router_loss(logits, topk_ids, topk_w, d_topk_w, token_mask, T, k, E, bal
                     prob_mean, loss, d_logits, ctx):
     """Balance and z losses, per-expert counts and d_logits [T, E] (with the gradient d_topk_w of
     the routing weights, if given).  loss [3] = total, balance, z."""
-    f32, i32 = _DTYPES["f32"], _DTYPES["i32"]
-    return _check(load().moe_router_loss(
-        _tensor(logits, "logits", f32, T * E), _tensor(topk_ids, "topk_ids", i32, T * k),
-        _tensor(topk_w, "topk_w", f32, T * k), _tensor(d_topk_w, "d_topk_w", f32, T * k),
-        _tensor(token_mask, "token_mask", _DTYPES["u8"], T), T, k, E, balance_coef, z_coef,
-        _tensor(counts, "counts", i32, E), _tensor(prob_mean, "prob_mean", f32, E), _tensor(loss, "loss", f32, 3),
-        _tensor(d_logits, "d_logits", f32, T * E), _ctx(ctx)))
+    c = ctx or Ctx()
+    return _check((_native or _load_native()).router_loss(
+        logits, topk_ids, topk_w, d_topk_w, token_mask, T, k, E, balance_coef, z_coef, counts, prob_mean, loss, d_logits,
+        c.address))
 
 
 def moe_act_checkpoint(gu, row_w, rows, I, activation, h, codes, scales, ctx=None):
     """gu [rows, N1] bf16 -> h [rows, I] bf16 and the MXFP8 checkpoint of gu (N1 = 2I for
     "swiglu", I for "relu2")."""
-    a = _act(activation)
-    n1 = I if a == 1 else 2 * I
-    bf, u8 = _DTYPES["bf16"], _DTYPES["u8"]
-    return _check(load().moe_act_checkpoint(
-        _tensor(gu, "gu", bf, rows * n1), _tensor(row_w, "row_w", _DTYPES["f32"], rows), rows, I, a,
-        _tensor(h, "h", bf, rows * I), _tensor(codes, "codes", u8, rows * n1),
-        _tensor(scales, "scales", u8, rows * n1 // 32), _ctx(ctx)))
+    c = ctx or Ctx()
+    return _check((_native or _load_native()).act_checkpoint(gu, row_w, rows, I, _act(activation), h, codes, scales,
+                                                            c.address))
 
 
 def moe_act_backward(codes, scales, dh, row_w, rows, I, activation, d_gu, h=None, d_row_w=None, ctx=None):
     """The checkpoint and dh [rows, I] bf16 -> d_gu [rows, N1] bf16, the activations h again and
     the row weights' gradient d_row_w [rows] fp32."""
-    a = _act(activation)
-    n1 = I if a == 1 else 2 * I
-    bf, u8, f32 = _DTYPES["bf16"], _DTYPES["u8"], _DTYPES["f32"]
-    return _check(load().moe_act_backward(
-        _tensor(codes, "codes", u8, rows * n1), _tensor(scales, "scales", u8, rows * n1 // 32),
-        _tensor(dh, "dh", bf, rows * I), _tensor(row_w, "row_w", f32, rows), rows, I, a,
-        _tensor(d_gu, "d_gu", bf, rows * n1), _tensor(h, "h", bf, rows * I),
-        _tensor(d_row_w, "d_row_w", f32, rows), _ctx(ctx)))
+    c = ctx or Ctx()
+    return _check((_native or _load_native()).act_backward(codes, scales, dh, row_w, rows, I, _act(activation), d_gu, h,
+                                                          d_row_w, c.address))
 
 
 def moe_dense_gemm(x, w, w_layout, bias, residual, residual_scale, M, N, K, activation, out, ctx=None,
@@ -336,30 +332,24 @@ def moe_dense_gemm(x, w, w_layout, bias, residual, residual_scale, M, N, K, acti
     """out [M, N] = act(x [M, K] . W^T + bias) + residual_scale * residual.  w_layout "nk" (w [N1, K])
     or "kn" (w [K, N1]); activation "none", "relu2" or "swiglu" (N1 = 2N).  out is bf16 or fp32
     (``out_f32`` says which for a raw pointer), residual of the same type."""
-    a = ACTIVATION[activation] if activation.__class__ is str else int(activation)
-    n1 = 2 * N if a == 0 else N
     lay = W_LAYOUT[w_layout] if w_layout.__class__ is str else int(w_layout)
-    bf, f32 = _DTYPES["bf16"], _DTYPES["f32"]
     if out_f32 is None:
-        out_f32 = out is not None and out.__class__ is not int and out.dtype is f32
-    ot = f32 if out_f32 else bf
-    return _check(load().moe_dense_gemm(
-        _tensor(x, "x", bf, M * K), _tensor(w, "w", bf, n1 * K), lay, _tensor(bias, "bias", bf, n1),
-        _tensor(residual, "residual", ot, M * N), residual_scale, M, N, K, a, _tensor(out, "out", ot, M * N),
-        int(out_f32), _ctx(ctx)))
+        out_f32 = out is not None and out.__class__ is not int and out.dtype.itemsize == 4
+    c = ctx or Ctx()
+    return _check((_native or _load_native()).dense_gemm(x, w, lay, bias, residual, residual_scale, M, N, K, _act(activation),
+                                                        out, int(out_f32), c.address))
 
 
 def moe_dense_bias_grad(dz, M, N, d_bias, ctx=None):
     """d_bias [N] fp32 = the column sums of dz [M, N] bf16."""
-    return _check(load().moe_dense_bias_grad(_tensor(dz, "dz", _DTYPES["bf16"], M * N), M, N,
-                                             _tensor(d_bias, "d_bias", _DTYPES["f32"], N), _ctx(ctx)))
+    c = ctx or Ctx()
+    return _check((_native or _load_native()).dense_bias_grad(dz, M, N, d_bias, c.address))
 
 
 def moe_pair_sum(o, residual, T, k, K, y, ctx=None):
     """y [T, K] bf16 = the sums of o [T*k, K]'s rows of each token (+ residual [T, K])."""
-    bf = _DTYPES["bf16"]
-    return _check(load().moe_pair_sum(_tensor(o, "o", bf, T * k * K), _tensor(residual, "residual", bf, T * K), T, k, K,
-                                      _tensor(y, "y", bf, T * K), _ctx(ctx)))
+    c = ctx or Ctx()
+    return _check((_native or _load_native()).pair_sum(o, residual, T, k, K, y, c.address))
 
 
 def moe_debug_stall_tensor_kernels(stall_ns: int) -> None:

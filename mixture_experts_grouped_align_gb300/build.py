@@ -1,14 +1,16 @@
 """Builds the CUDA library libmoe_gb300.so in-tree for sm_103a with nvcc.
 
 Every translation unit is compiled in parallel to an object file, then linked into a
-shared library next to this file (``_lib/libmoe_gb300.so``).  Rebuilds only when a
-source or header is newer than the library.
+shared library next to this file (``_lib/libmoe_gb300.so``); the CPython marshalling of
+``csrc/binding.c`` becomes ``_lib/_binding.so`` (gcc, Python's headers).  Rebuilds only when a
+source or header is newer than the libraries.
 """
 import concurrent.futures as cf
 import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -16,6 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libmoe_gb300.so")
+BINDING_SRC = os.path.join(CSRC, "binding.c")
+BINDING = os.path.join(OUT_DIR, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
               "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]
@@ -33,10 +37,10 @@ def sources():
 
 
 def _stale():
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    deps = sources() + [BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
     deps += glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -58,14 +62,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout, r.stderr)
         return obj
 
+    def compile_binding():
+        tmp = BINDING + ".tmp"
+        cmd = ["gcc", "-O2", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"], "-I" + INCLUDE, BINDING_SRC,
+               "-o", tmp]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"gcc failed for {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+        return tmp
+
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, sources()))
+        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [cc] + ARCH + ["-shared", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    os.replace(binding, BINDING)
     return LIB
 
 
