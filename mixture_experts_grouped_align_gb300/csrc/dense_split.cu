@@ -14,10 +14,15 @@
 // The tensor core's accumulator loses up to one unit in the last place with every MMA, always
 // towards zero, which a bf16 output hides and an fp32 output does not (relative error 6e-8 for
 // every 64 of K, measured).  For fp32 outputs K is therefore also split over G accumulators in
-// TMEM of at most kGroupBlocks stages each, which are added in fp32 registers.
-//   warp 0 loads stages (64 of K: the weight tiles, BN rows of x) by TMA, as many stages as fit,
-//   from before the block's other roles are ready;
+// TMEM of at most kGroupBlocks blocks of 64 each, which are added in fp32 registers.
+//   warp 0 loads stages (64 or 128 of K: the weight tiles, BN rows of x) by TMA, as many stages as
+//   fit, from before the block's other roles are ready;
 //   warp 1 issues the MMAs; then all sixteen warps drain, add and store.
+//
+// Measured (weights from HBM, back to back): 64 x 2880 -> 2 x 2880 SwiGLU 8.8 us, the weight at
+// 3.8 TB/s; 64 x 7168 -> 2048 7.4 us, 4.0 TB/s; one row 2688 -> 1856 5.0 us; 4099 x 7168 -> 256 in
+// fp32 21.1 us.  Of the small ones about 3 us are the launch's start, the ring's first loads and
+// the cluster's sum, which a longer K hides no part of.
 #include <math.h>
 
 #include <atomic>
@@ -34,13 +39,14 @@ constexpr int kMaxStages = 12;
 constexpr int kAlone = 116 * 1024;  // more than half of an SM's shared memory
 constexpr int kRing = 208 * 1024;  // shared memory of the stages, at most
 
-constexpr int kGroupBlocks = 14;   // stages (64 of K) an accumulator takes for fp32 outputs
+constexpr int kGroupBlocks = 14;   // blocks of 64 of K an accumulator takes for fp32 outputs
 
 struct Split {
   int BN;        // rows of x per tile: 16, 32, 64, 128 or 256
   int NA;        // weight tiles (128 features) per tile
   int C;         // CTAs of a cluster: the shares of K
   int G;         // accumulators a share is split over
+  int sub;       // blocks of 64 of K in a stage
   int phase;     // rows of x that leave through shared memory at a time
   int stages;
   int slot;      // bytes of a stage
@@ -109,7 +115,7 @@ __device__ __forceinline__ void store4(const Dense& d, int64_t m, int64_t n, flo
   }
 }
 
-template <int NA, bool GATED>
+template <int NA, bool GATED, int SUB>
 __global__ void __launch_bounds__(kThreads, 1)
     dense_split_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w, Dense d,
                        Split sp) {
@@ -127,24 +133,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t wb = d.wait_ns > 0 ? (uint64_t)d.wait_ns : tc::kWaitNs;
   const uint32_t tile = blockIdx.x / (uint32_t)sp.C, mt = tile / (uint32_t)sp.n_tiles, nt = tile - mt * (uint32_t)sp.n_tiles;
   const int64_t n0 = (int64_t)nt * NA * kOut;  // the tile's first output feature
-  const int nk = (d.K + kBK - 1) / kBK;
+  const int nk = (d.K + SUB * kBK - 1) / (SUB * kBK);
   const int k0 = (int)((int64_t)nk * rank / sp.C), share = (int)((int64_t)nk * (rank + 1) / sp.C) - k0;
   const int kx = NA * kFeat * 128;  // x rows of a stage, behind the weight tiles
+  const int sub_bytes = kx + sp.BN * 128;
   auto load_stage = [&](int it, int s) {
-    const uint32_t sl = smem_s + s * sp.slot;
-    const int kb = k0 + it;
-    tma::mbar_arrive_expect_tx(&full[s], (uint32_t)(kx + sp.BN * 128));
+    tma::mbar_arrive_expect_tx(&full[s], (uint32_t)(SUB * sub_bytes));
 #pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      const uint32_t w = sl + a * kFeat * 128;
-      if (GATED) {
-        load_w(w, &tm_w, kn, n0 + a * kOut, kOut, kb, &full[s]);
-        load_w(w + kOut * 128, &tm_w, kn, d.N + n0 + a * kOut, kOut, kb, &full[s]);
-      } else {
-        load_w(w, &tm_w, kn, n0 + a * kOut, kOut, kb, &full[s]);
+    for (int sub = 0; sub < SUB; ++sub) {  // past K: zeros
+      const uint32_t sl = smem_s + s * sp.slot + sub * sub_bytes;
+      const int kb = (k0 + it) * SUB + sub;
+#pragma unroll
+      for (int a = 0; a < NA; ++a) {
+        const uint32_t w = sl + a * kFeat * 128;
+        if (GATED) {
+          load_w(w, &tm_w, kn, n0 + a * kOut, kOut, kb, &full[s]);
+          load_w(w + kOut * 128, &tm_w, kn, d.N + n0 + a * kOut, kOut, kb, &full[s]);
+        } else {
+          load_w(w, &tm_w, kn, n0 + a * kOut, kOut, kb, &full[s]);
+        }
       }
+      tma::load_2d(sl + kx, &tm_x, kb * 128, (int32_t)(mt * sp.BN), &full[s]);
     }
-    tma::load_2d(sl + kx, &tm_x, kb * 128, (int32_t)(mt * sp.BN), &full[s]);
   };
   // two stages are under way before the block's other warps are ready
   const int first = share < 2 ? share : (sp.stages < 2 ? sp.stages : 2);
@@ -201,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every lane, so they stay in uniform registers and a stage's issue takes few instructions.
     const bool leader = elect_one();
     const uint32_t idesc = tc::idesc_f16(kFeat, sp.BN, 1) | (kn ? 1u << 15 : 0u);
-    const uint32_t wstep = w_step(kn), slot16 = (uint32_t)sp.slot / 16;
+    const uint32_t wstep = w_step(kn), slot16 = (uint32_t)sp.slot / 16, sub16 = (uint32_t)sub_bytes / 16;
     const uint64_t w0 = w_desc(smem_s, kn, 0), x0 = tc::sdesc_sw128(smem_s + kx);
     // accumulator group g takes the stages up to (g + 1) share / G
     int s = 0, g = 0, last_of_g = share / sp.G;
@@ -222,10 +232,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::tc_fence_after();
       if (leader) {
 #pragma unroll
-        for (int a = 0; a < NA; ++a)
+        for (int sub = 0; sub < SUB; ++sub)
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j)
-            tc::mma_f16_ss(d_tmem + a * sp.BN, wd + a * (kFeat * 128 / 16) + j * wstep, xd + j * kXStep, idesc, j > 0 || !fresh);
+          for (int a = 0; a < NA; ++a)
+#pragma unroll
+            for (int j = 0; j < kBK / 16; ++j)
+              tc::mma_f16_ss(d_tmem + a * sp.BN, wd + sub * sub16 + a * (kFeat * 128 / 16) + j * wstep, xd + sub * sub16 + j * kXStep,
+                             idesc, sub > 0 || j > 0 || !fresh);
         tc::mma_commit(&empty[s]);
       }
       __syncwarp();
@@ -354,9 +367,9 @@ int resident_ctas(int C) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int clusters = 0;
-    if (cudaFuncSetAttribute(dense_split_kernel<1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024) !=
+    if (cudaFuncSetAttribute(dense_split_kernel<1, false, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024) !=
             cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&clusters, dense_split_kernel<1, false>, &cfg) != cudaSuccess || clusters < 1) {
+        cudaOccupancyMaxActiveClusters(&clusters, dense_split_kernel<1, false, 1>, &cfg) != cudaSuccess || clusters < 1) {
       (void)cudaGetLastError();
       clusters = 1;
     }
@@ -374,7 +387,6 @@ int resident_ctas(int C) {
 // 128-row tiles whole in K, 18.2 as 2 x 128 split in two, 20.7 on CTA pairs; 2000 x 2048 x 2048:
 // 18.2 us here, 16.7 on CTA pairs).
 Split plan(const Dense& d, double* clocks) {
-  const uint32_t nk = (uint32_t)(d.K + kBK - 1) / kBK;
   const int kOut = d.gated ? kFeat / 2 : kFeat;
   Split best{};
   double least = 0;
@@ -385,9 +397,14 @@ Split plan(const Dense& d, double* clocks) {
       s.BN = BN;
       s.n_tiles = (d.N + NA * kOut - 1) / (NA * kOut);
       s.m_tiles = (d.M + BN - 1) / BN;
+      // small tiles' MMAs take less than a stage's handshake (about 190 clocks), so two blocks of
+      // 64 share one (64 x 7168 x 2048: 8.1 -> 7.5 us); large tiles need the ring's finer slots
+      // (4099 x 256 x 7168: 21.2 us so, 22.5 with two)
+      s.sub = BN <= 64 ? 2 : 1;
+      const uint32_t nk = (uint32_t)(d.K + s.sub * kBK - 1) / (uint32_t)(s.sub * kBK);
       const int64_t tiles = s.n_tiles * s.m_tiles;
       if (tiles < (1 << 27)) {
-        const double load = (NA * kFeat + BN) * (128 / 60.0), mma = BN * 2.0 * NA, stage = mma > load ? mma : load;
+        const double load = s.sub * (NA * kFeat + BN) * (128 / 60.0), mma = s.sub * BN * 2.0 * NA, stage = mma > load ? mma : load;
         for (uint32_t C = 1; C <= 8 && C <= nk; ++C) {
           const uint32_t at_once = (uint32_t)resident_ctas((int)C);
           // more shares than fill a wave only shorten fp32 sums
@@ -395,7 +412,7 @@ Split plan(const Dense& d, double* clocks) {
           const uint32_t share = (nk + C - 1) / C, waves = ((uint32_t)tiles * C + at_once - 1) / at_once;
           uint32_t G = 1;
           if (d.out_f32) {
-            G = (share + kGroupBlocks - 1) / kGroupBlocks;
+            G = (share * s.sub + kGroupBlocks - 1) / kGroupBlocks;
             if (G > (uint32_t)(512 / (NA * BN))) continue;  // too long a sum in one accumulator
           }
           // each wave: its stages, about 3000 clocks to start, the drain and the cluster's sum
@@ -415,8 +432,8 @@ Split plan(const Dense& d, double* clocks) {
     *clocks = INFINITY;
     return best;
   }
-  const int share = (int)((nk + best.C - 1) / best.C);
-  best.slot = (best.NA * kFeat + best.BN) * 128;
+  const int nk = (d.K + best.sub * kBK - 1) / (best.sub * kBK), share = (nk + best.C - 1) / best.C;
+  best.slot = best.sub * (best.NA * kFeat + best.BN) * 128;
   best.stages = kRing / best.slot;
   if (best.stages > kMaxStages) best.stages = kMaxStages;
   if (best.stages > share) best.stages = share;
@@ -433,7 +450,7 @@ Split plan(const Dense& d, double* clocks) {
   return best;
 }
 
-template <int NA, bool GATED>
+template <int NA, bool GATED, int SUB>
 cudaError_t launch(const Dense& d, const Split& s, cudaStream_t stream) {
   const uint64_t K2 = (uint64_t)d.K * 2, N1 = GATED ? 2 * (uint64_t)d.N : (uint64_t)d.N;
   CUtensorMap mx{}, mw{};
@@ -441,7 +458,7 @@ cudaError_t launch(const Dense& d, const Split& s, cudaStream_t stream) {
   const bool okw = d.w_kn ? tma::encode_2d_u8(&mw, d.w, N1 * 2, (uint64_t)d.K, N1 * 2, 128, kBK, true)
                           : tma::encode_2d_u8(&mw, d.w, K2, N1, K2, 128, GATED ? kFeat / 2 : kFeat, true);
   if (!okw) return cudaErrorInvalidValue;
-  auto kern = dense_split_kernel<NA, GATED>;
+  auto kern = dense_split_kernel<NA, GATED, SUB>;
   static std::atomic<uint64_t> sized{0};
   cudaError_t err = moe_launch::allow_smem(reinterpret_cast<const void*>(kern), kRing + 1024, sized);
   if (err != cudaSuccess) return err;
@@ -460,8 +477,11 @@ bool dense_split(const Dense& d, cudaStream_t stream, cudaError_t* err) {
   const int64_t pairs = sm_count_current() / 2, nk = (d.K + kBK - 1) / kBK;
   const int64_t tiles = ((d.M + 255) / 256) * ((d.N + (d.gated ? 127 : 255)) / (d.gated ? 128 : 256));
   if (split >= (double)((tiles + pairs - 1) / pairs) * nk * 512 + 7000) return false;
-  if (d.gated) *err = s.NA == 2 ? launch<2, true>(d, s, stream) : launch<1, true>(d, s, stream);
-  else *err = s.NA == 2 ? launch<2, false>(d, s, stream) : launch<1, false>(d, s, stream);
+  const int which = (d.gated ? 4 : 0) + (s.NA == 2 ? 2 : 0) + (s.sub == 2 ? 1 : 0);
+  using Launch = cudaError_t (*)(const Dense&, const Split&, cudaStream_t);
+  static const Launch launches[8] = {launch<1, false, 1>, launch<1, false, 2>, launch<2, false, 1>, launch<2, false, 2>,
+                                     launch<1, true, 1>,  launch<1, true, 2>,  launch<2, true, 1>,  launch<2, true, 2>};
+  *err = launches[which](d, s, stream);
   return true;
 }
 
