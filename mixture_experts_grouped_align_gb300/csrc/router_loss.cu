@@ -13,14 +13,18 @@
 //
 // The counts f are no function of the logits' values, so one pass over the logits gives both
 // the sums of p and the gradient: T E floats read once and written once, which is the floor.
-// Two launches: the counts (T k ids), then the pass; a small batch is one launch of one cluster,
-// which counts for itself.
+// Two launches: the counts (T k ids), then the pass (above 512 experts a third for the column
+// sums); a small batch is one launch of one cluster, which counts for itself.
 //
 // The pass gives a row to LANES lanes (4 to 32, NV vectors of four values each) and keeps it in
 // registers from the load to the store.
 // Every lane keeps the column sums of its own columns over its rows; blocks add theirs in a
 // fixed order into one row of partial sums each, and the last block to finish adds those rows
 // in order, so that repeated calls give the same bits (no floating-point atomics).
+//
+// Measured: 61440 x 128, k 4: 20.5 us for 62.9 MB of rows (3.1 TB/s); 8192 x 256, k 8: 13.6 us; 64 x 128:
+// 5.5 us.  Bound, in that order, by the counts before the pass and its instructions, by the chain
+// counts - rows - column sums, and by one launch with two rounds of loads.
 #include "moe_common.cuh"
 #include "moe_launch.h"
 #include "tcgen05.cuh"
@@ -33,14 +37,16 @@ constexpr int kCountThreads = 512;
 constexpr int kMaxCountBlocks = 64;
 constexpr int kMaxPassBlocks = 256;       // one block per SM
 constexpr int kClusterBlocks = 8;
+constexpr int kFinishThreads = 256;       // >= the pass's blocks and the vectors of a block's columns
 constexpr unsigned kAll = 0xffffffffu;
 
-// Workspace: ticket (256 bytes) | counts of the count blocks [kMaxCountBlocks][E + 1] (the last
-// word: its real tokens) | column sums of the pass's blocks [kMaxPassBlocks][part_pitch(E)] | their
-// sums of lse^2 [kMaxPassBlocks].
+// Workspace: ticket (256 bytes) | the choices' counts [E], then the real tokens | counts of the
+// count blocks [kMaxCountBlocks][E + 1] (the last word: its real tokens) | column sums of the
+// pass's blocks [kMaxPassBlocks][part_pitch(E)] | their sums of lse^2 [kMaxPassBlocks].
 __host__ __device__ inline int part_pitch(int E) { return (E + 3) / 4 * 4; }
 struct Ws {
   unsigned* ticket;
+  int* total;
   int* counts;
   float* part;
 };
@@ -48,8 +54,9 @@ __host__ __device__ inline Ws carve(void* ws, int E) {
   uint8_t* p = static_cast<uint8_t*>(ws);
   Ws w;
   w.ticket = reinterpret_cast<unsigned*>(p);
-  w.counts = reinterpret_cast<int*>(p + 256);
-  w.part = reinterpret_cast<float*>(p + 256 + ((size_t)kMaxCountBlocks * (E + 1) * 4 + 255) / 256 * 256);
+  w.total = reinterpret_cast<int*>(p + 256);
+  w.counts = w.total + E + 1;
+  w.part = reinterpret_cast<float*>(p + 256 + ((size_t)(kMaxCountBlocks + 1) * (E + 1) * 4 + 255) / 256 * 256);
   return w;
 }
 
@@ -283,9 +290,25 @@ MOE_DEV float ld_cluster_f32(const float* p, uint32_t rank) {
   return v;
 }
 
+// g_e = f_e - 1 of expert e's count c among n real tokens' k choices, the numerator from integers.
+MOE_DEV float g_of(int E, int k, int n, int c) {
+  const int64_t nk = (int64_t)n * k;
+  return n > 0 ? (float)((int64_t)E * c - nk) / (float)nk : 0.f;
+}
+
+MOE_DEV void store_loss(const RouterLoss& a, float bal, float zs) {
+  // a part whose coefficient is 0 is off, also where its value is infinite
+  a.loss[0] = (a.balance_coef != 0.f ? a.balance_coef * bal : 0.f) + (a.z_coef != 0.f ? a.z_coef * zs : 0.f);
+  a.loss[1] = bal;
+  a.loss[2] = zs;
+}
+
 // CLUSTER: the grid is one cluster, whose blocks count a share of the choices each and exchange
 // counts and column sums through distributed shared memory.  Otherwise the counts come from
-// router_count_kernel, and the last block to finish adds the blocks' column sums.
+// router_count_kernel, and the last block to finish adds the blocks' column sums.  Above 512
+// experts that is router_finish_kernel's: one SM alone would read up to 152 rows of 4 KB (7000
+// tokens of 1001 experts: 33 us so, 26 with a cluster of its own; 8192 of 256: 13.6 and 13.5, 20000
+// of 64: 11.3 and 12.1).
 // Shared memory: g [kCols] | this block's counts, later its column sums [kCols] | at the end the
 // column sums of its warps [kWarps][kCols], or four of other blocks a thread.
 template <int LANES, int NV, bool VEC, bool WHOLE, bool CLUSTER>
@@ -294,6 +317,7 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
   constexpr int kGroups = 32 / LANES;       // rows of a warp
   constexpr int kCols = 4 * NV * LANES;     // columns the lanes can hold, >= E
   constexpr int kWide = kCols < 32 ? 32 : (kCols < 256 ? kCols : 256);  // threads across columns
+  constexpr bool kFinish = !CLUSTER && NV > 4;  // router_finish_kernel follows
   extern __shared__ float sm[];
   __shared__ int n_sh;
   __shared__ unsigned last;
@@ -343,9 +367,11 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
     count_tokens<kThreads>(a, t0, t1, hist, &n_sh);
     if (gridDim.x > 1) tc::cluster_sync();
     int n = 0;
+#pragma unroll 1
     for (uint32_t r = 0; r < gridDim.x; ++r) n += ld_cluster_s32(&n_sh, r);
     for (int e = tid; e < E; e += kThreads) {
       int s = 0;
+#pragma unroll 1
       for (uint32_t r = 0; r < gridDim.x; ++r) s += ld_cluster_s32(hist + e, r);
       cs[e] = s;
     }
@@ -388,9 +414,14 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
     float g = 0.f;
     if (e < E) {
       const int c = cs[e];
-      if (blockIdx.x == 0 && a.counts) a.counts[e] = c;
-      const int64_t nk = (int64_t)n * k;
-      if (n > 0) g = (float)((int64_t)E * c - nk) / (float)nk;  // the numerator from integers
+      if (blockIdx.x == 0) {
+        if (a.counts) a.counts[e] = c;
+        if (kFinish) {
+          ws.total[e] = c;
+          if (e == 0) ws.total[E] = n;
+        }
+      }
+      g = g_of(E, k, n, c);
     }
     gs[e] = g;  // the same word cs[e] was read from, by the same thread
   }
@@ -511,16 +542,21 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
     if (blockIdx.x == 0) {
       for (int e = tid; e < E; e += kThreads) {
         float s = 0.f;
+#pragma unroll 1
         for (uint32_t r = 0; r < gridDim.x; ++r) s += ld_cluster_f32(mine + e, r);
         s *= inv_n;
         if (a.prob_mean) a.prob_mean[e] = s;
         bal += (gs[e] + 1.f) * s;
       }
+#pragma unroll 1
       for (uint32_t r = 0; r < gridDim.x; ++r) zs += ld_cluster_f32(&z_sh, r);
       zs *= inv_n;
     }
     if (gridDim.x > 1) tc::cluster_sync();  // no block leaves before its sums are read
     if (blockIdx.x != 0) return;
+  } else if (kFinish) {
+    if (tid == 0) zpart[blockIdx.x] = z;
+    return;
   } else {
     if (tid == 0) zpart[blockIdx.x] = z;
     __threadfence();
@@ -565,12 +601,74 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
     }
   }
   bal = block_sum<kThreads>(bal, red);
-  if (tid == 0) {
-    // a part whose coefficient is 0 is off, also where its value is infinite
-    a.loss[0] = (a.balance_coef != 0.f ? a.balance_coef * bal : 0.f) + (a.z_coef != 0.f ? a.z_coef * zs : 0.f);
-    a.loss[1] = bal;
-    a.loss[2] = zs;
+  if (tid == 0) store_loss(a, bal, zs);
+}
+
+// The column sums of the pass's blocks, added in order, and the losses from them.  One cluster whose
+// blocks own a range of columns each, four of them a thread, the other threads sharing the rows.
+__global__ void __launch_bounds__(kFinishThreads) router_finish_kernel(RouterLoss a, int rows) {
+  constexpr int kBatch = 8;
+  __shared__ float4 sums[kFinishThreads];
+  __shared__ float red[kFinishThreads / 32];
+  __shared__ float bal_sh;
+  moe::wait_for_stream();
+  moe::let_next_start();
+  const int E = a.E, pitch = part_pitch(E), tid = threadIdx.x;
+  const Ws ws = carve(a.ws, E);
+  const int per = (pitch / 4 + gridDim.x - 1) / gridDim.x;  // vectors of four columns of this block
+  const int across = kFinishThreads / per, c = (blockIdx.x * per + tid % per) * 4, r0 = tid / per;
+  const int n = ws.total[E];
+  const float inv_n = n > 0 ? 1.f / (float)n : 0.f;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < pitch && r0 < across)
+    for (int b0 = r0; b0 < rows; b0 += across * kBatch) {
+      float4 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int b = b0 + i * across;
+        v[i] = b < rows ? __ldcg(reinterpret_cast<const float4*>(ws.part + (size_t)b * pitch + c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        s.x += v[i].x;
+        s.y += v[i].y;
+        s.z += v[i].z;
+        s.w += v[i].w;
+      }
+    }
+  const float z = blockIdx.x == 0 && tid < rows ? __ldcg(ws.part + (size_t)kMaxPassBlocks * pitch + tid) : 0.f;
+  int cnt[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) cnt[i] = tid < per && c + i < E ? ws.total[c + i] : 0;
+  sums[tid] = s;
+  __syncthreads();
+  float bal = 0.f;
+  if (tid < per && c < pitch) {
+#pragma unroll 8
+    for (int r = 1; r < across; ++r) {
+      const float4 v = sums[r * per + tid];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    const float p[4] = {s.x * inv_n, s.y * inv_n, s.z * inv_n, s.w * inv_n};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < E) {
+        if (a.prob_mean) a.prob_mean[c + i] = p[i];
+        bal += (g_of(E, a.k, n, cnt[i]) + 1.f) * p[i];
+      }
   }
+  bal = block_sum<kFinishThreads>(bal, red);
+  const float zs = block_sum<kFinishThreads>(z, red) * inv_n;
+  if (tid == 0) bal_sh = bal;
+  if (gridDim.x > 1) tc::cluster_sync();
+  if (blockIdx.x == 0 && tid == 0) {
+    for (uint32_t r = 1; r < gridDim.x; ++r) bal += ld_cluster_f32(&bal_sh, r);
+    store_loss(a, bal, zs);
+  }
+  if (gridDim.x > 1) tc::cluster_sync();
 }
 
 template <int LANES, int NV, bool VEC, bool WHOLE>
@@ -600,7 +698,11 @@ cudaError_t launch_pass(RouterLoss a, cudaStream_t stream) {
   int64_t cap = moe_launch::sm_count_current();
   if (cap > kMaxPassBlocks) cap = kMaxPassBlocks;
   // the pass's first loads run under the counts, which it then waits for
-  return moe_launch::launch_staged(kern, dim3((unsigned)(turns < cap ? turns : cap)), dim3(kThreads), kSmem, stream, 1, a);
+  const unsigned pass = (unsigned)(turns < cap ? turns : cap);
+  const cudaError_t passed = moe_launch::launch_staged(kern, dim3(pass), dim3(kThreads), kSmem, stream, 1, a);
+  if (NV <= 4 || passed != cudaSuccess) return passed;
+  return moe_launch::launch_staged(router_finish_kernel, dim3(kClusterBlocks), dim3(kFinishThreads), 0, stream, kClusterBlocks, a,
+                                   (int)pass);
 }
 
 template <int LANES, int NV>
@@ -628,7 +730,7 @@ cudaError_t launch(const RouterLoss& a, cudaStream_t s) {
 namespace moe_launch {
 
 size_t router_loss_workspace_bytes(int E) {
-  return 512 + (size_t)kMaxCountBlocks * (E + 1) * 4 + (size_t)kMaxPassBlocks * (part_pitch(E) + 1) * 4;
+  return 512 + (size_t)(kMaxCountBlocks + 1) * (E + 1) * 4 + (size_t)kMaxPassBlocks * (part_pitch(E) + 1) * 4;
 }
 
 cudaError_t router_loss(const RouterLoss& a, cudaStream_t stream) {

@@ -237,3 +237,16 @@ def test_more_choices_than_lanes(moe, E, k):
     x, ids, w, dw = make(900, E, k, 17)
     ids[3, 0] = ids[3, 1]
     check(call(moe, x, ids, w, dw), x, ids, w, dw, None)
+
+
+@pytest.mark.parametrize("T,E,k", [(2000, 513, 4), (4001, 1001, 6), (3000, 1024, 8)])
+def test_many_experts_and_tokens(moe, T, E, k):
+    """Wide rows over every SM, with masked tokens: the losses come from a launch of their own."""
+    x, ids, w, dw = make(T, E, k, 18)
+    mask = (np.random.default_rng(19).random(T) < 0.8).astype(np.uint8)
+    got = call(moe, x, ids, w, dw, mask)
+    check(got, x, ids, w, dw, mask)
+    again = call(moe, x, ids, w, dw, mask)
+    assert all(np.array_equal(a, b) for a, b in zip(got[:4], again[:4]))
+    got = call(moe, x, ids, w, dw, np.zeros(T, np.uint8))
+    assert not got[0].any() and not got[1].any() and not got[2].any() and not got[3].any()
