@@ -22,9 +22,10 @@
 // fixed order into one row of partial sums each, and the last block to finish adds those rows
 // in order, so that repeated calls give the same bits (no floating-point atomics).
 //
-// Measured: 61440 x 128, k 4: 20.5 us for 62.9 MB of rows (3.1 TB/s); 8192 x 256, k 8: 13.6 us; 64 x 128:
-// 5.5 us.  Bound, in that order, by the counts before the pass and its instructions, by the chain
-// counts - rows - column sums, and by one launch with two rounds of loads.
+// Measured: 61440 x 128, k 4: 19.6 us for 62.9 MB of rows (3.2 TB/s); 8192 x 256, k 8: 12.7 us; 30000 x
+// 1024, k 8: 53 us (4.6 TB/s); 64 x 128: 5.5 us.  Bound, in that order, by the counts before the pass and the sums behind it (about 6
+// and 4 us; the rows between them run at 6.6 TB/s), by that chain alone, by the rows, and by one
+// launch with two rounds of loads.
 #include "moe_common.cuh"
 #include "moe_launch.h"
 #include "tcgen05.cuh"
@@ -41,9 +42,10 @@ constexpr int kFinishThreads = 256;       // >= the pass's blocks and the vector
 constexpr unsigned kAll = 0xffffffffu;
 
 // Workspace: ticket (256 bytes) | the choices' counts [E], then the real tokens | counts of the
-// count blocks [kMaxCountBlocks][E + 1] (the last word: its real tokens) | column sums of the
+// count blocks [kMaxCountBlocks][count_pitch(E)] (their word E: its real tokens) | column sums of the
 // pass's blocks [kMaxPassBlocks][part_pitch(E)] | their sums of lse^2 [kMaxPassBlocks].
 __host__ __device__ inline int part_pitch(int E) { return (E + 3) / 4 * 4; }
+__host__ __device__ inline int count_pitch(int E) { return (E + 4) / 4 * 4; }
 struct Ws {
   unsigned* ticket;
   int* total;
@@ -55,8 +57,8 @@ __host__ __device__ inline Ws carve(void* ws, int E) {
   Ws w;
   w.ticket = reinterpret_cast<unsigned*>(p);
   w.total = reinterpret_cast<int*>(p + 256);
-  w.counts = w.total + E + 1;
-  w.part = reinterpret_cast<float*>(p + 256 + ((size_t)(kMaxCountBlocks + 1) * (E + 1) * 4 + 255) / 256 * 256);
+  w.counts = w.total + count_pitch(E);
+  w.part = reinterpret_cast<float*>(p + 256 + ((size_t)(kMaxCountBlocks + 1) * count_pitch(E) * 4 + 255) / 256 * 256);
   return w;
 }
 
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kCountThreads) router_count_kernel(RouterLoss 
   const int64_t t0 = blockIdx.x * per_block;
   const int64_t t1 = t0 + per_block < a.T ? t0 + per_block : a.T;
   count_tokens<kCountThreads>(a, t0, t1 > t0 ? t1 : t0, sm_count, &n_real);
-  int* out = w.counts + (size_t)blockIdx.x * (a.E + 1);
+  int* out = w.counts + (size_t)blockIdx.x * count_pitch(a.E);
   for (int e = threadIdx.x; e < a.E; e += kCountThreads) out[e] = sm_count[e];
   if (threadIdx.x == 0) {
     out[a.E] = n_real;
@@ -307,8 +309,7 @@ MOE_DEV void store_loss(const RouterLoss& a, float bal, float zs) {
 // counts and column sums through distributed shared memory.  Otherwise the counts come from
 // router_count_kernel, and the last block to finish adds the blocks' column sums.  Above 512
 // experts that is router_finish_kernel's: one SM alone would read up to 152 rows of 4 KB (7000
-// tokens of 1001 experts: 33 us so, 26 with a cluster of its own; 8192 of 256: 13.6 and 13.5, 20000
-// of 64: 11.3 and 12.1).
+// tokens of 1001 experts: 33 us so, 26 with a cluster of its own; 20000 of 64: 11.3 and 12.1).
 // Shared memory: g [kCols] | this block's counts, later its column sums [kCols] | at the end the
 // column sums of its warps [kWarps][kCols], or four of other blocks a thread.
 template <int LANES, int NV, bool VEC, bool WHOLE, bool CLUSTER>
@@ -316,12 +317,11 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
   constexpr int kThreads = pass_threads(NV), kWarps = kThreads / 32;
   constexpr int kGroups = 32 / LANES;       // rows of a warp
   constexpr int kCols = 4 * NV * LANES;     // columns the lanes can hold, >= E
-  constexpr int kWide = kCols < 32 ? 32 : (kCols < 256 ? kCols : 256);  // threads across columns
   constexpr bool kFinish = !CLUSTER && NV > 4;  // router_finish_kernel follows
   extern __shared__ float sm[];
   __shared__ int n_sh;
   __shared__ unsigned last;
-  __shared__ float red[kThreads];
+  __shared__ float red[kWarps];
   __shared__ float z_sh;
   const int E = a.E, k = a.k;
   float* gs = sm;
@@ -382,30 +382,43 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
   } else {
     moe::wait_for_stream();
     moe::let_next_start();
-    // kThreads / kWide threads share a column's count blocks
-    int* redi = reinterpret_cast<int*>(red);
+    // four columns a thread, kShare threads sharing a column's count blocks, all loads in flight
+    constexpr int kAcross = kCols / 4, kShare = kThreads / kAcross < 16 ? kThreads / kAcross : 16, kBatch = 8;
     if (warp == 0) {
       int c = 0;
-      for (int b = lane; b < a.count_blocks; b += 32) c += __ldcg(ws.counts + (size_t)b * (E + 1) + E);
+      for (int b = lane; b < a.count_blocks; b += 32) c += __ldcg(ws.counts + (size_t)b * count_pitch(E) + E);
       c = __reduce_add_sync(kAll, c);
       if (lane == 0) n_sh = c;
     }
-    for (int e0 = 0; e0 < E; e0 += kWide) {
-      const int e = e0 + tid % kWide;
-      int s = 0;
-      if (e < E) {
-#pragma unroll 8
-        for (int b = tid / kWide; b < a.count_blocks; b += kThreads / kWide) s += __ldcg(ws.counts + (size_t)b * (E + 1) + e);
-      }
-      redi[tid] = s;
-      __syncthreads();
-      if (tid < kWide && e < E) {
+    const int c = (tid % kAcross) * 4, r0 = tid / kAcross;
+    int4 s = make_int4(0, 0, 0, 0);
+    if (c < E && r0 < kShare)
+      for (int b0 = r0; b0 < a.count_blocks; b0 += kShare * kBatch) {
+        int4 v[kBatch];
 #pragma unroll
-        for (int i = 1; i < kThreads / kWide; ++i) s += redi[i * kWide + tid];
-        cs[e] = s;
+        for (int i = 0; i < kBatch; ++i) {
+          const int b = b0 + i * kShare;
+          v[i] = b < a.count_blocks ? __ldcg(reinterpret_cast<const int4*>(ws.counts + (size_t)b * count_pitch(E) + c))
+                                    : make_int4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          s.x += v[i].x;
+          s.y += v[i].y;
+          s.z += v[i].z;
+          s.w += v[i].w;
+        }
       }
-      __syncthreads();
+    int* shares = reinterpret_cast<int*>(sums);
+    if (r0 < kShare) *reinterpret_cast<int4*>(shares + r0 * kCols + c) = s;
+    __syncthreads();
+    for (int e = tid; e < E; e += kThreads) {
+      int s = 0;
+#pragma unroll
+      for (int i = 0; i < kShare; ++i) s += shares[i * kCols + e];
+      cs[e] = s;
     }
+    __syncthreads();
   }
   const int n = n_sh;
   const float inv_n = n > 0 ? 1.f / (float)n : 0.f;
@@ -567,10 +580,10 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
     __threadfence();
     // the last block: four columns a thread, kRowsAt threads sharing a column's blocks, eight
     // blocks in flight
-    constexpr int kAcross = kCols / 4, kRowsAt = kThreads / kAcross, kBatch = 8;
+    constexpr int kAcross = kCols / 4, kRowsAt = kThreads / kAcross < 32 ? kThreads / kAcross : 32, kBatch = 8;
     const int c = (tid % kAcross) * 4, r0 = tid / kAcross;
     float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < E)
+    if (c < E && r0 < kRowsAt)
       for (unsigned b0 = r0; b0 < gridDim.x; b0 += kRowsAt * kBatch) {
         float4 v[kBatch];
 #pragma unroll
@@ -589,7 +602,7 @@ __global__ void __launch_bounds__(pass_threads(NV), 1) router_pass_kernel(Router
       }
     zs = tid < gridDim.x ? __ldcg(zpart + tid) : 0.f;
     zs = block_sum<kThreads>(zs, red) * inv_n;
-    *reinterpret_cast<float4*>(sums + (size_t)r0 * kCols + c) = s4;
+    if (r0 < kRowsAt) *reinterpret_cast<float4*>(sums + (size_t)r0 * kCols + c) = s4;
     __syncthreads();
     for (int e = tid; e < E; e += kThreads) {
       float s = 0.f;
@@ -730,7 +743,7 @@ cudaError_t launch(const RouterLoss& a, cudaStream_t s) {
 namespace moe_launch {
 
 size_t router_loss_workspace_bytes(int E) {
-  return 512 + (size_t)(kMaxCountBlocks + 1) * (E + 1) * 4 + (size_t)kMaxPassBlocks * (part_pitch(E) + 1) * 4;
+  return 512 + (size_t)(kMaxCountBlocks + 1) * count_pitch(E) * 4 + (size_t)kMaxPassBlocks * (part_pitch(E) + 1) * 4;
 }
 
 cudaError_t router_loss(const RouterLoss& a, cudaStream_t stream) {
