@@ -13,12 +13,13 @@
 // backward reads 33/32 N1 + 2 I and writes 2 N1 + 2 I (N1 = 2I or I), and nothing is read
 // twice.  A thread owns eight consecutive columns (16 bytes of bf16, 8 of codes), so the four
 // lanes of a quad own one 32-value block of each half: its maximum takes two shuffles.  A
-// row's columns belong to one warp (LANES < 32 lanes of it for narrow rows), or with few rows
+// row's columns belong to one warp (LANES < 32 lanes of it for narrow rows), or with few values
 // to one block, and d w is a shuffle reduction over them in a fixed order.
 //
 // Measured: 65536 x 2048 SwiGLU 161 us forward and 197 us backward (6.7 and 6.9 TB/s, HBM's copy
 // rate); 12345 x 1856 relu^2 19.8 and 26.1 us (5.8 and 6.2 TB/s, a launch's start and end being a
-// tenth of it); 168 x 928 SwiGLU 1.8 us each, a launch.
+// tenth of it); 100000 x 352 SwiGLU 49.6 and 57 us (5.7 and 6.2 TB/s); 168 x 928 SwiGLU 1.8 us each, a
+// launch.
 #include <cuda_fp8.h>
 
 #include "moe_common.cuh"
@@ -100,9 +101,9 @@ MOE_DEV float sigmoid(float g) {
 }
 
 // The rows of a block: WIDE = the whole block on one row, otherwise 32 / LANES rows a warp.
-// A warp on a row of its own takes kTurns turns of 256 columns at a time, all loads first: that
-// many bytes in flight are what the stream needs, and the 32 scale bytes of the turns are one
-// sector, moved by one byte per lane.
+// A row's lanes take kTurns turns of 8 LANES columns at a time, all loads first: that many bytes in
+// flight are what the stream needs, and the turns' scale bytes lie together, moved by one byte per
+// lane.
 template <int LANES, bool WIDE, int TURNS>
 struct Map {
   static constexpr int kRowsPerBlock = WIDE ? 1 : kWarps * (32 / LANES);
@@ -166,12 +167,13 @@ __global__ void __launch_bounds__(kThreads, TURNS > 1 ? 3 : 4) act_checkpoint_ke
       packed[0] |= sg << (8 * t);
       if (GATED) packed[kH - 1] |= su << (8 * t);
     }
-    if (kT > 1) {  // lane 8 t + q stores the scale of turn t's quad q
-      const int b = c0 / 4 + lane;
+    if (kT > 1) {  // lane kQ t + q of a row stores the scale of turn t's quad q
+      constexpr int kQ = LANES / 4;
+      const int sub = lane % LANES, b = c0 / 4 + sub;
 #pragma unroll
       for (int p = 0; p < kH; ++p) {
-        const uint32_t v = __shfl_sync(kAll, packed[p], (lane & 7) * 4);
-        if (in && lane < 8 * kT && b * 4 < units) scales[p * (units / 4) + b] = (uint8_t)(v >> (8 * (lane >> 3)));
+        const uint32_t v = __shfl_sync(kAll, packed[p], (sub % kQ) * 4, LANES);
+        if (in && sub < kQ * kT && b * 4 < units) scales[p * (units / 4) + b] = (uint8_t)(v >> (8 * (sub / kQ)));
       }
     }
   }
@@ -211,13 +213,14 @@ __global__ void __launch_bounds__(kThreads, TURNS > 1 ? 3 : 4) act_backward_kern
         if (kT == 1) rs[t][p] = live ? scales[(p * units + c) >> 2] : 0;
       }
     }
-    if (kT > 1) {  // lane 8 t + q holds the scale of turn t's quad q
-      const int b = c0 / 4 + lane;
+    if (kT > 1) {  // lane kQ t + q of a row holds the scale of turn t's quad q
+      constexpr int kQ = LANES / 4;
+      const int sub = lane % LANES, b = c0 / 4 + sub;
 #pragma unroll
       for (int p = 0; p < kH; ++p) {
-        turns[p] = read && lane < 8 * kT && b * 4 < units ? scales[p * (units / 4) + b] : 0;
+        turns[p] = read && sub < kQ * kT && b * 4 < units ? scales[p * (units / 4) + b] : 0;
 #pragma unroll
-        for (int t = 0; t < kT; ++t) rs[t][p] = __shfl_sync(kAll, turns[p], 8 * t + (lane >> 2));
+        for (int t = 0; t < kT; ++t) rs[t][p] = __shfl_sync(kAll, turns[p], kQ * t + (sub >> 2), LANES);
       }
     }
 #pragma unroll
@@ -265,11 +268,7 @@ __global__ void __launch_bounds__(kThreads, TURNS > 1 ? 3 : 4) act_backward_kern
   }
 }
 
-// A block per row while the rows are few (a warp per row would leave SMs empty: 1500 rows of
-// I = 2048, forward 7.1 us as blocks and 9.7 as warps; 20000 rows, 71 and 60 us), otherwise 32,
-// 16, 8 or 4 lanes per row: the fewest that hold it in one turn, at most a warp, which then takes
-// two or four turns at a time.
-constexpr int64_t kWideBelow = 400000;  // eights of columns in all
+constexpr int64_t kFew = 400000;  // eights of columns in all
 
 template <int LANES, bool WIDE, int TURNS>
 struct Pick {
@@ -278,15 +277,33 @@ struct Pick {
   static constexpr bool kWide = WIDE;
 };
 
+// Few values: as many threads as there are eights, so that SMs are not left empty (a block per row
+// above 512 columns: 1500 rows of I = 2048, forward 7.1 us so and 9.7 as warps; 3000 of 512: 3.0 as
+// 32 lanes and 3.7 as 16).  Many: the fewest lanes that hold a row in three or four turns, whichever
+// leaves fewer of them idle (two where that is all), at most a warp, which then takes the turns over (forward and backward:
+// 20000 rows of 2048, 134 us as blocks and 114 as warps; 100000 of 352, 140 us as 32 lanes in two
+// turns and 107 as 16 in three; 80000 of 512, 125 and 113; 60000 of 768, 136 in four turns and 130
+// in three).
 template <typename Args, typename F>
 cudaError_t pick(const Args& a, F launch) {
-  const int units = a.I / 8;
-  if (units > 64 && a.rows * units < kWideBelow) return launch(Pick<32, true, 1>{});
+  const int units = a.I / 8, warps = (units + 31) / 32;
+  if (a.rows * units < kFew) {
+    if (units <= 4) return launch(Pick<4, false, 1>{});
+    if (units <= 8) return launch(Pick<8, false, 1>{});
+    if (units <= 16) return launch(Pick<16, false, 1>{});
+    if (units <= 32) return launch(Pick<32, false, 1>{});
+    if (units <= 64) return launch(Pick<32, false, 2>{});
+    return launch(Pick<32, true, 1>{});
+  }
   if (units <= 4) return launch(Pick<4, false, 1>{});
-  if (units <= 8) return launch(Pick<8, false, 1>{});
-  if (units <= 16) return launch(Pick<16, false, 1>{});
-  if (units <= 32) return launch(Pick<32, false, 1>{});
-  if (units <= 64) return launch(Pick<32, false, 2>{});
+  if (units <= 8) return launch(Pick<4, false, 2>{});
+  if (units <= 12) return launch(Pick<4, false, 3>{});
+  if (units <= 16) return launch(Pick<4, false, 4>{});
+  if (units <= 24) return launch(Pick<8, false, 3>{});
+  if (units <= 32) return launch(Pick<8, false, 4>{});
+  if (units <= 48) return launch(Pick<16, false, 3>{});
+  if (units <= 64) return launch(Pick<16, false, 4>{});
+  if ((warps + 2) / 3 * 3 < (warps + 3) / 4 * 4) return launch(Pick<32, false, 3>{});
   return launch(Pick<32, false, 4>{});
 }
 

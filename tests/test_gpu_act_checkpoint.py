@@ -215,3 +215,15 @@ def test_rows_of_several_turns(moe, R, I, gated):
     w = rng.uniform(0.01, 1, R)
     w[::7] = 0.0
     check(moe, z, rng.standard_normal((R, I)) * 0.05, w, gated)
+
+
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("R,I", [(100001, 32), (50003, 64), (33341, 96), (25009, 128), (20011, 160), (16673, 192), (14293, 224),
+                                 (12503, 256), (8347, 384), (6257, 512), (4201, 768), (2301, 1408)])
+def test_narrow_rows_in_turns(moe, R, I, gated):
+    """Several rows a warp with up to four turns of columns each, the last rows and columns ragged."""
+    rng = np.random.default_rng(R)
+    z = rng.standard_normal((R, 2 * I if gated else I)) * np.exp2(rng.integers(-6, 4, (R, 1)))
+    w = rng.random(R) + 0.1
+    w[rng.random(R) < 0.1] = 0.0
+    check(moe, z, rng.standard_normal((R, I)), w, gated)
