@@ -250,3 +250,9 @@ def test_many_experts_and_tokens(moe, T, E, k):
     assert all(np.array_equal(a, b) for a, b in zip(got[:4], again[:4]))
     got = call(moe, x, ids, w, dw, np.zeros(T, np.uint8))
     assert not got[0].any() and not got[1].any() and not got[2].any() and not got[3].any()
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1001, 6), (12, 1024, 32), (13, 513, 4), (90, 700, 8), (97, 1001, 6)])
+def test_many_experts_few_tokens(moe, T, E, k):
+    x, ids, w, dw = make(T, E, k, 20)
+    check(call(moe, x, ids, w, dw), x, ids, w, dw, None)
