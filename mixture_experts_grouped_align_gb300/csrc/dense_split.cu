@@ -21,7 +21,7 @@
 //
 // Measured (weights from HBM, back to back): 64 x 2880 -> 2 x 2880 SwiGLU 8.8 us, the weight at
 // 3.8 TB/s; 64 x 7168 -> 2048 7.4 us, 4.0 TB/s; one row 2688 -> 1856 5.0 us; 4099 x 7168 -> 256 in
-// fp32 21.1 us.  Of the small ones about 3 us are the launch's start, the ring's first loads and
+// fp32 20.4 us.  Of the small ones about 3 us are the launch's start, the ring's first loads and
 // the cluster's sum, which a longer K hides no part of.
 #include <math.h>
 
@@ -42,12 +42,12 @@ constexpr int kRing = 208 * 1024;  // shared memory of the stages, at most
 constexpr int kGroupBlocks = 14;   // blocks of 64 of K an accumulator takes for fp32 outputs
 
 struct Split {
-  int BN;        // rows of x per tile: 16, 32, 64, 128 or 256
+  int BN;        // rows of x per tile: 16, 32, or 64 to 256 in steps of 16
   int NA;        // weight tiles (128 features) per tile
   int C;         // CTAs of a cluster: the shares of K
   int G;         // accumulators a share is split over
   int sub;       // blocks of 64 of K in a stage
-  int phase;     // rows of x that leave through shared memory at a time
+  int phase;     // rows of x that leave through shared memory at a time, a multiple of 16
   int stages;
   int slot;      // bytes of a stage
   int smem;
@@ -385,13 +385,15 @@ int resident_ctas(int C) {
 // cluster moves about 16 bytes a clock into an SM.  Against every variant timed, over 20 shapes
 // from 47 to 16000 rows: at most 8% from the best (e.g. 300 x 2 x 2880 x 2880 SwiGLU: 15.4 us as
 // 128-row tiles whole in K, 18.2 as 2 x 128 split in two, 20.7 on CTA pairs; 2000 x 2048 x 2048:
-// 18.2 us here, 16.7 on CTA pairs).
+// 18.2 us here, 16.7 on CTA pairs).  Above 64 rows BN goes in steps of 16, which fits ragged M and
+// the number of SMs (4099 x 256 x 7168 20.9 -> 20.3 us, 8192 x 64 x 2880 13.5 -> 13.2, 1000 x 2048 x
+// 2048 10.6 -> 10.3; 300 x 2048 x 2048 8.0 -> 8.3).
 Split plan(const Dense& d, double* clocks) {
   const int kOut = d.gated ? kFeat / 2 : kFeat;
   Split best{};
   double least = 0;
   for (int NA = 1; NA <= 2; ++NA)
-    for (int BN = 16; BN <= 256; BN *= 2) {
+    for (int BN = 16; BN <= 256; BN = BN < 64 ? BN * 2 : BN + 16) {
       Split s{};
       s.NA = NA;
       s.BN = BN;
@@ -399,7 +401,7 @@ Split plan(const Dense& d, double* clocks) {
       s.m_tiles = (d.M + BN - 1) / BN;
       // small tiles' MMAs take less than a stage's handshake (about 190 clocks), so two blocks of
       // 64 share one (64 x 7168 x 2048: 8.1 -> 7.5 us); large tiles need the ring's finer slots
-      // (4099 x 256 x 7168: 21.2 us so, 22.5 with two)
+      // (4099 x 256 x 7168: 21.1 us so, 22.5 with two)
       s.sub = BN <= 64 ? 2 : 1;
       const uint32_t nk = (uint32_t)(d.K + s.sub * kBK - 1) / (uint32_t)(s.sub * kBK);
       const int64_t tiles = s.n_tiles * s.m_tiles;
@@ -437,8 +439,8 @@ Split plan(const Dense& d, double* clocks) {
   best.stages = kRing / best.slot;
   if (best.stages > kMaxStages) best.stages = kMaxStages;
   if (best.stages > share) best.stages = share;
-  best.phase = best.BN;
-  while (best.NA * best.phase * kFeat * 4 > kRing) best.phase /= 2;
+  const int fit = kRing / (best.NA * kFeat * 4) / 16 * 16, turns = (best.BN + fit - 1) / fit;
+  best.phase = (best.BN + 16 * turns - 1) / (16 * turns) * 16;
   const int part = best.NA * best.phase * kFeat * 4;
   best.smem = (best.stages * best.slot > part ? best.stages * best.slot : part) + 1024;
   // Never two CTAs of this kernel on an SM: one could wait for tensor memory that the other holds
