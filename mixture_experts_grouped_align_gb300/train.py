@@ -10,8 +10,9 @@ Backward, from dy [T, K]: the activations' gradients come from the checkpoints, 
 the activations again for the weight gradients; the routing weights' gradients join the
 balance and z losses' in d_logits.
 
-Marshalling only: every step runs in the library's kernels.  ``TrainLayer`` holds the weights,
-the buffers that live from a forward to its backward, and the workspaces.
+Marshalling only: every step runs in the library's kernels.  ``TrainLayer`` refers to the caller's
+weights, which may change in place between steps (not between a forward and its backward), and
+holds the buffers that live from a forward to its backward, and the workspaces.
 """
 from __future__ import annotations
 
@@ -38,13 +39,14 @@ class TrainLayer:
         dev, bf = wr.device, torch.bfloat16
         T, P, E, K, I, Is = max_rows, max_rows * k, self.E, self.K, self.I, self.Is
         self.max_rows = T
-        # the experts' input gradients contract over their outputs: transposed copies of the weights
-        self.w1t, self.w2t = w1.transpose(1, 2).contiguous(), w2.transpose(1, 2).contiguous()
         new = lambda *shape, dtype=bf: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
         i32, u8, f32 = torch.int32, torch.uint8, torch.float32
         self.logits, self.ids, self.w = new(T, E, dtype=f32), new(T, k, dtype=i32), new(T, k, dtype=f32)
         self.cap, blocks = moe_align_capacity(P, E, BLOCK_M)
         self.sorted, self.expert_ids, self.ntpp = new(self.cap, dtype=i32), new(blocks, dtype=i32), new(4, dtype=i32)
+        # the experts' input gradients contract over their outputs: room for a transposed copy of w2,
+        # then of w1, made by every backward from the weights as they are then
+        self.wt = new(E * 2 * I * K)
         self.gu, self.h, self.o = new(P, 2 * I), new(P, I), new(P, K)
         self.codes, self.scales = new(P, 2 * I, dtype=u8), new(P, 2 * I // 32, dtype=u8)
         self.gs, self.hs, self.routed = new(T, 2 * Is), new(T, Is), new(T, K)
@@ -95,11 +97,13 @@ class TrainLayer:
         cap, _ = moe_align_capacity(T * k, E, BLOCK_M)
         args = (T, k, self.sorted, self.expert_ids, self.ntpp, BLOCK_M, cap)
         # routed experts: dh, then the activation from its checkpoint (h is w h again)
-        moe_grouped_gemm("bf16", E, I, K, dy, None, 0, self.w2t, None, None, *args, self.dh, c)
+        w2t = self.wt[:E * I * K].view(E, I, K).copy_(self.w2.transpose(1, 2))
+        moe_grouped_gemm("bf16", E, I, K, dy, None, 0, w2t, None, None, *args, self.dh, c)
         moe_act_backward(self.codes, self.scales, self.dh, self.w, T * k, I, "swiglu", self.dgu, self.h, self.dw, c)
         moe_wgrad(self.h, dy, 0, T, k, E, I, K, *args[2:], g["w2t"], 0, c)
         moe_wgrad(self.dgu, x, 0, T, k, E, 2 * I, K, *args[2:], g["w1"], 0, c)
-        moe_grouped_gemm("bf16", E, K, 2 * I, self.dgu, None, 1, self.w1t, None, None, *args, self.dx_pairs, c)
+        w1t = self.wt.view(E, K, 2 * I).copy_(self.w1.transpose(1, 2))
+        moe_grouped_gemm("bf16", E, K, 2 * I, self.dgu, None, 1, w1t, None, None, *args, self.dx_pairs, c)
         # router: the routing weights' gradient joins the auxiliary losses'
         moe_router_loss(self.logits, self.ids, self.w, self.dw, token_mask, T, k, E, *self.coef, self.counts,
                         self.prob_mean, self.loss, self.d_logits, c)

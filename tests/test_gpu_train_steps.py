@@ -1,0 +1,94 @@
+"""Training steps of TrainLayer on the GPU against the float64 oracle at the checkpoint's values.
+
+Bounds.  A value stored between two kernels in bf16 is within 2^-9 of itself, in norm too.  No
+output has more than eight such roundings before it, so 8 * 2^-9 = 1.6e-2; a pre-activation whose
+fp32 sum lies at a rounding's border may fall to the checkpoint's next value, for fewer than one in
+10^4 of them: 1e-3 in norm.  2e-2 holds for both together.
+"""
+import numpy as np
+import pytest
+
+from helpers import bf16_to_np
+from oracle import activation, train_step
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+TOL = 2e-2
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_grouped_align_gb300 as m
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    m.build()
+    m.load()
+    return m
+
+
+def held(v):
+    return activation.held(train_step.bf16_round(v))[2]
+
+
+def make(seed, E, K=256, I=128, Is=384):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s, std=1.0: (torch.randn(s, generator=g, device="cuda") * std).to(torch.bfloat16)  # noqa: E731
+    W = {"wr": rnd(E, K, std=0.1), "w1": rnd(E, 2 * I, K, std=0.08), "w2": rnd(E, K, I, std=0.08),
+         "ws1": rnd(2 * Is, K, std=0.08), "bs1": rnd(2 * Is, std=0.1), "ws2": rnd(K, Is, std=0.08), "bs2": rnd(K, std=0.1)}
+    return W, rnd
+
+
+def layer(W, k, rows, coef=(2.0, 0.5), **kw):
+    from mixture_experts_grouped_align_gb300.train import TrainLayer
+    return TrainLayer(W["wr"], W["w1"], W["w2"], W["ws1"], W["bs1"], W["ws2"], W["bs2"], k, max_rows=rows,
+                      balance_coef=coef[0], z_coef=coef[1], **kw)
+
+
+def near(got, ref, tol, what):
+    got, ref = np.asarray(got, np.float64), np.asarray(ref, np.float64)
+    assert got.shape == ref.shape, (what, got.shape, ref.shape)
+    e = float(np.linalg.norm(got - ref) / np.linalg.norm(ref))
+    assert e <= tol, (what, e)
+
+
+def compare(L, W, x, dy, y, dx, mask=None, full=None):
+    """The layer's results of a step against the oracle's (``full``: other expected gradients)."""
+    T = len(x)
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    Wd, xd, dyd, ids = {n: f(w) for n, w in W.items()}, f(x), f(dy), L.ids[:T].cpu().numpy().astype(np.int64)
+    ry, kept = train_step.forward(Wd, xd, ids)
+    r = full(Wd, kept, dyd) if full else train_step.backward(Wd, kept, dyd, *L.coef, mask, held)
+    if y is not None:
+        near(bf16_to_np(y), ry, TOL, "y")
+    for n in ("wr", "w1", "ws1", "bs1", "ws2", "bs2"):
+        if np.any(r[n]):
+            near(f(L.grads[n]), r[n], TOL, n)
+        else:
+            assert not L.grads[n].any(), n
+    near(f(L.grads["w2t"].transpose(1, 2)), r["w2"], TOL, "w2") if np.any(r["w2"]) else None
+    near(bf16_to_np(dx), r["dx"], TOL, "dx")
+    assert np.array_equal(L.counts.cpu().numpy(), r["counts"])
+    near(L.loss.cpu().numpy(), r["loss"], 1e-4, "loss")
+    assert int(L.status[0]) == 0
+    return r
+
+
+def step(L, x, dy, mask=None):
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    L.forward(x, y)
+    L.backward(dy, dx, mask)
+    torch.cuda.synchronize()
+    return y, dx
+
+
+def test_weights_changed_between_steps(moe):
+    """An optimiser's in-place update: the second step's gradients are those of the new weights."""
+    T, k = 300, 4
+    W, rnd = make(1, 64)
+    L = layer(W, k, T)
+    for _ in range(2):
+        x, dy = rnd(T, 256), rnd(T, 256)
+        y, dx = step(L, x, dy)
+        compare(L, W, x, dy, y, dx)
+        for n, w in W.items():
+            w.copy_(w + rnd(*w.shape, std=float(w.float().std())))
