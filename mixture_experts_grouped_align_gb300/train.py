@@ -18,27 +18,53 @@ from __future__ import annotations
 
 import torch
 
-from . import (Ctx, moe_act_backward, moe_act_checkpoint, moe_align, moe_align_capacity, moe_dense_bias_grad,
+from . import (Ctx, MoeError, moe_act_backward, moe_act_checkpoint, moe_align, moe_align_capacity, moe_dense_bias_grad,
                moe_dense_gemm, moe_grouped_gemm, moe_pair_sum, moe_router_loss, moe_router_loss_workspace_size,
                moe_wgrad, moe_wgrad_workspace_size)
 
 BLOCK_M = 128
 
 
+def _check(t, what, dtype, device, shape=None, numel=0):
+    """MoeError unless ``t`` is a dense, 16-byte aligned tensor of ``dtype`` on ``device``, of exactly
+    ``shape`` or of at least ``numel`` elements: the kernels read and write whole rows from its
+    address on."""
+    if not isinstance(t, torch.Tensor):
+        raise MoeError(-1, f"{what}: need a torch tensor, got {type(t).__name__}")
+    size_ok = t.numel() >= numel if shape is None else tuple(t.shape) == tuple(shape)
+    if t.dtype != dtype or not size_ok or not t.is_contiguous() or t.data_ptr() % 16 or t.device != device:
+        need = f"shape {tuple(shape)}" if shape is not None else f"at least {numel} elements"
+        raise MoeError(-1, f"{what}: need a contiguous, 16-byte aligned {dtype} tensor of {need} on {device}, got {t.dtype} "
+                           f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+
+
+def _apart(a, b, what):
+    """MoeError if the two dense tensors share memory."""
+    if a.data_ptr() < b.data_ptr() + b.numel() * b.element_size() and b.data_ptr() < a.data_ptr() + a.numel() * a.element_size():
+        raise MoeError(-1, f"{what} must not overlap")
+
+
 class TrainLayer:
     """wr [E, K], w1 [E, 2I, K], w2 [E, K, I], ws1 [2Is, K], ws2 [K, Is], bs1 [2Is], bs2 [K]: bf16
-    device tensors; E, K, I and Is multiples of 64.  Batches of up to ``max_rows`` tokens."""
+    device tensors; E, K, I and Is multiples of 64.  Batches of up to ``max_rows`` tokens.
+
+    Every operand is checked before anything is launched (MoeError): type, shape, density,
+    alignment and device, and that what a pass writes lies apart from what it still reads."""
 
     def __init__(self, wr, w1, w2, ws1, bs1, ws2, bs2, k, max_rows, balance_coef=0.01, z_coef=0.001):
+        for what, t, dims in (("wr", wr, 2), ("w2", w2, 3), ("ws2", ws2, 2)):  # those that the sizes come from
+            if not isinstance(t, torch.Tensor) or t.dim() != dims:
+                raise MoeError(-1, f"{what}: need a torch tensor of {dims} dimensions")
         self.wr, self.w1, self.w2, self.ws1, self.bs1, self.ws2, self.bs2 = wr, w1, w2, ws1, bs1, ws2, bs2
         self.E, self.K, self.k = wr.shape[0], wr.shape[1], k
         self.I, self.Is = w2.shape[2], ws2.shape[1]
         if any(n % 64 for n in (self.E, self.K, self.I, self.Is)):
             raise ValueError("E, K, I and Is must be multiples of 64 (moe_wgrad)")
+        self._check_weights()
         self.coef = (balance_coef, z_coef)
         dev, bf = wr.device, torch.bfloat16
         T, P, E, K, I, Is = max_rows, max_rows * k, self.E, self.K, self.I, self.Is
-        self.max_rows = T
+        self.max_rows, self.x = T, None
         new = lambda *shape, dtype=bf: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
         i32, u8, f32 = torch.int32, torch.uint8, torch.float32
         self.logits, self.ids, self.w = new(T, E, dtype=f32), new(T, k, dtype=i32), new(T, k, dtype=f32)
@@ -68,11 +94,26 @@ class TrainLayer:
                      [(E, 2 * I, K, self.cap), (E, I, K, self.cap), (1, 2 * Is, K, self.cap1), (1, K, Is, self.cap1)]))
         self.workspace = torch.empty(need, dtype=u8, device=dev)
 
+    def _check_weights(self):
+        E, K, I, Is, dev = self.E, self.K, self.I, self.Is, self.wr.device
+        for what, shape in (("wr", (E, K)), ("w1", (E, 2 * I, K)), ("w2", (E, K, I)), ("ws1", (2 * Is, K)), ("bs1", (2 * Is,)),
+                            ("ws2", (K, Is)), ("bs2", (K,))):
+            _check(getattr(self, what), what, torch.bfloat16, dev, shape)
+        if dev.type != "cuda":
+            raise MoeError(-1, f"wr: need weights on a CUDA device, got {dev}")
+
     def _ctx(self):
         return Ctx(workspace=self.workspace, dev_status=self.status)
 
     def forward(self, x, y):
         """x [T, K] bf16 -> y [T, K] bf16.  x is needed again by ``backward``."""
+        dev, bf = self.wr.device, torch.bfloat16
+        self._check_weights()
+        _check(x, "x", bf, dev, (x.shape[0] if isinstance(x, torch.Tensor) and x.dim() else 0, self.K))
+        if x.shape[0] > self.max_rows:
+            raise MoeError(-3, f"x: {x.shape[0]} rows, the layer was made for up to {self.max_rows}")
+        _check(y, "y", bf, dev, numel=x.numel())
+        _apart(x, y, "x and y")
         T, k, E, K, I, Is, c = x.shape[0], self.k, self.E, self.K, self.I, self.Is, self._ctx()
         self.T, self.x = T, x
         moe_dense_gemm(x, self.wr, "nk", None, None, 1.0, T, E, K, "none", self.logits, c)
@@ -92,8 +133,17 @@ class TrainLayer:
         """dy [T, K] bf16, the gradient of y -> dx [T, K] bf16, the weights' gradients in
         ``grads`` (fp32; "w2t" is [E, I, K]), the losses in ``loss`` (total, balance, z) and the
         experts' counts in ``counts``.  token_mask [T]: 0 for tokens the losses leave out."""
+        if self.x is None:
+            raise MoeError(-1, "backward needs a forward before it")
+        x, dev, bf = self.x, self.wr.device, torch.bfloat16
+        self._check_weights()
+        for t, what in ((dy, "dy"), (dx, "dx")):
+            _check(t, what, bf, dev, numel=x.numel())
+        for t, what in ((dy, "dy and dx"), (x, "x and dx")):
+            _apart(t, dx, what)
+        if token_mask is not None:
+            _check(token_mask, "token_mask", torch.uint8, dev, numel=x.shape[0])
         T, k, E, K, I, Is, c, g = self.T, self.k, self.E, self.K, self.I, self.Is, self._ctx(), self.grads
-        x = self.x
         cap, _ = moe_align_capacity(T * k, E, BLOCK_M)
         args = (T, k, self.sorted, self.expert_ids, self.ntpp, BLOCK_M, cap)
         # routed experts: dh, then the activation from its checkpoint (h is w h again)
