@@ -92,3 +92,26 @@ def test_weights_changed_between_steps(moe):
         compare(L, W, x, dy, y, dx)
         for n, w in W.items():
             w.copy_(w + rnd(*w.shape, std=float(w.float().std())))
+
+
+@pytest.mark.parametrize("T,masked", [(300, False), (700, True), (3, False), (1, False)])
+def test_step_at_the_checkpoint_s_values(moe, T, masked):
+    W, rnd = make(T, 64)
+    x, dy = rnd(T, 256), rnd(T, 256)
+    mask = torch.from_numpy((np.random.default_rng(T).random(T) < 0.8).astype(np.uint8)).cuda() if masked else None
+    L = layer(W, 4, T + 5)
+    y, dx = step(L, x, dy, mask)
+    compare(L, W, x, dy, y, dx, None if mask is None else mask.cpu().numpy())
+
+
+@pytest.mark.parametrize("coef", [(2.0, 0.0), (0.0, 0.5), (2.0, 0.5)])
+def test_gradients_of_the_losses_alone(moe, coef):
+    """dy = 0: what reaches x and the router's weights comes from the balance and z losses."""
+    T = 300
+    W, rnd = make(5, 64)
+    x, dy = rnd(T, 256), torch.zeros((T, 256), dtype=torch.bfloat16, device="cuda")
+    L = layer(W, 4, T, coef)
+    y, dx = step(L, x, dy)
+    r = compare(L, W, x, dy, y, dx)
+    # fp32 logits within 1e-6 of their magnitude, probabilities and gradients with them
+    near(L.d_logits[:T].double().cpu().numpy(), r["d_logits"], 1e-4, "d_logits")
