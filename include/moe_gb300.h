@@ -490,6 +490,16 @@ moe_status moe_pair_sum(const void* o, const void* residual, int64_t T, int32_t 
  * have no counterpart to this call. */
 void moe_debug_stall_tensor_kernels(int64_t stall_ns);
 
+/* How moe_dense_gemm runs a product of this size on the current device, in plan[8]:
+ *   plan[0] = 0: the kernel of CTA pairs (tiles of 256 x 256); the rest is 0
+ *   plan[0] = 1: the kernel for few tiles; plan[1] rows of x in a tile, plan[2] weight tiles of
+ *     128 features in it, plan[3] CTAs that share K, plan[4] accumulators a share is split
+ *     over, plan[5] blocks of 64 of K in a stage, plan[6] rows that leave at a time, plan[7]
+ *     stages
+ * The same limits as moe_dense_gemm's, and M >= 1; both weight layouts run alike.  Nothing is
+ * launched.  Tests and measurements use it to say which kernel they ran. */
+moe_status moe_dense_gemm_plan(int64_t M, int32_t N, int32_t K, int32_t activation, int32_t out_f32, int32_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,7 +22,7 @@ __all__ = [
     "moe_forward_no_alloc", "moe_grouped_gemm", "moe_grouped_gemm_workspace_size", "moe_mx_quantize",
     "moe_gemm_per_token", "moe_wgrad", "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels",
     "moe_router_loss", "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward",
-    "moe_dense_gemm", "moe_dense_bias_grad", "moe_pair_sum", "W_LAYOUT", "EXPORTED_SYMBOLS",
+    "moe_dense_gemm", "moe_dense_gemm_plan", "moe_dense_bias_grad", "moe_pair_sum", "W_LAYOUT", "EXPORTED_SYMBOLS",
 ]
 
 MOE_OK = 0
@@ -40,7 +40,7 @@ EXPORTED_SYMBOLS = [
     "moe_grouped_gemm", "moe_grouped_gemm_workspace_size", "moe_mx_quantize", "moe_gemm_per_token", "moe_wgrad",
     "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels", "moe_router_loss",
     "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward", "moe_dense_gemm",
-    "moe_dense_bias_grad", "moe_pair_sum",
+    "moe_dense_bias_grad", "moe_pair_sum", "moe_dense_gemm_plan",
 ]
 
 
@@ -121,6 +121,7 @@ def load(path: str | None = None):
         "moe_act_checkpoint": (I32, [P, P, I64, I32, I32, P, P, P, P]),
         "moe_act_backward": (I32, [P, P, P, P, I64, I32, I32, P, P, P, P]),
         "moe_dense_gemm": (I32, [P, P, I32, P, P, F32, I64, I32, I32, I32, P, I32, P]),
+        "moe_dense_gemm_plan": (I32, [I64, I32, I32, I32, I32, P]),
         "moe_dense_bias_grad": (I32, [P, I64, I32, P, P]),
         "moe_pair_sum": (I32, [P, P, I64, I32, I32, P, P]),
     }
@@ -338,6 +339,17 @@ def moe_dense_gemm(x, w, w_layout, bias, residual, residual_scale, M, N, K, acti
     c = ctx or Ctx()
     return _check((_native or _load_native()).dense_gemm(x, w, lay, bias, residual, residual_scale, M, N, K, _act(activation),
                                                         out, int(out_f32), c.address))
+
+
+def moe_dense_gemm_plan(M, N, K, activation="none", out_f32=False) -> dict:
+    """How moe_dense_gemm runs a product of this size on the current device: ``kernel`` "pairs" or
+    "split", and for "split" the tile's ``rows``, ``weight_tiles``, ``cluster``, ``accumulators``,
+    ``sub``, ``phase`` and ``stages``."""
+    p = (ctypes.c_int32 * 8)()
+    _check(load().moe_dense_gemm_plan(M, N, K, _act(activation), int(out_f32), p))
+    if not p[0]:
+        return {"kernel": "pairs"}
+    return {"kernel": "split", **dict(zip(("rows", "weight_tiles", "cluster", "accumulators", "sub", "phase", "stages"), p[1:]))}
 
 
 def moe_dense_bias_grad(dz, M, N, d_bias, ctx=None):

@@ -468,23 +468,39 @@ cudaError_t launch(const Dense& d, const Split& s, cudaStream_t stream) {
                                    s.C, mx, mw, d, s);
 }
 
+// Whether the split kernel is estimated faster than the pairs', and how it would run.
+bool pick(const Dense& d, Split* s) {
+  double split = 0;
+  *s = plan(d, &split);
+  // the pairs' kernel: 512 clocks a stage of a 256 x 256 tile, its start and its last epilogue
+  const int64_t pairs = moe_launch::sm_count_current() / 2, nk = (d.K + kBK - 1) / kBK;
+  const int64_t tiles = ((d.M + 255) / 256) * ((d.N + (d.gated ? 127 : 255)) / (d.gated ? 128 : 256));
+  return split < (double)((tiles + pairs - 1) / pairs) * nk * 512 + 7000;
+}
+
 }  // namespace
 
 namespace moe_launch {
 
 bool dense_split(const Dense& d, cudaStream_t stream, cudaError_t* err) {
-  double split = 0;
-  const Split s = plan(d, &split);
-  // the pairs' kernel: 512 clocks a stage of a 256 x 256 tile, its start and its last epilogue
-  const int64_t pairs = sm_count_current() / 2, nk = (d.K + kBK - 1) / kBK;
-  const int64_t tiles = ((d.M + 255) / 256) * ((d.N + (d.gated ? 127 : 255)) / (d.gated ? 128 : 256));
-  if (split >= (double)((tiles + pairs - 1) / pairs) * nk * 512 + 7000) return false;
+  Split s;
+  if (!pick(d, &s)) return false;
   const int which = (d.gated ? 4 : 0) + (s.NA == 2 ? 2 : 0) + (s.sub == 2 ? 1 : 0);
   using Launch = cudaError_t (*)(const Dense&, const Split&, cudaStream_t);
   static const Launch launches[8] = {launch<1, false, 1>, launch<1, false, 2>, launch<2, false, 1>, launch<2, false, 2>,
                                      launch<1, true, 1>,  launch<1, true, 2>,  launch<2, true, 1>,  launch<2, true, 2>};
   *err = launches[which](d, s, stream);
   return true;
+}
+
+void dense_plan(const Dense& d, int32_t* p) {
+  Split s;
+  if (pick(d, &s)) {
+    const int32_t v[8] = {1, s.BN, s.NA, s.C, s.G, s.sub, s.phase, s.stages};
+    for (int i = 0; i < 8; ++i) p[i] = v[i];
+  } else {
+    for (int i = 0; i < 8; ++i) p[i] = 0;
+  }
 }
 
 }  // namespace moe_launch

@@ -726,9 +726,7 @@ moe_status moe_act_backward(const uint8_t* codes, const uint8_t* scales, const v
   return st;
 }
 
-moe_status moe_dense_gemm(const void* x, const void* w, int32_t w_layout, const void* bias, const void* residual,
-                          float residual_scale, int64_t M, int32_t N, int32_t K, int32_t activation, void* out,
-                          int32_t out_f32, const moe_ctx* ctx) {
+static moe_status check_dense(int32_t w_layout, int64_t M, int32_t N, int32_t K, int32_t activation) {
   MOE_REQUIRE(activation == MOE_ACT_SWIGLU || activation == MOE_ACT_RELU2 || activation == MOE_ACT_NONE,
               MOE_ERR_INVALID_ARG, "unknown activation");
   MOE_REQUIRE(w_layout == MOE_W_NK || w_layout == MOE_W_KN, MOE_ERR_INVALID_ARG, "unknown weight layout");
@@ -737,6 +735,14 @@ moe_status moe_dense_gemm(const void* x, const void* w, int32_t w_layout, const 
   MOE_REQUIRE(M < most && N < most / 2 && K < most, MOE_ERR_UNSUPPORTED, "M, N1 and K must be < 2^30");
   MOE_REQUIRE(K % 8 == 0, MOE_ERR_UNSUPPORTED, "K must be a multiple of 8");
   MOE_REQUIRE(w_layout == MOE_W_NK || N % 8 == 0, MOE_ERR_UNSUPPORTED, "N must be a multiple of 8 for [K, N] weights");
+  return MOE_OK;
+}
+
+moe_status moe_dense_gemm(const void* x, const void* w, int32_t w_layout, const void* bias, const void* residual,
+                          float residual_scale, int64_t M, int32_t N, int32_t K, int32_t activation, void* out,
+                          int32_t out_f32, const moe_ctx* ctx) {
+  moe_status st = check_dense(w_layout, M, N, K, activation);
+  if (st != MOE_OK) return st;
   if (M == 0) return MOE_OK;
   MOE_REQUIRE(x && w && out, MOE_ERR_INVALID_ARG, "null tensor pointer");
   MOE_REQUIRE(aligned16(x) && aligned16(w) && aligned16(bias) && aligned16(residual) && aligned16(out),
@@ -747,9 +753,20 @@ moe_status moe_dense_gemm(const void* x, const void* w, int32_t w_layout, const 
   d.relu2 = activation == MOE_ACT_RELU2; d.out_f32 = out_f32 ? 1 : 0; d.status = status_of(ctx);
   moe_launch::apply_debug_stall(d);
   rec(ctx, 0, 2);
-  const moe_status st = cuda_status(moe_launch::dense_gemm(d, stream_of(ctx)), "moe_dense_gemm");
+  st = cuda_status(moe_launch::dense_gemm(d, stream_of(ctx)), "moe_dense_gemm");
   rec(ctx, 1, 2);
   return st;
+}
+
+moe_status moe_dense_gemm_plan(int64_t M, int32_t N, int32_t K, int32_t activation, int32_t out_f32, int32_t* plan) {
+  const moe_status st = check_dense(MOE_W_NK, M, N, K, activation);
+  if (st != MOE_OK) return st;
+  MOE_REQUIRE(plan && M >= 1, MOE_ERR_INVALID_ARG, "need a plan to fill and M >= 1");
+  moe_launch::Dense d{};
+  d.M = M; d.N = N; d.K = K; d.gated = activation == MOE_ACT_SWIGLU; d.relu2 = activation == MOE_ACT_RELU2;
+  d.out_f32 = out_f32 ? 1 : 0;
+  moe_launch::dense_plan(d, plan);
+  return MOE_OK;
 }
 
 moe_status moe_dense_bias_grad(const void* dz, int64_t M, int32_t N, float* d_bias, const moe_ctx* ctx) {

@@ -280,6 +280,8 @@ void apply_debug_stall(Dense& d);
 cudaError_t dense_gemm(Dense d, cudaStream_t stream);
 // Runs the product on the split kernel and says so, unless the tiled kernel is estimated faster.
 bool dense_split(const Dense& d, cudaStream_t stream, cudaError_t* err);
+// moe_dense_gemm_plan's eight values for the product.
+void dense_plan(const Dense& d, int32_t* plan);
 // out[n] = sum_m x[m, n], x [M, N] bf16 (column_sum.cu)
 cudaError_t column_sum(const void* x, int64_t M, int64_t N, float* out, cudaStream_t stream);
 
