@@ -221,7 +221,7 @@ def moe_forward_workspace_size(T_rows, k, K, I, cap_tokens) -> int:
 
 
 def _act(activation):
-    return ACTIVATION[activation] if activation.__class__ is str else int(activation)
+    return ACTIVATION[activation] if isinstance(activation, str) else int(activation)
 
 
 def moe_forward(quant, E, K, I, w1, w1_scale, b1, w2, w2_scale, b2, x, x_scale, T_rows, T_real, k,
@@ -333,9 +333,9 @@ def moe_dense_gemm(x, w, w_layout, bias, residual, residual_scale, M, N, K, acti
     """out [M, N] = act(x [M, K] . W^T + bias) + residual_scale * residual.  w_layout "nk" (w [N1, K])
     or "kn" (w [K, N1]); activation "none", "relu2" or "swiglu" (N1 = 2N).  out is bf16 or fp32
     (``out_f32`` says which for a raw pointer), residual of the same type."""
-    lay = W_LAYOUT[w_layout] if w_layout.__class__ is str else int(w_layout)
+    lay = W_LAYOUT[w_layout] if isinstance(w_layout, str) else int(w_layout)
     if out_f32 is None:
-        out_f32 = out is not None and out.__class__ is not int and out.dtype.itemsize == 4
+        out_f32 = out is not None and not isinstance(out, int) and out.dtype.itemsize == 4
     c = ctx or Ctx()
     return _check((_native or _load_native()).dense_gemm(x, w, lay, bias, residual, residual_scale, M, N, K, _act(activation),
                                                         out, int(out_f32), c.address))
