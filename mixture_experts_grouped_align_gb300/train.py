@@ -132,7 +132,13 @@ class TrainLayer:
     def backward(self, dy, dx, token_mask=None):
         """dy [T, K] bf16, the gradient of y -> dx [T, K] bf16, the weights' gradients in
         ``grads`` (fp32; "w2t" is [E, I, K]), the losses in ``loss`` (total, balance, z) and the
-        experts' counts in ``counts``.  token_mask [T]: 0 for tokens the losses leave out."""
+        experts' counts in ``counts``.
+
+        token_mask [T] bytes: 0 for padding rows.  They count for nothing in the losses, and their
+        routing weights are constants: d_logits is zero there, whatever dy is.  So dy has to be zero
+        in padding rows, as it is where nothing reads y's; otherwise the terms that run through
+        those tokens' routing weights are missing from dx and the router's gradient, while the
+        experts' gradients have the tokens' terms."""
         if self.x is None:
             raise MoeError(-1, "backward needs a forward before it")
         x, dev, bf = self.x, self.wr.device, torch.bfloat16

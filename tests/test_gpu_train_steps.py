@@ -115,3 +115,21 @@ def test_gradients_of_the_losses_alone(moe, coef):
     r = compare(L, W, x, dy, y, dx)
     # fp32 logits within 1e-6 of their magnitude, probabilities and gradients with them
     near(L.d_logits[:T].double().cpu().numpy(), r["d_logits"], 1e-4, "d_logits")
+
+
+def test_padding_rows_have_no_part_in_any_gradient(moe):
+    """Tokens of mask 0 whose dy is zero, as padding's is: every gradient is the whole one."""
+    T, k = 500, 4
+    W, rnd = make(6, 64)
+    x, dy = rnd(T, 256), rnd(T, 256)
+    mask = (np.random.default_rng(6).random(T) < 0.7).astype(np.uint8)
+    dy[torch.from_numpy(mask == 0).cuda()] = 0
+    L = layer(W, k, T)
+
+    def full(Wd, kept, dyd):  # the output's gradient through every weight, and the losses' alone
+        a = train_step.backward(Wd, kept, dyd, 0.0, 0.0, None, held)
+        b = train_step.backward(Wd, kept, np.zeros_like(dyd), *L.coef, mask, held)
+        return {n: b[n] if n in ("loss", "counts") else a[n] + b[n] for n in a}
+
+    y, dx = step(L, x, dy, torch.from_numpy(mask).cuda())
+    compare(L, W, x, dy, y, dx, full=full)
