@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 8; ++i) up[i] += bb[i];
               }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] = moe::silu(o[i]) * up[i];
+              for (int i = 0; i < 8; ++i) o[i] = (F32 ? moe::silu_f32(o[i]) : moe::silu(o[i])) * up[i];
             } else if (d.relu2) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) o[i] = moe::relu2(o[i]);

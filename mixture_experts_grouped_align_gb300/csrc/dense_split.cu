@@ -78,7 +78,7 @@ __device__ __forceinline__ void store4(const Dense& d, int64_t m, int64_t n, flo
       }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (GATED) z[i] = moe::silu(z[i]) * u[i];
+    if (GATED) z[i] = (d.out_f32 ? moe::silu_f32(z[i]) : moe::silu(z[i])) * u[i];
     else if (d.relu2) z[i] = moe::relu2(z[i]);
   }
   const int64_t at = m * d.N + n;

@@ -135,6 +135,9 @@ MOE_DEV uint4 ldg_nc_u128(const void* p) {
 // silu(g) = g * sigmoid(g) with the hardware exponential and reciprocal (relative error
 // near 1e-6, far below the f16 / bf16 rounding of the value it feeds); 0 for g -> -inf.
 MOE_DEV float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// The same for fp32 outputs, within 3 units of the last place: __expf's error grows with |g|, to 80
+// units of the result at g = -72.
+MOE_DEV float silu_f32(float g) { return g / (1.0f + expf(-g)); }
 
 // relu(a)^2, exact up to the one rounding of the product; a NaN passes through.
 MOE_DEV float relu2(float a) {
