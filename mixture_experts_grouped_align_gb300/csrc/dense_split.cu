@@ -28,6 +28,7 @@
 #include <atomic>
 
 #include "dense_common.cuh"
+#include "per_device.h"
 
 namespace {
 
@@ -348,35 +349,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// CTAs of clusters of C that the device holds at once with one CTA per SM (queried once).
-int resident_ctas(int C) {
-  static std::atomic<int> seen[9];
-  int n = seen[C].load(std::memory_order_relaxed);
-  if (n > 0) return n;
+// CTAs of clusters of C, 1 to 8, that the current device holds at once with one CTA per SM (queried
+// once per device).
+void resident_ctas(int (&at_once)[9]) {
+  static moe_host::PerDevice<9> seen;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
   const int sms = moe_launch::sm_count_current();
-  n = sms;
-  if (C > 1) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(C * sms));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kRing + 1024;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = C;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    int clusters = 0;
-    if (cudaFuncSetAttribute(dense_split_kernel<1, false, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&clusters, dense_split_kernel<1, false, 1>, &cfg) != cudaSuccess || clusters < 1) {
-      (void)cudaGetLastError();
-      clusters = 1;
-    }
-    n = clusters * C;
-  }
-  seen[C].store(n, std::memory_order_relaxed);
-  return n;
+  at_once[0] = 0;
+  at_once[1] = sms;
+  for (int C = 2; C <= 8; ++C)
+    at_once[C] = seen.get(dev, C, C, [=] {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3((unsigned)(C * sms));
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = kRing + 1024;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = C;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      if (cudaFuncSetAttribute(dense_split_kernel<1, false, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024) !=
+              cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&clusters, dense_split_kernel<1, false, 1>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+      }
+      return clusters * C;
+    });
 }
 
 // The variant with the least estimated time in clocks.  Per CTA a stage costs what its operands
@@ -392,6 +394,8 @@ Split plan(const Dense& d, double* clocks) {
   const int kOut = d.gated ? kFeat / 2 : kFeat;
   Split best{};
   double least = 0;
+  int resident[9];
+  resident_ctas(resident);
   for (int NA = 1; NA <= 2; ++NA)
     for (int BN = 16; BN <= 256; BN = BN < 64 ? BN * 2 : BN + 16) {
       Split s{};
@@ -408,7 +412,7 @@ Split plan(const Dense& d, double* clocks) {
       if (tiles < (1 << 27)) {
         const double load = s.sub * (NA * kFeat + BN) * (128 / 60.0), mma = s.sub * BN * 2.0 * NA, stage = mma > load ? mma : load;
         for (uint32_t C = 1; C <= 8 && C <= nk; ++C) {
-          const uint32_t at_once = (uint32_t)resident_ctas((int)C);
+          const uint32_t at_once = (uint32_t)resident[C];
           // more shares than fill a wave only shorten fp32 sums
           if (C > 1 && (uint32_t)tiles * (C - 1) >= at_once && !d.out_f32) break;
           const uint32_t share = (nk + C - 1) / C, waves = ((uint32_t)tiles * C + at_once - 1) / at_once;
