@@ -46,7 +46,8 @@ def _apart(a, b, what):
 
 class TrainLayer:
     """wr [E, K], w1 [E, 2I, K], w2 [E, K, I], ws1 [2Is, K], ws2 [K, Is], bs1 [2Is], bs2 [K]: bf16
-    device tensors; E, K, I and Is multiples of 64.  Batches of up to ``max_rows`` tokens.
+    device tensors; K, I and Is multiples of 64, 1 <= k <= 32, k <= E <= 1024.  Batches of up to
+    ``max_rows`` tokens.
 
     Every operand is checked before anything is launched (MoeError): type, shape, density,
     alignment and device, and that what a pass writes lies apart from what it still reads."""
@@ -58,8 +59,10 @@ class TrainLayer:
         self.wr, self.w1, self.w2, self.ws1, self.bs1, self.ws2, self.bs2 = wr, w1, w2, ws1, bs1, ws2, bs2
         self.E, self.K, self.k = wr.shape[0], wr.shape[1], k
         self.I, self.Is = w2.shape[2], ws2.shape[1]
-        if any(n % 64 for n in (self.E, self.K, self.I, self.Is)):
-            raise ValueError("E, K, I and Is must be multiples of 64 (moe_wgrad)")
+        if any(n % 64 for n in (self.K, self.I, self.Is)):
+            raise ValueError("K, I and Is must be multiples of 64 (moe_wgrad)")
+        if not (1 <= k <= 32 and k <= self.E <= 1024):
+            raise ValueError("need 1 <= k <= 32 and k <= E <= 1024 (moe_router_loss)")
         self._check_weights()
         self.coef = (balance_coef, z_coef)
         dev, bf = wr.device, torch.bfloat16
@@ -83,10 +86,15 @@ class TrainLayer:
         self.zeros = torch.zeros((T, 1), dtype=i32, device=dev)
         self.dh, self.dgu, self.dw, self.dx_pairs = new(P, I), new(P, 2 * I), new(T, k, dtype=f32), new(P, K)
         self.dhs, self.dgs = new(T, Is), new(T, 2 * Is)
-        self.d_logits, self.d_logits16, self.dx_router = new(T, E, dtype=f32), new(T, E), new(T, K)
+        # the router's gradient products take E in multiples of 64: columns of zeros in d_logits and,
+        # where there are any, a copy of wr with rows of zeros, made by every backward
+        self.Ep = (E + 63) // 64 * 64
+        self.d_logits, self.d_logits16, self.dx_router = new(T, E, dtype=f32), torch.zeros((T, self.Ep), dtype=bf, device=dev), new(T, K)
+        self.wr_rows = None if self.Ep == E else torch.zeros((self.Ep, K), dtype=bf, device=dev)
+        self.grad_wr = new(self.Ep, K, dtype=f32)
         self.counts, self.prob_mean, self.loss = new(E, dtype=i32), new(E, dtype=f32), new(3, dtype=f32)
         self.status = torch.zeros(4, dtype=i32, device=dev)
-        self.grads = {"wr": new(E, K, dtype=f32), "w1": new(E, 2 * I, K, dtype=f32), "w2t": new(E, I, K, dtype=f32),
+        self.grads = {"wr": self.grad_wr[:E], "w1": new(E, 2 * I, K, dtype=f32), "w2t": new(E, I, K, dtype=f32),
                       "ws1": new(2 * Is, K, dtype=f32), "ws2": new(K, Is, dtype=f32), "bs1": new(2 * Is, dtype=f32),
                       "bs2": new(K, dtype=f32)}
         need = max(moe_router_loss_workspace_size(E), 256,
@@ -163,8 +171,12 @@ class TrainLayer:
         # router: the routing weights' gradient joins the auxiliary losses'
         moe_router_loss(self.logits, self.ids, self.w, self.dw, token_mask, T, k, E, *self.coef, self.counts,
                         self.prob_mean, self.loss, self.d_logits, c)
-        self.d_logits16[:T].copy_(self.d_logits[:T])
-        moe_dense_gemm(self.d_logits16, self.wr, "kn", None, None, 1.0, T, K, E, "none", self.dx_router, c)
+        self.d_logits16[:T, :E].copy_(self.d_logits[:T])
+        wr = self.wr
+        if self.wr_rows is not None:
+            wr = self.wr_rows
+            wr[:E].copy_(self.wr)
+        moe_dense_gemm(self.d_logits16, wr, "kn", None, None, 1.0, T, K, self.Ep, "none", self.dx_router, c)
         moe_pair_sum(self.dx_pairs, self.dx_router, T, k, K, dx, c)
         # shared expert
         cap1, _ = moe_align_capacity(T, 1, BLOCK_M)
@@ -176,6 +188,6 @@ class TrainLayer:
         moe_wgrad(self.dgs, x, 0, T, 1, 1, 2 * Is, K, *one, g["ws1"], 0, c)
         moe_dense_bias_grad(dy, T, K, g["bs2"], c)
         moe_dense_bias_grad(self.dgs, T, 2 * Is, g["bs1"], c)
-        moe_wgrad(self.d_logits16, x, 0, T, 1, 1, E, K, *one, g["wr"], 0, c)
+        moe_wgrad(self.d_logits16, x, 0, T, 1, 1, self.Ep, K, *one, self.grad_wr, 0, c)
         moe_dense_gemm(self.dgs, self.ws1, "kn", None, dx, 1.0, T, K, 2 * Is, "none", dx, c)
         return dx

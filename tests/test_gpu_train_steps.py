@@ -133,3 +133,15 @@ def test_padding_rows_have_no_part_in_any_gradient(moe):
 
     y, dx = step(L, x, dy, torch.from_numpy(mask).cuda())
     compare(L, W, x, dy, y, dx, full=full)
+
+
+@pytest.mark.parametrize("E,k", [(6, 2), (8, 2), (60, 6), (160, 8)])
+def test_any_number_of_experts(moe, E, k):
+    T = 257
+    W, rnd = make(E, E)
+    L = layer(W, k, T)
+    for _ in range(2):
+        x, dy = rnd(T, 256), rnd(T, 256)
+        y, dx = step(L, x, dy)
+        compare(L, W, x, dy, y, dx)
+        W["wr"].copy_(rnd(E, 256, std=0.1))

@@ -49,6 +49,14 @@ def test_host_weights_are_refused():
         layer(weights())
 
 
+@pytest.mark.parametrize("name,shape", [("K", (E, 96)), ("I", (E, K, 96)), ("Is", (K, 96)), ("k", (1, K)), ("E", (1025, K))])
+def test_sizes_are_refused(name, shape):
+    W = weights()
+    W[{"I": "w2", "Is": "ws2"}.get(name, "wr")] = torch.zeros(shape, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="multiples of 64" if name in ("K", "I", "Is") else "1024"):
+        layer(W)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", list(SHAPES))
 @pytest.mark.parametrize("how", ["type", "strides", "expanded", "address"])
