@@ -12,9 +12,12 @@ balance and z losses' in d_logits.
 
 Marshalling only: every step runs in the library's kernels.  ``TrainLayer`` refers to the caller's
 weights, which may change in place between steps (not between a forward and its backward), and
-holds the buffers that live from a forward to its backward, and the workspaces.
+holds what lives from a forward to its backward: the routing, and the pre-activations as MXFP8
+checkpoints (33/64 of their bf16 bytes).  Everything else is scratch, which layers can share.
 """
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -44,15 +47,42 @@ def _apart(a, b, what):
         raise MoeError(-1, f"{what} must not overlap")
 
 
+class Scratch:
+    """Device buffers of which nothing is needed between two passes of a layer: pre-activations and
+    their gradients (one buffer), activations, pair rows, transposed weights, workspaces.  Layers
+    whose passes follow one another in one stream can share one; it grows as layers are made (so make them
+    before a pass is captured into a graph)."""
+
+    def __init__(self, device):
+        self.device, self.version, self._buffers = torch.device(device), 0, {}
+
+    def reserve(self, name, nbytes):
+        have = self._buffers.get(name)
+        if have is None or have.numel() < nbytes:
+            self._buffers[name] = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            self.version += 1
+
+    def view(self, name, dtype, *shape):
+        n = dtype.itemsize
+        for s in shape:
+            n *= s
+        return self._buffers[name][:n].view(dtype).view(shape)
+
+    def nbytes(self):
+        return sum(b.numel() for b in self._buffers.values())
+
+
 class TrainLayer:
     """wr [E, K], w1 [E, 2I, K], w2 [E, K, I], ws1 [2Is, K], ws2 [K, Is], bs1 [2Is], bs2 [K]: bf16
     device tensors; K, I and Is multiples of 64, 1 <= k <= 32, k <= E <= 1024.  Batches of up to
     ``max_rows`` tokens.
 
     Every operand is checked before anything is launched (MoeError): type, shape, density,
-    alignment and device, and that what a pass writes lies apart from what it still reads."""
+    alignment and device, and that what a pass writes lies apart from what it still reads.
 
-    def __init__(self, wr, w1, w2, ws1, bs1, ws2, bs2, k, max_rows, balance_coef=0.01, z_coef=0.001):
+    ``scratch``: a ``Scratch`` to share with other layers (``other.scratch``); its own by default."""
+
+    def __init__(self, wr, w1, w2, ws1, bs1, ws2, bs2, k, max_rows, balance_coef=0.01, z_coef=0.001, scratch=None):
         for what, t, dims in (("wr", wr, 2), ("w2", w2, 3), ("ws2", ws2, 2)):  # those that the sizes come from
             if not isinstance(t, torch.Tensor) or t.dim() != dims:
                 raise MoeError(-1, f"{what}: need a torch tensor of {dims} dimensions")
@@ -73,24 +103,16 @@ class TrainLayer:
         self.logits, self.ids, self.w = new(T, E, dtype=f32), new(T, k, dtype=i32), new(T, k, dtype=f32)
         self.cap, blocks = moe_align_capacity(P, E, BLOCK_M)
         self.sorted, self.expert_ids, self.ntpp = new(self.cap, dtype=i32), new(blocks, dtype=i32), new(4, dtype=i32)
-        # the experts' input gradients contract over their outputs: room for a transposed copy of w2,
-        # then of w1, made by every backward from the weights as they are then
-        self.wt = new(E * 2 * I * K)
-        self.gu, self.h, self.o = new(P, 2 * I), new(P, I), new(P, K)
         self.codes, self.scales = new(P, 2 * I, dtype=u8), new(P, 2 * I // 32, dtype=u8)
-        self.gs, self.hs, self.routed = new(T, 2 * Is), new(T, Is), new(T, K)
         self.codes_s, self.scales_s = new(T, 2 * Is, dtype=u8), new(T, 2 * Is // 32, dtype=u8)
         # every token once, for the dense layers' weight gradients (one expert)
         self.cap1, blocks1 = moe_align_capacity(T, 1, BLOCK_M)
         self.sorted1, self.expert_ids1, self.ntpp1 = new(self.cap1, dtype=i32), new(blocks1, dtype=i32), new(4, dtype=i32)
         self.zeros = torch.zeros((T, 1), dtype=i32, device=dev)
-        self.dh, self.dgu, self.dw, self.dx_pairs = new(P, I), new(P, 2 * I), new(T, k, dtype=f32), new(P, K)
-        self.dhs, self.dgs = new(T, Is), new(T, 2 * Is)
-        # the router's gradient products take E in multiples of 64: columns of zeros in d_logits and,
-        # where there are any, a copy of wr with rows of zeros, made by every backward
+        self.d_logits = new(T, E, dtype=f32)
+        # the router's gradient products take E in multiples of 64: columns of zeros in d_logits and
+        # rows of zeros in a copy of wr
         self.Ep = (E + 63) // 64 * 64
-        self.d_logits, self.d_logits16, self.dx_router = new(T, E, dtype=f32), torch.zeros((T, self.Ep), dtype=bf, device=dev), new(T, K)
-        self.wr_rows = None if self.Ep == E else torch.zeros((self.Ep, K), dtype=bf, device=dev)
         self.grad_wr = new(self.Ep, K, dtype=f32)
         self.counts, self.prob_mean, self.loss = new(E, dtype=i32), new(E, dtype=f32), new(3, dtype=f32)
         self.status = torch.zeros(4, dtype=i32, device=dev)
@@ -100,7 +122,32 @@ class TrainLayer:
         need = max(moe_router_loss_workspace_size(E), 256,
                    *(moe_wgrad_workspace_size(e, n, kin, BLOCK_M, c) for e, n, kin, c in
                      [(E, 2 * I, K, self.cap), (E, I, K, self.cap), (1, 2 * Is, K, self.cap1), (1, K, Is, self.cap1)]))
-        self.workspace = torch.empty(need, dtype=u8, device=dev)
+        self.scratch = Scratch(dev) if scratch is None else scratch
+        if self.scratch.device != dev:
+            raise MoeError(-1, f"scratch: need one on {dev}, got {self.scratch.device}")
+        # name: (type, shape, what it is reserved as)
+        self._views, self._bound = {
+            "workspace": (u8, (need,), "workspace"),
+            # the experts' input gradients contract over their outputs: a transposed copy of w2, then of
+            # w1, made by every backward from the weights as they are then
+            "wt": (bf, (E * 2 * I * K,), "wt"),
+            "gu": (bf, (P, 2 * I), "gu"), "dgu": (bf, (P, 2 * I), "gu"),  # gu is done with when its checkpoint is written
+            "h": (bf, (P, I), "h"), "dh": (bf, (P, I), "dh"), "dw": (f32, (T, k), "dw"),
+            "o": (bf, (P, K), "pairs"), "dx_pairs": (bf, (P, K), "pairs"),
+            "gs": (bf, (T, 2 * Is), "gs"), "dgs": (bf, (T, 2 * Is), "gs"),
+            "hs": (bf, (T, Is), "hs"), "dhs": (bf, (T, Is), "dhs"),
+            "routed": (bf, (T, K), "rows"), "dx_router": (bf, (T, K), "rows"),
+            "d_logits16": (bf, (T, self.Ep), "d_logits16"), "wr_rows": (bf, (self.Ep if self.Ep != E else 0, K), "wr_rows"),
+        }, None
+        for dtype, shape, buffer in self._views.values():
+            self.scratch.reserve(buffer, dtype.itemsize * math.prod(shape))
+
+    def _bind(self):
+        """Attributes for the scratch, again where another layer has made it grow."""
+        if self._bound != self.scratch.version:
+            for name, (dtype, shape, buffer) in self._views.items():
+                setattr(self, name, self.scratch.view(buffer, dtype, *shape))
+            self._bound = self.scratch.version
 
     def _check_weights(self):
         E, K, I, Is, dev = self.E, self.K, self.I, self.Is, self.wr.device
@@ -111,6 +158,7 @@ class TrainLayer:
             raise MoeError(-1, f"wr: need weights on a CUDA device, got {dev}")
 
     def _ctx(self):
+        self._bind()
         return Ctx(workspace=self.workspace, dev_status=self.status)
 
     def forward(self, x, y):
@@ -173,9 +221,11 @@ class TrainLayer:
                         self.prob_mean, self.loss, self.d_logits, c)
         self.d_logits16[:T, :E].copy_(self.d_logits[:T])
         wr = self.wr
-        if self.wr_rows is not None:
+        if self.Ep != E:
+            self.d_logits16[:T, E:].zero_()
             wr = self.wr_rows
             wr[:E].copy_(self.wr)
+            wr[E:].zero_()
         moe_dense_gemm(self.d_logits16, wr, "kn", None, None, 1.0, T, K, self.Ep, "none", self.dx_router, c)
         moe_pair_sum(self.dx_pairs, self.dx_router, T, k, K, dx, c)
         # shared expert

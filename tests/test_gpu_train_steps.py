@@ -145,3 +145,36 @@ def test_any_number_of_experts(moe, E, k):
         y, dx = step(L, x, dy)
         compare(L, W, x, dy, y, dx)
         W["wr"].copy_(rnd(E, 256, std=0.1))
+
+
+def test_layers_that_share_scratch(moe):
+    """Two layers of different sizes, both forward before either goes back."""
+    k, T = 4, 300
+    (Wa, rnd), (Wb, _) = make(21, 64), make(22, 60, I=192, Is=128)
+    A = layer(Wa, k, T)
+    B = layer(Wb, k, T + 50, scratch=A.scratch)
+    x, dy = [rnd(T, 256) for _ in range(2)], [rnd(T, 256) for _ in range(2)]
+    y, dx = [torch.empty_like(x[0]) for _ in range(2)], [torch.empty_like(x[0]) for _ in range(2)]
+    for _ in range(2):
+        A.forward(x[0], y[0])
+        B.forward(x[1], y[1])
+        B.backward(dy[1], dx[1])
+        A.backward(dy[0], dx[0])
+        torch.cuda.synchronize()
+        compare(A, Wa, x[0], dy[0], y[0], dx[0])
+        compare(B, Wb, x[1], dy[1], y[1], dx[1])
+
+
+def test_a_layer_holds_checkpoints_and_not_pre_activations(moe):
+    """What a further layer holds beside its gradients is below the bf16 pre-activations' bytes."""
+    E, K, I, Is, k, T = 8, 256, 512, 512, 8, 4096
+    W, _ = make(23, E, K, I, Is)
+    A = layer(W, k, T)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    B = layer(W, k, T, scratch=A.scratch)
+    more = torch.cuda.memory_allocated() - before
+    grads = sum(t.numel() * 4 for t in B.grads.values())
+    bf16 = 2 * (T * k * 2 * I + T * 2 * Is)
+    assert more - grads < 0.6 * bf16, (more, grads, bf16)
+    assert A.scratch.nbytes() > bf16
