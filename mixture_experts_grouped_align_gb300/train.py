@@ -172,6 +172,8 @@ class TrainLayer:
         _apart(x, y, "x and y")
         T, k, E, K, I, Is, c = x.shape[0], self.k, self.E, self.K, self.I, self.Is, self._ctx()
         self.T, self.x = T, x
+        if T == 0:
+            return y
         moe_dense_gemm(x, self.wr, "nk", None, None, 1.0, T, E, K, "none", self.logits, c)
         cap, _ = moe_align_capacity(T * k, E, BLOCK_M)
         moe_align(self.logits, self.ids, self.w, T, k, E, BLOCK_M, self.sorted, cap, self.expert_ids, self.ntpp, None, c)
@@ -206,6 +208,10 @@ class TrainLayer:
         if token_mask is not None:
             _check(token_mask, "token_mask", torch.uint8, dev, numel=x.shape[0])
         T, k, E, K, I, Is, c, g = self.T, self.k, self.E, self.K, self.I, self.Is, self._ctx(), self.grads
+        if T == 0:
+            for t in (*g.values(), self.loss, self.counts, self.prob_mean):
+                t.zero_()
+            return dx
         cap, _ = moe_align_capacity(T * k, E, BLOCK_M)
         args = (T, k, self.sorted, self.expert_ids, self.ntpp, BLOCK_M, cap)
         # routed experts: dh, then the activation from its checkpoint (h is w h again)

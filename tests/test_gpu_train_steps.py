@@ -178,3 +178,15 @@ def test_a_layer_holds_checkpoints_and_not_pre_activations(moe):
     bf16 = 2 * (T * k * 2 * I + T * 2 * Is)
     assert more - grads < 0.6 * bf16, (more, grads, bf16)
     assert A.scratch.nbytes() > bf16
+
+
+def test_a_step_without_tokens(moe):
+    W, rnd = make(24, 64)
+    L = layer(W, 4, 10)
+    x, dy = rnd(10, 256), rnd(10, 256)
+    step(L, x, dy)  # leaves gradients behind
+    y, dx = step(L, x[:0], dy[:0])
+    assert y.shape == dx.shape == (0, 256) and int(L.status[0]) == 0
+    assert not L.loss.any() and not L.counts.any() and not any(g.any() for g in L.grads.values())
+    y, dx = step(L, x, dy)
+    compare(L, W, x, dy, y, dx)
