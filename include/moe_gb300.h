@@ -429,7 +429,9 @@ moe_status moe_act_checkpoint(const void* gu, const float* row_w, int64_t rows, 
  *   d_row_w = sum_i dh_i a_i                                        [rows] fp32, or NULL: the
  *       gradient of the routing weight (moe_router_loss takes it as d_topk_w)
  * in fp32, each rounded once; the sum runs in a fixed order.  A row of weight exactly 0 is left
- * out: its outputs are zeros, whatever dh and the checkpoint hold. */
+ * out: its outputs are zeros, whatever dh and the checkpoint hold -- d_row_w too, which loses
+ * nothing where the weights are a softmax (its gradient takes d_row_w times the weight), but keeps
+ * a weight that is trained by itself at 0 once it is there. */
 moe_status moe_act_backward(const uint8_t* codes, const uint8_t* scales, const void* dh, const float* row_w,
                             int64_t rows, int32_t I, int32_t activation, void* d_gu, void* h, float* d_row_w,
                             const moe_ctx* ctx);

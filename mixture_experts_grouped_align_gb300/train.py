@@ -10,8 +10,13 @@ Backward, from dy [T, K]: the activations' gradients come from the checkpoints, 
 the activations again for the weight gradients; the routing weights' gradients join the
 balance and z losses' in d_logits.
 
-Marshalling only: every step runs in the library's kernels.  ``TrainLayer`` refers to the caller's
-weights, which may change in place between steps (not between a forward and its backward), and
+Marshalling only: products, activations, losses and sums run in the library's kernels; torch moves
+data, namely the transposed copies of w1 and w2 and the rounding of d_logits to bf16.  The products take
+bf16 operands, so dx and the router's gradient see the logits' gradient within 2^-9 of itself, as
+every gradient that passes from one product to the next here; ``d_logits`` itself is fp32.  A
+caller who wants more of the router's gradient has it there.
+
+``TrainLayer`` refers to the caller's weights, which may change in place between steps (not between a forward and its backward), and
 holds what lives from a forward to its backward: the routing, and the pre-activations as MXFP8
 checkpoints (33/64 of their bf16 bytes).  Everything else is scratch, which layers can share.
 """
