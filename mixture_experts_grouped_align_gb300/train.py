@@ -16,9 +16,10 @@ bf16 operands, so dx and the router's gradient see the logits' gradient within 2
 every gradient that passes from one product to the next here; ``d_logits`` itself is fp32.  A
 caller who wants more of the router's gradient has it there.
 
-``TrainLayer`` refers to the caller's weights, which may change in place between steps (not between a forward and its backward), and
-holds what lives from a forward to its backward: the routing, and the pre-activations as MXFP8
-checkpoints (33/64 of their bf16 bytes).  Everything else is scratch, which layers can share.
+``TrainLayer`` refers to the caller's weights, which may change in place between steps (not between
+a forward and its backward), and holds what lives from a forward to its backward: the routing, and
+the pre-activations as MXFP8 checkpoints (33/64 of their bf16 bytes).  Everything else is scratch,
+which layers can share.
 """
 from __future__ import annotations
 
