@@ -1,5 +1,5 @@
-// The dense product (dense_gemm.cu) where its 128 x 256 tiles would leave SMs idle (few rows, or
-// few columns).
+// The dense product where the 256 x 256 tiles of dense_gemm.cu's CTA pairs would leave SMs idle (few
+// rows, or few columns).
 //
 // Bound with few rows: reading W once.  A tile is 128 NA features x BN rows of x with the roles
 // of the operands exchanged (A = 128 weight rows, B = the rows of x), so that one row of x costs
@@ -19,10 +19,13 @@
 //   fit, from before the block's other roles are ready;
 //   warp 1 issues the MMAs; then all sixteen warps drain, add and store.
 //
-// Measured (weights from HBM, back to back): 64 x 2880 -> 2 x 2880 SwiGLU 8.8 us, the weight at
-// 3.8 TB/s; 64 x 7168 -> 2048 7.4 us, 4.0 TB/s; one row 2688 -> 1856 5.0 us; 4099 x 7168 -> 256 in
-// fp32 20.4 us.  Of the small ones about 3 us are the launch's start, the ring's first loads and
-// the cluster's sum, which a longer K hides no part of.
+// Measured back to back in a graph.  Weights from HBM (inputs of 270 MB, twice the L2, in turn): 64 x
+// 2880 -> 2 x 2880 SwiGLU 10.7 us, the weight at 3.1 TB/s; 64 x 7168 -> 2048 10.3 us, 2.8 TB/s; one row
+// 2688 -> 1856 5.7 us; 4099 x 7168 -> 256 in fp32 21.5 us.  With three sets of inputs in turn, whose
+// weights stay in L2: 9.1, 7.4, 5.3 and 20.4.  Of the small ones about 3 us are the launch's start, the
+// ring's first loads and the cluster's sum, which a longer K hides no part of.  Clocks from the work
+// before to the first MMA, the last one, the cluster's meeting, the end (from HBM): 64 rows 5000, 10100,
+// 13500, 17000; one row 3700, 4800, 7400, 9600; 4099 rows 3900, 23200, 27600, 35600.
 #include <math.h>
 
 #include <atomic>
@@ -384,12 +387,13 @@ void resident_ctas(int (&at_once)[9]) {
 // The variant with the least estimated time in clocks.  Per CTA a stage costs what its operands
 // take from L2 (about 60 bytes a clock and SM) or its MMAs on the tensor core (BN / 2 clocks
 // each), whichever is more; a wave of CTAs is as long as its longest share; the sum over the
-// cluster moves about 16 bytes a clock into an SM.  Against every variant timed, over 20 shapes
-// from 47 to 16000 rows: at most 8% from the best (e.g. 300 x 2 x 2880 x 2880 SwiGLU: 15.4 us as
-// 128-row tiles whole in K, 18.2 as 2 x 128 split in two, 20.7 on CTA pairs; 2000 x 2048 x 2048:
-// 18.2 us here, 16.7 on CTA pairs).  Above 64 rows BN goes in steps of 16, which fits ragged M and
-// the number of SMs (4099 x 256 x 7168 20.9 -> 20.3 us, 8192 x 64 x 2880 13.5 -> 13.2, 1000 x 2048 x
-// 2048 10.6 -> 10.3; 300 x 2048 x 2048 8.0 -> 8.3).
+// cluster moves about 16 bytes a clock into an SM.  Against every variant timed, over 25 shapes of 1
+// to 16000 rows with weights from HBM: within 2% of the best in 20, 4 to 5% off in three (128 x 2048 x 2048
+// 6.9 us against 6.7; 4099 x 256 x 7168 fp32 21.6 against 20.6; 2000 x 2 x 2048 x 2048 SwiGLU 26.0 against
+// 24.9 on CTA pairs), 8% in one (47 x 520 x 2880 5.4 against 5.0), and 17% in the worst: 512 x 2 x 2048 x
+// 7168 SwiGLU, 33.4 us as 2 x 256 split in four against 28.6 as 128-row tiles whole in K, whose loads it
+// takes for slower than they are.  Above 64 rows BN goes in steps of 16, which fits ragged M and the
+// number of SMs.
 Split plan(const Dense& d, double* clocks) {
   const int kOut = d.gated ? kFeat / 2 : kFeat;
   Split best{};
