@@ -29,7 +29,9 @@
 // 308 us, 8 303, 16 296, 32 317).
 // Measured: 8192 x 7168 -> 2 x 2048 SwiGLU with bias, short runs 253 us (1.90 PFLOP/s, the library's
 // rate for the product alone; 284 us on single CTAs' 128 x 256 tiles), under the power limit 290 to
-// 300; 8191 x 4096 -> 7168 on the other layout with the residual 279 us.
+// 300; 8191 x 4096 -> 7168 on the other layout with the residual 279 us.  fp32 outputs cost the drain of
+// every chunk besides twice the bytes: 8000 x 4104 -> 7168 368 us (bf16 308, both under the power
+// limit), 4096 x 1032 -> 4104 47 (38), 8192 x 7168 -> 2 x 2048 SwiGLU 263 to 269 (250 to 253).
 // Every wait is bounded; one that runs out sets MOE_ERR_TIMEOUT, all roles leave their loops,
 // the loads in flight are waited for, and both CTAs meet before either ends.
 #include "dense_common.cuh"

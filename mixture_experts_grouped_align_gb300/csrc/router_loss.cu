@@ -22,8 +22,8 @@
 // fixed order into one row of partial sums each, and the last block to finish adds those rows
 // in order, so that repeated calls give the same bits (no floating-point atomics).
 //
-// Measured: 61440 x 128, k 4: 19.6 us for 62.9 MB of rows (3.2 TB/s); 8192 x 256, k 8: 12.7 us;
-// 30000 x 1024, k 8: 53 us (4.6 TB/s); 64 x 128: 5.5 us.  Bound, in that order, by the counts before
+// Measured: 61440 x 128, k 4: 20 us for 62.9 MB of rows (3.1 TB/s), 22 with a mask; 8192 x 256, k 8:
+// 12.7 us; 30000 x 1024, k 8: 53 us (4.6 TB/s); 64 x 128: 4.9 us.  Bound, in that order, by the counts before
 // the pass and the sums behind it (about 6 and 4 us; the rows between them run at 6.6 TB/s), by
 // that chain alone, by the rows, and by one launch with two rounds of loads.
 #include "moe_common.cuh"
