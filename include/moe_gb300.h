@@ -12,7 +12,9 @@
  * (moe_act_checkpoint, moe_act_backward); and, for the dense layers beside the experts (a
  * shared expert, the router's projection), a matrix product with bias, activation and residual
  * in its epilogue and its backward products (moe_dense_gemm, moe_dense_bias_grad), and the sum
- * of a token's pair rows (moe_pair_sum).
+ * of a token's pair rows (moe_pair_sum).  Between layers: dropout, the residual's addition and the
+ * RMS norm, whose output can be the 8-bit operands of the calls above (moe_residual_norm,
+ * moe_residual_norm_backward).
  *
  * Sources of the definitions (pull-request pages):
  *  [BUCKET] "Bound Triton MoE JIT specializations via token-dim bucketing and warmup",
@@ -475,6 +477,67 @@ moe_status moe_dense_bias_grad(const void* dz, int64_t M, int32_t N, float* d_bi
  * y may be residual.  K a multiple of 8, 1 <= k <= 1024, T*k < 2^31. */
 moe_status moe_pair_sum(const void* o, const void* residual, int64_t T, int32_t k, int32_t K, void* y,
                         const moe_ctx* ctx);
+
+/* ------------------------------------------------------------------------------------ *
+ * Residual addition with dropout, and RMS norm                                           *
+ * ------------------------------------------------------------------------------------ */
+
+#define MOE_SCALES_NONE 0 /* no 8-bit output                                              */
+#define MOE_SCALES_MX 1   /* E8M0 bytes [T, K/32]: x_scale of the MXFP8 calls             */
+#define MOE_SCALES_ROW 2  /* fp32 [T]: a_scale of moe_gemm_per_token                      */
+
+/* Dropout of the calls below.  It applies to x: element i (of the flat tensor) is dropped if its
+ * 16-bit number is below d = round(65536 p) (at most 65535), else multiplied by 65536 / (65536 - d)
+ * in fp32.  The number is half of a word of Philox 4x32-10 (Salmon, Moraes, Dror and Shaw, SC 2011):
+ * key words rng[0] mod 2^32 and rng[0] / 2^32, counter words (b mod 2^32, b / 2^32, rng[1] mod 2^32,
+ * rng_stream) with b = i / 8; word (i mod 8) / 2, its low half for even i.  rng (a seed and a step)
+ * lies in device memory, so that a captured call draws other numbers once the program has changed it
+ * there; forward and backward are given the same numbers in it.  rng_stream tells the dropouts of a
+ * model apart. */
+typedef struct {
+  float p;              /* probability, 0 <= p < 1; 0: no dropout, rng is not read        */
+  const int64_t* rng;   /* device [2]: seed, step                                         */
+  uint32_t rng_stream;
+} moe_dropout;
+
+/* Rows that count (token_mask[t] != 0, or all where it is NULL):
+ *   s = residual + dropout(x)                              -> stream [T, K], rounded once
+ *   n = s * (mean_k s^2 + eps)^(-1/2) * weight             (fp32, from s before its rounding)
+ *   out = n in bf16;  codes, scales = n in E4M3: MOE_SCALES_MX by the rule of moe_mx_quantize,
+ *   MOE_SCALES_ROW with scale = max(max_k |n| / 448, 2^-120) and codes of n / scale
+ * x [T, K] bf16 or NULL (nothing is added); residual [T, K] in the stream's type or NULL (zeros), one
+ * of the two at least; token_mask [T] bytes or NULL; weight [K] bf16; stream [T, K] bf16
+ * (stream_f32 == 0) or fp32, or NULL; out [T, K] bf16 or NULL; codes [T, K] and scales as the scale
+ * mode says (MOE_SCALES_NONE: both NULL).  dropout may be NULL (none).
+ *  - Rows that do not count are not read; their rows of stream, out and codes are zeros and their
+ *    scales those of a row of zeros (bytes 0, or 2^-120).
+ *  - A NaN or an infinity in s leaves NaN in its row: row scales NaN with codes 0x7F, MX NaN in the
+ *    blocks that hold a NaN n.  Sums of squares above fp32's range (|s| near 10^18) give n = 0.
+ *  - stream may be residual, and out may be x; other overlaps are not allowed.
+ * Limits: K a multiple of 8 (MOE_SCALES_MX: of 32), K <= 16384, T < 2^31, eps > 0 and finite.  T = 0:
+ * nothing is done.  Needs no workspace. */
+moe_status moe_residual_norm(const void* x, const void* residual, const uint8_t* token_mask, const void* weight,
+                             int64_t T, int32_t K, float eps, const moe_dropout* dropout, int32_t stream_f32, void* stream,
+                             void* out, uint8_t* codes, void* scales, int32_t scale_mode, const moe_ctx* ctx);
+
+/* Workspace bytes of moe_residual_norm_backward with d_weight (0 for K outside its limits). */
+size_t moe_residual_norm_workspace_size(int32_t K);
+
+/* From the stream s as moe_residual_norm stored it, r = (mean_k s^2 + eps)^(-1/2), g = d_out * weight:
+ *   ds = r (g - s r^2 mean_k(g s)) + d_stream
+ *   d_residual = ds;  d_x = ds where x was kept, times its factor, and 0 where it was dropped
+ *   d_weight = sum_t d_out s r
+ * d_out [T, K] bf16: the gradient of out (and of the values that codes stand for); d_stream [T, K] in
+ * the stream's type: what reaches the stream from behind, or NULL; d_residual [T, K] in the stream's
+ * type, d_x [T, K] bf16 and d_weight [K] fp32 may each be NULL.  In fp32, rounded once; d_weight is
+ * summed in a fixed order: repeated calls on a device give identical bits.  Rows that do not count are
+ * not read, add nothing to d_weight, and their rows of d_residual and d_x are zeros.  d_residual may be
+ * d_stream, and d_x may be d_out; other overlaps are not allowed.  Limits as above; d_weight needs
+ * moe_residual_norm_workspace_size(K) bytes of workspace (T = 0 gives zeros). */
+moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, const void* stream,
+                                      const uint8_t* token_mask, const void* weight, int64_t T, int32_t K, float eps,
+                                      const moe_dropout* dropout, int32_t stream_f32, void* d_residual, void* d_x,
+                                      float* d_weight, const moe_ctx* ctx);
 
 /* ------------------------------------------------------------------------------------ *
  * Diagnostics: failure detection of the bounded waits                                    *

@@ -22,7 +22,8 @@ __all__ = [
     "moe_forward_no_alloc", "moe_grouped_gemm", "moe_grouped_gemm_workspace_size", "moe_mx_quantize",
     "moe_gemm_per_token", "moe_wgrad", "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels",
     "moe_router_loss", "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward",
-    "moe_dense_gemm", "moe_dense_gemm_plan", "moe_dense_bias_grad", "moe_pair_sum", "W_LAYOUT", "EXPORTED_SYMBOLS",
+    "moe_dense_gemm", "moe_dense_gemm_plan", "moe_dense_bias_grad", "moe_pair_sum", "moe_residual_norm",
+    "moe_residual_norm_backward", "moe_residual_norm_workspace_size", "W_LAYOUT", "SCALES", "EXPORTED_SYMBOLS",
 ]
 
 MOE_OK = 0
@@ -33,6 +34,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_WARN_PAD_IGNORED", -1: "MOE_ERR_INVALID_ARG
 QUANT = {"bf16": 0, "mxfp4": 1, "mxfp8": 2}
 ACTIVATION = {"swiglu": 0, "relu2": 1, "none": 2}
 W_LAYOUT = {"nk": 0, "kn": 1}
+SCALES = {"none": 0, "mx": 1, "row": 2}
 
 EXPORTED_SYMBOLS = [
     "moe_last_error", "moe_align_capacity", "moe_align", "moe_bucket", "moe_bucket_count",
@@ -40,7 +42,8 @@ EXPORTED_SYMBOLS = [
     "moe_grouped_gemm", "moe_grouped_gemm_workspace_size", "moe_mx_quantize", "moe_gemm_per_token", "moe_wgrad",
     "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels", "moe_router_loss",
     "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward", "moe_dense_gemm",
-    "moe_dense_bias_grad", "moe_pair_sum", "moe_dense_gemm_plan",
+    "moe_dense_bias_grad", "moe_pair_sum", "moe_dense_gemm_plan", "moe_residual_norm", "moe_residual_norm_backward",
+    "moe_residual_norm_workspace_size",
 ]
 
 
@@ -79,8 +82,8 @@ def _load_native():
     loader.exec_module(mod)
     lib = load()
     names = ("moe_router_loss", "moe_act_checkpoint", "moe_act_backward", "moe_dense_gemm", "moe_dense_bias_grad",
-             "moe_pair_sum")
-    mod.setup(_refuse, torch.float32, torch.int32, torch.bfloat16, torch.uint8,
+             "moe_pair_sum", "moe_residual_norm", "moe_residual_norm_backward")
+    mod.setup(_refuse, torch.float32, torch.int32, torch.bfloat16, torch.uint8, torch.int64,
               tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
     _native = mod
     return mod
@@ -124,6 +127,9 @@ def load(path: str | None = None):
         "moe_dense_gemm_plan": (I32, [I64, I32, I32, I32, I32, P]),
         "moe_dense_bias_grad": (I32, [P, I64, I32, P, P]),
         "moe_pair_sum": (I32, [P, P, I64, I32, I32, P, P]),
+        "moe_residual_norm": (I32, [P, P, P, P, I64, I32, F32, P, I32, P, P, P, P, I32, P]),
+        "moe_residual_norm_backward": (I32, [P, P, P, P, P, I64, I32, F32, P, I32, P, P, P, P]),
+        "moe_residual_norm_workspace_size": (SZ, [I32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -362,6 +368,44 @@ def moe_pair_sum(o, residual, T, k, K, y, ctx=None):
     """y [T, K] bf16 = the sums of o [T*k, K]'s rows of each token (+ residual [T, K])."""
     c = ctx or Ctx()
     return _check((_native or _load_native()).pair_sum(o, residual, T, k, K, y, c.address))
+
+
+def _is_f32(t):
+    return t is not None and not isinstance(t, int) and t.dtype.itemsize == 4
+
+
+def moe_residual_norm(x, residual, token_mask, weight, T, K, eps, p, rng, rng_stream, stream, out, codes=None, scales=None,
+                      ctx=None, stream_f32=None, scale_mode=None):
+    """stream [T, K] = residual + dropout(x); out [T, K] bf16 and codes [T, K] (uint8) with scales = its
+    RMS norm times weight.  Dropout of probability ``p`` by the numbers of ``rng`` (int64 [2]: seed, step)
+    and ``rng_stream``.  The stream is bf16 or fp32, the scales E8M0 bytes [T, K / 32] (uint8) or fp32 [T];
+    ``stream_f32`` and ``scale_mode`` ("mx", "row") say which for raw pointers."""
+    if stream_f32 is None:
+        stream_f32 = _is_f32(stream) or _is_f32(residual)
+    if scale_mode is None:
+        scale_mode = 0 if scales is None else 2 if _is_f32(scales) else 1
+    elif isinstance(scale_mode, str):
+        scale_mode = SCALES[scale_mode]
+    c = ctx or Ctx()
+    return _check((_native or _load_native()).residual_norm(x, residual, token_mask, weight, T, K, eps, p, rng, rng_stream,
+                                                            int(stream_f32), stream, out, codes, scales, int(scale_mode),
+                                                            c.address))
+
+
+def moe_residual_norm_workspace_size(K) -> int:
+    return load().moe_residual_norm_workspace_size(K)
+
+
+def moe_residual_norm_backward(d_out, d_stream, stream, token_mask, weight, T, K, eps, p, rng, rng_stream, d_residual,
+                               d_x, d_weight, ctx=None, stream_f32=None):
+    """The gradients of moe_residual_norm's residual, x and weight (fp32 [K]; it takes a workspace) from
+    those of out (and its codes' values) and of the stream, and the stream itself."""
+    if stream_f32 is None:
+        stream_f32 = _is_f32(stream)
+    c = ctx or Ctx()
+    return _check((_native or _load_native()).residual_norm_backward(d_out, d_stream, stream, token_mask, weight, T, K, eps, p,
+                                                                     rng, rng_stream, int(stream_f32), d_residual, d_x,
+                                                                     d_weight, c.address))
 
 
 def moe_debug_stall_tensor_kernels(stall_ns: int) -> None:

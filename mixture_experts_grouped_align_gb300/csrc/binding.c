@@ -16,8 +16,8 @@
 
 #include "moe_gb300.h"
 
-enum { F_ROUTER, F_ACT_FWD, F_ACT_BWD, F_DENSE, F_BIAS, F_PAIRS, F_COUNT };
-enum { T_F32, T_I32, T_BF16, T_U8, T_COUNT };
+enum { F_ROUTER, F_ACT_FWD, F_ACT_BWD, F_DENSE, F_BIAS, F_PAIRS, F_NORM, F_NORM_BWD, F_COUNT };
+enum { T_F32, T_I32, T_BF16, T_U8, T_I64, T_COUNT };
 
 static void* g_fn[F_COUNT];
 static PyObject* g_type[T_COUNT];
@@ -192,10 +192,67 @@ static PyObject* pair_sum(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   CALL(moe_pair_sum, F_PAIRS, o, res, T, (int32_t)k, (int32_t)K, y, ctx);
 }
 
+/* mask [T], weight [K], T, K, eps, p, rng [2], rng_stream, stream_f32: the arguments that both norm calls
+   have, from a[0] on. */
+typedef struct {
+  void *mask, *weight;
+  long long T, K, f32;
+  float eps;
+  moe_dropout drop;
+} norm_args;
+
+static int norm_common(PyObject* const* a, norm_args* v) {
+  long long id;
+  void* rng;
+  if (!I64(a[2], v->T) || !I32(a[3], v->K) || !float_arg(a[4], &v->eps) || !float_arg(a[5], &v->drop.p) ||
+      !int_arg(a[7], 0, UINT32_MAX, &id) || !I32(a[8], v->f32) || !tensor_arg(a[0], "token_mask", T_U8, v->T, &v->mask) ||
+      !tensor_arg(a[1], "weight", T_BF16, v->K, &v->weight) || !tensor_arg(a[6], "rng", T_I64, 2, &rng))
+    return 0;
+  v->drop.rng = rng;
+  v->drop.rng_stream = (uint32_t)id;
+  return 1;
+}
+
+/* x, residual, mask, weight, T, K, eps, p, rng, rng_stream, stream_f32, stream, out, codes, scales, scale mode, ctx */
+static PyObject* residual_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  norm_args v;
+  long long mode;
+  void *x, *res, *stream, *out, *codes, *scales, *ctx;
+  if (!count(n, 17) || !norm_common(a + 2, &v) || !I32(a[15], mode)) return NULL;
+  const int64_t tk = elems(v.T, v.K);
+  const int type = v.f32 ? T_F32 : T_BF16;
+  if (!tensor_arg(a[0], "x", T_BF16, tk, &x) || !tensor_arg(a[1], "residual", type, tk, &res) ||
+      !tensor_arg(a[11], "stream", type, tk, &stream) || !tensor_arg(a[12], "out", T_BF16, tk, &out) ||
+      !tensor_arg(a[13], "codes", T_U8, tk, &codes) ||
+      !tensor_arg(a[14], "scales", mode == MOE_SCALES_ROW ? T_F32 : T_U8, mode == MOE_SCALES_ROW ? v.T : elems(v.T, v.K / 32),
+                  &scales) ||
+      !CTX(a[16], ctx))
+    return NULL;
+  CALL(moe_residual_norm, F_NORM, x, res, v.mask, v.weight, v.T, (int32_t)v.K, v.eps, &v.drop, (int32_t)v.f32, stream, out, codes,
+       scales, (int32_t)mode, ctx);
+}
+
+/* d_out, d_stream, stream, mask, weight, T, K, eps, p, rng, rng_stream, stream_f32, d_residual, d_x, d_weight, ctx */
+static PyObject* residual_norm_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  norm_args v;
+  void *d_out, *d_stream, *stream, *d_res, *d_x, *d_w, *ctx;
+  if (!count(n, 16) || !norm_common(a + 3, &v)) return NULL;
+  const int64_t tk = elems(v.T, v.K);
+  const int type = v.f32 ? T_F32 : T_BF16;
+  if (!tensor_arg(a[0], "d_out", T_BF16, tk, &d_out) || !tensor_arg(a[1], "d_stream", type, tk, &d_stream) ||
+      !tensor_arg(a[2], "stream", type, tk, &stream) || !tensor_arg(a[12], "d_residual", type, tk, &d_res) ||
+      !tensor_arg(a[13], "d_x", T_BF16, tk, &d_x) || !tensor_arg(a[14], "d_weight", T_F32, v.K, &d_w) || !CTX(a[15], ctx))
+    return NULL;
+  CALL(moe_residual_norm_backward, F_NORM_BWD, d_out, d_stream, stream, v.mask, v.weight, v.T, (int32_t)v.K, v.eps, &v.drop,
+       (int32_t)v.f32, d_res, d_x, d_w, ctx);
+}
+
 static PyObject* setup(PyObject* self, PyObject* args) {
   (void)self;
   PyObject *error, *type[T_COUNT], *fns;
-  if (!PyArg_ParseTuple(args, "OOOOOO!", &error, &type[0], &type[1], &type[2], &type[3], &PyTuple_Type, &fns)) return NULL;
+  if (!PyArg_ParseTuple(args, "OOOOOOO!", &error, &type[0], &type[1], &type[2], &type[3], &type[4], &PyTuple_Type, &fns)) return NULL;
   if (PyTuple_GET_SIZE(fns) != F_COUNT) {
     PyErr_Format(PyExc_ValueError, "need %d addresses", (int)F_COUNT);
     return NULL;
@@ -216,7 +273,8 @@ static PyObject* setup(PyObject* self, PyObject* args) {
 
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {{"setup", setup, METH_VARARGS, NULL}, FAST(router_loss), FAST(act_checkpoint), FAST(act_backward),
-                                FAST(dense_gemm), FAST(dense_bias_grad), FAST(pair_sum), {NULL, NULL, 0, NULL}};
+                                FAST(dense_gemm), FAST(dense_bias_grad), FAST(pair_sum), FAST(residual_norm), FAST(residual_norm_backward),
+                                {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__binding(void) {

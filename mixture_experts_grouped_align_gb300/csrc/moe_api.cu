@@ -1,4 +1,5 @@
 // The C ABI (include/moe_gb300.h): argument validation, workspace carving and launches.
+#include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -84,6 +85,8 @@ using moe_host::set_error;
     }                                \
   } while (0)
 
+constexpr int32_t kNormMost = 16384;  // values of a row that moe_residual_norm takes
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 moe_status cuda_status(cudaError_t err, const char* what) {
@@ -141,6 +144,21 @@ int64_t used_blocks_bound(int64_t P, int32_t E, int32_t bm, int64_t cap_tokens) 
   int64_t b = (P + bm - 1) / bm + (E < P ? E : P);
   int64_t cap_blocks = cap_tokens / bm;
   return b < cap_blocks ? b : cap_blocks;
+}
+
+// The dropout's fields of a launch.
+template <typename P>
+void set_dropout(P& p, const moe_dropout* d) {
+  p.drop_below = 0;
+  p.gain = 1.f;
+  p.rng = nullptr;
+  p.rng_stream = 0;
+  if (d == nullptr || d->p == 0.f) return;
+  const double below = nearbyint((double)d->p * 65536.0);
+  p.drop_below = below > 65535.0 ? 65535u : (uint32_t)below;
+  p.gain = (float)(65536.0 / (65536.0 - p.drop_below));
+  p.rng = d->rng;
+  p.rng_stream = d->rng_stream;
 }
 
 }  // namespace
@@ -791,6 +809,77 @@ moe_status moe_pair_sum(const void* o, const void* residual, int64_t T, int32_t 
               "all pointers must be 16-byte aligned");
   rec(ctx, 0, 2);
   const moe_status st = cuda_status(moe_launch::pair_sum(o, residual, T, k, K, y, stream_of(ctx)), "moe_pair_sum");
+  rec(ctx, 1, 2);
+  return st;
+}
+
+size_t moe_residual_norm_workspace_size(int32_t K) {
+  return K >= 8 && K % 8 == 0 && K <= kNormMost ? moe_launch::residual_norm_workspace_bytes(K) : 0;
+}
+
+static moe_status check_norm(int64_t T, int32_t K, float eps, const moe_dropout* d) {
+  MOE_REQUIRE(T >= 0 && K >= 1, MOE_ERR_INVALID_ARG, "need T >= 0 and K >= 1");
+  MOE_REQUIRE(K % 8 == 0 && K <= kNormMost, MOE_ERR_UNSUPPORTED, "K must be a multiple of 8 and at most %d", kNormMost);
+  MOE_REQUIRE(T < ((int64_t)1 << 31), MOE_ERR_UNSUPPORTED, "T must be < 2^31");
+  MOE_REQUIRE(eps > 0.f && eps <= 3.4028235e38f, MOE_ERR_INVALID_ARG, "eps must be positive and finite");
+  if (d) {
+    MOE_REQUIRE(d->p >= 0.f && d->p < 1.f, MOE_ERR_INVALID_ARG, "the dropout probability must be in [0, 1)");
+    MOE_REQUIRE(d->p == 0.f || d->rng, MOE_ERR_INVALID_ARG, "dropout needs rng");
+    MOE_REQUIRE(d->p == 0.f || aligned16(d->rng), MOE_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+  }
+  return MOE_OK;
+}
+
+moe_status moe_residual_norm(const void* x, const void* residual, const uint8_t* token_mask, const void* weight,
+                             int64_t T, int32_t K, float eps, const moe_dropout* dropout, int32_t stream_f32, void* stream,
+                             void* out, uint8_t* codes, void* scales, int32_t scale_mode, const moe_ctx* ctx) {
+  moe_status st = check_norm(T, K, eps, dropout);
+  if (st != MOE_OK) return st;
+  MOE_REQUIRE(scale_mode == MOE_SCALES_NONE || scale_mode == MOE_SCALES_MX || scale_mode == MOE_SCALES_ROW,
+              MOE_ERR_INVALID_ARG, "unknown scale mode");
+  MOE_REQUIRE(scale_mode != MOE_SCALES_MX || K % 32 == 0, MOE_ERR_UNSUPPORTED, "K must be a multiple of 32 for MX scales");
+  if (T == 0) return MOE_OK;
+  MOE_REQUIRE((x || residual) && weight, MOE_ERR_INVALID_ARG, "null x and residual, or null weight");
+  MOE_REQUIRE(scale_mode == MOE_SCALES_NONE ? !codes && !scales : codes && scales, MOE_ERR_INVALID_ARG,
+              "codes and scales go with a scale mode, both or none");
+  MOE_REQUIRE(stream || out || codes, MOE_ERR_INVALID_ARG, "no output");
+  MOE_REQUIRE(aligned16(x) && aligned16(residual) && aligned16(token_mask) && aligned16(weight) && aligned16(stream) &&
+                  aligned16(out) && aligned16(codes) && aligned16(scales),
+              MOE_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+  moe_launch::ResidualNorm p{};
+  p.x = x; p.residual = residual; p.mask = token_mask; p.weight = weight; p.T = T; p.K = K; p.eps = eps;
+  p.stream_f32 = stream_f32 ? 1 : 0; p.stream = stream; p.out = out; p.quant = scale_mode; p.codes = codes;
+  p.scales = scales;
+  set_dropout(p, dropout);
+  rec(ctx, 0, 2);
+  st = cuda_status(moe_launch::residual_norm(p, stream_of(ctx)), "moe_residual_norm");
+  rec(ctx, 1, 2);
+  return st;
+}
+
+moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, const void* stream,
+                                      const uint8_t* token_mask, const void* weight, int64_t T, int32_t K, float eps,
+                                      const moe_dropout* dropout, int32_t stream_f32, void* d_residual, void* d_x,
+                                      float* d_weight, const moe_ctx* ctx) {
+  moe_status st = check_norm(T, K, eps, dropout);
+  if (st != MOE_OK) return st;
+  MOE_REQUIRE(T == 0 || (d_out && stream && weight), MOE_ERR_INVALID_ARG, "null tensor pointer");
+  MOE_REQUIRE(T == 0 || d_residual || d_x || d_weight, MOE_ERR_INVALID_ARG, "no output");
+  MOE_REQUIRE(aligned16(d_out) && aligned16(d_stream) && aligned16(stream) && aligned16(token_mask) && aligned16(weight) &&
+                  aligned16(d_residual) && aligned16(d_x) && aligned16(d_weight),
+              MOE_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+  moe_launch::ResidualNormBackward p{};
+  if (d_weight && T > 0) {
+    const size_t need = moe_residual_norm_workspace_size(K);
+    MOE_REQUIRE(ctx && ctx->workspace && ctx->workspace_bytes >= need && aligned16(ctx->workspace), MOE_ERR_CAPACITY,
+                "workspace of %zu bytes needed", need);
+    p.parts = static_cast<float*>(ctx->workspace);
+  }
+  p.d_out = d_out; p.d_stream = d_stream; p.stream = stream; p.mask = token_mask; p.weight = weight; p.T = T; p.K = K;
+  p.eps = eps; p.stream_f32 = stream_f32 ? 1 : 0; p.d_residual = d_residual; p.d_x = d_x;
+  set_dropout(p, dropout);
+  rec(ctx, 0, 2);
+  st = cuda_status(moe_launch::residual_norm_backward(p, d_weight, stream_of(ctx)), "moe_residual_norm_backward");
   rec(ctx, 1, 2);
   return st;
 }

@@ -288,4 +288,46 @@ cudaError_t column_sum(const void* x, int64_t M, int64_t N, float* out, cudaStre
 // ---- sum of a token's pair rows (pair_sum.cu)
 cudaError_t pair_sum(const void* o, const void* residual, int64_t T, int k, int K, void* y, cudaStream_t stream);
 
+// ---- residual addition, dropout and RMS norm (residual_norm.cu)
+struct ResidualNorm {
+  const void* x;         // [T, K] bf16 or null
+  const void* residual;  // [T, K] in the stream's type or null
+  const uint8_t* mask;   // [T] or null
+  const void* weight;    // [K] bf16
+  int64_t T;
+  int K;
+  float eps;
+  uint32_t drop_below;   // a value is dropped if its 16-bit number is below this (0: no dropout)
+  float gain;            // factor of the kept ones
+  const int64_t* rng;    // seed, step
+  uint32_t rng_stream;
+  int stream_f32;
+  void* stream;          // [T, K] bf16 or fp32, or null
+  void* out;             // [T, K] bf16 or null
+  int quant;             // 0 none, 1 MX, 2 a scale per row
+  uint8_t* codes;        // [T, K]
+  void* scales;          // uint8 [T, K / 32] or fp32 [T]
+};
+struct ResidualNormBackward {
+  const void* d_out;     // [T, K] bf16
+  const void* d_stream;  // [T, K] in the stream's type or null
+  const void* stream;    // [T, K]
+  const uint8_t* mask;
+  const void* weight;
+  int64_t T;
+  int K;
+  float eps;
+  uint32_t drop_below;
+  float gain;
+  const int64_t* rng;
+  uint32_t rng_stream;
+  int stream_f32;
+  void* d_residual;      // [T, K] in the stream's type or null
+  void* d_x;             // [T, K] bf16 or null
+  float* parts;          // scratch for d_weight, or null
+};
+size_t residual_norm_workspace_bytes(int K);
+cudaError_t residual_norm(const ResidualNorm& p, cudaStream_t stream);
+cudaError_t residual_norm_backward(ResidualNormBackward p, float* d_weight, cudaStream_t stream);
+
 }  // namespace moe_launch

@@ -1,0 +1,500 @@
+// Residual addition with dropout and the root-mean-square norm, with 8-bit outputs, and the backward
+// pass.
+//
+// Forward, per row of K values that counts (mask):
+//   s = residual + drop(x)                          stored in the stream's type (bf16 or fp32)
+//   n = s r w,  r = (mean(s^2) + eps)^(-1/2)        from the unrounded s, in fp32
+//   out = bf16(n);  MX: mxq's rule per 32 values;  row: max |n| / 448 and E4M3(n 448 / max |n|)
+// Backward, from the stored stream s alone (its row gives r again), with g = d_out w:
+//   ds = r (g - s r^2 mean(g s)) + d_stream;  d_residual = ds;  d_x = drop'(ds)
+//   d_w = sum over rows of d_out s r
+// Dropout draws its numbers again in both passes, so there is no mask to write or read: Philox 4x32
+// with ten rounds (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC
+// 2011) on the counter (index / 8, step, stream) under the seed.  Its 128 bits are eight 16-bit
+// numbers, one for each of the eight values that a thread moves as 16 bytes: 20 wide multiplications
+// for eight values instead of the 40 that 32-bit numbers would take, at the price of a probability in
+// steps of 2^-16.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "moe_common.cuh"
+#include "moe_launch.h"
+#include "mx_quant.cuh"
+
+namespace {
+
+using moe_launch::ResidualNorm;
+using moe_launch::ResidualNormBackward;
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kThreads = 256;  // of a block whose rows are narrow
+
+MOE_DEV void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+MOE_DEV uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight values of the residual stream as they are loaded and stored.
+template <bool F32>
+struct Eight {
+  uint4 v[F32 ? 2 : 1];
+  MOE_DEV void load(const void* p, int64_t unit) {
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) v[i] = __ldcs(static_cast<const uint4*>(p) + unit * (F32 ? 2 : 1) + i);
+  }
+  MOE_DEV void zero() {
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  MOE_DEV void get(float (&f)[8]) const {
+    if (F32) {
+      const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[F32].x, v[F32].y, v[F32].z, v[F32].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    } else {
+      unpack8(v[0], f);
+    }
+  }
+  MOE_DEV static void store(void* p, int64_t unit, const float (&f)[8]) {
+    uint4* q = static_cast<uint4*>(p) + unit * (F32 ? 2 : 1);
+    if (F32) {
+      __stcs(q, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+      __stcs(q + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+    } else {
+      __stcs(q, pack8(f));
+    }
+  }
+};
+
+// The generator's key and the counter's constant half; below is what drops an element (16 bits).
+struct Dropout {
+  uint32_t k0, k1, step, stream, below;
+  float gain;
+  MOE_DEV void init(const int64_t* rng, uint32_t stream_id, uint32_t drop_below, float kept_gain) {
+    below = drop_below;
+    gain = kept_gain;
+    stream = stream_id;
+    k0 = k1 = step = 0;
+    if (below) {
+      const uint64_t seed = (uint64_t)rng[0];
+      k0 = (uint32_t)seed;
+      k1 = (uint32_t)(seed >> 32);
+      step = (uint32_t)rng[1];
+    }
+  }
+  // f = gain f or 0, for the eight values of unit `unit` of the flat tensor
+  MOE_DEV void apply(int64_t unit, float (&f)[8]) const {
+    if (!below) return;
+    uint32_t c0 = (uint32_t)unit, c1 = (uint32_t)((uint64_t)unit >> 32), c2 = step, c3 = stream, a = k0, b = k1;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+      const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
+      c0 = (uint32_t)(p1 >> 32) ^ c1 ^ a;
+      c1 = (uint32_t)p1;
+      c2 = (uint32_t)(p0 >> 32) ^ c3 ^ b;
+      c3 = (uint32_t)p0;
+      a += 0x9E3779B9u;
+      b += 0xBB67AE85u;
+    }
+    const uint32_t w[4] = {c0, c1, c2, c3};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = (w[i] & 0xffffu) >= below ? __fmul_rn(f[2 * i], gain) : 0.f;
+      f[2 * i + 1] = (w[i] >> 16) >= below ? __fmul_rn(f[2 * i + 1], gain) : 0.f;
+    }
+  }
+};
+
+// Rows of a block: WIDE = the whole block on one row, otherwise 32 / LANES rows a warp.  A thread
+// holds V eights of its row, kStep apart, so that a row is loaded at once and read once.
+template <int LANES, bool WIDE, int V>
+struct Map {
+  static constexpr int kLanes = LANES, kV = V;
+  static constexpr bool kWide = WIDE;
+  static constexpr int kMost = !WIDE ? kThreads : (V >= 4 ? 512 : 1024);  // threads of a block
+  MOE_DEV static int rows() { return WIDE ? 1 : kThreads / LANES; }
+  MOE_DEV static int group() { return WIDE ? 0 : threadIdx.x / LANES; }
+  MOE_DEV static int col() { return WIDE ? threadIdx.x : threadIdx.x % LANES; }
+  MOE_DEV static int step() { return WIDE ? blockDim.x : LANES; }
+};
+
+// Sums (and a maximum of non-negative float bits) over the lanes of a row, in a fixed order; every
+// thread of the block calls.  `red`: 2 x 32 words of shared memory for WIDE; the caller separates
+// two uses of it by a barrier.
+template <typename M>
+MOE_DEV void reduce(float& a, float& b, float (*red)[32]) {
+#pragma unroll
+  for (int o = M::kLanes / 2; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(kAll, a, o);
+    b += __shfl_xor_sync(kAll, b, o);
+  }
+  if (M::kWide) {
+    if ((threadIdx.x & 31) == 0) {
+      red[0][threadIdx.x >> 5] = a;
+      red[1][threadIdx.x >> 5] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+    const int warps = blockDim.x >> 5;
+    for (int i = 0; i < warps; ++i) {
+      a += red[0][i];
+      b += red[1][i];
+    }
+  }
+}
+template <typename M>
+MOE_DEV void reduce_max(float& a, uint32_t& m, float (*red)[32]) {
+#pragma unroll
+  for (int o = M::kLanes / 2; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(kAll, a, o);
+    m = max(m, __shfl_xor_sync(kAll, m, o));
+  }
+  if (M::kWide) {
+    if ((threadIdx.x & 31) == 0) {
+      red[0][threadIdx.x >> 5] = a;
+      red[1][threadIdx.x >> 5] = __uint_as_float(m);
+    }
+    __syncthreads();
+    a = 0.f;
+    m = 0;
+    const int warps = blockDim.x >> 5;
+    for (int i = 0; i < warps; ++i) {
+      a += red[0][i];
+      m = max(m, __float_as_uint(red[1][i]));
+    }
+  }
+}
+
+// E4M3 codes of eight values, saturated at 448, NaN kept.
+MOE_DEV uint2 codes8(const float (&v)[8], float by) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * by, v[2 * i + 1] * by), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// MXFP8 of a 32-value block held eight values a lane by four neighbouring lanes, all of which call:
+// mxq::quant32's rule.
+MOE_DEV uint2 quant8(const float (&v)[8], uint32_t& scale) {
+  uint32_t b = 0;  // magnitudes are ordered like their bits, NaN above all
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b = max(b, __float_as_uint(v[i]) & 0x7fffffffu);
+  b = max(b, __shfl_xor_sync(kAll, b, 1));
+  b = max(b, __shfl_xor_sync(kAll, b, 2));
+  if (b > 0x7f800000u) {
+    scale = 255u;
+    return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+  }
+  const int e = mxq::block_exponent(__uint_as_float(b));
+  scale = (uint32_t)(e + 127);
+  return codes8(v, e >= 127 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(127 - e) << 23));
+}
+
+// The smallest scale of a row: zero rows have it, and 1 / scale stays finite.
+constexpr float kRowScaleMin = 0x1p-120f;
+
+// QUANT: 0 no codes, 1 a power of two per 32 values, 2 a scale per row.
+template <bool F32, int QUANT, typename M>
+__global__ void __launch_bounds__(M::kMost) residual_norm_kernel(ResidualNorm p) {
+  constexpr int V = M::kV;
+  __shared__ float red[2][32];
+  moe::wait_for_stream();
+  moe::let_next_start();
+  const int64_t row = (int64_t)blockIdx.x * M::rows() + M::group();
+  const int units = p.K / 8;
+  const bool in = row < p.T;
+  const bool live = in && (p.mask == nullptr || p.mask[row] != 0);
+  const int64_t u0 = row * units;
+  Dropout drop;
+  drop.init(p.rng, p.rng_stream, p.x ? p.drop_below : 0u, p.gain);
+
+  Eight<F32> res[V];
+  uint4 x[V], w[V];
+#pragma unroll
+  for (int t = 0; t < V; ++t) {
+    const int c = M::col() + t * M::step();
+    const bool on = live && c < units;
+    if (on && p.residual) res[t].load(p.residual, u0 + c);
+    else res[t].zero();
+    x[t] = on && p.x ? __ldcs(static_cast<const uint4*>(p.x) + u0 + c) : make_uint4(0, 0, 0, 0);
+    w[t] = c < units ? static_cast<const uint4*>(p.weight)[c] : make_uint4(0, 0, 0, 0);
+  }
+  float s[V][8], sum = 0.f;
+  uint32_t top = 0;
+#pragma unroll
+  for (int t = 0; t < V; ++t) {
+    const int c = M::col() + t * M::step();
+    float f[8];
+    res[t].get(s[t]);
+    if (p.x) {
+      unpack8(x[t], f);
+      if (live && c < units) drop.apply(u0 + c, f);
+      // a product and a sum, each rounded: the stored stream does not depend on how they are contracted
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[t][i] = __fadd_rn(s[t][i], f[i]);
+    }
+    if (p.stream && in && c < units) Eight<F32>::store(p.stream, u0 + c, s[t]);
+    if (QUANT == 2) unpack8(w[t], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sum += s[t][i] * s[t][i];
+      if (QUANT == 2) top = max(top, __float_as_uint(s[t][i] * f[i]) & 0x7fffffffu);
+    }
+  }
+  if (QUANT == 2) {
+    reduce_max<M>(sum, top, red);
+  } else {
+    float none = 0.f;
+    reduce<M>(sum, none, red);
+  }
+  const float r = 1.f / sqrtf(sum / (float)p.K + p.eps);
+  float by = 0.f;
+  if (QUANT == 2) {
+    // the largest |n| is that of the same products in the same order up to two roundings: taken as
+    // |s w| r it may be 2^-23 off the largest code's value, which saturates at 448 all the same
+    const float most = __uint_as_float(top) * r;
+    const bool nan = !(most <= 3.4028235e38f);  // an infinity, too, leaves NaN in its row
+    const float scale = nan ? __uint_as_float(0x7fc00000u) : fmaxf(most / 448.f, kRowScaleMin);
+    by = nan ? scale : (most / 448.f >= kRowScaleMin ? 448.f / most : 1.f / kRowScaleMin);
+    if (in && M::col() == 0) static_cast<float*>(p.scales)[row] = scale;
+  }
+#pragma unroll
+  for (int t = 0; t < V; ++t) {
+    const int c = M::col() + t * M::step();
+    const bool on = in && c < units;
+    float f[8];
+    unpack8(w[t], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = live ? s[t][i] * r * f[i] : 0.f;
+    if (on && p.out) __stcs(static_cast<uint4*>(p.out) + u0 + c, pack8(f));
+    if (QUANT == 1) {
+      uint32_t e;
+      const uint2 q = quant8(f, e);
+      if (on) {
+        __stcs(reinterpret_cast<uint2*>(p.codes) + u0 + c, q);
+        if ((c & 3) == 0) static_cast<uint8_t*>(p.scales)[(u0 + c) >> 2] = (uint8_t)e;
+      }
+    }
+    if (QUANT == 2 && on) __stcs(reinterpret_cast<uint2*>(p.codes) + u0 + c, codes8(f, by));
+  }
+}
+
+// A block walks over rows, so that a thread keeps its columns: their weights and their share of d_w
+// stay in registers.  The shares of a block's rows are added (narrow rows: over its groups), and the
+// blocks' by column_parts_kernel.
+template <bool F32, typename M>
+__global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(ResidualNormBackward p) {
+  constexpr int V = M::kV;
+  __shared__ float red[2][2][32];
+  extern __shared__ float shares[];  // narrow rows: [groups][8 V LANES]
+  moe::wait_for_stream();
+  moe::let_next_start();
+  const int units = p.K / 8;
+  Dropout drop;
+  drop.init(p.rng, p.rng_stream, p.d_x ? p.drop_below : 0u, p.gain);
+  uint4 w[V];
+  float dw[V][8];
+#pragma unroll
+  for (int t = 0; t < V; ++t) {
+    const int c = M::col() + t * M::step();
+    w[t] = c < units ? static_cast<const uint4*>(p.weight)[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[t][i] = 0.f;
+  }
+  int turn = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * M::rows(); row0 < p.T; row0 += (int64_t)gridDim.x * M::rows(), turn ^= 1) {
+    const int64_t row = row0 + M::group();
+    const bool in = row < p.T;
+    const bool live = in && (p.mask == nullptr || p.mask[row] != 0);
+    const int64_t u0 = row * units;
+    Eight<F32> st[V], ds[V];
+    uint4 d[V];
+#pragma unroll
+    for (int t = 0; t < V; ++t) {
+      const int c = M::col() + t * M::step();
+      const bool on = live && c < units;
+      if (on) st[t].load(p.stream, u0 + c);
+      else st[t].zero();
+      d[t] = on ? __ldcs(static_cast<const uint4*>(p.d_out) + u0 + c) : make_uint4(0, 0, 0, 0);
+      if (on && p.d_stream) ds[t].load(p.d_stream, u0 + c);
+      else ds[t].zero();
+    }
+    float sum = 0.f, dot = 0.f;
+#pragma unroll
+    for (int t = 0; t < V; ++t) {
+      float s[8], g[8], f[8];
+      st[t].get(s);
+      unpack8(d[t], g);
+      unpack8(w[t], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum += s[i] * s[i];
+        dot += g[i] * f[i] * s[i];
+      }
+    }
+    reduce<M>(sum, dot, red[turn]);  // two sets in turn: one barrier a row is enough
+    const float r = 1.f / sqrtf(sum / (float)p.K + p.eps), q = r * r * (dot / (float)p.K);
+#pragma unroll
+    for (int t = 0; t < V; ++t) {
+      const int c = M::col() + t * M::step();
+      float s[8], g[8], f[8], o[8];
+      st[t].get(s);
+      unpack8(d[t], g);
+      unpack8(w[t], f);
+      ds[t].get(o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i] = live ? r * (g[i] * f[i] - s[i] * q) + o[i] : 0.f;
+        if (live) dw[t][i] += g[i] * (s[i] * r);
+      }
+      if (in && c < units) {
+        if (p.d_residual) Eight<F32>::store(p.d_residual, u0 + c, o);
+        if (p.d_x) {
+          if (live) drop.apply(u0 + c, o);
+          __stcs(static_cast<uint4*>(p.d_x) + u0 + c, pack8(o));
+        }
+      }
+    }
+  }
+  if (p.parts == nullptr) return;
+  float* mine = p.parts + (int64_t)blockIdx.x * p.K;
+  if (M::kWide) {
+#pragma unroll
+    for (int t = 0; t < V; ++t) {
+      const int c = M::col() + t * M::step();
+      if (c < units) {
+        reinterpret_cast<float4*>(mine)[2 * c] = make_float4(dw[t][0], dw[t][1], dw[t][2], dw[t][3]);
+        reinterpret_cast<float4*>(mine)[2 * c + 1] = make_float4(dw[t][4], dw[t][5], dw[t][6], dw[t][7]);
+      }
+    }
+  } else {
+    constexpr int kCols = 8 * V * M::kLanes;
+#pragma unroll
+    for (int t = 0; t < V; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) shares[M::group() * kCols + (M::col() + t * M::step()) * 8 + i] = dw[t][i];
+    __syncthreads();
+    for (int k = threadIdx.x; k < p.K; k += kThreads) {
+      float a = 0.f;
+      for (int g = 0; g < kThreads / M::kLanes; ++g) a += shares[g * kCols + k];
+      mine[k] = a;
+    }
+  }
+}
+
+// out[k] = the sum over n parts of parts[i][k], in a fixed order: 32 columns a block, eight lanes of
+// four of them, 32 groups of parts.
+__global__ void __launch_bounds__(kThreads) column_parts_kernel(const float* parts, int n, int K, float* out) {
+  __shared__ float4 sums[32][8];
+  moe::wait_for_stream();
+  moe::let_next_start();
+  const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
+  const int k4 = blockIdx.x * 8 + lane;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (4 * k4 < K)
+    for (int i = group; i < n; i += 32) {
+      const float4 v = reinterpret_cast<const float4*>(parts + (int64_t)i * K)[k4];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+  sums[group][lane] = a;
+  __syncthreads();
+  if (group == 0 && 4 * k4 < K) {
+    for (int i = 1; i < 32; ++i) {
+      const float4 v = sums[i][lane];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    reinterpret_cast<float4*>(out)[k4] = a;
+  }
+}
+
+// Rows narrower than a warp's 1024 values share warps; others have a block each.
+template <typename F>
+cudaError_t pick(int64_t T, int K, F launch) {
+  const int units = K / 8;
+  const bool few = T * units < 200000;
+  if (units <= 8) return launch(Map<8, false, 1>{});
+  if (units <= 32) return few ? launch(Map<32, false, 1>{}) : launch(Map<8, false, 4>{});
+  if (units <= 64 && !few) return launch(Map<16, false, 4>{});
+  if (units <= 128 && !few) return launch(Map<32, false, 4>{});
+  if (few && units <= 1024) return launch(Map<32, true, 1>{});
+  return few ? launch(Map<32, true, 2>{}) : launch(Map<32, true, 4>{});
+}
+
+template <typename M>
+int threads_of(int K) {
+  return M::kWide ? ((K / 8 + M::kV - 1) / M::kV + 31) / 32 * 32 : kThreads;
+}
+template <typename M>
+int64_t blocks_of(int64_t T) {
+  const int rows = M::kWide ? 1 : kThreads / M::kLanes;
+  return (T + rows - 1) / rows;
+}
+
+template <bool F32, int QUANT>
+cudaError_t forward(const ResidualNorm& p, cudaStream_t stream) {
+  return pick(p.T, p.K, [&](auto m) {
+    using M = decltype(m);
+    return moe_launch::launch_staged(residual_norm_kernel<F32, QUANT, M>, dim3((unsigned)blocks_of<M>(p.T)),
+                                     dim3((unsigned)threads_of<M>(p.K)), 0, stream, 1, p);
+  });
+}
+
+constexpr int kPartsMost = 608;  // blocks that leave a part of d_w
+
+template <bool F32>
+cudaError_t backward(ResidualNormBackward p, float* d_weight, cudaStream_t stream) {
+  int64_t parts = 0;
+  cudaError_t err = pick(p.T, p.K, [&](auto m) {
+    using M = decltype(m);
+    const int threads = threads_of<M>(p.K);
+    const int64_t most = std::min<int64_t>(kPartsMost, (int64_t)moe_launch::sm_count_current() * std::max(1, 768 / threads));
+    parts = std::min(blocks_of<M>(p.T), most);
+    const size_t smem = M::kWide ? 0 : (size_t)kThreads * 8 * M::kV * 4;
+    return moe_launch::launch_staged(residual_norm_backward_kernel<F32, M>, dim3((unsigned)parts), dim3((unsigned)threads), smem,
+                                     stream, 1, p);
+  });
+  if (err != cudaSuccess || d_weight == nullptr) return err;
+  return moe_launch::launch_staged(column_parts_kernel, dim3((unsigned)((p.K + 31) / 32)), dim3(kThreads), 0, stream, 1,
+                                   (const float*)p.parts, (int)parts, p.K, d_weight);
+}
+
+}  // namespace
+
+namespace moe_launch {
+
+size_t residual_norm_workspace_bytes(int K) { return (size_t)kPartsMost * K * 4; }
+
+cudaError_t residual_norm(const ResidualNorm& p, cudaStream_t stream) {
+  if (p.T == 0) return cudaSuccess;
+  if (p.stream_f32)
+    return p.quant == 0 ? forward<true, 0>(p, stream) : p.quant == 1 ? forward<true, 1>(p, stream) : forward<true, 2>(p, stream);
+  return p.quant == 0 ? forward<false, 0>(p, stream) : p.quant == 1 ? forward<false, 1>(p, stream) : forward<false, 2>(p, stream);
+}
+
+cudaError_t residual_norm_backward(ResidualNormBackward p, float* d_weight, cudaStream_t stream) {
+  if (p.T == 0) return d_weight ? zero_f32(d_weight, p.K, stream) : cudaSuccess;
+  return p.stream_f32 ? backward<true>(p, d_weight, stream) : backward<false>(p, d_weight, stream);
+}
+
+}  // namespace moe_launch
