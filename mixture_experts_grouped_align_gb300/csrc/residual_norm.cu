@@ -18,9 +18,12 @@
 
 #include <algorithm>
 
+#include "cp_async.cuh"
 #include "moe_common.cuh"
 #include "moe_launch.h"
 #include "mx_quant.cuh"
+#include "per_device.h"
+#include "tcgen05.cuh"
 
 namespace {
 
@@ -85,7 +88,7 @@ struct Dropout {
   uint32_t k0, k1, step, stream, below;
   float gain;
   MOE_DEV void init(const int64_t* rng, uint32_t stream_id, uint32_t drop_below, float kept_gain) {
-    below = drop_below;
+    below = drop_below << 16;
     gain = kept_gain;
     stream = stream_id;
     k0 = k1 = step = 0;
@@ -112,9 +115,9 @@ struct Dropout {
     }
     const uint32_t w[4] = {c0, c1, c2, c3};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = (w[i] & 0xffffu) >= below ? __fmul_rn(f[2 * i], gain) : 0.f;
-      f[2 * i + 1] = (w[i] >> 16) >= below ? __fmul_rn(f[2 * i + 1], gain) : 0.f;
+    for (int i = 0; i < 4; ++i) {  // `below` is in the upper half: the lower half of w does not change the comparison
+      f[2 * i] = (w[i] << 16) >= below ? __fmul_rn(f[2 * i], gain) : 0.f;
+      f[2 * i + 1] = w[i] >= below ? __fmul_rn(f[2 * i + 1], gain) : 0.f;
     }
   }
 };
@@ -177,6 +180,14 @@ MOE_DEV void reduce_max(float& a, uint32_t& m, float (*red)[32]) {
       m = max(m, __float_as_uint(red[1][i]));
     }
   }
+}
+
+// (sum / K + eps)^(-1/2): rsqrtf and a Newton step, within 2 units of the last place; 0 for an infinite
+// sum.
+MOE_DEV float inverse_rms(float sum, float inv_k, float eps) {
+  const float m = __fmaf_rn(sum, inv_k, eps), r = rsqrtf(m);
+  const float e = __fmaf_rn(-m * r, r, 1.f);
+  return m <= 3.4028235e38f ? __fmaf_rn(0.5f * r, e, r) : (m > 3.4028235e38f ? 0.f : m);
 }
 
 // E4M3 codes of eight values, saturated at 448, NaN kept.
@@ -262,7 +273,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_kernel(ResidualNorm p)
     float none = 0.f;
     reduce<M>(sum, none, red);
   }
-  const float r = 1.f / sqrtf(sum / (float)p.K + p.eps);
+  const float r = inverse_rms(sum, 1.f / (float)p.K, p.eps);
   float by = 0.f;
   if (QUANT == 2) {
     // the largest |n| is that of the same products in the same order up to two roundings: taken as
@@ -294,81 +305,201 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_kernel(ResidualNorm p)
   }
 }
 
-// A block walks over rows, so that a thread keeps its columns: their weights and their share of d_w
-// stay in registers.  The shares of a block's rows are added (narrow rows: over its groups), and the
-// blocks' by column_parts_kernel.
-template <bool F32, typename M>
-__global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(ResidualNormBackward p) {
-  constexpr int V = M::kV;
-  __shared__ float red[2][2][32];
-  extern __shared__ float shares[];  // narrow rows: [groups][8 V LANES]
+// ---------------------------------------------------------------------------------------------
+// Many rows.  A block walks over batches of rows (one, or as many narrow ones as its threads hold), so
+// that a thread keeps its columns.  Its lanes bring their columns of the next kAhead batches into
+// shared memory by asynchronous copies and read nobody else's, so the ring needs no barrier of the
+// block: the copies of the next rows are in flight through the sums and stores of this one, whatever
+// the registers hold.
+
+// Planes of 16 bytes a thread; a stage has several.
+template <typename M>
+struct Ring {
+  uint32_t base, step;  // the first thread of this one's row group in plane 0, bytes of a plane
+  int lane;             // within the row group
+  MOE_DEV void init(uint8_t* smem) {
+    lane = threadIdx.x % M::kLanes;
+    base = tc::smem_addr(smem) + (threadIdx.x - lane) * 16;
+    step = blockDim.x * 16;
+  }
+  static MOE_DEV uint4 read(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+  }
+  MOE_DEV uint32_t at(int plane) const { return base + plane * step + lane * 16; }
+  // Chunk j < 2 kLanes of the group's, in two planes: lanes that copy neighbours and lanes that read
+  // every second one both meet each bank once.
+  MOE_DEV uint32_t pair_at(int plane, int j) const {
+    const int p = j ^ ((j >> 3) & 1);
+    return base + (plane + p / M::kLanes) * step + (p % M::kLanes) * 16;
+  }
+  // This lane's eight bf16 of unit u (c: its unit in the row), into one plane.
+  MOE_DEV void fetch16(int plane, const void* p, int64_t u, int c, int units) const {
+    if (c < units) cpa::cp_async16(at(plane), static_cast<const uint4*>(p) + u);
+  }
+  // The same of a stream's values.  fp32: two planes; a lane copies two chunks of its group that lie
+  // kLanes apart, so that a warp copies whole lines, and reads its own two after stream_ready().
+  template <bool F32>
+  MOE_DEV void fetch_stream(int plane, const void* p, int64_t u, int c, int units) const {
+    if (!F32) return fetch16(plane, p, u, c, units);
+    const int64_t first = 2 * (u - lane);
+    const int last = 2 * (units - (c - lane));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = h * M::kLanes + lane;
+      if (j < last) cpa::cp_async16(pair_at(plane, j), static_cast<const uint4*>(p) + first + j);
+    }
+  }
+  template <bool F32>
+  MOE_DEV Eight<F32> stream(int plane) const {
+    Eight<F32> e;
+    if (!F32) {
+      e.v[0] = read(at(plane));
+    } else {
+      e.v[0] = read(pair_at(plane, 2 * lane));
+      e.v[F32] = read(pair_at(plane, 2 * lane + 1));
+    }
+    return e;
+  }
+};
+
+// Sums of a and b over the threads of a row, in a fixed order.
+template <typename M>
+MOE_DEV void reduce_pair(float& a, float& b, float2* red) {
+#pragma unroll
+  for (int o = M::kLanes / 2; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(kAll, a, o);
+    b += __shfl_xor_sync(kAll, b, o);
+  }
+  if (M::kWide) {
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    const float2 v = lane < warps ? red[lane] : make_float2(0.f, 0.f);
+    a = v.x;
+    b = v.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(kAll, a, o);
+      b += __shfl_xor_sync(kAll, b, o);
+    }
+  }
+}
+
+// Backward.  HOLD: a row's values stay in registers from the sums to the outputs and its stage is filled
+// again at once; otherwise (two eights a thread of a large block) they are read again.
+template <bool F32, typename M, int kAhead>
+__global__ void __launch_bounds__(M::kWide ? 1024 : kThreads, 1) residual_norm_backward_kernel(ResidualNormBackward p) {
+  constexpr int V = M::kV, kS = F32 ? 2 : 1, kPer = 1 + 2 * kS, kChunks = V * kPer;  // a stage's: d_out, stream, d_stream
+  constexpr bool kHold = !M::kWide || V == 1;
+  constexpr int kHeld = kHold ? V : 1;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 red[2][32];
   moe::wait_for_stream();
   moe::let_next_start();
-  const int units = p.K / 8;
+  const int rows = M::rows(), units = p.K / 8;
+  const int64_t stride = (int64_t)gridDim.x * rows;
+  const float inv_k = 1.f / (float)p.K;
   Dropout drop;
   drop.init(p.rng, p.rng_stream, p.d_x ? p.drop_below : 0u, p.gain);
-  uint4 w[V];
+  Ring<M> ring;
+  ring.init(smem);
+  uint4 w[kHeld];
   float dw[V][8];
 #pragma unroll
   for (int t = 0; t < V; ++t) {
     const int c = M::col() + t * M::step();
-    w[t] = c < units ? static_cast<const uint4*>(p.weight)[c] : make_uint4(0, 0, 0, 0);
+    if (kHold) w[t] = c < units ? static_cast<const uint4*>(p.weight)[c] : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[t][i] = 0.f;
   }
-  int turn = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * M::rows(); row0 < p.T; row0 += (int64_t)gridDim.x * M::rows(), turn ^= 1) {
-    const int64_t row = row0 + M::group();
-    const bool in = row < p.T;
-    const bool live = in && (p.mask == nullptr || p.mask[row] != 0);
-    const int64_t u0 = row * units;
-    Eight<F32> st[V], ds[V];
-    uint4 d[V];
+  const auto fetch = [&](int64_t row, int s) {
+    if (row < p.T) {
 #pragma unroll
-    for (int t = 0; t < V; ++t) {
-      const int c = M::col() + t * M::step();
-      const bool on = live && c < units;
-      if (on) st[t].load(p.stream, u0 + c);
-      else st[t].zero();
-      d[t] = on ? __ldcs(static_cast<const uint4*>(p.d_out) + u0 + c) : make_uint4(0, 0, 0, 0);
-      if (on && p.d_stream) ds[t].load(p.d_stream, u0 + c);
-      else ds[t].zero();
+      for (int t = 0; t < V; ++t) {
+        const int c = M::col() + t * M::step(), k = s * kChunks + t * kPer;
+        const int64_t u = row * units + c;
+        ring.fetch16(k, p.d_out, u, c, units);
+        ring.template fetch_stream<F32>(k + 1, p.stream, u, c, units);
+        if (p.d_stream) ring.template fetch_stream<F32>(k + 1 + kS, p.d_stream, u, c, units);
+      }
     }
+    cpa::cp_async_commit();
+  };
+  int64_t row = (int64_t)blockIdx.x * rows + M::group();
+  for (int s = 0; s < kAhead; ++s) fetch(row + s * stride, s);
+  uint32_t counts = p.mask == nullptr || (row < p.T && p.mask[row] != 0);
+  int s = 0, turn = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * rows; row0 < p.T; row0 += stride, row += stride, turn ^= 1) {
+    const bool in = row < p.T, live = in && counts;
+    if (p.mask) counts = row + stride < p.T ? p.mask[row + stride] : 0;  // the next row's, a turn ahead
+    cpa::cp_async_wait<kAhead - 1>();
+    if (F32) __syncwarp();  // other lanes' copies
+    Eight<F32> st[kHeld], ds[kHeld];
+    uint4 d[kHeld];
     float sum = 0.f, dot = 0.f;
 #pragma unroll
     for (int t = 0; t < V; ++t) {
-      float s[8], g[8], f[8];
-      st[t].get(s);
-      unpack8(d[t], g);
-      unpack8(w[t], f);
+      const int k = s * kChunks + t * kPer, h = kHold ? t : 0, c = M::col() + t * M::step();
+      d[h] = make_uint4(0, 0, 0, 0);
+      st[h].zero();
+      ds[h].zero();
+      if (!kHold) w[0] = make_uint4(0, 0, 0, 0);
+      if (live && c < units) {
+        d[h] = ring.read(ring.at(k));
+        st[h] = ring.template stream<F32>(k + 1);
+        if (kHold && p.d_stream) ds[h] = ring.template stream<F32>(k + 1 + kS);
+        if (!kHold) w[0] = static_cast<const uint4*>(p.weight)[c];
+      }
+      float v[8], g[8], f[8];
+      st[h].get(v);
+      unpack8(d[h], g);
+      unpack8(w[h], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sum += s[i] * s[i];
-        dot += g[i] * f[i] * s[i];
+        sum += v[i] * v[i];
+        dot += g[i] * f[i] * v[i];
       }
     }
-    reduce<M>(sum, dot, red[turn]);  // two sets in turn: one barrier a row is enough
-    const float r = 1.f / sqrtf(sum / (float)p.K + p.eps), q = r * r * (dot / (float)p.K);
+    const int stage = s;
+    s = s + 1 == kAhead ? 0 : s + 1;
+    if (kHold) {
+      if (F32) __syncwarp();
+      fetch(row + kAhead * stride, stage);
+    }
+    reduce_pair<M>(sum, dot, red[turn]);  // two sets in turn: one barrier a row is enough
+    const float r = inverse_rms(sum, inv_k, p.eps), q = r * r * (dot * inv_k);
 #pragma unroll
     for (int t = 0; t < V; ++t) {
-      const int c = M::col() + t * M::step();
-      float s[8], g[8], f[8], o[8];
-      st[t].get(s);
-      unpack8(d[t], g);
-      unpack8(w[t], f);
-      ds[t].get(o);
+      const int c = M::col() + t * M::step(), h = kHold ? t : 0, k = stage * kChunks + t * kPer;
+      if (!in || c >= units) continue;
+      const int64_t u = row * units + c;
+      if (!kHold && live) {
+        d[0] = ring.read(ring.at(k));
+        st[0] = ring.template stream<F32>(k + 1);
+        if (p.d_stream) ds[0] = ring.template stream<F32>(k + 1 + kS);
+        w[0] = static_cast<const uint4*>(p.weight)[c];
+      }
+      float v[8], g[8], f[8], o[8];
+      st[h].get(v);
+      unpack8(d[h], g);
+      unpack8(w[h], f);
+      ds[h].get(o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[i] = live ? r * (g[i] * f[i] - s[i] * q) + o[i] : 0.f;
-        if (live) dw[t][i] += g[i] * (s[i] * r);
+      for (int i = 0; i < 8; ++i) {  // a row that does not count: zeros all along (r is finite, as eps > 0)
+        o[i] = r * (g[i] * f[i] - v[i] * q) + o[i];
+        dw[t][i] += g[i] * (v[i] * r);
       }
-      if (in && c < units) {
-        if (p.d_residual) Eight<F32>::store(p.d_residual, u0 + c, o);
-        if (p.d_x) {
-          if (live) drop.apply(u0 + c, o);
-          __stcs(static_cast<uint4*>(p.d_x) + u0 + c, pack8(o));
-        }
+      if (p.d_residual) Eight<F32>::store(p.d_residual, u, o);
+      if (p.d_x) {
+        if (live) drop.apply(u, o);
+        __stcs(static_cast<uint4*>(p.d_x) + u, pack8(o));
       }
+    }
+    if (!kHold) {
+      if (F32) __syncwarp();
+      fetch(row + kAhead * stride, stage);
     }
   }
   if (p.parts == nullptr) return;
@@ -384,6 +515,9 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(Residu
     }
   } else {
     constexpr int kCols = 8 * V * M::kLanes;
+    float* shares = reinterpret_cast<float*>(smem);  // [groups][columns], once no thread reads the ring
+    cpa::cp_async_wait<0>();
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < V; ++t)
 #pragma unroll
@@ -391,7 +525,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(Residu
     __syncthreads();
     for (int k = threadIdx.x; k < p.K; k += kThreads) {
       float a = 0.f;
-      for (int g = 0; g < kThreads / M::kLanes; ++g) a += shares[g * kCols + k];
+      for (int g = 0; g < rows; ++g) a += shares[g * kCols + k];
       mine[k] = a;
     }
   }
@@ -460,19 +594,49 @@ cudaError_t forward(const ResidualNorm& p, cudaStream_t stream) {
   });
 }
 
-constexpr int kPartsMost = 608;  // blocks that leave a part of d_w
+constexpr int kPartsMost = 608;      // blocks that leave a part of d_w
+constexpr int kRingMost = 224 * 1024;  // shared memory of an SM for the rings of its blocks
+
+// Columns of a thread where blocks walk over rows: narrow rows share warps; wide ones have a block.
+template <typename F>
+cudaError_t pick_walk(int K, F launch) {
+  const int units = K / 8;
+  if (units <= 8) return launch(Map<8, false, 1>{});
+  if (units <= 32) return launch(Map<16, false, 2>{});
+  if (units <= 64) return launch(Map<32, false, 2>{});
+  if (units <= 1024) return launch(Map<32, true, 1>{});
+  return launch(Map<32, true, 2>{});
+}
+
+// Blocks of `kern` that walk over T rows: as many as fit beside one another.  `known`: one for each kernel.
+template <typename M, typename K>
+int64_t walkers(int64_t T, K kern, int threads, int smem, moe_host::PerDevice<33>& known) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+  const int fit = known.get(dev, threads / 32, 1, [&] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) == cudaSuccess ? n : 0;
+  });
+  return std::min<int64_t>(blocks_of<M>(T), (int64_t)std::min(fit, 4) * moe_launch::sm_count_current());
+}
 
 template <bool F32>
 cudaError_t backward(ResidualNormBackward p, float* d_weight, cudaStream_t stream) {
   int64_t parts = 0;
-  cudaError_t err = pick(p.T, p.K, [&](auto m) {
+  cudaError_t err = pick_walk(p.K, [&](auto m) {
     using M = decltype(m);
-    const int threads = threads_of<M>(p.K);
-    const int64_t most = std::min<int64_t>(kPartsMost, (int64_t)moe_launch::sm_count_current() * std::max(1, 768 / threads));
-    parts = std::min(blocks_of<M>(p.T), most);
-    const size_t smem = M::kWide ? 0 : (size_t)kThreads * 8 * M::kV * 4;
-    return moe_launch::launch_staged(residual_norm_backward_kernel<F32, M>, dim3((unsigned)parts), dim3((unsigned)threads), smem,
-                                     stream, 1, p);
+    static std::atomic<uint64_t> done[3] = {};
+    static moe_host::PerDevice<33> known[3];
+    const int threads = threads_of<M>(p.K), chunk = threads * 16 * M::kV, chunks = F32 ? 5 : 3;
+    // three rows ahead where one block has the SM to itself
+    const int deep = threads > 512 && 3 * chunks * chunk <= kRingMost, ahead = deep ? 3 : std::min(2, kRingMost / (chunks * chunk));
+    const auto kern = deep ? residual_norm_backward_kernel<F32, M, 3> : ahead == 2 ? residual_norm_backward_kernel<F32, M, 2> : residual_norm_backward_kernel<F32, M, 1>;
+    const int which = ahead - 1;
+    const int smem = std::max(ahead * chunks * chunk, M::kWide ? 0 : kThreads * 8 * M::kV * 4);
+    const cudaError_t e = moe_launch::allow_smem((const void*)kern, kRingMost, done[which]);
+    if (e != cudaSuccess) return e;
+    parts = std::min<int64_t>(walkers<M>(p.T, kern, threads, smem, known[which]), kPartsMost);
+    return moe_launch::launch_staged(kern, dim3((unsigned)parts), dim3((unsigned)threads), smem, stream, 1, p);
   });
   if (err != cudaSuccess || d_weight == nullptr) return err;
   return moe_launch::launch_staged(column_parts_kernel, dim3((unsigned)((p.K + 31) / 32)), dim3(kThreads), 0, stream, 1,
