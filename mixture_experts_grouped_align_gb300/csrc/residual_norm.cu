@@ -128,57 +128,33 @@ template <int LANES, bool WIDE, int V>
 struct Map {
   static constexpr int kLanes = LANES, kV = V;
   static constexpr bool kWide = WIDE;
-  static constexpr int kMost = !WIDE ? kThreads : (V >= 4 ? 512 : 1024);  // threads of a block
+  static constexpr int kMost = WIDE ? 1024 : kThreads;  // threads of a block
   MOE_DEV static int rows() { return WIDE ? 1 : kThreads / LANES; }
   MOE_DEV static int group() { return WIDE ? 0 : threadIdx.x / LANES; }
   MOE_DEV static int col() { return WIDE ? threadIdx.x : threadIdx.x % LANES; }
   MOE_DEV static int step() { return WIDE ? blockDim.x : LANES; }
 };
 
-// Sums (and a maximum of non-negative float bits) over the lanes of a row, in a fixed order; every
-// thread of the block calls.  `red`: 2 x 32 words of shared memory for WIDE; the caller separates
-// two uses of it by a barrier.
-template <typename M>
-MOE_DEV void reduce(float& a, float& b, float (*red)[32]) {
-#pragma unroll
-  for (int o = M::kLanes / 2; o > 0; o >>= 1) {
+// Sums of a and b (MAX: the largest of b's non-negative bits, NaN above all) over the threads of a row,
+// in a fixed order.  `red`: shared memory for WIDE; the caller separates two uses of it by a barrier.
+template <typename M, bool MAX = false>
+MOE_DEV void reduce_pair(float& a, float& b, float2* red) {
+  const auto add = [&](int o) {
     a += __shfl_xor_sync(kAll, a, o);
-    b += __shfl_xor_sync(kAll, b, o);
-  }
-  if (M::kWide) {
-    if ((threadIdx.x & 31) == 0) {
-      red[0][threadIdx.x >> 5] = a;
-      red[1][threadIdx.x >> 5] = b;
-    }
-    __syncthreads();
-    a = b = 0.f;
-    const int warps = blockDim.x >> 5;
-    for (int i = 0; i < warps; ++i) {
-      a += red[0][i];
-      b += red[1][i];
-    }
-  }
-}
-template <typename M>
-MOE_DEV void reduce_max(float& a, uint32_t& m, float (*red)[32]) {
+    const float c = __shfl_xor_sync(kAll, b, o);
+    b = MAX ? __uint_as_float(max(__float_as_uint(b), __float_as_uint(c))) : b + c;
+  };
 #pragma unroll
-  for (int o = M::kLanes / 2; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(kAll, a, o);
-    m = max(m, __shfl_xor_sync(kAll, m, o));
-  }
+  for (int o = M::kLanes / 2; o > 0; o >>= 1) add(o);
   if (M::kWide) {
-    if ((threadIdx.x & 31) == 0) {
-      red[0][threadIdx.x >> 5] = a;
-      red[1][threadIdx.x >> 5] = __uint_as_float(m);
-    }
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
-    a = 0.f;
-    m = 0;
-    const int warps = blockDim.x >> 5;
-    for (int i = 0; i < warps; ++i) {
-      a += red[0][i];
-      m = max(m, __float_as_uint(red[1][i]));
-    }
+    const float2 v = lane < warps ? red[lane] : make_float2(0.f, 0.f);
+    a = v.x;
+    b = v.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) add(o);
   }
 }
 
@@ -219,11 +195,42 @@ MOE_DEV uint2 quant8(const float (&v)[8], uint32_t& scale) {
 // The smallest scale of a row: zero rows have it, and 1 / scale stays finite.
 constexpr float kRowScaleMin = 0x1p-120f;
 
+// The scale of a row whose largest magnitude is `most`, and what its values are multiplied by.  `most`
+// is taken as |s w| r: it may be two roundings off the largest |s r w|, which then saturates at 448.
+MOE_DEV float row_scale(float most, float& by) {
+  if (!(most <= 3.4028235e38f)) {  // an infinity, too, leaves NaN in its row
+    by = __uint_as_float(0x7fc00000u);
+    return by;
+  }
+  const bool small = most / 448.f < kRowScaleMin;
+  by = small ? 1.f / kRowScaleMin : 448.f / most;
+  return small ? kRowScaleMin : most / 448.f;
+}
+
+// The outputs of eight values s of unit u (c: its unit in the row); every lane calls.
+template <int QUANT>
+MOE_DEV void finish(const ResidualNorm& p, const float (&s)[8], const uint4& w, float r, float by, int64_t u, int c, bool on) {
+  float f[8];
+  unpack8(w, f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = s[i] * r * f[i];  // zeros where a row does not count: its s are
+  if (on && p.out) __stcs(static_cast<uint4*>(p.out) + u, pack8(f));
+  if (QUANT == 1) {
+    uint32_t e;
+    const uint2 q = quant8(f, e);
+    if (on) {
+      __stcs(reinterpret_cast<uint2*>(p.codes) + u, q);
+      if ((c & 3) == 0) static_cast<uint8_t*>(p.scales)[u >> 2] = (uint8_t)e;
+    }
+  }
+  if (QUANT == 2 && on) __stcs(reinterpret_cast<uint2*>(p.codes) + u, codes8(f, by));
+}
+
 // QUANT: 0 no codes, 1 a power of two per 32 values, 2 a scale per row.
 template <bool F32, int QUANT, typename M>
 __global__ void __launch_bounds__(M::kMost) residual_norm_kernel(ResidualNorm p) {
   constexpr int V = M::kV;
-  __shared__ float red[2][32];
+  __shared__ float2 red[32];
   moe::wait_for_stream();
   moe::let_next_start();
   const int64_t row = (int64_t)blockIdx.x * M::rows() + M::group();
@@ -245,8 +252,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_kernel(ResidualNorm p)
     x[t] = on && p.x ? __ldcs(static_cast<const uint4*>(p.x) + u0 + c) : make_uint4(0, 0, 0, 0);
     w[t] = c < units ? static_cast<const uint4*>(p.weight)[c] : make_uint4(0, 0, 0, 0);
   }
-  float s[V][8], sum = 0.f;
-  uint32_t top = 0;
+  float s[V][8], sum = 0.f, top = 0.f;
 #pragma unroll
   for (int t = 0; t < V; ++t) {
     const int c = M::col() + t * M::step();
@@ -264,44 +270,20 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_kernel(ResidualNorm p)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       sum += s[t][i] * s[t][i];
-      if (QUANT == 2) top = max(top, __float_as_uint(s[t][i] * f[i]) & 0x7fffffffu);
+      if (QUANT == 2) top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(s[t][i] * f[i]) & 0x7fffffffu));
     }
   }
-  if (QUANT == 2) {
-    reduce_max<M>(sum, top, red);
-  } else {
-    float none = 0.f;
-    reduce<M>(sum, none, red);
-  }
+  reduce_pair<M, QUANT == 2>(sum, top, red);
   const float r = inverse_rms(sum, 1.f / (float)p.K, p.eps);
   float by = 0.f;
   if (QUANT == 2) {
-    // the largest |n| is that of the same products in the same order up to two roundings: taken as
-    // |s w| r it may be 2^-23 off the largest code's value, which saturates at 448 all the same
-    const float most = __uint_as_float(top) * r;
-    const bool nan = !(most <= 3.4028235e38f);  // an infinity, too, leaves NaN in its row
-    const float scale = nan ? __uint_as_float(0x7fc00000u) : fmaxf(most / 448.f, kRowScaleMin);
-    by = nan ? scale : (most / 448.f >= kRowScaleMin ? 448.f / most : 1.f / kRowScaleMin);
+    const float scale = row_scale(top * r, by);
     if (in && M::col() == 0) static_cast<float*>(p.scales)[row] = scale;
   }
 #pragma unroll
   for (int t = 0; t < V; ++t) {
     const int c = M::col() + t * M::step();
-    const bool on = in && c < units;
-    float f[8];
-    unpack8(w[t], f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = live ? s[t][i] * r * f[i] : 0.f;
-    if (on && p.out) __stcs(static_cast<uint4*>(p.out) + u0 + c, pack8(f));
-    if (QUANT == 1) {
-      uint32_t e;
-      const uint2 q = quant8(f, e);
-      if (on) {
-        __stcs(reinterpret_cast<uint2*>(p.codes) + u0 + c, q);
-        if ((c & 3) == 0) static_cast<uint8_t*>(p.scales)[(u0 + c) >> 2] = (uint8_t)e;
-      }
-    }
-    if (QUANT == 2 && on) __stcs(reinterpret_cast<uint2*>(p.codes) + u0 + c, codes8(f, by));
+    finish<QUANT>(p, s[t], w[t], r, by, u0 + c, c, in && c < units);
   }
 }
 
@@ -326,6 +308,9 @@ struct Ring {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
+  }
+  static MOE_DEV void write(uint32_t a, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
   }
   MOE_DEV uint32_t at(int plane) const { return base + plane * step + lane * 16; }
   // Chunk j < 2 kLanes of the group's, in two planes: lanes that copy neighbours and lanes that read
@@ -364,33 +349,10 @@ struct Ring {
   }
 };
 
-// Sums of a and b over the threads of a row, in a fixed order.
-template <typename M>
-MOE_DEV void reduce_pair(float& a, float& b, float2* red) {
-#pragma unroll
-  for (int o = M::kLanes / 2; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(kAll, a, o);
-    b += __shfl_xor_sync(kAll, b, o);
-  }
-  if (M::kWide) {
-    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) red[threadIdx.x >> 5] = make_float2(a, b);
-    __syncthreads();
-    const float2 v = lane < warps ? red[lane] : make_float2(0.f, 0.f);
-    a = v.x;
-    b = v.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(kAll, a, o);
-      b += __shfl_xor_sync(kAll, b, o);
-    }
-  }
-}
-
 // Backward.  HOLD: a row's values stay in registers from the sums to the outputs and its stage is filled
 // again at once; otherwise (two eights a thread of a large block) they are read again.
 template <bool F32, typename M, int kAhead>
-__global__ void __launch_bounds__(M::kWide ? 1024 : kThreads, 1) residual_norm_backward_kernel(ResidualNormBackward p) {
+__global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(ResidualNormBackward p) {
   constexpr int V = M::kV, kS = F32 ? 2 : 1, kPer = 1 + 2 * kS, kChunks = V * kPer;  // a stage's: d_out, stream, d_stream
   constexpr bool kHold = !M::kWide || V == 1;
   constexpr int kHeld = kHold ? V : 1;
@@ -410,7 +372,9 @@ __global__ void __launch_bounds__(M::kWide ? 1024 : kThreads, 1) residual_norm_b
 #pragma unroll
   for (int t = 0; t < V; ++t) {
     const int c = M::col() + t * M::step();
-    if (kHold) w[t] = c < units ? static_cast<const uint4*>(p.weight)[c] : make_uint4(0, 0, 0, 0);
+    const uint4 z = c < units ? static_cast<const uint4*>(p.weight)[c] : make_uint4(0, 0, 0, 0);
+    if (kHold) w[t] = z;
+    else ring.write(ring.at(kAhead * kChunks + t), z);  // planes of their own
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[t][i] = 0.f;
   }
@@ -445,12 +409,11 @@ __global__ void __launch_bounds__(M::kWide ? 1024 : kThreads, 1) residual_norm_b
       d[h] = make_uint4(0, 0, 0, 0);
       st[h].zero();
       ds[h].zero();
-      if (!kHold) w[0] = make_uint4(0, 0, 0, 0);
+      if (!kHold) w[0] = ring.read(ring.at(kAhead * kChunks + t));
       if (live && c < units) {
         d[h] = ring.read(ring.at(k));
         st[h] = ring.template stream<F32>(k + 1);
         if (kHold && p.d_stream) ds[h] = ring.template stream<F32>(k + 1 + kS);
-        if (!kHold) w[0] = static_cast<const uint4*>(p.weight)[c];
       }
       float v[8], g[8], f[8];
       st[h].get(v);
@@ -479,7 +442,7 @@ __global__ void __launch_bounds__(M::kWide ? 1024 : kThreads, 1) residual_norm_b
         d[0] = ring.read(ring.at(k));
         st[0] = ring.template stream<F32>(k + 1);
         if (p.d_stream) ds[0] = ring.template stream<F32>(k + 1 + kS);
-        w[0] = static_cast<const uint4*>(p.weight)[c];
+        w[0] = ring.read(ring.at(kAhead * kChunks + t));
       }
       float v[8], g[8], f[8], o[8];
       st[h].get(v);
@@ -531,6 +494,98 @@ __global__ void __launch_bounds__(M::kWide ? 1024 : kThreads, 1) residual_norm_b
   }
 }
 
+// Forward.
+template <bool F32, int QUANT, typename M, int kAhead>
+__global__ void __launch_bounds__(M::kMost) residual_norm_walk_kernel(ResidualNorm p) {
+  constexpr int V = M::kV, kS = F32 ? 2 : 1, kPer = 1 + kS, kChunks = V * kPer;  // a stage's: x, residual
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 red[2][32];
+  moe::wait_for_stream();
+  moe::let_next_start();
+  const int rows = M::rows(), units = p.K / 8;
+  const int64_t stride = (int64_t)gridDim.x * rows;
+  const float inv_k = 1.f / (float)p.K;
+  Dropout drop;
+  drop.init(p.rng, p.rng_stream, p.x ? p.drop_below : 0u, p.gain);
+  Ring<M> ring;
+  ring.init(smem);
+  uint4 w[V];
+#pragma unroll
+  for (int t = 0; t < V; ++t) {
+    const int c = M::col() + t * M::step();
+    w[t] = c < units ? static_cast<const uint4*>(p.weight)[c] : make_uint4(0, 0, 0, 0);
+  }
+  const auto fetch = [&](int64_t row, int s) {
+    if (row < p.T) {
+#pragma unroll
+      for (int t = 0; t < V; ++t) {
+        const int c = M::col() + t * M::step(), k = s * kChunks + t * kPer;
+        const int64_t u = row * units + c;
+        if (p.x) ring.fetch16(k, p.x, u, c, units);
+        if (p.residual) ring.template fetch_stream<F32>(k + 1, p.residual, u, c, units);
+      }
+    }
+    cpa::cp_async_commit();
+  };
+  int64_t row = (int64_t)blockIdx.x * rows + M::group();
+  for (int s = 0; s < kAhead; ++s) fetch(row + s * stride, s);
+  uint32_t counts = p.mask == nullptr || (row < p.T && p.mask[row] != 0);
+  int stage = 0, turn = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * rows; row0 < p.T; row0 += stride, row += stride, turn ^= 1) {
+    const bool in = row < p.T, live = in && counts;
+    if (p.mask) counts = row + stride < p.T ? p.mask[row + stride] : 0;  // the next row's, a turn ahead
+    cpa::cp_async_wait<kAhead - 1>();
+    if (F32) __syncwarp();  // other lanes' copies
+    Eight<F32> res[V];
+    uint4 x[V];
+#pragma unroll
+    for (int t = 0; t < V; ++t) {
+      const int k = stage * kChunks + t * kPer;
+      const bool on = live && M::col() + t * M::step() < units;
+      x[t] = make_uint4(0, 0, 0, 0);
+      res[t].zero();
+      if (on && p.x) x[t] = ring.read(ring.at(k));
+      if (on && p.residual) res[t] = ring.template stream<F32>(k + 1);
+    }
+    if (F32) __syncwarp();
+    fetch(row + kAhead * stride, stage);
+    stage = stage + 1 == kAhead ? 0 : stage + 1;
+    float s[V][8], sum = 0.f, top = 0.f;
+#pragma unroll
+    for (int t = 0; t < V; ++t) {
+      const int c = M::col() + t * M::step();
+      const int64_t u = row * units + c;
+      float f[8];
+      res[t].get(s[t]);
+      if (p.x) {
+        unpack8(x[t], f);
+        if (live && c < units) drop.apply(u, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[t][i] = __fadd_rn(s[t][i], f[i]);
+      }
+      if (p.stream && in && c < units) Eight<F32>::store(p.stream, u, s[t]);
+      if (QUANT == 2) unpack8(w[t], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum += s[t][i] * s[t][i];
+        if (QUANT == 2) top = __uint_as_float(max(__float_as_uint(top), __float_as_uint(s[t][i] * f[i]) & 0x7fffffffu));
+      }
+    }
+    reduce_pair<M, QUANT == 2>(sum, top, red[turn]);  // two sets in turn: one barrier a row is enough
+    const float r = inverse_rms(sum, inv_k, p.eps);
+    float by = 0.f;
+    if (QUANT == 2) {
+      const float scale = row_scale(top * r, by);
+      if (in && M::col() == 0) static_cast<float*>(p.scales)[row] = scale;
+    }
+#pragma unroll
+    for (int t = 0; t < V; ++t) {
+      const int c = M::col() + t * M::step();
+      finish<QUANT>(p, s[t], w[t], r, by, row * units + c, c, in && c < units);
+    }
+  }
+}
+
 // out[k] = the sum over n parts of parts[i][k], in a fixed order: 32 columns a block, eight lanes of
 // four of them, 32 groups of parts.
 __global__ void __launch_bounds__(kThreads) column_parts_kernel(const float* parts, int n, int K, float* out) {
@@ -562,17 +617,22 @@ __global__ void __launch_bounds__(kThreads) column_parts_kernel(const float* par
   }
 }
 
-// Rows narrower than a warp's 1024 values share warps; others have a block each.
+constexpr int64_t kFew = 200000;  // eights of columns in all
+
+// A block or a part of a warp for each row: as many threads as there are eights in wide rows and in few
+// narrow ones, which leaves registers for most threads an SM has (8192 x 7168 80 us as four eights a
+// thread, 78 as one; 20388 x 2880 MX 105 and 84), up to four eights a lane in many narrow ones, so that
+// a row stays within a warp.
 template <typename F>
-cudaError_t pick(int64_t T, int K, F launch) {
+cudaError_t pick_once(int64_t T, int K, F launch) {
   const int units = K / 8;
-  const bool few = T * units < 200000;
   if (units <= 8) return launch(Map<8, false, 1>{});
+  const bool few = T * units < kFew;
   if (units <= 32) return few ? launch(Map<32, false, 1>{}) : launch(Map<8, false, 4>{});
   if (units <= 64 && !few) return launch(Map<16, false, 4>{});
   if (units <= 128 && !few) return launch(Map<32, false, 4>{});
-  if (few && units <= 1024) return launch(Map<32, true, 1>{});
-  return few ? launch(Map<32, true, 2>{}) : launch(Map<32, true, 4>{});
+  if (units <= 1024) return launch(Map<32, true, 1>{});
+  return launch(Map<32, true, 2>{});
 }
 
 template <typename M>
@@ -583,15 +643,6 @@ template <typename M>
 int64_t blocks_of(int64_t T) {
   const int rows = M::kWide ? 1 : kThreads / M::kLanes;
   return (T + rows - 1) / rows;
-}
-
-template <bool F32, int QUANT>
-cudaError_t forward(const ResidualNorm& p, cudaStream_t stream) {
-  return pick(p.T, p.K, [&](auto m) {
-    using M = decltype(m);
-    return moe_launch::launch_staged(residual_norm_kernel<F32, QUANT, M>, dim3((unsigned)blocks_of<M>(p.T)),
-                                     dim3((unsigned)threads_of<M>(p.K)), 0, stream, 1, p);
-  });
 }
 
 constexpr int kPartsMost = 608;      // blocks that leave a part of d_w
@@ -620,6 +671,38 @@ int64_t walkers(int64_t T, K kern, int threads, int smem, moe_host::PerDevice<33
   return std::min<int64_t>(blocks_of<M>(T), (int64_t)std::min(fit, 4) * moe_launch::sm_count_current());
 }
 
+template <bool F32, int QUANT>
+cudaError_t forward(const ResidualNorm& p, cudaStream_t stream) {
+  // Blocks that walk over rows pay where a block of its own leaves a row too few neighbours beside it to
+  // hide what it computes: wide rows with dropout or codes, and those above 1024 eights, in bf16
+  // (8192 x 7168: dropout 79 us and 88 as blocks of their own, row scales 85 and 94, MX 91 and 92, the
+  // norm alone 82 and 78; 4778 x 12288: 80 and 86, dropout 78 and 103; 14336 x 4096 MX 95 and 81; fp32
+  // streams 121 and 101 and more).
+  if constexpr (!F32) {
+    if (p.K > 8192 ? p.T * (p.K / 8) >= kFew : p.K > 4096 && p.T * (p.K / 8) >= 4 * kFew && (p.drop_below || QUANT)) {
+      const auto walk = [&](auto m) {
+        using M = decltype(m);
+        static std::atomic<uint64_t> done[2] = {};
+        static moe_host::PerDevice<33> known[2];
+        const int threads = threads_of<M>(p.K), stage = threads * 16 * M::kV * 2;
+        const bool deep = 4 * stage <= kRingMost;  // rows ahead: four, or two where they do not fit
+        const auto kern = deep ? residual_norm_walk_kernel<F32, QUANT, M, 4> : residual_norm_walk_kernel<F32, QUANT, M, 2>;
+        const int smem = (deep ? 4 : 2) * stage;
+        const cudaError_t e = moe_launch::allow_smem((const void*)kern, kRingMost, done[deep]);
+        if (e != cudaSuccess) return e;
+        const int64_t blocks = walkers<M>(p.T, kern, threads, smem, known[deep]);
+        return moe_launch::launch_staged(kern, dim3((unsigned)blocks), dim3((unsigned)threads), smem, stream, 1, p);
+      };
+      return p.K <= 8192 ? walk(Map<32, true, 1>{}) : walk(Map<32, true, 2>{});
+    }
+  }
+  return pick_once(p.T, p.K, [&](auto m) {
+    using M = decltype(m);
+    return moe_launch::launch_staged(residual_norm_kernel<F32, QUANT, M>, dim3((unsigned)blocks_of<M>(p.T)),
+                                     dim3((unsigned)threads_of<M>(p.K)), 0, stream, 1, p);
+  });
+}
+
 template <bool F32>
 cudaError_t backward(ResidualNormBackward p, float* d_weight, cudaStream_t stream) {
   int64_t parts = 0;
@@ -628,11 +711,13 @@ cudaError_t backward(ResidualNormBackward p, float* d_weight, cudaStream_t strea
     static std::atomic<uint64_t> done[3] = {};
     static moe_host::PerDevice<33> known[3];
     const int threads = threads_of<M>(p.K), chunk = threads * 16 * M::kV, chunks = F32 ? 5 : 3;
-    // three rows ahead where one block has the SM to itself
-    const int deep = threads > 512 && 3 * chunks * chunk <= kRingMost, ahead = deep ? 3 : std::min(2, kRingMost / (chunks * chunk));
-    const auto kern = deep ? residual_norm_backward_kernel<F32, M, 3> : ahead == 2 ? residual_norm_backward_kernel<F32, M, 2> : residual_norm_backward_kernel<F32, M, 1>;
-    const int which = ahead - 1;
-    const int smem = std::max(ahead * chunks * chunk, M::kWide ? 0 : kThreads * 8 * M::kV * 4);
+    // three rows ahead where one block has the SM to itself; the weights of a row that is not held
+    const int stage = chunks * chunk, weights = M::kWide && M::kV > 1 ? chunk : 0, fit = (kRingMost - weights) / stage;
+    const int ahead = threads > 512 && fit >= 3 ? 3 : std::min(2, fit), which = ahead - 1;
+    const auto kern = ahead == 3   ? residual_norm_backward_kernel<F32, M, 3>
+                      : ahead == 2 ? residual_norm_backward_kernel<F32, M, 2>
+                                   : residual_norm_backward_kernel<F32, M, 1>;
+    const int smem = std::max(ahead * stage + weights, M::kWide ? 0 : kThreads * 8 * M::kV * 4);
     const cudaError_t e = moe_launch::allow_smem((const void*)kern, kRingMost, done[which]);
     if (e != cudaSuccess) return e;
     parts = std::min<int64_t>(walkers<M>(p.T, kern, threads, smem, known[which]), kPartsMost);

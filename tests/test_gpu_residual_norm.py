@@ -117,7 +117,7 @@ class Case:
 
 # a size of every kernel: few and many rows, groups of 8, 16 and 32 lanes, blocks of one, two and four eights a thread
 SIZES = [(1, 8), (1, 16384), (3, 64), (5, 136), (37, 256), (300, 520), (28, 2688), (1, 7168), (64, 2880), (100, 12288),
-         (30000, 64), (7000, 256), (4000, 512), (2000, 1000), (900, 2880), (130, 16384), (1001, 1856)]
+         (30000, 64), (7000, 256), (4000, 512), (2000, 1000), (900, 2880), (130, 16384), (1001, 1856), (900, 7168)]
 
 
 @pytest.mark.parametrize("T,K", SIZES)
