@@ -14,7 +14,8 @@
  * in its epilogue and its backward products (moe_dense_gemm, moe_dense_bias_grad), and the sum
  * of a token's pair rows (moe_pair_sum).  Between layers: dropout, the residual's addition and the
  * RMS norm, whose output can be the 8-bit operands of the calls above (moe_residual_norm,
- * moe_residual_norm_backward).
+ * moe_residual_norm_backward); beside a dense layer: the low-rank adapters of many requests
+ * (moe_adapter_gemm).
  *
  * Sources of the definitions (pull-request pages):
  *  [BUCKET] "Bound Triton MoE JIT specializations via token-dim bucketing and warmup",
@@ -538,6 +539,31 @@ moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, c
                                       const uint8_t* token_mask, const void* weight, int64_t T, int32_t K, float eps,
                                       const moe_dropout* dropout, int32_t stream_f32, void* d_residual, void* d_x,
                                       float* d_weight, const moe_ctx* ctx);
+
+/* ------------------------------------------------------------------------------------ *
+ * Low-rank adapters of many requests beside a dense product                              *
+ * ------------------------------------------------------------------------------------ */
+
+/* For the rows m of request i (row_offsets[i] <= m < row_offsets[i+1]) and its adapter l = adapter[i]:
+ *   out[m] = base[m] + scale[l] * (x[m] . a[l]^T) . b[l]^T      (l >= 0)
+ *   out[m] = base[m]                                            (l = -1: no adapter)
+ * x [M, K] bf16; a [L, r, K] bf16; b [L, N, r] bf16 (an adapter of a lower rank has zeros in the rest);
+ * scale [L] fp32 or NULL (1); row_offsets [R+1] and adapter [R] int32 in device memory; base [M, N] in
+ * out's type or NULL (zeros), it may be out itself: the output of moe_dense_gemm with the shared weight,
+ * say; out [M, N] bf16 (out_f32 == 0) or fp32.  Rows of no request (before row_offsets[0], or from
+ * row_offsets[R] on) are neither read nor written, and of requests without an adapter x is not read.
+ * Products and sums in fp32 -- x . a^T enters the second product as a sum of two bf16 numbers, within
+ * 2^-17 of itself -- rounded once; out must not overlap x, a or b.  A row depends on its own request's
+ * adapter alone, also where another's is not finite.  Sums run in one fixed order for given sizes, offsets
+ * and adapters: repeated calls give identical bits.
+ * Data errors in ctx->dev_status: offsets that decrease or leave [0, M] (MOE_ERR_CAPACITY; such a request
+ * has no rows; where requests overlap, their rows are undefined), adapters outside [-1, L)
+ * (MOE_ERR_INVALID_EXPERT; read as -1).
+ * Limits: K and N multiples of 8, r a multiple of 8 up to 128, M, N, K, R < 2^30, L >= 1.  M = 0 or R = 0:
+ * nothing is done. */
+moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const float* scale, const int32_t* row_offsets,
+                            const int32_t* adapter, const void* base, int64_t M, int32_t N, int32_t K, int32_t r,
+                            int32_t L, int32_t R, void* out, int32_t out_f32, const moe_ctx* ctx);
 
 /* ------------------------------------------------------------------------------------ *
  * Diagnostics: failure detection of the bounded waits                                    *

@@ -23,7 +23,7 @@ __all__ = [
     "moe_gemm_per_token", "moe_wgrad", "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels",
     "moe_router_loss", "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward",
     "moe_dense_gemm", "moe_dense_gemm_plan", "moe_dense_bias_grad", "moe_pair_sum", "moe_residual_norm",
-    "moe_residual_norm_backward", "moe_residual_norm_workspace_size", "W_LAYOUT", "SCALES", "EXPORTED_SYMBOLS",
+    "moe_residual_norm_backward", "moe_residual_norm_workspace_size", "moe_adapter_gemm", "W_LAYOUT", "SCALES", "EXPORTED_SYMBOLS",
 ]
 
 MOE_OK = 0
@@ -43,7 +43,7 @@ EXPORTED_SYMBOLS = [
     "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels", "moe_router_loss",
     "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward", "moe_dense_gemm",
     "moe_dense_bias_grad", "moe_pair_sum", "moe_dense_gemm_plan", "moe_residual_norm", "moe_residual_norm_backward",
-    "moe_residual_norm_workspace_size",
+    "moe_residual_norm_workspace_size", "moe_adapter_gemm",
 ]
 
 
@@ -82,7 +82,7 @@ def _load_native():
     loader.exec_module(mod)
     lib = load()
     names = ("moe_router_loss", "moe_act_checkpoint", "moe_act_backward", "moe_dense_gemm", "moe_dense_bias_grad",
-             "moe_pair_sum", "moe_residual_norm", "moe_residual_norm_backward")
+             "moe_pair_sum", "moe_residual_norm", "moe_residual_norm_backward", "moe_adapter_gemm")
     mod.setup(_refuse, torch.float32, torch.int32, torch.bfloat16, torch.uint8, torch.int64,
               tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
     _native = mod
@@ -130,6 +130,7 @@ def load(path: str | None = None):
         "moe_residual_norm": (I32, [P, P, P, P, I64, I32, F32, P, I32, P, P, P, P, I32, P]),
         "moe_residual_norm_backward": (I32, [P, P, P, P, P, I64, I32, F32, P, I32, P, P, P, P]),
         "moe_residual_norm_workspace_size": (SZ, [I32]),
+        "moe_adapter_gemm": (I32, [P, P, P, P, P, P, P, I64, I32, I32, I32, I32, I32, P, I32, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -406,6 +407,17 @@ def moe_residual_norm_backward(d_out, d_stream, stream, token_mask, weight, T, K
     return _check((_native or _load_native()).residual_norm_backward(d_out, d_stream, stream, token_mask, weight, T, K, eps, p,
                                                                      rng, rng_stream, int(stream_f32), d_residual, d_x,
                                                                      d_weight, c.address))
+
+
+def moe_adapter_gemm(x, a, b, scale, row_offsets, adapter, base, M, N, K, r, L, R, out, ctx=None, out_f32=None):
+    """out [M, N] = base + scale (x [M, K] . a^T) . b^T with the adapter (a [L, r, K], b [L, N, r]) of each
+    row's request: rows row_offsets[i] to row_offsets[i + 1] use adapter[i] (-1: none).  out is bf16 or
+    fp32 (``out_f32`` says which for a raw pointer); base of the same type, None or out itself."""
+    if out_f32 is None:
+        out_f32 = _is_f32(out)
+    c = ctx or Ctx()
+    return _check((_native or _load_native()).adapter_gemm(x, a, b, scale, row_offsets, adapter, base, M, N, K, r, L, R, out,
+                                                           int(out_f32), c.address))
 
 
 def moe_debug_stall_tensor_kernels(stall_ns: int) -> None:

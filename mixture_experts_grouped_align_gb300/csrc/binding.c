@@ -16,7 +16,7 @@
 
 #include "moe_gb300.h"
 
-enum { F_ROUTER, F_ACT_FWD, F_ACT_BWD, F_DENSE, F_BIAS, F_PAIRS, F_NORM, F_NORM_BWD, F_COUNT };
+enum { F_ROUTER, F_ACT_FWD, F_ACT_BWD, F_DENSE, F_BIAS, F_PAIRS, F_NORM, F_NORM_BWD, F_ADAPTER, F_COUNT };
 enum { T_F32, T_I32, T_BF16, T_U8, T_I64, T_COUNT };
 
 static void* g_fn[F_COUNT];
@@ -249,6 +249,24 @@ static PyObject* residual_norm_backward(PyObject* self, PyObject* const* a, Py_s
        (int32_t)v.f32, d_res, d_x, d_w, ctx);
 }
 
+/* x, a, b, scale, row_offsets, adapter, base, M, N, K, r, L, R, out, out_f32, ctx */
+static PyObject* adapter_gemm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  (void)self;
+  long long M, N, K, r, L, R, f32;
+  void *x, *wa, *wb, *scale, *off, *ad, *base, *out, *ctx;
+  if (!count(n, 16) || !I64(a[7], M) || !I32(a[8], N) || !I32(a[9], K) || !I32(a[10], r) || !I32(a[11], L) || !I32(a[12], R) ||
+      !I32(a[14], f32))
+    return NULL;
+  const int ot = f32 ? T_F32 : T_BF16;
+  if (!tensor_arg(a[0], "x", T_BF16, elems(M, K), &x) || !tensor_arg(a[1], "a", T_BF16, elems(elems(L, r), K), &wa) ||
+      !tensor_arg(a[2], "b", T_BF16, elems(elems(L, N), r), &wb) || !tensor_arg(a[3], "scale", T_F32, L, &scale) ||
+      !tensor_arg(a[4], "row_offsets", T_I32, R + 1, &off) || !tensor_arg(a[5], "adapter", T_I32, R, &ad) ||
+      !tensor_arg(a[6], "base", ot, elems(M, N), &base) || !tensor_arg(a[13], "out", ot, elems(M, N), &out) || !CTX(a[15], ctx))
+    return NULL;
+  CALL(moe_adapter_gemm, F_ADAPTER, x, wa, wb, scale, off, ad, base, M, (int32_t)N, (int32_t)K, (int32_t)r, (int32_t)L, (int32_t)R,
+       out, (int32_t)f32, ctx);
+}
+
 static PyObject* setup(PyObject* self, PyObject* args) {
   (void)self;
   PyObject *error, *type[T_COUNT], *fns;
@@ -274,7 +292,7 @@ static PyObject* setup(PyObject* self, PyObject* args) {
 #define FAST(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {{"setup", setup, METH_VARARGS, NULL}, FAST(router_loss), FAST(act_checkpoint), FAST(act_backward),
                                 FAST(dense_gemm), FAST(dense_bias_grad), FAST(pair_sum), FAST(residual_norm), FAST(residual_norm_backward),
-                                {NULL, NULL, 0, NULL}};
+                                FAST(adapter_gemm), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__binding(void) {

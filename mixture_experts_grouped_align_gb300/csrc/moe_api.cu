@@ -884,6 +884,31 @@ moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, c
   return st;
 }
 
+moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const float* scale, const int32_t* row_offsets,
+                            const int32_t* adapter, const void* base, int64_t M, int32_t N, int32_t K, int32_t r,
+                            int32_t L, int32_t R, void* out, int32_t out_f32, const moe_ctx* ctx) {
+  MOE_REQUIRE(M >= 0 && N >= 1 && K >= 1 && r >= 1 && L >= 1 && R >= 0, MOE_ERR_INVALID_ARG,
+              "need M >= 0, N >= 1, K >= 1, r >= 1, L >= 1, R >= 0");
+  const int64_t most = (int64_t)1 << 30;
+  MOE_REQUIRE(M < most && N < most && K < most && R < most, MOE_ERR_UNSUPPORTED, "M, N, K and R must be < 2^30");
+  MOE_REQUIRE(N % 8 == 0 && K % 8 == 0, MOE_ERR_UNSUPPORTED, "N and K must be multiples of 8");
+  MOE_REQUIRE(r % 8 == 0 && r <= 128, MOE_ERR_UNSUPPORTED, "r must be a multiple of 8, up to 128");
+  MOE_REQUIRE(weights_fit(L, r, K) && weights_fit(L, N, r), MOE_ERR_UNSUPPORTED, "adapters too large for 64-bit indexing");
+  if (M == 0 || R == 0) return MOE_OK;
+  MOE_REQUIRE(x && a && b && row_offsets && adapter && out, MOE_ERR_INVALID_ARG, "null tensor pointer");
+  MOE_REQUIRE(aligned16(x) && aligned16(a) && aligned16(b) && aligned16(scale) && aligned16(row_offsets) &&
+                  aligned16(adapter) && aligned16(base) && aligned16(out),
+              MOE_ERR_INVALID_ARG, "all pointers must be 16-byte aligned");
+  moe_launch::Adapter p{};
+  p.x = x; p.a = a; p.b = b; p.scale = scale; p.row_offsets = row_offsets; p.adapter = adapter; p.base = base;
+  p.M = M; p.N = N; p.K = K; p.r = r; p.L = L; p.R = R; p.out = out; p.out_f32 = out_f32 ? 1 : 0;
+  p.status = status_of(ctx);
+  rec(ctx, 0, 2);
+  const moe_status st = cuda_status(moe_launch::adapter_few(p, stream_of(ctx)), "moe_adapter_gemm");
+  rec(ctx, 1, 2);
+  return st;
+}
+
 void moe_debug_stall_tensor_kernels(int64_t stall_ns) {
   moe_launch::g_debug_stall_ns.store(stall_ns > 0 ? stall_ns : 0, std::memory_order_relaxed);
 }

@@ -330,4 +330,21 @@ size_t residual_norm_workspace_bytes(int K);
 cudaError_t residual_norm(const ResidualNorm& p, cudaStream_t stream);
 cudaError_t residual_norm_backward(ResidualNormBackward p, float* d_weight, cudaStream_t stream);
 
+// ---- low-rank adapters of many requests (adapter_few.cu)
+struct Adapter {
+  const void* x;               // [M, K] bf16
+  const void* a;               // [L, r, K] bf16
+  const void* b;               // [L, N, r] bf16
+  const float* scale;          // [L] or null
+  const int32_t* row_offsets;  // [R + 1]
+  const int32_t* adapter;      // [R]
+  const void* base;            // [M, N] in out's type or null
+  int64_t M;
+  int N, K, r, L, R;
+  void* out;                   // [M, N] bf16 or fp32
+  int out_f32;
+  int32_t* status;
+};
+cudaError_t adapter_few(const Adapter& p, cudaStream_t stream);
+
 }  // namespace moe_launch
