@@ -544,6 +544,10 @@ moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, c
  * Low-rank adapters of many requests beside a dense product                              *
  * ------------------------------------------------------------------------------------ */
 
+/* Workspace bytes of moe_adapter_gemm for M rows of R requests and rank r: 0 where the requests are short
+ * on average (decode batches). */
+size_t moe_adapter_gemm_workspace_size(int64_t M, int32_t R, int32_t r);
+
 /* For the rows m of request i (row_offsets[i] <= m < row_offsets[i+1]) and its adapter l = adapter[i]:
  *   out[m] = base[m] + scale[l] * (x[m] . a[l]^T) . b[l]^T      (l >= 0)
  *   out[m] = base[m]                                            (l = -1: no adapter)
@@ -560,7 +564,7 @@ moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, c
  * has no rows; where requests overlap, their rows are undefined), adapters outside [-1, L)
  * (MOE_ERR_INVALID_EXPERT; read as -1).
  * Limits: K and N multiples of 8, r a multiple of 8 up to 128, M, N, K, R < 2^30, L >= 1.  M = 0 or R = 0:
- * nothing is done. */
+ * nothing is done.  Needs moe_adapter_gemm_workspace_size() bytes of workspace. */
 moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const float* scale, const int32_t* row_offsets,
                             const int32_t* adapter, const void* base, int64_t M, int32_t N, int32_t K, int32_t r,
                             int32_t L, int32_t R, void* out, int32_t out_f32, const moe_ctx* ctx);

@@ -23,7 +23,8 @@ __all__ = [
     "moe_gemm_per_token", "moe_wgrad", "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels",
     "moe_router_loss", "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward",
     "moe_dense_gemm", "moe_dense_gemm_plan", "moe_dense_bias_grad", "moe_pair_sum", "moe_residual_norm",
-    "moe_residual_norm_backward", "moe_residual_norm_workspace_size", "moe_adapter_gemm", "W_LAYOUT", "SCALES", "EXPORTED_SYMBOLS",
+    "moe_residual_norm_backward", "moe_residual_norm_workspace_size", "moe_adapter_gemm",
+    "moe_adapter_gemm_workspace_size", "W_LAYOUT", "SCALES", "EXPORTED_SYMBOLS",
 ]
 
 MOE_OK = 0
@@ -43,7 +44,7 @@ EXPORTED_SYMBOLS = [
     "moe_wgrad_workspace_size", "moe_debug_stall_tensor_kernels", "moe_router_loss",
     "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward", "moe_dense_gemm",
     "moe_dense_bias_grad", "moe_pair_sum", "moe_dense_gemm_plan", "moe_residual_norm", "moe_residual_norm_backward",
-    "moe_residual_norm_workspace_size", "moe_adapter_gemm",
+    "moe_residual_norm_workspace_size", "moe_adapter_gemm", "moe_adapter_gemm_workspace_size",
 ]
 
 
@@ -130,6 +131,7 @@ def load(path: str | None = None):
         "moe_residual_norm": (I32, [P, P, P, P, I64, I32, F32, P, I32, P, P, P, P, I32, P]),
         "moe_residual_norm_backward": (I32, [P, P, P, P, P, I64, I32, F32, P, I32, P, P, P, P]),
         "moe_residual_norm_workspace_size": (SZ, [I32]),
+        "moe_adapter_gemm_workspace_size": (SZ, [I64, I32, I32]),
         "moe_adapter_gemm": (I32, [P, P, P, P, P, P, P, I64, I32, I32, I32, I32, I32, P, I32, P]),
     }
     for name, (res, args) in sig.items():
@@ -407,6 +409,10 @@ def moe_residual_norm_backward(d_out, d_stream, stream, token_mask, weight, T, K
     return _check((_native or _load_native()).residual_norm_backward(d_out, d_stream, stream, token_mask, weight, T, K, eps, p,
                                                                      rng, rng_stream, int(stream_f32), d_residual, d_x,
                                                                      d_weight, c.address))
+
+
+def moe_adapter_gemm_workspace_size(M, R, r) -> int:
+    return load().moe_adapter_gemm_workspace_size(M, R, r)
 
 
 def moe_adapter_gemm(x, a, b, scale, row_offsets, adapter, base, M, N, K, r, L, R, out, ctx=None, out_f32=None):

@@ -47,6 +47,12 @@ void apply_debug_stall(Dense& d) {
   d.stall = ns > 0 ? 1 : 0;
 }
 
+void apply_debug_stall(Adapter& a) {
+  const int64_t ns = debug_stall_ns();
+  a.wait_ns = ns > 0 ? ns : 0;
+  a.stall = ns > 0 ? 1 : 0;
+}
+
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
   int dev = -1;
   const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
@@ -884,6 +890,10 @@ moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, c
   return st;
 }
 
+size_t moe_adapter_gemm_workspace_size(int64_t M, int32_t R, int32_t r) {
+  return M >= 1 && M < ((int64_t)1 << 30) && R >= 1 && r >= 1 && r <= 128 ? moe_launch::adapter_workspace_bytes(M, R, r) : 0;
+}
+
 moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const float* scale, const int32_t* row_offsets,
                             const int32_t* adapter, const void* base, int64_t M, int32_t N, int32_t K, int32_t r,
                             int32_t L, int32_t R, void* out, int32_t out_f32, const moe_ctx* ctx) {
@@ -903,8 +913,19 @@ moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const f
   p.x = x; p.a = a; p.b = b; p.scale = scale; p.row_offsets = row_offsets; p.adapter = adapter; p.base = base;
   p.M = M; p.N = N; p.K = K; p.r = r; p.L = L; p.R = R; p.out = out; p.out_f32 = out_f32 ? 1 : 0;
   p.status = status_of(ctx);
+  // the kernels for long requests address the adapters' rows with 31 bits
+  const bool many = moe_launch::adapter_many_takes(M, R) && (int64_t)L * N < ((int64_t)1 << 31) - 256 &&
+                    (int64_t)L * r < ((int64_t)1 << 31) - 256;
+  if (many) {
+    const size_t need = moe_adapter_gemm_workspace_size(M, R, r);
+    MOE_REQUIRE(ctx && ctx->workspace && ctx->workspace_bytes >= need && aligned16(ctx->workspace), MOE_ERR_CAPACITY,
+                "workspace of %zu bytes needed", need);
+    p.v = static_cast<float*>(ctx->workspace);
+    moe_launch::apply_debug_stall(p);
+  }
   rec(ctx, 0, 2);
-  const moe_status st = cuda_status(moe_launch::adapter_few(p, stream_of(ctx)), "moe_adapter_gemm");
+  const moe_status st = cuda_status(many ? moe_launch::adapter_many(p, stream_of(ctx)) : moe_launch::adapter_few(p, stream_of(ctx)),
+                                    "moe_adapter_gemm");
   rec(ctx, 1, 2);
   return st;
 }
