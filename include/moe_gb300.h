@@ -544,8 +544,7 @@ moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, c
  * Low-rank adapters of many requests beside a dense product                              *
  * ------------------------------------------------------------------------------------ */
 
-/* Workspace bytes of moe_adapter_gemm for M rows of R requests and rank r: 0 where the requests are short
- * on average (decode batches). */
+/* Workspace bytes of moe_adapter_gemm for M rows of R requests and rank r (0 for sizes it refuses). */
 size_t moe_adapter_gemm_workspace_size(int64_t M, int32_t R, int32_t r);
 
 /* For the rows m of request i (row_offsets[i] <= m < row_offsets[i+1]) and its adapter l = adapter[i]:

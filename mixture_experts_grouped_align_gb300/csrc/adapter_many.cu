@@ -649,8 +649,8 @@ bool adapter_many_takes(int64_t M, int R) {
 }
 
 // The pieces of v: one for each tile and one for each CTA.
-size_t adapter_workspace_bytes(int64_t M, int R, int r) {
-  return adapter_many_takes(M, R) ? (size_t)(M / kRows + R + kCtasMost) * kRows * r * 4 : 0;
+size_t adapter_many_workspace_bytes(int64_t M, int R, int r) {
+  return (size_t)(M / kRows + R + kCtasMost) * kRows * r * 4;
 }
 
 cudaError_t adapter_many(const Adapter& p, cudaStream_t stream) {

@@ -4,6 +4,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "moe_common.cuh"
@@ -891,7 +892,9 @@ moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, c
 }
 
 size_t moe_adapter_gemm_workspace_size(int64_t M, int32_t R, int32_t r) {
-  return M >= 1 && M < ((int64_t)1 << 30) && R >= 1 && r >= 1 && r <= 128 ? moe_launch::adapter_workspace_bytes(M, R, r) : 0;
+  if (M < 1 || M >= (int64_t)1 << 30 || R < 1 || r < 1 || r > 128) return 0;
+  const size_t few = moe_launch::adapter_few_workspace_bytes(M, r);
+  return moe_launch::adapter_many_takes(M, R) ? std::max(few, moe_launch::adapter_many_workspace_bytes(M, R, r)) : few;
 }
 
 moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const float* scale, const int32_t* row_offsets,
@@ -916,13 +919,11 @@ moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const f
   // the kernels for long requests address the adapters' rows with 31 bits
   const bool many = moe_launch::adapter_many_takes(M, R) && (int64_t)L * N < ((int64_t)1 << 31) - 256 &&
                     (int64_t)L * r < ((int64_t)1 << 31) - 256;
-  if (many) {
-    const size_t need = moe_adapter_gemm_workspace_size(M, R, r);
-    MOE_REQUIRE(ctx && ctx->workspace && ctx->workspace_bytes >= need && aligned16(ctx->workspace), MOE_ERR_CAPACITY,
-                "workspace of %zu bytes needed", need);
-    p.v = static_cast<float*>(ctx->workspace);
-    moe_launch::apply_debug_stall(p);
-  }
+  const size_t need = moe_adapter_gemm_workspace_size(M, R, r);
+  MOE_REQUIRE(ctx && ctx->workspace && ctx->workspace_bytes >= need && aligned16(ctx->workspace), MOE_ERR_CAPACITY,
+              "workspace of %zu bytes needed", need);
+  p.v = static_cast<float*>(ctx->workspace);
+  moe_launch::apply_debug_stall(p);
   rec(ctx, 0, 2);
   const moe_status st = cuda_status(many ? moe_launch::adapter_many(p, stream_of(ctx)) : moe_launch::adapter_few(p, stream_of(ctx)),
                                     "moe_adapter_gemm");

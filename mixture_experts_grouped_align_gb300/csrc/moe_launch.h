@@ -343,16 +343,17 @@ struct Adapter {
   int N, K, r, L, R;
   void* out;                   // [M, N] bf16 or fp32
   int out_f32;
-  float* v;                    // scratch of the kernels for long requests
+  float* v;                    // scratch
   int32_t* status;
   int64_t wait_ns;             // limit of every wait (0: the 2 s default)
   int stall;                   // failure-detection self-test: the copy and MMA roles off
 };
 void apply_debug_stall(Adapter& a);
+size_t adapter_few_workspace_bytes(int64_t M, int r);
 cudaError_t adapter_few(const Adapter& p, cudaStream_t stream);
 // Whether M rows of R requests run on the kernels for long requests, and their scratch.
 bool adapter_many_takes(int64_t M, int R);
-size_t adapter_workspace_bytes(int64_t M, int R, int r);
+size_t adapter_many_workspace_bytes(int64_t M, int R, int r);
 cudaError_t adapter_many(const Adapter& p, cudaStream_t stream);
 
 }  // namespace moe_launch
