@@ -3,12 +3,11 @@
 //   out[m] = base[m] + scale[a] (x[m] A[a]^T) B[a]^T,  a the adapter of m's request
 //
 // Bound by the adapters' bytes: with few rows each of them is read for a handful of rows.  So rows
-// are gathered by adapter, whatever their order: a block looks at 512 rows, finds each one's
+// are gathered by adapter, whatever their order: a block looks at 256 rows, finds each one's
 // occurrence among the rows of its adapter, and every sixteenth is the first of a tile of up to
 // sixteen rows of one adapter, the rows of an m16n8k16 MMA.  (250 rows over five adapters are 20
 // tiles, and not 250 readings of an adapter.)  Two kernels, v = x A^T and out = base + v B^T; in each
-// every CTA takes an equal run of all tiles' blocks of K, or of features, so that one tile and 500
-// alike use every SM.  A tile's pieces of v are added in order by those who read them.  The second
+// the CTAs share the tiles' blocks of K, or of features, so that one tile and 200 alike use many SMs.  A tile's pieces of v are added in order by those who read them.  The second
 // kernel starts under the first one: its tables, the rows without an adapter and B's way into L2 do
 // not wait for v.
 // The operands of an MMA are read from global memory in their own layout, 16 or 8 bytes a lane: the
@@ -24,8 +23,8 @@ namespace {
 
 using moe_launch::Adapter;
 
-constexpr int kThreads = 512, kWarps = 16;
-constexpr int kChunk = 512;   // rows that a block looks at
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kChunk = kThreads;  // rows that a block looks at
 constexpr int kTile = 16;     // rows of a tile
 constexpr int kRankMost = 128;
 constexpr unsigned kAll = 0xffffffffu;
@@ -37,7 +36,7 @@ struct Rows {
   int32_t start[kChunk];     // the last request that starts at a row, -1: none
   int32_t start_id[kChunk];  // its adapter and its end
   int32_t start_end[kChunk];
-  int32_t warp_sum[kWarps];
+  int32_t warp_sum[kWarps], lead_sum[kWarps];
   int32_t tiles;
   int32_t rows[kTile];       // of the tile at hand
 };
@@ -51,31 +50,24 @@ struct UpSmem {
   alignas(16) uint32_t vb[2][kTile * (kRankMost + 8) / 2];  // v's high and low parts: [row][rank], rows 8 ranks apart
 };
 
-// A CTA's run over the tiles' blocks: `blocks` a tile, in pieces of one tile each.
-struct Run {
-  int64_t at, end;
-  int blocks;
-  MOE_DEV Run(int64_t total, int blocks, int cta, int ctas) : blocks(blocks) {
-    at = cta < ctas ? total * cta / ctas : 0;
-    end = cta < ctas ? total * (cta + 1) / ctas : 0;
-  }
-  MOE_DEV bool next(int& tile, int& b0, int& b1) {
-    if (at >= end) return false;
-    tile = (int)(at / blocks);
-    b0 = (int)(at - (int64_t)tile * blocks);
-    b1 = (int)min((int64_t)blocks, b0 + end - at);
-    at += b1 - b0;
+// Equal shares of the tiles' blocks for the CTAs of a chunk.  Up to as many tiles as CTAs: `parts` CTAs a
+// tile, a piece of one tile each, as every further piece costs a CTA the latency of its first loads (64
+// tokens over 100 adapters: 3.2 us of loads for two pieces, 1.6 for one).  More tiles: whole ones in turn.
+constexpr int kPieces = 32;
+struct Share {
+  int tiles, blocks, parts, cta, ctas;
+  MOE_DEV Share(int tiles, int blocks, int most, int cta, int ctas)
+      : tiles(tiles), blocks(blocks), parts(tiles ? max(1, min(min(most, blocks), ctas / tiles)) : 1), cta(cta), ctas(ctas) {}
+  // The n-th tile of this CTA, and its blocks of it.
+  MOE_DEV bool get(int n, int& tile, int& b0, int& b1) const {
+    const int part = parts > 1 ? cta % parts : 0;
+    tile = parts > 1 ? cta / parts : cta + n * ctas;
+    if (tile >= tiles || (parts > 1 && n > 0)) return false;
+    b0 = (int)((int64_t)blocks * part / parts);
+    b1 = (int)((int64_t)blocks * (part + 1) / parts);
     return true;
   }
 };
-// The CTA whose run has block x (no run is empty).
-MOE_DEV int owner(int64_t x, int64_t total, int ctas) { return (int)(((x + 1) * ctas - 1) / total); }
-// CTAs of the first kernel on `tiles` tiles of `blocks` blocks: a tile is cut into at most kPieces
-// pieces, or kPieces / 2 + 1 where there are several, whose sums cost as much as they gain.
-constexpr int kPieces = 32;
-MOE_DEV int down_ctas(int tiles, int blocks, int ctas) {
-  return min(ctas, min(tiles <= 4 ? kPieces - 1 : kPieces / 2, blocks) * tiles);
-}
 
 MOE_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
@@ -86,11 +78,11 @@ MOE_DEV void mma32(float (&d)[4], const uint4& x0, const uint4& x1, const uint4&
   moe::mma_bf16(d, b, w.z, w.w, d);
 }
 
-// The chunk's rows: adapters, occurrences and tiles.
+// The chunk's rows: adapters, occurrences and tiles.  `start` is all -1 by then.
 __device__ __forceinline__ void make_tables(const Adapter& p, Rows& sm, int64_t row0, int rows, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // Where a request starts in the chunk, or -1.  Of several at one place (offsets that decrease) the last
-  // is taken, by every CTA: they meet in the barriers of the same tiles.
+  // is taken, by every CTA and in both kernels.
   const auto place = [&](int i, int& end, int& id) {
     const int64_t lo = p.row_offsets[i], hi = p.row_offsets[i + 1];
     id = p.adapter[i];
@@ -101,22 +93,25 @@ __device__ __forceinline__ void make_tables(const Adapter& p, Rows& sm, int64_t 
     if (!bounds || lo == hi || hi <= row0 || lo >= row0 + rows) return -1;
     return lo > row0 ? (int)(lo - row0) : 0;
   };
-  int end, a;
-  sm.start[tid] = -1;
-  __syncthreads();
-  for (int i = tid; i < p.R; i += kThreads) {
-    const int at = place(i, end, a);
+  int first_end = 0, first_id = 0, end, id_of;
+  const int first_at = tid < p.R ? place(tid, first_end, first_id) : -1;  // most calls have no more requests than threads
+  if (first_at >= 0) atomicMax(&sm.start[first_at], tid);
+  for (int i = tid + kThreads; i < p.R; i += kThreads) {
+    const int at = place(i, end, id_of);
     if (at >= 0) atomicMax(&sm.start[at], i);
   }
   __syncthreads();
-  for (int i = tid; i < p.R; i += kThreads) {
-    const int at = place(i, end, a);
+  if (first_at >= 0 && sm.start[first_at] == tid) {
+    sm.start_id[first_at] = first_id;
+    sm.start_end[first_at] = first_end;
+  }
+  for (int i = tid + kThreads; i < p.R; i += kThreads) {
+    const int at = place(i, end, id_of);
     if (at >= 0 && sm.start[at] == i) {
-      sm.start_id[at] = a;
+      sm.start_id[at] = id_of;
       sm.start_end[at] = end;
     }
   }
-  __syncthreads();
   // the request of a row is the last that starts at or before it
   int at = sm.start[tid] >= 0 ? tid : -1;
 #pragma unroll
@@ -126,63 +121,68 @@ __device__ __forceinline__ void make_tables(const Adapter& p, Rows& sm, int64_t 
   }
   if (lane == 31) sm.warp_sum[warp] = at;
   __syncthreads();
-  for (int w = 0; w < warp; ++w) at = max(at, sm.warp_sum[w]);
+  {
+    const int before = lane < warp ? sm.warp_sum[lane] : -1;
+    at = max(at, __reduce_max_sync(kAll, before));
+  }
   const int id = tid < rows && at >= 0 && tid < sm.start_end[at] ? sm.start_id[at] : -2;
   sm.id[tid] = id;
   __syncthreads();
   int occ = 0;
-  if (id >= 0) {
+  {  // rows before this warp's, then its own
     const int4* ids = reinterpret_cast<const int4*>(sm.id);
-    for (int j = 0; j < tid / 4; ++j) {
-      const int4 q = ids[j];
-      occ += (q.x == id) + (q.y == id) + (q.z == id) + (q.w == id);
-    }
-    for (int j = tid & ~3; j < tid; ++j) occ += sm.id[j] == id;
+    if (id >= 0)
+#pragma unroll 4
+      for (int j = 0; j < warp * 8; ++j) {
+        const int4 q = ids[j];
+        occ += (q.x == id) + (q.y == id) + (q.z == id) + (q.w == id);
+      }
+    occ += __popc(__match_any_sync(kAll, id) & ((1u << lane) - 1));
   }
   sm.occ[tid] = (int16_t)occ;
   const unsigned leads = __ballot_sync(kAll, id >= 0 && occ % kTile == 0);
-  if (lane == 0) sm.warp_sum[warp] = __popc(leads);
+  if (lane == 0) sm.lead_sum[warp] = __popc(leads);
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    const int n = sm.warp_sum[w];
-    before += w < warp ? n : 0;
-    all += n;
-  }
+  const int n = lane < kWarps ? sm.lead_sum[lane] : 0;
+  const int before = __reduce_add_sync(kAll, lane < warp ? n : 0), all = __reduce_add_sync(kAll, n);
   if (leads >> lane & 1) sm.leader[before + __popc(leads & ((1u << lane) - 1))] = (int16_t)tid;
   if (tid == 0) sm.tiles = all;
   __syncthreads();
 }
 
-// Eight features of a row: base (or zeros) plus add, to out.
+// Eight features of a row.
 template <bool F32>
-__device__ __forceinline__ void add_to_base(const Adapter& p, int64_t at, const float (&add)[8]) {
-  if (F32) {
-    float4 b[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    if (p.base) {
-      b[0] = reinterpret_cast<const float4*>(static_cast<const float*>(p.base) + at)[0];
-      b[1] = reinterpret_cast<const float4*>(static_cast<const float*>(p.base) + at)[1];
-    }
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-    o[0] = make_float4(b[0].x + add[0], b[0].y + add[1], b[0].z + add[2], b[0].w + add[3]);
-    o[1] = make_float4(b[1].x + add[4], b[1].y + add[5], b[1].z + add[6], b[1].w + add[7]);
-  } else {
-    uint4 b = make_uint4(0, 0, 0, 0);
-    if (p.base) b = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) + at);
-    uint32_t w[4] = {b.x, b.y, b.z, b.w};
+struct Out8 {
+  uint4 v[F32 ? 2 : 1];
+  MOE_DEV void load(const void* base, int64_t at, bool on) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 s = __floats2bfloat162_rn(__uint_as_float(w[i] << 16) + add[2 * i],
-                                                     __uint_as_float(w[i] & 0xffff0000u) + add[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&s);
-    }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < (F32 ? 2 : 1); ++i)
+      v[i] = on && base ? static_cast<const uint4*>(base)[at / 8 * (F32 ? 2 : 1) + i] : make_uint4(0, 0, 0, 0);
   }
-}
+  MOE_DEV void add_and_store(void* out, int64_t at, const float (&f)[8]) {
+    uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[F32].x, v[F32].y, v[F32].z, v[F32].w};
+    uint4* o = static_cast<uint4*>(out) + at / 8 * (F32 ? 2 : 1);
+    if (F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) + f[i]);
+      o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      o[F32] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 s = __floats2bfloat162_rn(__uint_as_float(w[i] << 16) + f[2 * i],
+                                                       __uint_as_float(w[i] & 0xffff0000u) + f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&s);
+      }
+      o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+};
 
 // The rows of tile t, -1 where it has fewer than sixteen; every thread calls.
 __device__ __forceinline__ int tile_rows(Rows& sm, int t) {
   const int tid = threadIdx.x, lead = sm.leader[t], id = sm.id[lead], from = sm.occ[lead];
+  __syncthreads();  // the rows of the tile before have been read
   if (tid < kTile) sm.rows[tid] = -1;
   __syncthreads();
   if (sm.id[tid] == id && sm.occ[tid] >= from && sm.occ[tid] < from + kTile) sm.rows[sm.occ[tid] - from] = tid;
@@ -190,7 +190,10 @@ __device__ __forceinline__ int tile_rows(Rows& sm, int t) {
   return id;
 }
 
-// blockIdx.x: a chunk of 512 rows, a CTA of the chunk's.
+// blockIdx.x: a chunk of 256 rows, a CTA of the chunk's.  A warp takes NJ eights of ranks and a share of
+// the run's blocks, U of them at once: what the loads in flight take of registers is what the run's time
+// goes by (512 threads of one block at a time: 250 rows of rank 64 over five adapters 23 us).
+template <int NJ, int U>
 __global__ void __launch_bounds__(kThreads, 2) adapter_few_down_kernel(Adapter p, int ctas) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   DownSmem& sm = *reinterpret_cast<DownSmem*>(smem_raw);
@@ -198,53 +201,63 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_down_kernel(Adapter p
   const int chunk = blockIdx.x / ctas, cta = blockIdx.x - chunk * ctas;
   const int64_t row0 = (int64_t)chunk * kChunk;
   const int rows = p.M - row0 < kChunk ? (int)(p.M - row0) : kChunk;
+  sm.t.start[tid] = -1;
+  __syncthreads();
   moe::wait_for_stream();
   moe::let_next_start();
   make_tables(p, sm.t, row0, rows, blockIdx.x == 0);
 
-  const int nk = (p.K + 31) / 32, used = down_ctas(sm.t.tiles, nk, ctas);
-  const int64_t total = (int64_t)sm.t.tiles * nk;
-  const int groups = (p.r + 31) / 32;  // of 32 ranks
-  const int slices = kWarps / groups, rg = warp % groups, slice = warp / groups, rp = groups * 32;
+  const int nk = (p.K + 31) / 32;
+  const Share share(sm.t.tiles, nk, kPieces, cta, ctas);
+  const int groups = (p.r + 8 * NJ - 1) / (8 * NJ);
+  const int slices = kWarps / groups, rg = warp % groups, slice = warp / groups, rp = groups * 8 * NJ;
   const uint16_t* x = static_cast<const uint16_t*>(p.x);
-  Run run(total, nk, cta, used);
   int t, k0, k1;
-  while (run.next(t, k0, k1)) {
+  for (int turn = 0; share.get(turn, t, k0, k1); ++turn) {
+    int t1, l0, l1;
+    if (share.get(turn + 1, t1, l0, l1)) {  // the next tile's A on its way into L2 meanwhile
+      const char* A = reinterpret_cast<const char*>(static_cast<const uint16_t*>(p.a) + (int64_t)sm.t.id[sm.t.leader[t1]] * p.r * p.K);
+      for (int64_t i = (int64_t)tid * 128; i < (int64_t)p.r * p.K * 2; i += kThreads * 128) prefetch_l2(A + i);
+    }
     const int id = tile_rows(sm.t, t);
     const uint16_t* A = static_cast<const uint16_t*>(p.a) + (int64_t)id * p.r * p.K;
     if (slice < slices) {
       const int ra = sm.t.rows[g], rb = sm.t.rows[g + 8];
-      float d[4][4];
+      float d[NJ][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[j][i] = 0.f;
       const uint4 none = make_uint4(0, 0, 0, 0);
       const uint16_t* xa = x + (row0 + (ra < 0 ? 0 : ra)) * p.K;
       const uint16_t* xb = x + (row0 + (rb < 0 ? 0 : rb)) * p.K;
-      for (int c = k0 + slice; c < k1; c += slices) {
-        const int k = c * 32 + q * 8;
-        const bool on = k < p.K;
-        uint4 w[4];
+      const uint16_t* wa = A + (int64_t)(rg * 8 * NJ + g) * p.K;
+      for (int c = k0 + slice; c < k1; c += U * slices) {
+        uint4 w[U][NJ], x0[U], x1[U];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = rg * 32 + j * 8 + g;
-          w[j] = on && n < p.r ? moe::ldg_nc_u128(A + (int64_t)n * p.K + k) : none;
+        for (int u = 0; u < U; ++u) {
+          const int k = (c + u * slices) * 32 + q * 8;
+          const bool on = c + u * slices < k1 && k < p.K;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            w[u][j] = on && rg * 8 * NJ + j * 8 + g < p.r ? moe::ldg_nc_u128(wa + (int64_t)j * 8 * p.K + k) : none;
+          x0[u] = on && ra >= 0 ? moe::ldg_nc_u128(xa + k) : none;
+          x1[u] = on && rb >= 0 ? moe::ldg_nc_u128(xb + k) : none;
         }
-        const uint4 x0 = on && ra >= 0 ? *reinterpret_cast<const uint4*>(xa + k) : none;
-        const uint4 x1 = on && rb >= 0 ? *reinterpret_cast<const uint4*>(xb + k) : none;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mma32(d[j], x0, x1, w[j]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) mma32(d[j], x0[u], x1[u], w[u][j]);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float* at = sm.part + (slice * kTile + g) * rp + rg * 32 + j * 8 + q * 2;
+      for (int j = 0; j < NJ; ++j) {
+        float* at = sm.part + (slice * kTile + g) * rp + (rg * NJ + j) * 8 + q * 2;
         *reinterpret_cast<float2*>(at) = make_float2(d[j][0], d[j][1]);
         *reinterpret_cast<float2*>(at + 8 * rp) = make_float2(d[j][2], d[j][3]);
       }
     }
     __syncthreads();
-    const int piece = cta - owner((int64_t)t * nk, total, used);
+    const int piece = share.parts > 1 ? cta % share.parts : 0;
     float* v = p.v + ((int64_t)piece * p.M + row0) * p.r;
     for (int i = tid; i < kTile * rp / 2; i += kThreads) {  // two ranks each
       const int m = sm.t.rows[2 * i / rp], k = 2 * i % rp;
@@ -260,7 +273,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_down_kernel(Adapter p
   }
 }
 
-template <bool F32>
+// A warp takes U blocks of 32 features at once, S steps of 16 ranks each.
+template <bool F32, int S, int U>
 __global__ void __launch_bounds__(kThreads, 2) adapter_few_up_kernel(Adapter p, int ctas) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   UpSmem& sm = *reinterpret_cast<UpSmem*>(smem_raw);
@@ -268,22 +282,28 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_up_kernel(Adapter p, 
   const int chunk = blockIdx.x / ctas, cta = blockIdx.x - chunk * ctas;
   const int64_t row0 = (int64_t)chunk * kChunk;
   const int rows = p.M - row0 < kChunk ? (int)(p.M - row0) : kChunk;
+  sm.t.start[tid] = -1;
+  __syncthreads();
   // The first kernel lets this one start when all before it is complete: what is not v can be read and
   // written already.
   make_tables(p, sm.t, row0, rows, false);
-  const int nk = (p.K + 31) / 32, nb = (p.N + 31) / 32, used = down_ctas(sm.t.tiles, nk, ctas);
-  const int64_t total = (int64_t)sm.t.tiles * nk;
+  const int nk = (p.K + 31) / 32, nb = (p.N + 31) / 32, pieces = Share(sm.t.tiles, nk, kPieces, 0, ctas).parts;
   const int rp = (p.r + 31) / 32 * 32, vs = (kRankMost + 8) / 2, steps = (p.r + 15) / 16;
-  Run run((int64_t)sm.t.tiles * nb, nb, cta, ctas);
+  const Share share(sm.t.tiles, nb, nb, cta, ctas);
   int t, b0, b1;
-  {  // this CTA's parts of B on their way into L2
-    Run ahead = run;
-    while (ahead.next(t, b0, b1)) {
-      const uint16_t* B = static_cast<const uint16_t*>(p.b) + ((int64_t)sm.t.id[sm.t.leader[t]] * p.N + b0 * 32) * p.r;
-      const int64_t bytes = ((int64_t)min(b1 * 32, p.N) - b0 * 32) * p.r * 2;
-      for (int64_t i = (int64_t)tid * 128; i < bytes; i += kThreads * 128) prefetch_l2(reinterpret_cast<const char*>(B) + i);
-    }
-  }
+  // A tile's part of B and of its rows of base on their way into L2; every thread calls.
+  const auto ahead = [&](int turn) {
+    if (!share.get(turn, t, b0, b1)) return;
+    const int id = tile_rows(sm.t, t);
+    const char* B = reinterpret_cast<const char*>(static_cast<const uint16_t*>(p.b) + ((int64_t)id * p.N + b0 * 32) * p.r);
+    const int wide = min(b1 * 32, p.N) - b0 * 32;
+    for (int64_t i = (int64_t)tid * 128; i < (int64_t)wide * p.r * 2; i += kThreads * 128) prefetch_l2(B + i);
+    if (p.base == nullptr) return;
+    const int m = sm.t.rows[tid / (kThreads / kTile)], size = F32 ? 4 : 2;
+    const char* at = static_cast<const char*>(p.base) + ((row0 + m) * p.N + b0 * 32) * size;
+    for (int i = tid % (kThreads / kTile) * 128; m >= 0 && i < wide * size; i += kThreads / kTile * 128) prefetch_l2(at + i);
+  };
+  ahead(0);
   // rows of requests without an adapter: base as it is
   if (p.base != p.out) {
     const int units = p.N / 8 * (F32 ? 2 : 1);
@@ -296,61 +316,112 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_up_kernel(Adapter p, 
   }
   moe::wait_for_stream();
   moe::let_next_start();
-  while (run.next(t, b0, b1)) {
+  for (int turn = 0; share.get(turn, t, b0, b1); ++turn) {
     const int id = tile_rows(sm.t, t);
     const uint16_t* B = static_cast<const uint16_t*>(p.b) + (int64_t)id * p.N * p.r;
-    const int c0 = owner((int64_t)t * nk, total, used), pieces = owner((int64_t)(t + 1) * nk - 1, total, used) - c0 + 1;
+    int t1, e0, e1;
+    if (share.get(turn + 1, t1, e0, e1)) {  // the next tile's B on its way into L2 meanwhile
+      const char* next = reinterpret_cast<const char*>(static_cast<const uint16_t*>(p.b) + (int64_t)sm.t.id[sm.t.leader[t1]] * p.N * p.r);
+      for (int64_t i = (int64_t)tid * 128; i < (int64_t)p.N * p.r * 2; i += kThreads * 128) prefetch_l2(next + i);
+    }
     const float scale = p.scale ? p.scale[id] : 1.f;
-    for (int i = tid; i < kTile * rp / 2; i += kThreads) {  // two ranks each
-      const int j = 2 * i / rp, m = sm.t.rows[j], k = 2 * i % rp;
-      float2 s = make_float2(0.f, 0.f);
+    // four ranks to each lane, or to 2 or 4 lanes with every second or fourth piece where threads are left
+    const int items = kTile * rp / 4, by = items >= kThreads ? 1 : kThreads / items, mine = tid % by;
+    for (int i = tid / by; i < items; i += kThreads / by) {
+      const int j = 4 * i / rp, m = sm.t.rows[j], k = 4 * i % rp;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       if (m >= 0 && k < p.r) {
         const float* v = p.v + (row0 + m) * p.r + k;
-        for (int c = 0; c < pieces; ++c) {
-          const float2 u = *reinterpret_cast<const float2*>(v + (int64_t)c * p.M * p.r);
-          s.x += u.x;
-          s.y += u.y;
+        for (int c0 = mine; c0 < pieces; c0 += 8 * by) {
+          float4 u[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            u[c] = c0 + c * by < pieces ? *reinterpret_cast<const float4*>(v + (int64_t)(c0 + c * by) * p.M * p.r)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            s.x += u[c].x;
+            s.y += u[c].y;
+            s.z += u[c].z;
+            s.w += u[c].w;
+          }
         }
       }
-      s.x *= scale;
-      s.y *= scale;
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(s.x, s.y);
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x - __low2float(hi), s.y - __high2float(hi));
-      sm.vb[0][j * vs + k / 2] = *reinterpret_cast<const uint32_t*>(&hi);
-      sm.vb[1][j * vs + k / 2] = *reinterpret_cast<const uint32_t*>(&lo);
+      for (int o = 1; o < by; o <<= 1) {
+        s.x += __shfl_xor_sync(kAll, s.x, o);
+        s.y += __shfl_xor_sync(kAll, s.y, o);
+        s.z += __shfl_xor_sync(kAll, s.z, o);
+        s.w += __shfl_xor_sync(kAll, s.w, o);
+      }
+      if (mine == 0) {
+        const float f[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
+        uint32_t w[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(f[2 * h], f[2 * h + 1]);
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(f[2 * h] - __low2float(hi), f[2 * h + 1] - __high2float(hi));
+          w[0][h] = *reinterpret_cast<const uint32_t*>(&hi);
+          w[1][h] = *reinterpret_cast<const uint32_t*>(&lo);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint2*>(&sm.vb[h][j * vs + k / 2]) = make_uint2(w[h][0], w[h][1]);
+      }
     }
     __syncthreads();
     const int ra = sm.t.rows[g], rb = sm.t.rows[g + 8];
     // v B^T, 32 features at a time: feature 8 (c / 2) + 2 j + c % 2 is column c of product j, so that a
     // lane ends with eight neighbouring ones of its rows
-    for (int b = b0 + warp; b < b1; b += kWarps) {
-      float d[4][4];
+    for (int b = b0 + warp; b < b1; b += U * kWarps) {
+      float d[U][4][4];
+      Out8<F32> oa[U], ob[U];  // base, on its way with the weights
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[j][i] = 0.f;
-      const int f0 = b * 32 + 8 * (g >> 1) + (g & 1);
-      for (int s = 0; s < steps; ++s) {
-        const int k = s * 16 + q * 4;
-        uint2 w[4];
+      for (int u = 0; u < U; ++u) {
+        const int n = (b + u * kWarps) * 32 + 8 * q;
+        const bool on = b + u * kWarps < b1 && n < p.N;
+        oa[u].load(p.base, (row0 + ra) * p.N + n, on && ra >= 0);
+        ob[u].load(p.base, (row0 + rb) * p.N + n, on && rb >= 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          w[j] = f0 + 2 * j < p.N && k < p.r ? moe::ldg_nc_u64(B + (int64_t)(f0 + 2 * j) * p.r + k) : make_uint2(0, 0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint2 va = *reinterpret_cast<const uint2*>(&sm.vb[h][g * vs + k / 2]);
-          const uint2 vc = *reinterpret_cast<const uint2*>(&sm.vb[h][(g + 8) * vs + k / 2]);
-          const uint32_t a[4] = {va.x, vc.x, va.y, vc.y};
+          for (int i = 0; i < 4; ++i) d[u][j][i] = 0.f;
+      }
+      for (int s0 = 0; s0 < steps; s0 += S) {
+        uint2 w[U][S][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) moe::mma_bf16(d[j], a, w[j].x, w[j].y, d[j]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int s = 0; s < S; ++s) {
+            const int f0 = (b + u * kWarps) * 32 + 8 * (g >> 1) + (g & 1), k = (s0 + s) * 16 + q * 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[u][s][j] = b + u * kWarps < b1 && f0 + 2 * j < p.N && k < p.r ? moe::ldg_nc_u64(B + (int64_t)(f0 + 2 * j) * p.r + k)
+                                                                              : make_uint2(0, 0);
+          }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          if (s0 + s >= steps) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int at = (s0 + s) * 8 + q * 2;
+            const uint2 va = *reinterpret_cast<const uint2*>(&sm.vb[h][g * vs + at]);
+            const uint2 vc = *reinterpret_cast<const uint2*>(&sm.vb[h][(g + 8) * vs + at]);
+            const uint32_t a[4] = {va.x, vc.x, va.y, vc.y};
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) moe::mma_bf16(d[u][j], a, w[u][s][j].x, w[u][s][j].y, d[u][j]);
+          }
         }
       }
-      const int n = b * 32 + 8 * q;
-      if (n < p.N) {
-        const float u[8] = {d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]};
-        const float v[8] = {d[0][2], d[0][3], d[1][2], d[1][3], d[2][2], d[2][3], d[3][2], d[3][3]};
-        if (ra >= 0) add_to_base<F32>(p, (row0 + ra) * p.N + n, u);
-        if (rb >= 0) add_to_base<F32>(p, (row0 + rb) * p.N + n, v);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int n = (b + u * kWarps) * 32 + 8 * q;
+        if (b + u * kWarps >= b1 || n >= p.N) continue;
+        const auto& e = d[u];
+        const float lo[8] = {e[0][0], e[0][1], e[1][0], e[1][1], e[2][0], e[2][1], e[3][0], e[3][1]};
+        const float hi[8] = {e[0][2], e[0][3], e[1][2], e[1][3], e[2][2], e[2][3], e[3][2], e[3][3]};
+        if (ra >= 0) oa[u].add_and_store(p.out, (row0 + ra) * p.N + n, lo);
+        if (rb >= 0) ob[u].add_and_store(p.out, (row0 + rb) * p.N + n, hi);
       }
     }
     __syncthreads();
@@ -373,15 +444,14 @@ size_t adapter_few_workspace_bytes(int64_t M, int r) {
 }
 
 cudaError_t adapter_few(const Adapter& p, cudaStream_t stream) {
-  static std::atomic<uint64_t> done[3] = {};
-  const auto up = p.out_f32 ? adapter_few_up_kernel<true> : adapter_few_up_kernel<false>;
-  cudaError_t e = allow_smem((const void*)adapter_few_down_kernel, sizeof(DownSmem), done[0]);
-  if (e == cudaSuccess) e = allow_smem((const void*)up, sizeof(UpSmem), done[1 + (p.out_f32 != 0)]);
-  if (e != cudaSuccess) return e;
   const int ctas = ctas_of(p.M, sm_count_current());
   const dim3 grid((unsigned)(chunks_of(p.M) * ctas));
-  e = launch_staged(adapter_few_down_kernel, grid, dim3(kThreads), sizeof(DownSmem), stream, 1, p, ctas);
+  const auto down = p.r <= 16 ? adapter_few_down_kernel<2, 4> : adapter_few_down_kernel<4, 3>;
+  cudaError_t e = launch_staged(down, grid, dim3(kThreads), sizeof(DownSmem), stream, 1, p, ctas);
   if (e != cudaSuccess) return e;
+  const auto up = p.r <= 16   ? (p.out_f32 ? adapter_few_up_kernel<true, 1, 2> : adapter_few_up_kernel<false, 1, 2>)
+                  : p.r <= 32 ? (p.out_f32 ? adapter_few_up_kernel<true, 2, 1> : adapter_few_up_kernel<false, 2, 2>)
+                              : (p.out_f32 ? adapter_few_up_kernel<true, 4, 1> : adapter_few_up_kernel<false, 4, 1>);
   return launch_staged(up, grid, dim3(kThreads), sizeof(UpSmem), stream, 1, p, ctas);
 }
 
