@@ -23,8 +23,9 @@ namespace {
 
 using moe_launch::Adapter;
 
-constexpr int kThreads = 256, kWarps = 8;
-constexpr int kChunk = kThreads;  // rows that a block looks at
+constexpr int kThreads = 256, kWarps = 8;       // of the first kernel
+constexpr int kUpThreads = 512, kUpWarps = 16;  // of the second
+constexpr int kChunk = 256;                     // rows that a block looks at
 constexpr int kTile = 16;     // rows of a tile
 constexpr int kRankMost = 128;
 constexpr unsigned kAll = 0xffffffffu;
@@ -36,7 +37,7 @@ struct Rows {
   int32_t start[kChunk];     // the last request that starts at a row, -1: none
   int32_t start_id[kChunk];  // its adapter and its end
   int32_t start_end[kChunk];
-  int32_t warp_sum[kWarps], lead_sum[kWarps];
+  int32_t warp_sum[kChunk / 32], lead_sum[kChunk / 32];
   int32_t tiles;
   int32_t rows[kTile];       // of the tile at hand
 };
@@ -78,9 +79,11 @@ MOE_DEV void mma32(float (&d)[4], const uint4& x0, const uint4& x1, const uint4&
   moe::mma_bf16(d, b, w.z, w.w, d);
 }
 
-// The chunk's rows: adapters, occurrences and tiles.  `start` is all -1 by then.
+// The chunk's rows: adapters, occurrences and tiles.  `start` is all -1 by then.  Every thread calls, the
+// first kChunk of them have a row.
 __device__ __forceinline__ void make_tables(const Adapter& p, Rows& sm, int64_t row0, int rows, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool mine = tid < kChunk;
   // Where a request starts in the chunk, or -1.  Of several at one place (offsets that decrease) the last
   // is taken, by every CTA and in both kernels.
   const auto place = [&](int i, int& end, int& id) {
@@ -94,9 +97,9 @@ __device__ __forceinline__ void make_tables(const Adapter& p, Rows& sm, int64_t 
     return lo > row0 ? (int)(lo - row0) : 0;
   };
   int first_end = 0, first_id = 0, end, id_of;
-  const int first_at = tid < p.R ? place(tid, first_end, first_id) : -1;  // most calls have no more requests than threads
+  const int first_at = mine && tid < p.R ? place(tid, first_end, first_id) : -1;  // most calls have no more requests
   if (first_at >= 0) atomicMax(&sm.start[first_at], tid);
-  for (int i = tid + kThreads; i < p.R; i += kThreads) {
+  for (int i = kChunk + tid; i < p.R; i += blockDim.x) {
     const int at = place(i, end, id_of);
     if (at >= 0) atomicMax(&sm.start[at], i);
   }
@@ -105,7 +108,7 @@ __device__ __forceinline__ void make_tables(const Adapter& p, Rows& sm, int64_t 
     sm.start_id[first_at] = first_id;
     sm.start_end[first_at] = first_end;
   }
-  for (int i = tid + kThreads; i < p.R; i += kThreads) {
+  for (int i = kChunk + tid; i < p.R; i += blockDim.x) {
     const int at = place(i, end, id_of);
     if (at >= 0 && sm.start[at] == i) {
       sm.start_id[at] = id_of;
@@ -113,23 +116,25 @@ __device__ __forceinline__ void make_tables(const Adapter& p, Rows& sm, int64_t 
     }
   }
   // the request of a row is the last that starts at or before it
-  int at = sm.start[tid] >= 0 ? tid : -1;
+  int at = mine && sm.start[tid] >= 0 ? tid : -1;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int up = __shfl_up_sync(kAll, at, o);
     if (lane >= o && up > at) at = up;
   }
-  if (lane == 31) sm.warp_sum[warp] = at;
+  if (mine && lane == 31) sm.warp_sum[warp] = at;
   __syncthreads();
-  {
+  int id = -2;
+  if (mine) {
     const int before = lane < warp ? sm.warp_sum[lane] : -1;
     at = max(at, __reduce_max_sync(kAll, before));
+    if (tid < rows && at >= 0 && tid < sm.start_end[at]) id = sm.start_id[at];
+    sm.id[tid] = id;
   }
-  const int id = tid < rows && at >= 0 && tid < sm.start_end[at] ? sm.start_id[at] : -2;
-  sm.id[tid] = id;
   __syncthreads();
-  int occ = 0;
-  {  // rows before this warp's, then its own
+  unsigned leads = 0;
+  if (mine) {  // rows before this warp's, then its own
+    int occ = 0;
     const int4* ids = reinterpret_cast<const int4*>(sm.id);
     if (id >= 0)
 #pragma unroll 4
@@ -138,15 +143,17 @@ __device__ __forceinline__ void make_tables(const Adapter& p, Rows& sm, int64_t 
         occ += (q.x == id) + (q.y == id) + (q.z == id) + (q.w == id);
       }
     occ += __popc(__match_any_sync(kAll, id) & ((1u << lane) - 1));
+    sm.occ[tid] = (int16_t)occ;
+    leads = __ballot_sync(kAll, id >= 0 && occ % kTile == 0);
+    if (lane == 0) sm.lead_sum[warp] = __popc(leads);
   }
-  sm.occ[tid] = (int16_t)occ;
-  const unsigned leads = __ballot_sync(kAll, id >= 0 && occ % kTile == 0);
-  if (lane == 0) sm.lead_sum[warp] = __popc(leads);
   __syncthreads();
-  const int n = lane < kWarps ? sm.lead_sum[lane] : 0;
-  const int before = __reduce_add_sync(kAll, lane < warp ? n : 0), all = __reduce_add_sync(kAll, n);
-  if (leads >> lane & 1) sm.leader[before + __popc(leads & ((1u << lane) - 1))] = (int16_t)tid;
-  if (tid == 0) sm.tiles = all;
+  if (mine) {
+    const int n = lane < kChunk / 32 ? sm.lead_sum[lane] : 0;
+    const int before = __reduce_add_sync(kAll, lane < warp ? n : 0), all = __reduce_add_sync(kAll, n);
+    if (leads >> lane & 1) sm.leader[before + __popc(leads & ((1u << lane) - 1))] = (int16_t)tid;
+    if (tid == 0) sm.tiles = all;
+  }
   __syncthreads();
 }
 
@@ -159,7 +166,7 @@ struct Out8 {
     for (int i = 0; i < (F32 ? 2 : 1); ++i)
       v[i] = on && base ? static_cast<const uint4*>(base)[at / 8 * (F32 ? 2 : 1) + i] : make_uint4(0, 0, 0, 0);
   }
-  MOE_DEV void add_and_store(void* out, int64_t at, const float (&f)[8]) {
+  MOE_DEV void add_and_store(void* out, int64_t at, const float (&f)[8]) const {
     uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[F32].x, v[F32].y, v[F32].z, v[F32].w};
     uint4* o = static_cast<uint4*>(out) + at / 8 * (F32 ? 2 : 1);
     if (F32) {
@@ -185,7 +192,7 @@ __device__ __forceinline__ int tile_rows(Rows& sm, int t) {
   __syncthreads();  // the rows of the tile before have been read
   if (tid < kTile) sm.rows[tid] = -1;
   __syncthreads();
-  if (sm.id[tid] == id && sm.occ[tid] >= from && sm.occ[tid] < from + kTile) sm.rows[sm.occ[tid] - from] = tid;
+  if (tid < kChunk && sm.id[tid] == id && sm.occ[tid] >= from && sm.occ[tid] < from + kTile) sm.rows[sm.occ[tid] - from] = tid;
   __syncthreads();
   return id;
 }
@@ -273,43 +280,47 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_down_kernel(Adapter p
   }
 }
 
-// A warp takes U blocks of 32 features at once, S steps of 16 ranks each.
-template <bool F32, int S, int U>
-__global__ void __launch_bounds__(kThreads, 2) adapter_few_up_kernel(Adapter p, int ctas) {
+// A warp takes a block of 32 features at a time, its weights S steps of 16 ranks at a time; up to S steps
+// in all (WHOLE) the next block's loads are under way meanwhile.
+template <bool F32, int S, bool WHOLE>
+__global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p, int ctas) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   UpSmem& sm = *reinterpret_cast<UpSmem*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int chunk = blockIdx.x / ctas, cta = blockIdx.x - chunk * ctas;
   const int64_t row0 = (int64_t)chunk * kChunk;
   const int rows = p.M - row0 < kChunk ? (int)(p.M - row0) : kChunk;
-  sm.t.start[tid] = -1;
+  if (tid < kChunk) sm.t.start[tid] = -1;
   __syncthreads();
   // The first kernel lets this one start when all before it is complete: what is not v can be read and
   // written already.
   make_tables(p, sm.t, row0, rows, false);
   const int nk = (p.K + 31) / 32, nb = (p.N + 31) / 32, pieces = Share(sm.t.tiles, nk, kPieces, 0, ctas).parts;
-  const int rp = (p.r + 31) / 32 * 32, vs = (kRankMost + 8) / 2, steps = (p.r + 15) / 16;
+  const int lr = p.r <= 32 ? 5 : p.r <= 64 ? 6 : 7, rp = 1 << lr, vs = (kRankMost + 8) / 2, steps = (p.r + 15) / 16;
   const Share share(sm.t.tiles, nb, nb, cta, ctas);
+  float scale = 1.f;
   int t, b0, b1;
-  // A tile's part of B and of its rows of base on their way into L2; every thread calls.
-  const auto ahead = [&](int turn) {
-    if (!share.get(turn, t, b0, b1)) return;
-    const int id = tile_rows(sm.t, t);
+  // A tile's rows; its scale, and its part of B and of its rows of base on their way into L2.
+  const auto begin = [&] {
+    const int id = tile_rows(sm.t, t), wide = min(b1 * 32, p.N) - b0 * 32;
+    if (p.scale) scale = p.scale[id];
     const char* B = reinterpret_cast<const char*>(static_cast<const uint16_t*>(p.b) + ((int64_t)id * p.N + b0 * 32) * p.r);
-    const int wide = min(b1 * 32, p.N) - b0 * 32;
-    for (int64_t i = (int64_t)tid * 128; i < (int64_t)wide * p.r * 2; i += kThreads * 128) prefetch_l2(B + i);
-    if (p.base == nullptr) return;
-    const int m = sm.t.rows[tid / (kThreads / kTile)], size = F32 ? 4 : 2;
-    const char* at = static_cast<const char*>(p.base) + ((row0 + m) * p.N + b0 * 32) * size;
-    for (int i = tid % (kThreads / kTile) * 128; m >= 0 && i < wide * size; i += kThreads / kTile * 128) prefetch_l2(at + i);
+    for (int64_t i = (int64_t)tid * 128; i < (int64_t)wide * p.r * 2; i += kUpThreads * 128) prefetch_l2(B + i);
+    constexpr int kSize = F32 ? 4 : 2;
+    const int m = sm.t.rows[warp];
+    if (p.base && m >= 0) {
+      const char* at = static_cast<const char*>(p.base) + ((row0 + m) * p.N + b0 * 32) * kSize;
+      for (int i = lane * 128; i < wide * kSize; i += 32 * 128) prefetch_l2(at + i);
+    }
+    return id;
   };
-  ahead(0);
+  int id = share.get(0, t, b0, b1) ? begin() : 0;
   // rows of requests without an adapter: base as it is
   if (p.base != p.out) {
     const int units = p.N / 8 * (F32 ? 2 : 1);
     for (int i = cta; i < rows; i += ctas)
       if (sm.t.id[i] == -1)
-        for (int c = tid; c < units; c += kThreads) {
+        for (int c = tid; c < units; c += kUpThreads) {
           const int64_t at = (row0 + i) * units + c;
           static_cast<uint4*>(p.out)[at] = p.base ? static_cast<const uint4*>(p.base)[at] : make_uint4(0, 0, 0, 0);
         }
@@ -317,18 +328,11 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_up_kernel(Adapter p, 
   moe::wait_for_stream();
   moe::let_next_start();
   for (int turn = 0; share.get(turn, t, b0, b1); ++turn) {
-    const int id = tile_rows(sm.t, t);
-    const uint16_t* B = static_cast<const uint16_t*>(p.b) + (int64_t)id * p.N * p.r;
-    int t1, e0, e1;
-    if (share.get(turn + 1, t1, e0, e1)) {  // the next tile's B on its way into L2 meanwhile
-      const char* next = reinterpret_cast<const char*>(static_cast<const uint16_t*>(p.b) + (int64_t)sm.t.id[sm.t.leader[t1]] * p.N * p.r);
-      for (int64_t i = (int64_t)tid * 128; i < (int64_t)p.N * p.r * 2; i += kThreads * 128) prefetch_l2(next + i);
-    }
-    const float scale = p.scale ? p.scale[id] : 1.f;
+    if (turn > 0) id = begin();
     // four ranks to each lane, or to 2 or 4 lanes with every second or fourth piece where threads are left
-    const int items = kTile * rp / 4, by = items >= kThreads ? 1 : kThreads / items, mine = tid % by;
-    for (int i = tid / by; i < items; i += kThreads / by) {
-      const int j = 4 * i / rp, m = sm.t.rows[j], k = 4 * i % rp;
+    const int by = 128 >> lr, mine = tid & (by - 1);  // as many lanes as fill the block
+    for (int i = tid / by; i < kTile * rp / 4; i += kUpThreads / by) {
+      const int j = 4 * i >> lr, m = sm.t.rows[j], k = 4 * i & (rp - 1);
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       if (m >= 0 && k < p.r) {
         const float* v = p.v + (row0 + m) * p.r + k;
@@ -368,35 +372,40 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_up_kernel(Adapter p, 
       }
     }
     __syncthreads();
-    const int ra = sm.t.rows[g], rb = sm.t.rows[g + 8];
     // v B^T, 32 features at a time: feature 8 (c / 2) + 2 j + c % 2 is column c of product j, so that a
     // lane ends with eight neighbouring ones of its rows
-    for (int b = b0 + warp; b < b1; b += U * kWarps) {
-      float d[U][4][4];
-      Out8<F32> oa[U], ob[U];  // base, on its way with the weights
+    const int ra = sm.t.rows[g], rb = sm.t.rows[g + 8];
+    const uint16_t* B = static_cast<const uint16_t*>(p.b) + ((int64_t)id * p.N + 8 * (g >> 1) + (g & 1)) * p.r + q * 4;
+    const int64_t at_a = (row0 + ra) * p.N + 8 * q, at_b = (row0 + rb) * p.N + 8 * q;
+    uint2 w[S][4];
+    Out8<F32> oa, ob;  // base
+    const auto load_w = [&](int b, int s0) {  // eight features are all within N, or none
+      const bool on = b < b1 && b * 32 + 8 * (g >> 1) < p.N;
+      const uint16_t* at = B + (int64_t)b * 32 * p.r + s0 * 16;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int n = (b + u * kWarps) * 32 + 8 * q;
-        const bool on = b + u * kWarps < b1 && n < p.N;
-        oa[u].load(p.base, (row0 + ra) * p.N + n, on && ra >= 0);
-        ob[u].load(p.base, (row0 + rb) * p.N + n, on && rb >= 0);
+      for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
+          w[s][j] = on && (s0 + s) * 16 + q * 4 < p.r ? moe::ldg_nc_u64(at + 2 * j * p.r + s * 16) : make_uint2(0, 0);
+    };
+    const auto load_o = [&](int b) {
+      const bool on = b < b1 && b * 32 + 8 * q < p.N;
+      oa.load(p.base, at_a + b * 32, on && ra >= 0);
+      ob.load(p.base, at_b + b * 32, on && rb >= 0);
+    };
+    if (WHOLE) {
+      load_w(b0 + warp, 0);
+      load_o(b0 + warp);
+    }
+    for (int b = b0 + warp; b < b1; b += kUpWarps) {
+      float d[4][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[u][j][i] = 0.f;
-      }
-      for (int s0 = 0; s0 < steps; s0 += S) {
-        uint2 w[U][S][4];
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int s = 0; s < S; ++s) {
-            const int f0 = (b + u * kWarps) * 32 + 8 * (g >> 1) + (g & 1), k = (s0 + s) * 16 + q * 4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[u][s][j] = b + u * kWarps < b1 && f0 + 2 * j < p.N && k < p.r ? moe::ldg_nc_u64(B + (int64_t)(f0 + 2 * j) * p.r + k)
-                                                                              : make_uint2(0, 0);
-          }
+        for (int i = 0; i < 4; ++i) d[j][i] = 0.f;
+      if (!WHOLE) load_o(b);
+      for (int s0 = 0; s0 < (WHOLE ? S : steps); s0 += S) {
+        if (!WHOLE) load_w(b, s0);
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           if (s0 + s >= steps) break;
@@ -407,24 +416,22 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_up_kernel(Adapter p, 
             const uint2 vc = *reinterpret_cast<const uint2*>(&sm.vb[h][(g + 8) * vs + at]);
             const uint32_t a[4] = {va.x, vc.x, va.y, vc.y};
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) moe::mma_bf16(d[u][j], a, w[u][s][j].x, w[u][s][j].y, d[u][j]);
+            for (int j = 0; j < 4; ++j) moe::mma_bf16(d[j], a, w[s][j].x, w[s][j].y, d[j]);
           }
         }
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int n = (b + u * kWarps) * 32 + 8 * q;
-        if (b + u * kWarps >= b1 || n >= p.N) continue;
-        const auto& e = d[u];
-        const float lo[8] = {e[0][0], e[0][1], e[1][0], e[1][1], e[2][0], e[2][1], e[3][0], e[3][1]};
-        const float hi[8] = {e[0][2], e[0][3], e[1][2], e[1][3], e[2][2], e[2][3], e[3][2], e[3][3]};
-        if (ra >= 0) oa[u].add_and_store(p.out, (row0 + ra) * p.N + n, lo);
-        if (rb >= 0) ob[u].add_and_store(p.out, (row0 + rb) * p.N + n, hi);
+      const Out8<F32> ea = oa, eb = ob;
+      if (WHOLE) {
+        load_w(b + kUpWarps, 0);
+        load_o(b + kUpWarps);
+      }
+      if (b * 32 + 8 * q < p.N) {
+        const float lo[8] = {d[0][0], d[0][1], d[1][0], d[1][1], d[2][0], d[2][1], d[3][0], d[3][1]};
+        const float hi[8] = {d[0][2], d[0][3], d[1][2], d[1][3], d[2][2], d[2][3], d[3][2], d[3][3]};
+        if (ra >= 0) ea.add_and_store(p.out, at_a + b * 32, lo);
+        if (rb >= 0) eb.add_and_store(p.out, at_b + b * 32, hi);
       }
     }
-    __syncthreads();
   }
 }
 
@@ -449,10 +456,10 @@ cudaError_t adapter_few(const Adapter& p, cudaStream_t stream) {
   const auto down = p.r <= 16 ? adapter_few_down_kernel<2, 4> : adapter_few_down_kernel<4, 3>;
   cudaError_t e = launch_staged(down, grid, dim3(kThreads), sizeof(DownSmem), stream, 1, p, ctas);
   if (e != cudaSuccess) return e;
-  const auto up = p.r <= 16   ? (p.out_f32 ? adapter_few_up_kernel<true, 1, 2> : adapter_few_up_kernel<false, 1, 2>)
-                  : p.r <= 32 ? (p.out_f32 ? adapter_few_up_kernel<true, 2, 1> : adapter_few_up_kernel<false, 2, 2>)
-                              : (p.out_f32 ? adapter_few_up_kernel<true, 4, 1> : adapter_few_up_kernel<false, 4, 1>);
-  return launch_staged(up, grid, dim3(kThreads), sizeof(UpSmem), stream, 1, p, ctas);
+  const auto up = p.r <= 16   ? (p.out_f32 ? adapter_few_up_kernel<true, 1, true> : adapter_few_up_kernel<false, 1, true>)
+                  : p.r <= 32 ? (p.out_f32 ? adapter_few_up_kernel<true, 2, true> : adapter_few_up_kernel<false, 2, true>)
+                              : (p.out_f32 ? adapter_few_up_kernel<true, 2, false> : adapter_few_up_kernel<false, 2, false>);
+  return launch_staged(up, grid, dim3(kUpThreads), sizeof(UpSmem), stream, 1, p, ctas);
 }
 
 }  // namespace moe_launch
