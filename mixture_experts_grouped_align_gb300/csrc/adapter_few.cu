@@ -26,7 +26,9 @@ using moe_launch::Adapter;
 constexpr int kThreads = 256, kWarps = 8;       // of the first kernel
 constexpr int kUpThreads = 512, kUpWarps = 16;  // of the second
 constexpr int kChunk = 256;                     // rows that a block looks at
+constexpr int kSlotBits = 9, kSlots = 1 << kSlotBits;  // twice the rows: a free place is near
 constexpr int kTile = 16;     // rows of a tile
+constexpr int kFewest = 4;    // rows of a tile that the second kernel takes without the tensor cores
 constexpr int kRankMost = 128;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -34,6 +36,8 @@ struct Rows {
   alignas(16) int32_t id[kChunk];  // a row's adapter, -1: none, -2: of no request
   int16_t occ[kChunk];       // rows of its adapter before it
   int16_t leader[kChunk];    // first rows of the tiles
+  int32_t slot_id[kSlots];   // adapters of the chunk's rows, hashed; -1: free
+  uint32_t slot_rows[kSlots][kChunk / 32];  // an adapter's rows
   int32_t start[kChunk];     // the last request that starts at a row, -1: none
   int32_t start_id[kChunk];  // its adapter and its end
   int32_t start_end[kChunk];
@@ -79,8 +83,15 @@ MOE_DEV void mma32(float (&d)[4], const uint4& x0, const uint4& x1, const uint4&
   moe::mma_bf16(d, b, w.z, w.w, d);
 }
 
-// The chunk's rows: adapters, occurrences and tiles.  `start` is all -1 by then.  Every thread calls, the
-// first kChunk of them have a row.
+// What make_tables wants to find.
+__device__ __forceinline__ void clear_tables(Rows& sm) {
+  for (int i = threadIdx.x; i < kSlots; i += blockDim.x) sm.slot_id[i] = -1;
+  for (int i = threadIdx.x; i < kSlots * kChunk / 32; i += blockDim.x) (&sm.slot_rows[0][0])[i] = 0;
+  if (threadIdx.x < kChunk) sm.start[threadIdx.x] = -1;
+}
+
+// The chunk's rows: adapters, occurrences and tiles, after clear_tables and a barrier.  Every thread calls,
+// the first kChunk of them have a row.
 __device__ __forceinline__ void make_tables(const Adapter& p, Rows& sm, int64_t row0, int rows, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool mine = tid < kChunk;
@@ -131,18 +142,23 @@ __device__ __forceinline__ void make_tables(const Adapter& p, Rows& sm, int64_t 
     if (tid < rows && at >= 0 && tid < sm.start_end[at]) id = sm.start_id[at];
     sm.id[tid] = id;
   }
+  // an adapter's rows as bits, in a place of its own in a table: its occurrence is the bits before a row's
+  int place_of = 0;
+  if (id >= 0) {
+    place_of = (int)(((uint32_t)id * 2654435769u) >> (32 - kSlotBits));
+    for (int old; (old = atomicCAS(&sm.slot_id[place_of], -1, id)) != -1 && old != id;) place_of = (place_of + 1) & (kSlots - 1);
+    atomicOr(&sm.slot_rows[place_of][warp], 1u << lane);
+  }
   __syncthreads();
   unsigned leads = 0;
-  if (mine) {  // rows before this warp's, then its own
+  if (mine) {
     int occ = 0;
-    const int4* ids = reinterpret_cast<const int4*>(sm.id);
     if (id >= 0)
-#pragma unroll 4
-      for (int j = 0; j < warp * 8; ++j) {
-        const int4 q = ids[j];
-        occ += (q.x == id) + (q.y == id) + (q.z == id) + (q.w == id);
+#pragma unroll
+      for (int w = 0; w < kChunk / 32; ++w) {
+        const uint32_t bits = sm.slot_rows[place_of][w];
+        occ += __popc(w < warp ? bits : w == warp ? bits & ((1u << lane) - 1) : 0u);
       }
-    occ += __popc(__match_any_sync(kAll, id) & ((1u << lane) - 1));
     sm.occ[tid] = (int16_t)occ;
     leads = __ballot_sync(kAll, id >= 0 && occ % kTile == 0);
     if (lane == 0) sm.lead_sum[warp] = __popc(leads);
@@ -208,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_down_kernel(Adapter p
   const int chunk = blockIdx.x / ctas, cta = blockIdx.x - chunk * ctas;
   const int64_t row0 = (int64_t)chunk * kChunk;
   const int rows = p.M - row0 < kChunk ? (int)(p.M - row0) : kChunk;
-  sm.t.start[tid] = -1;
+  clear_tables(sm.t);
   __syncthreads();
   moe::wait_for_stream();
   moe::let_next_start();
@@ -280,6 +296,125 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_down_kernel(Adapter p
   }
 }
 
+// The sum of a row's pieces of v, four ranks, in the order of the pieces.
+MOE_DEV float4 pieces_of(const Adapter& p, int64_t row, int k, int from, int step, int pieces) {
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* v = p.v + row * p.r + k;
+  for (int c0 = from; c0 < pieces; c0 += 8 * step) {
+    float4 u[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      u[c] = c0 + c * step < pieces ? *reinterpret_cast<const float4*>(v + (int64_t)(c0 + c * step) * p.M * p.r)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      s.x += u[c].x;
+      s.y += u[c].y;
+      s.z += u[c].z;
+      s.w += u[c].w;
+    }
+  }
+  return s;
+}
+
+// The tile's v times the scale as two bf16 numbers: four ranks to a lane, or to 2 or 4 lanes with every
+// second or fourth piece, as many as fill the block.  lr: log2 of the ranks, rounded up.
+__device__ __forceinline__ void sum_pieces(const Adapter& p, UpSmem& sm, int64_t row0, int pieces, int lr, float scale) {
+  constexpr int vs = (kRankMost + 8) / 2;
+  const int by = 128 >> lr, mine = threadIdx.x & (by - 1), i = threadIdx.x >> (7 - lr);
+  const int j = 4 * i >> lr, m = sm.t.rows[j], k = 4 * i & ((1 << lr) - 1);
+  float4 s = m >= 0 && k < p.r ? pieces_of(p, row0 + m, k, mine, by, pieces) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int o = 1; o < by; o <<= 1) {
+    s.x += __shfl_xor_sync(kAll, s.x, o);
+    s.y += __shfl_xor_sync(kAll, s.y, o);
+    s.z += __shfl_xor_sync(kAll, s.z, o);
+    s.w += __shfl_xor_sync(kAll, s.w, o);
+  }
+  if (mine == 0) {
+    const float f[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
+    uint32_t w[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(f[2 * h], f[2 * h + 1]);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(f[2 * h] - __low2float(hi), f[2 * h + 1] - __high2float(hi));
+      w[0][h] = *reinterpret_cast<const uint32_t*>(&hi);
+      w[1][h] = *reinterpret_cast<const uint32_t*>(&lo);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<uint2*>(&sm.vb[h][j * vs + k / 2]) = make_uint2(w[h][0], w[h][1]);
+  }
+}
+
+// A tile of up to kFewest rows, without the tensor cores: a lane has a feature, whose weights it reads
+// whole, and multiplies them with v in fp32.  Most of a tile of sixteen rows would be empty, and what an
+// MMA wants around it is five times the instructions (64 tokens over 100 adapters: 0.9 us for 32 features
+// of each warp).
+template <bool F32>
+__device__ __forceinline__ void few_rows(const Adapter& p, UpSmem& sm, int id, int64_t row0, int n0, int n1, int pieces, int lr,
+                                         float scale) {
+  const int tid = threadIdx.x;
+  float* v = reinterpret_cast<float*>(sm.vb);  // [row][rank] in fp32
+  {
+    const int i = tid >> 2, j = 4 * i >> lr, k = 4 * i & ((1 << lr) - 1);  // four lanes a sum
+    const int m = j < kFewest ? sm.t.rows[j] : -1;
+    float4 s = m >= 0 && k < p.r ? pieces_of(p, row0 + m, k, tid & 3, 4, pieces) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      s.x += __shfl_xor_sync(kAll, s.x, o);
+      s.y += __shfl_xor_sync(kAll, s.y, o);
+      s.z += __shfl_xor_sync(kAll, s.z, o);
+      s.w += __shfl_xor_sync(kAll, s.w, o);
+    }
+    if ((tid & 3) == 0 && j < kFewest)
+      reinterpret_cast<float4*>(v)[i] = make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
+  }
+  __syncthreads();
+  int rows = 0;
+  int64_t at[kFewest];
+#pragma unroll
+  for (int j = 0; j < kFewest; ++j) {
+    rows += sm.t.rows[j] >= 0;
+    at[j] = (row0 + sm.t.rows[j]) * p.N;
+  }
+  const uint16_t* B = static_cast<const uint16_t*>(p.b) + (int64_t)id * p.N * p.r;
+  for (int n = n0 + tid; n < n1; n += kUpThreads) {
+    float base[kFewest], d[kFewest];
+#pragma unroll
+    for (int j = 0; j < kFewest; ++j) {
+      d[j] = 0.f;
+      base[j] = 0.f;
+      if (j < rows && p.base)
+        base[j] = F32 ? static_cast<const float*>(p.base)[at[j] + n]
+                      : moe::bf16_bits_to_f32(static_cast<const uint16_t*>(p.base)[at[j] + n]);
+    }
+    const uint4* w = reinterpret_cast<const uint4*>(B + (int64_t)n * p.r);
+    for (int k = 0; k < p.r; k += 16) {
+      const bool two = k + 8 < p.r;
+      const uint4 a = moe::ldg_nc_u128(w + k / 8), b = two ? moe::ldg_nc_u128(w + k / 8 + 1) : make_uint4(0, 0, 0, 0);
+      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < kFewest; ++j) {
+        if (j >= rows) break;
+        const float* f = v + (j << lr) + k;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {  // what v has past the rank is 0
+          const float4 e = *reinterpret_cast<const float4*>(f + 2 * i);
+          d[j] = __fmaf_rn(e.x, __uint_as_float(u[i] << 16), d[j]);
+          d[j] = __fmaf_rn(e.y, __uint_as_float(u[i] & 0xffff0000u), d[j]);
+          d[j] = __fmaf_rn(e.z, __uint_as_float(u[i + 1] << 16), d[j]);
+          d[j] = __fmaf_rn(e.w, __uint_as_float(u[i + 1] & 0xffff0000u), d[j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kFewest; ++j)
+      if (j < rows) {
+        if (F32) static_cast<float*>(p.out)[at[j] + n] = base[j] + d[j];
+        else static_cast<uint16_t*>(p.out)[at[j] + n] = moe::f32_to_bf16_bits(base[j] + d[j]);
+      }
+  }
+}
+
 // A warp takes a block of 32 features at a time, its weights S steps of 16 ranks at a time; up to S steps
 // in all (WHOLE) the next block's loads are under way meanwhile.
 template <bool F32, int S, bool WHOLE>
@@ -290,13 +425,13 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
   const int chunk = blockIdx.x / ctas, cta = blockIdx.x - chunk * ctas;
   const int64_t row0 = (int64_t)chunk * kChunk;
   const int rows = p.M - row0 < kChunk ? (int)(p.M - row0) : kChunk;
-  if (tid < kChunk) sm.t.start[tid] = -1;
+  clear_tables(sm.t);
   __syncthreads();
   // The first kernel lets this one start when all before it is complete: what is not v can be read and
   // written already.
   make_tables(p, sm.t, row0, rows, false);
   const int nk = (p.K + 31) / 32, nb = (p.N + 31) / 32, pieces = Share(sm.t.tiles, nk, kPieces, 0, ctas).parts;
-  const int lr = p.r <= 32 ? 5 : p.r <= 64 ? 6 : 7, rp = 1 << lr, vs = (kRankMost + 8) / 2, steps = (p.r + 15) / 16;
+  const int lr = p.r <= 32 ? 5 : p.r <= 64 ? 6 : 7, vs = (kRankMost + 8) / 2, steps = (p.r + 15) / 16;
   const Share share(sm.t.tiles, nb, nb, cta, ctas);
   float scale = 1.f;
   int t, b0, b1;
@@ -329,48 +464,11 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
   moe::let_next_start();
   for (int turn = 0; share.get(turn, t, b0, b1); ++turn) {
     if (turn > 0) id = begin();
-    // four ranks to each lane, or to 2 or 4 lanes with every second or fourth piece where threads are left
-    const int by = 128 >> lr, mine = tid & (by - 1);  // as many lanes as fill the block
-    for (int i = tid / by; i < kTile * rp / 4; i += kUpThreads / by) {
-      const int j = 4 * i >> lr, m = sm.t.rows[j], k = 4 * i & (rp - 1);
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (m >= 0 && k < p.r) {
-        const float* v = p.v + (row0 + m) * p.r + k;
-        for (int c0 = mine; c0 < pieces; c0 += 8 * by) {
-          float4 u[8];
-#pragma unroll
-          for (int c = 0; c < 8; ++c)
-            u[c] = c0 + c * by < pieces ? *reinterpret_cast<const float4*>(v + (int64_t)(c0 + c * by) * p.M * p.r)
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            s.x += u[c].x;
-            s.y += u[c].y;
-            s.z += u[c].z;
-            s.w += u[c].w;
-          }
-        }
-      }
-      for (int o = 1; o < by; o <<= 1) {
-        s.x += __shfl_xor_sync(kAll, s.x, o);
-        s.y += __shfl_xor_sync(kAll, s.y, o);
-        s.z += __shfl_xor_sync(kAll, s.z, o);
-        s.w += __shfl_xor_sync(kAll, s.w, o);
-      }
-      if (mine == 0) {
-        const float f[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
-        uint32_t w[2][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const __nv_bfloat162 hi = __floats2bfloat162_rn(f[2 * h], f[2 * h + 1]);
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(f[2 * h] - __low2float(hi), f[2 * h + 1] - __high2float(hi));
-          w[0][h] = *reinterpret_cast<const uint32_t*>(&hi);
-          w[1][h] = *reinterpret_cast<const uint32_t*>(&lo);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint2*>(&sm.vb[h][j * vs + k / 2]) = make_uint2(w[h][0], w[h][1]);
-      }
+    if (sm.t.rows[kFewest] < 0) {
+      few_rows<F32>(p, sm, id, row0, b0 * 32, min(b1 * 32, p.N), pieces, lr, scale);
+      continue;
     }
+    sum_pieces(p, sm, row0, pieces, lr, scale);
     __syncthreads();
     // v B^T, 32 features at a time: feature 8 (c / 2) + 2 j + c % 2 is column c of product j, so that a
     // lane ends with eight neighbouring ones of its rows
