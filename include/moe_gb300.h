@@ -594,6 +594,10 @@ void moe_debug_stall_tensor_kernels(int64_t stall_ns);
  * launched.  Tests and measurements use it to say which kernel they ran. */
 moe_status moe_dense_gemm_plan(int64_t M, int32_t N, int32_t K, int32_t activation, int32_t out_f32, int32_t* plan);
 
+/* Which kernels moe_adapter_gemm runs a call of this size on, in *plan: 0 those for few rows a request, 1
+ * those for long requests.  The same limits as moe_adapter_gemm's, and M, R >= 1.  Nothing is launched. */
+moe_status moe_adapter_gemm_plan(int64_t M, int32_t N, int32_t K, int32_t r, int32_t L, int32_t R, int32_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

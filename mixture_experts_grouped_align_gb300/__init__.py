@@ -24,7 +24,7 @@ __all__ = [
     "moe_router_loss", "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward",
     "moe_dense_gemm", "moe_dense_gemm_plan", "moe_dense_bias_grad", "moe_pair_sum", "moe_residual_norm",
     "moe_residual_norm_backward", "moe_residual_norm_workspace_size", "moe_adapter_gemm",
-    "moe_adapter_gemm_workspace_size", "W_LAYOUT", "SCALES", "EXPORTED_SYMBOLS",
+    "moe_adapter_gemm_workspace_size", "moe_adapter_gemm_plan", "W_LAYOUT", "SCALES", "EXPORTED_SYMBOLS",
 ]
 
 MOE_OK = 0
@@ -45,6 +45,7 @@ EXPORTED_SYMBOLS = [
     "moe_router_loss_workspace_size", "moe_act_checkpoint", "moe_act_backward", "moe_dense_gemm",
     "moe_dense_bias_grad", "moe_pair_sum", "moe_dense_gemm_plan", "moe_residual_norm", "moe_residual_norm_backward",
     "moe_residual_norm_workspace_size", "moe_adapter_gemm", "moe_adapter_gemm_workspace_size",
+    "moe_adapter_gemm_plan",
 ]
 
 
@@ -132,6 +133,7 @@ def load(path: str | None = None):
         "moe_residual_norm_backward": (I32, [P, P, P, P, P, I64, I32, F32, P, I32, P, P, P, P]),
         "moe_residual_norm_workspace_size": (SZ, [I32]),
         "moe_adapter_gemm_workspace_size": (SZ, [I64, I32, I32]),
+        "moe_adapter_gemm_plan": (I32, [I64, I32, I32, I32, I32, I32, P]),
         "moe_adapter_gemm": (I32, [P, P, P, P, P, P, P, I64, I32, I32, I32, I32, I32, P, I32, P]),
     }
     for name, (res, args) in sig.items():
@@ -413,6 +415,13 @@ def moe_residual_norm_backward(d_out, d_stream, stream, token_mask, weight, T, K
 
 def moe_adapter_gemm_workspace_size(M, R, r) -> int:
     return load().moe_adapter_gemm_workspace_size(M, R, r)
+
+
+def moe_adapter_gemm_plan(M, N, K, r, L, R) -> str:
+    """Which kernels moe_adapter_gemm runs a call of this size on: "few" (rows a request) or "long" (requests)."""
+    plan = ctypes.c_int32()
+    _check(load().moe_adapter_gemm_plan(M, N, K, r, L, R, ctypes.byref(plan)))
+    return "long" if plan.value else "few"
 
 
 def moe_adapter_gemm(x, a, b, scale, row_offsets, adapter, base, M, N, K, r, L, R, out, ctx=None, out_f32=None):

@@ -22,8 +22,9 @@ namespace {
 
 using moe_launch::Adapter;
 
-constexpr int kRows = 128, kRequestsMost = 1024, kPiecesMost = 8;
+constexpr int kRows = 128, kRequestsMost = 1024;
 constexpr int kBox = kRows * 128;  // bytes of a box of 128 rows x 128 bytes
+constexpr int kPart = 32;          // rows of the boxes that a shorter tile takes instead
 
 // Of the requests: tiles before one [R + 1], and of those with an adapter [R + 1], first row, the row
 // behind the last, adapter (-1: none).
@@ -128,20 +129,37 @@ struct Run {
   }
 };
 
-// The first kernel's CTAs: few tiles are not cut into more pieces than are worth adding up, and each CTA
-// has a block at least.
-__device__ __forceinline__ int down_ctas(int tiles, int blocks, int ctas) { return min(ctas, min(kPiecesMost, blocks) * tiles); }
+// The first kernel's CTAs: each has a block at least, and few tiles are cut into few pieces, the fewer the
+// wider v is, since every CTA of the second kernel that has features of a tile reads all of its pieces.
+__device__ __forceinline__ int down_ctas(int tiles, int blocks, int ctas, int r) {
+  const int most = r <= 32 ? 8 : r <= 64 ? 4 : 2;
+  return min(ctas, min(most, blocks) * tiles);
+}
 // The CTA whose run has block x.
 __device__ __forceinline__ int owner(int64_t x, int64_t total, int ctas) { return (int)(((x + 1) * ctas - 1) / total); }
 // A piece's place in the workspace is its tile's number plus its CTA's: no two pieces share one, as from
 // piece to piece one of the two at least goes up.
+
+// A tile's rows of 128 bytes at x: one box, or boxes of 32 rows for a tile of fewer than 128.
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* whole, const CUtensorMap* part, int x, const Tile& tl,
+                                              uint64_t* bar) {
+  if (tl.rows == kRows) {
+    tma::load_2d(dst, whole, x, (int32_t)tl.row0, bar);
+  } else {
+    for (int r = 0; r < tl.rows; r += kPart) tma::load_2d(dst + r * 128, part, x, (int32_t)tl.row0 + r, bar);
+  }
+}
+__device__ __forceinline__ uint32_t rows_bytes(const Tile& tl) {
+  return tl.rows == kRows ? kBox : (uint32_t)((tl.rows + kPart - 1) / kPart * kPart * 128);
+}
 
 // ------------------------------------------------------------------------------------------ down
 
 constexpr int kDownThreads = 256, kDownStages = 10;
 
 __global__ void __launch_bounds__(kDownThreads, 1)
-    adapter_down_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_a, Adapter p, int stages) {
+    adapter_down_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x32,
+                        const __grid_constant__ CUtensorMap tm_a, Adapter p, int stages) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[kDownStages], empty[kDownStages], tfull[2], tempty[2], drain;
@@ -178,7 +196,7 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   tc::tc_fence_after();
   const uint32_t taddr = __shfl_sync(0xffffffffu, taddr_s, 0);
   const Tables t = tables_of(tab, p.R);
-  const int nk = (p.K + 63) / 64, tiles = t.first[p.R], ctas = down_ctas(tiles, nk, gridDim.x);
+  const int nk = (p.K + 63) / 64, tiles = t.first[p.R], ctas = down_ctas(tiles, nk, gridDim.x, p.r);
   Run run((int64_t)tiles * nk, nk, blockIdx.x, ctas);
   int tile, k0, k1;
 
@@ -198,8 +216,8 @@ __global__ void __launch_bounds__(kDownThreads, 1)
         }
         if (leader) {
           const uint32_t at = smem_s + s * slot;
-          tma::mbar_arrive_expect_tx(&full[s], (uint32_t)slot);
-          tma::load_2d(at, &tm_x, k * 128, (int32_t)tl.row0, &full[s]);
+          tma::mbar_arrive_expect_tx(&full[s], rows_bytes(tl) + (uint32_t)(rp * 128));
+          load_rows(at, &tm_x, &tm_x32, k * 128, tl, &full[s]);
           tma::load_2d(at + kBox, &tm_a, k * 128, tl.id * p.r, &full[s]);
         }
         __syncwarp();
@@ -312,15 +330,19 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ void sts8(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // Warps: 0 loads base, 1 issues the MMAs, 2 makes the tables, 3 loads B, 4..7 build v's operands,
-// 8..15 drain (two of a lane quarter take turns of 128 bytes of columns).
+// 8..15 drain (the two of a lane quarter take turns at boxes).
 template <bool F32>
 __global__ void __launch_bounds__(kUpThreads, 1)
-    adapter_up_kernel(const __grid_constant__ CUtensorMap tm_base, const __grid_constant__ CUtensorMap tm_b, Adapter p, UpPlan pl,
+    adapter_up_kernel(const __grid_constant__ CUtensorMap tm_base, const __grid_constant__ CUtensorMap tm_base32,
+                      const __grid_constant__ CUtensorMap tm_b, Adapter p, UpPlan pl,
                       int down_grid) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -392,8 +414,8 @@ __global__ void __launch_bounds__(kUpThreads, 1)
           }
           if (leader) {
             if (p.base) {
-              tma::mbar_arrive_expect_tx(&bfull[s], kBox);
-              tma::load_2d(smem_s + pl.base + s * kBox, &tm_base, (b * kFeat + c * kCols) * (F32 ? 4 : 2), (int32_t)tl.row0, &bfull[s]);
+              tma::mbar_arrive_expect_tx(&bfull[s], rows_bytes(tl));
+              load_rows(smem_s + pl.base + s * kBox, &tm_base, &tm_base32, (b * kFeat + c * kCols) * (F32 ? 4 : 2), tl, &bfull[s]);
             } else {
               tc::mbar_arrive(&bfull[s]);
             }
@@ -487,9 +509,9 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     __syncwarp();
   } else if (warp >= 4 && warp < 8) {
     // v of a tile: the pieces' sum times the adapter's scale, as two bf16 numbers
-    const int row = tid - 128, nk = (p.K + 63) / 64, own = t.own[p.R], ctas = down_ctas(own, nk, down_grid);
+    const int row = tid - 128, nk = (p.K + 63) / 64, own = t.own[p.R], ctas = down_ctas(own, nk, down_grid, p.r);
     const int64_t total = (int64_t)own * nk;
-    const int ranks = (p.r + 15) / 16 * 16;
+    const int per = p.r / 4;
     int tile_it = 0;
     while (run.next(tile, b0, b1)) {
       const Tile tl = tile_of(t, tile);
@@ -501,35 +523,49 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       }
       const float scale = p.scale ? p.scale[tl.id] : 1.f;
       const int c0 = owner((int64_t)tl.own * nk, total, ctas), pieces = owner((int64_t)(tl.own + 1) * nk - 1, total, ctas) - c0 + 1;
-      const float* at = p.v + ((int64_t)(tl.own + c0) * kRows + row) * p.r;
-      const bool on = row < tl.rows;
-      for (int k = 0; k < ranks; k += 8) {
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (on && k < p.r)
-          for (int s = 0; s < pieces; ++s) {
-            const float4* q = reinterpret_cast<const float4*>(at + (int64_t)s * kRows * p.r + k);
-            const float4 x = q[0], y = q[1];
-            f[0] += x.x;
-            f[1] += x.y;
-            f[2] += x.z;
-            f[3] += x.w;
-            f[4] += y.x;
-            f[5] += y.y;
-            f[6] += y.z;
-            f[7] += y.w;
-          }
-        uint32_t hi[4], lo[4];
+      const float4* at = reinterpret_cast<const float4*>(p.v + (int64_t)(tl.own + c0) * kRows * p.r);
+      const uint32_t mem = smem_s + pl.a + buf * 2 * pl.blocks * kBox;
+      const int quads = tl.rows * per, piece = kRows * per;  // four ranks each
+      for (int i0 = tid - 128; i0 < quads; i0 += 4 * kRows) {
+        float4 s[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = f[2 * i] * scale, b = f[2 * i + 1] * scale;
-          const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-          const __nv_bfloat162 l = __floats2bfloat162_rn(a - __low2float(h), b - __high2float(h));
-          hi[i] = *reinterpret_cast<const uint32_t*>(&h);
-          lo[i] = *reinterpret_cast<const uint32_t*>(&l);
+        for (int u = 0; u < 4; ++u) s[u] = i0 + u * kRows < quads ? at[i0 + u * kRows] : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 1; c < pieces; ++c) {
+          float4 e[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            e[u] = i0 + u * kRows < quads ? at[(int64_t)c * piece + i0 + u * kRows] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            s[u].x += e[u].x;
+            s[u].y += e[u].y;
+            s[u].z += e[u].z;
+            s[u].w += e[u].w;
+          }
         }
-        const uint32_t base = smem_s + pl.a + (buf * 2 * pl.blocks + k / 64) * kBox, off = tc::sw128_offset(row, (k & 63) / 8);
-        sts16(base + off, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-        sts16(base + pl.blocks * kBox + off, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = i0 + u * kRows;
+          if (i >= quads) break;
+          const int m = i / per, k = (i - m * per) * 4;
+          const float f[4] = {s[u].x * scale, s[u].y * scale, s[u].z * scale, s[u].w * scale};
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(f[2 * h], f[2 * h + 1]);
+            const __nv_bfloat162 l = __floats2bfloat162_rn(f[2 * h] - __low2float(a), f[2 * h + 1] - __high2float(a));
+            hi[h] = *reinterpret_cast<const uint32_t*>(&a);
+            lo[h] = *reinterpret_cast<const uint32_t*>(&l);
+          }
+          const uint32_t to = mem + (k >> 6) * kBox + tc::sw128_offset(m, (k & 63) >> 3) + (k & 4) * 2;
+          sts8(to, hi[0], hi[1]);
+          sts8(to + pl.blocks * kBox, lo[0], lo[1]);
+        }
+      }
+      if (p.r & 8) {  // the MMA's last ranks, past the adapters'
+        const uint32_t to = mem + (p.r >> 6) * kBox + tc::sw128_offset(row, (p.r & 63) >> 3);
+        sts16(to, make_uint4(0, 0, 0, 0));
+        sts16(to + pl.blocks * kBox, make_uint4(0, 0, 0, 0));
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
@@ -544,7 +580,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     bool ok = true;
     while (ok && run.next(tile, b0, b1)) {
       const Tile tl = tile_of(t, tile);
-      const bool has = tl.id >= 0;
+      const bool has = tl.id >= 0, live = quarter * 32 < tl.rows;
       for (int b = b0; b < b1 && ok; ++b) {
         const int acc = acc_it % kAccs;
         if (abort_flag || (has && !tc::mbar_wait(&tfull[acc], (acc_it / kAccs) & 1, wb))) {
@@ -566,55 +602,55 @@ __global__ void __launch_bounds__(kUpThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t mem = smem_s + pl.base + slot * kBox + quarter * 32 * 128;  // this warp's rows
-          const uint32_t from = taddr + acc * kFeat + ((uint32_t)(quarter * 32) << 16) + c * kCols;
-          if (has || !p.base) {
+          if (live) {
+            const uint32_t mem = smem_s + pl.base + slot * kBox + quarter * 32 * 128;  // this warp's rows
+            if (has || !p.base) {
+              const uint32_t from = taddr + acc * kFeat + ((uint32_t)(quarter * 32) << 16) + c * kCols;
 #pragma unroll
-            for (int h = 0; h < (F32 ? 1 : 2); ++h) {
-              uint32_t v[32];
+              for (int h = 0; h < (F32 ? 1 : 2); ++h) {
+                uint32_t v[32];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0;
-              if (has) {
-                tc::tmem_ld32(from + h * 32, v);
-                tc::tmem_ld_wait();
-              }
-#pragma unroll
-              for (int q = 0; q < (F32 ? 8 : 4); ++q) {
-                const uint32_t at = mem + chunk_at(lane, h * 4 + q);
-                uint4 e = p.base ? lds16(at) : make_uint4(0, 0, 0, 0);
-                if (F32) {
-                  e.x = __float_as_uint(__uint_as_float(e.x) + __uint_as_float(v[4 * q]));
-                  e.y = __float_as_uint(__uint_as_float(e.y) + __uint_as_float(v[4 * q + 1]));
-                  e.z = __float_as_uint(__uint_as_float(e.z) + __uint_as_float(v[4 * q + 2]));
-                  e.w = __float_as_uint(__uint_as_float(e.w) + __uint_as_float(v[4 * q + 3]));
-                } else {
-                  uint32_t w[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const int j = (8 * q + 2 * i) & 31;
-                    const __nv_bfloat162 o = __floats2bfloat162_rn(__uint_as_float(w[i] << 16) + __uint_as_float(v[j]),
-                                                                   __uint_as_float(w[i] & 0xffff0000u) + __uint_as_float(v[j + 1]));
-                    w[i] = *reinterpret_cast<const uint32_t*>(&o);
-                  }
-                  e = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < 32; ++i) v[i] = 0;
+                if (has) {
+                  tc::tmem_ld32(from + h * 32, v);
+                  tc::tmem_ld_wait();
                 }
-                sts16(at, e);
+#pragma unroll
+                for (int q = 0; q < (F32 ? 8 : 4); ++q) {
+                  const uint32_t at = mem + chunk_at(lane, h * 4 + q);
+                  uint4 e = p.base ? lds16(at) : make_uint4(0, 0, 0, 0);
+                  if (F32) {
+                    e.x = __float_as_uint(__uint_as_float(e.x) + __uint_as_float(v[4 * q]));
+                    e.y = __float_as_uint(__uint_as_float(e.y) + __uint_as_float(v[4 * q + 1]));
+                    e.z = __float_as_uint(__uint_as_float(e.z) + __uint_as_float(v[4 * q + 2]));
+                    e.w = __float_as_uint(__uint_as_float(e.w) + __uint_as_float(v[4 * q + 3]));
+                  } else {
+                    uint32_t w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      const int j = (8 * q + 2 * i) & 31;
+                      const __nv_bfloat162 o = __floats2bfloat162_rn(__uint_as_float(w[i] << 16) + __uint_as_float(v[j]),
+                                                                     __uint_as_float(w[i] & 0xffff0000u) + __uint_as_float(v[j + 1]));
+                      w[i] = *reinterpret_cast<const uint32_t*>(&o);
+                    }
+                    e = make_uint4(w[0], w[1], w[2], w[3]);
+                  }
+                  sts16(at, e);
+                }
               }
             }
-          }
-          __syncwarp();
-          // whole lines of the rows: eight lanes a row
-          const int col = b * kFeat + c * kCols + (lane & 7) * (kCols / 8);
+            __syncwarp();
+            // whole lines of the rows: eight lanes a row
+            const int col = b * kFeat + c * kCols + (lane & 7) * (kCols / 8);
+            uint8_t* out = static_cast<uint8_t*>(p.out) + ((tl.row0 + quarter * 32 + (lane >> 3)) * p.N + col) * (F32 ? 4 : 2);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 4 + (lane >> 3);
-            const uint4 e = lds16(mem + chunk_at(r, lane & 7));
-            if (quarter * 32 + r < tl.rows && col < p.N) {
-              const int64_t at = (tl.row0 + quarter * 32 + r) * p.N + col;
-              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at * (F32 ? 4 : 2)) = e;
+            for (int i = 0; i < 8; ++i) {
+              const int r = i * 4 + (lane >> 3);
+              const uint4 e = lds16(mem + chunk_at(r, lane & 7));
+              if (quarter * 32 + r < tl.rows && col < p.N) *reinterpret_cast<uint4*>(out + (int64_t)i * 4 * p.N * (F32 ? 4 : 2)) = e;
             }
+            tc::fence_proxy_async_smem();  // this box's writes, before the next one's load
           }
-          tc::fence_proxy_async_smem();  // this box's writes, before the next one's load
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bempty[slot]);
         }
@@ -643,9 +679,19 @@ constexpr int kCtasMost = 256;
 
 namespace moe_launch {
 
-bool adapter_many_takes(int64_t M, int R) {
-  // requests of 32 rows and more on average: below, most of a tile's rows are not the request's
-  return R <= kRequestsMost && M >= 256 && M >= 32 * (int64_t)R;
+bool adapter_many_can(int64_t M, int R) { return M >= 256 && R <= kRequestsMost; }
+
+// The estimated time against that of the kernels for few rows, in ns: a tile costs about the same whatever
+// it has of rows, since its adapter's B comes once for it, and a request ends with a tile that is not full
+// (0.8 of a tile a request in the fit); the others' time goes by the rows and the rank.  Times measured at
+// both (us, tiles of 128 rows first): 4096 -> 4096 of rank 16: 1000 rows of 16 requests 18.0 and 18.0, of
+// 100 48.6 and 21.8, 2000 of 60 35.3 and 32.7, 512 of 8 15.6 and 12.6; 2880 -> 2880 of rank 64: 1000 of 16
+// 21.3 and 29.0, 4096 of 128 53.8 and 102, of 400 125 and 107.
+bool adapter_many_takes(int64_t M, int R, int r, int N, int K) {
+  if (!adapter_many_can(M, R)) return false;
+  const double size = ((double)N + K) / 8192;
+  const double many = 12000 + 70.0 * r + 360 * (M / 128.0 + 0.8 * R) * size, few = 8500 + M * (6 + 0.375 * r) * size;
+  return many < few;
 }
 
 // The pieces of v: one for each tile and one for each CTA.
@@ -656,9 +702,11 @@ size_t adapter_many_workspace_bytes(int64_t M, int R, int r) {
 cudaError_t adapter_many(const Adapter& p, cudaStream_t stream) {
   const int rp = (p.r + 15) / 16 * 16, slot = kBox + rp * 128;
   const int tables = table_bytes(p.R);
-  CUtensorMap tm_x, tm_a, tm_base, tm_b;
+  CUtensorMap tm_x, tm_x32, tm_a, tm_base, tm_base32, tm_b;
   const int size = p.out_f32 ? 4 : 2;
   if (!tma::encode_2d_u8(&tm_x, p.x, (uint64_t)p.K * 2, p.M, (uint64_t)p.K * 2, 128, kRows, true) ||
+      !tma::encode_2d_u8(&tm_x32, p.x, (uint64_t)p.K * 2, p.M, (uint64_t)p.K * 2, 128, kPart, true) ||
+      !tma::encode_2d_u8(&tm_base32, p.base ? p.base : p.out, (uint64_t)p.N * size, p.M, (uint64_t)p.N * size, 128, kPart, true) ||
       !tma::encode_2d_u8(&tm_a, p.a, (uint64_t)p.K * 2, (uint64_t)p.L * p.r, (uint64_t)p.K * 2, 128, rp, true) ||
       !tma::encode_2d_u8(&tm_b, p.b, (uint64_t)p.r * 2, (uint64_t)p.L * p.N, (uint64_t)p.r * 2, 128, kFeat, true) ||
       !tma::encode_2d_u8(&tm_base, p.base ? p.base : p.out, (uint64_t)p.N * size, p.M, (uint64_t)p.N * size, 128, kRows, true))
@@ -669,7 +717,7 @@ cudaError_t adapter_many(const Adapter& p, cudaStream_t stream) {
   cudaError_t e = allow_smem((const void*)adapter_down_kernel, kSmemMost, done[0]);
   if (e == cudaSuccess)
     e = launch_staged(adapter_down_kernel, dim3((unsigned)sms), dim3(kDownThreads), stages * slot + tables + 1024, stream, 1, tm_x,
-                      tm_a, p, stages);
+                      tm_x32, tm_a, p, stages);
   if (e != cudaSuccess) return e;
   UpPlan pl{};
   pl.blocks = (p.r + 63) / 64;
@@ -684,7 +732,7 @@ cudaError_t adapter_many(const Adapter& p, cudaStream_t stream) {
   const auto kern = p.out_f32 ? adapter_up_kernel<true> : adapter_up_kernel<false>;
   e = allow_smem((const void*)kern, kSmemMost, done[1 + (p.out_f32 != 0)]);
   if (e != cudaSuccess) return e;
-  return launch_staged(kern, dim3((unsigned)sms), dim3(kUpThreads), pl.smem, stream, 1, tm_base, tm_b, p, pl, sms);
+  return launch_staged(kern, dim3((unsigned)sms), dim3(kUpThreads), pl.smem, stream, 1, tm_base, tm_base32, tm_b, p, pl, sms);
 }
 
 }  // namespace moe_launch

@@ -894,12 +894,10 @@ moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, c
 size_t moe_adapter_gemm_workspace_size(int64_t M, int32_t R, int32_t r) {
   if (M < 1 || M >= (int64_t)1 << 30 || R < 1 || r < 1 || r > 128) return 0;
   const size_t few = moe_launch::adapter_few_workspace_bytes(M, r);
-  return moe_launch::adapter_many_takes(M, R) ? std::max(few, moe_launch::adapter_many_workspace_bytes(M, R, r)) : few;
+  return moe_launch::adapter_many_can(M, R) ? std::max(few, moe_launch::adapter_many_workspace_bytes(M, R, r)) : few;
 }
 
-moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const float* scale, const int32_t* row_offsets,
-                            const int32_t* adapter, const void* base, int64_t M, int32_t N, int32_t K, int32_t r,
-                            int32_t L, int32_t R, void* out, int32_t out_f32, const moe_ctx* ctx) {
+static moe_status check_adapter(int64_t M, int32_t N, int32_t K, int32_t r, int32_t L, int32_t R) {
   MOE_REQUIRE(M >= 0 && N >= 1 && K >= 1 && r >= 1 && L >= 1 && R >= 0, MOE_ERR_INVALID_ARG,
               "need M >= 0, N >= 1, K >= 1, r >= 1, L >= 1, R >= 0");
   const int64_t most = (int64_t)1 << 30;
@@ -907,6 +905,28 @@ moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const f
   MOE_REQUIRE(N % 8 == 0 && K % 8 == 0, MOE_ERR_UNSUPPORTED, "N and K must be multiples of 8");
   MOE_REQUIRE(r % 8 == 0 && r <= 128, MOE_ERR_UNSUPPORTED, "r must be a multiple of 8, up to 128");
   MOE_REQUIRE(weights_fit(L, r, K) && weights_fit(L, N, r), MOE_ERR_UNSUPPORTED, "adapters too large for 64-bit indexing");
+  return MOE_OK;
+}
+
+// The kernels for long requests address the adapters' rows with 31 bits.
+static bool adapter_many(int64_t M, int32_t N, int32_t K, int32_t r, int32_t L, int32_t R) {
+  return moe_launch::adapter_many_takes(M, R, r, N, K) && (int64_t)L * N < ((int64_t)1 << 31) - 256 &&
+         (int64_t)L * r < ((int64_t)1 << 31) - 256;
+}
+
+moe_status moe_adapter_gemm_plan(int64_t M, int32_t N, int32_t K, int32_t r, int32_t L, int32_t R, int32_t* plan) {
+  const moe_status st = check_adapter(M, N, K, r, L, R);
+  if (st != MOE_OK) return st;
+  MOE_REQUIRE(plan && M >= 1 && R >= 1, MOE_ERR_INVALID_ARG, "need a plan to fill, M >= 1 and R >= 1");
+  *plan = adapter_many(M, N, K, r, L, R) ? 1 : 0;
+  return MOE_OK;
+}
+
+moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const float* scale, const int32_t* row_offsets,
+                            const int32_t* adapter, const void* base, int64_t M, int32_t N, int32_t K, int32_t r,
+                            int32_t L, int32_t R, void* out, int32_t out_f32, const moe_ctx* ctx) {
+  moe_status st = check_adapter(M, N, K, r, L, R);
+  if (st != MOE_OK) return st;
   if (M == 0 || R == 0) return MOE_OK;
   MOE_REQUIRE(x && a && b && row_offsets && adapter && out, MOE_ERR_INVALID_ARG, "null tensor pointer");
   MOE_REQUIRE(aligned16(x) && aligned16(a) && aligned16(b) && aligned16(scale) && aligned16(row_offsets) &&
@@ -916,17 +936,15 @@ moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const f
   p.x = x; p.a = a; p.b = b; p.scale = scale; p.row_offsets = row_offsets; p.adapter = adapter; p.base = base;
   p.M = M; p.N = N; p.K = K; p.r = r; p.L = L; p.R = R; p.out = out; p.out_f32 = out_f32 ? 1 : 0;
   p.status = status_of(ctx);
-  // the kernels for long requests address the adapters' rows with 31 bits
-  const bool many = moe_launch::adapter_many_takes(M, R) && (int64_t)L * N < ((int64_t)1 << 31) - 256 &&
-                    (int64_t)L * r < ((int64_t)1 << 31) - 256;
+  const bool many = adapter_many(M, N, K, r, L, R);
   const size_t need = moe_adapter_gemm_workspace_size(M, R, r);
   MOE_REQUIRE(ctx && ctx->workspace && ctx->workspace_bytes >= need && aligned16(ctx->workspace), MOE_ERR_CAPACITY,
               "workspace of %zu bytes needed", need);
   p.v = static_cast<float*>(ctx->workspace);
   moe_launch::apply_debug_stall(p);
   rec(ctx, 0, 2);
-  const moe_status st = cuda_status(many ? moe_launch::adapter_many(p, stream_of(ctx)) : moe_launch::adapter_few(p, stream_of(ctx)),
-                                    "moe_adapter_gemm");
+  st = cuda_status(many ? moe_launch::adapter_many(p, stream_of(ctx)) : moe_launch::adapter_few(p, stream_of(ctx)),
+                   "moe_adapter_gemm");
   rec(ctx, 1, 2);
   return st;
 }

@@ -351,8 +351,10 @@ struct Adapter {
 void apply_debug_stall(Adapter& a);
 size_t adapter_few_workspace_bytes(int64_t M, int r);
 cudaError_t adapter_few(const Adapter& p, cudaStream_t stream);
-// Whether M rows of R requests run on the kernels for long requests, and their scratch.
-bool adapter_many_takes(int64_t M, int R);
+// Whether the kernels for long requests can take M rows of R requests, whether they are faster, and their
+// scratch.
+bool adapter_many_can(int64_t M, int R);
+bool adapter_many_takes(int64_t M, int R, int r, int N, int K);
 size_t adapter_many_workspace_bytes(int64_t M, int R, int r);
 cudaError_t adapter_many(const Adapter& p, cudaStream_t stream);
 

@@ -40,6 +40,22 @@ def test_refusals(status, kw):
     refused(status, call, **kw)
 
 
+def test_plan_and_workspace_size():
+    plan = moe.moe_adapter_gemm_plan
+    assert plan(1, 2880, 2880, 16, 8, 1) == plan(64, 5760, 2880, 16, 100, 64) == "few"
+    assert plan(8192, 4096, 7168, 32, 8, 16) == plan(58879, 2880, 2880, 64, 6, 16) == "long"
+    assert plan(58879, 2880, 2880, 64, 1 << 20, 16) == "few"  # adapters of more than 2^31 rows
+    assert plan(100000, 2880, 2880, 16, 6, 1025) == "few"     # more requests than the other kernels' tables
+    for kw in (dict(M=0), dict(R=0), dict(N=12), dict(r=136)):
+        with pytest.raises(moe.MoeError):
+            plan(**{**dict(M=8, N=64, K=64, r=8, L=2, R=2), **kw})
+    size = moe.moe_adapter_gemm_workspace_size
+    assert size(0, 1, 16) == size(1, 0, 16) == size(1, 1, 0) == size(1, 1, 136) == size(1 << 30, 1, 16) == 0
+    assert 0 < size(1, 1, 8) < 1 << 20 and size(58879, 16, 64) < 64 << 20
+    refused(-3, call, ctx=moe.Ctx(stream=0, workspace=P, workspace_bytes=64))
+    refused(-3, call, ctx=moe.Ctx(stream=0))
+
+
 def test_empty_calls():
     assert call(x=None, out=None, M=0) == 0
     assert call(x=None, off=None, ad=None, out=None, R=0) == 0

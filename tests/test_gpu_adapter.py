@@ -56,11 +56,12 @@ class Case:
             self.base, _ = bf(rng.standard_normal((M, N)))
         self.out = self.base.clone() if base == "out" else torch.full((M, N), float("nan"), dtype=dt, device="cuda")
 
-    def run(self, moe, ctx=None):
+    def run(self, moe, ctx=None, plan=None):
+        if plan:
+            assert moe.moe_adapter_gemm_plan(self.M, self.N, self.K, self.r, self.L, self.R) == plan
         base = {"apart": self.base, "out": self.out, None: None}[self.base_is]
         status = torch.zeros(4, dtype=torch.int32, device="cuda")
-        ws = torch.full((moe.moe_adapter_gemm_workspace_size(self.M, self.R, self.r),), 0xFF, dtype=torch.uint8, device="cuda") \
-            if hasattr(moe, "moe_adapter_gemm_workspace_size") else None
+        ws = torch.full((moe.moe_adapter_gemm_workspace_size(self.M, self.R, self.r),), 0xFF, dtype=torch.uint8, device="cuda")
         moe.moe_adapter_gemm(self.x, self.a, self.b, self.scale, i32(self.offsets), i32(self.adapter), base, self.M, self.N,
                              self.K, self.r, self.L, self.R, self.out, ctx or moe.Ctx(workspace=ws, dev_status=status))
         torch.cuda.synchronize()
@@ -120,7 +121,10 @@ def test_many_requests(moe, M, L):
 
 
 PROMPTS = [lengths(600), lengths(1, 2, 130, 0, 128, 127, 129, 5), [3, 3, 300, 301, 900], lengths(*[17] * 60),
-           lengths(2000, 1, 1, 700), lengths(128, 128, 128), lengths(300, 300, 300, 300)]
+           lengths(300, 300, 300, 300)]
+# long enough, for their sizes, for the other kernels: tiles that end in each of their boxes' rows, requests
+# without rows, rows of no request
+LONG = [lengths(9000), lengths(1, 2, 8000, 0, 128, 127, 129, 5, 31, 32, 33, 1000), [3, 3, 300, 5001, 11900], lengths(*[600] * 16)]
 
 
 @pytest.mark.parametrize("offsets", PROMPTS)
@@ -128,43 +132,54 @@ PROMPTS = [lengths(600), lengths(1, 2, 130, 0, 128, 127, 129, 5), [3, 3, 300, 30
 def test_prompts(moe, offsets, r, N, K):
     R = len(offsets) - 1
     c = Case(offsets[-1] + 9, N, K, r, 3, offsets, [(i * 2) % 4 - 1 for i in range(R)], seed=1)
-    c.run(moe)
+    c.run(moe, plan="few")
+    c.check()
+
+
+@pytest.mark.parametrize("offsets", LONG)
+@pytest.mark.parametrize("r,N,K", [(16, 264, 200), (64, 520, 136), (128, 72, 328), (8, 1032, 72), (40, 136, 264), (72, 200, 136)])
+def test_long_prompts(moe, offsets, r, N, K):
+    R = len(offsets) - 1
+    c = Case(offsets[-1] + 9, N, K, r, 3, offsets, [(i * 2 + 1) % 4 - 1 for i in range(R)], seed=1)
+    c.run(moe, plan="long")
     c.check()
 
 
 @pytest.mark.parametrize("base", ["apart", "out", None])
 @pytest.mark.parametrize("f32", [False, True])
-@pytest.mark.parametrize("offsets", [[0, 1, 2, 3, 4, 9], [5, 400, 400, 900, 1111, 1130]])
-def test_base(moe, base, f32, offsets):
+@pytest.mark.parametrize("offsets,plan", [([0, 1, 2, 3, 4, 9], "few"), ([5, 400, 400, 900, 1111, 1130], "few"),
+                                          ([5, 4000, 4000, 4900, 6111, 9130], "long")])
+def test_base(moe, base, f32, offsets, plan):
     c = Case(offsets[-1] + 20, 328, 136, 24, 4, offsets, [1, 3, -1, 0, 1], f32=f32, base=base, scaled=f32, seed=2)
-    c.run(moe)
+    c.run(moe, plan=plan)
     c.check()
 
 
 def test_long_rows_of_fp32(moe):
-    for offsets in ([0, 1, 2, 3], [0, 700, 1400, 1500]):
+    for offsets, plan in (([0, 1, 2, 3], "few"), ([0, 700, 1400, 1500], "long")):
         c = Case(offsets[-1], 520, 7168, 32, 2, offsets, [0, 1, 0], f32=True, seed=3)
-        c.run(moe)
+        c.run(moe, plan=plan)
         c.check()
 
 
 def test_same_bits_twice(moe):
-    for offsets, ad in (decode(90, 7), ([0, 600, 1100, 1300], [1, 0, 1])):
+    for (offsets, ad), plan in ((decode(90, 7), "few"), (([0, 1200, 1800, 3000], [1, 0, 1]), "long")):
         outs = []
         for _ in range(2):
             c = Case(offsets[-1], 1032, 2056, 32, 7, offsets, ad, seed=4)
-            c.run(moe)
+            c.run(moe, plan=plan)
             outs.append(c.out)
         assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
 
 
 def test_adapters_that_are_not_finite_stay_with_their_requests(moe):
-    for offsets, ad in (([0, 1, 2, 3, 4], [0, 1, 0, 2]), ([0, 100, 230, 700, 1200], [0, 1, 0, 2]), ([0, 3, 4, 130, 140], [0, 1, 2, 1])):
+    for offsets, ad, plan in (([0, 1, 2, 3, 4], [0, 1, 0, 2], "few"), ([0, 3, 4, 130, 140], [0, 1, 2, 1], "few"),
+                              ([0, 100, 230, 20000, 20070], [0, 1, 0, 2], "long")):
         c = Case(offsets[-1], 136, 136, 16, 3, offsets, ad, seed=5)
         clean = Case(offsets[-1], 136, 136, 16, 3, offsets, ad, seed=5)
         c.a[1, 3, 5] = float("inf")
         c.b[1, 7] = float("nan")
-        c.run(moe)
+        c.run(moe, plan=plan)
         clean.run(moe)
         mine = torch.from_numpy(oracle.row_adapters(c.M, offsets, ad) == 1).cuda()
         assert torch.equal(c.out[~mine], clean.out[~mine])
@@ -172,11 +187,11 @@ def test_adapters_that_are_not_finite_stay_with_their_requests(moe):
 
 
 def test_rows_without_an_adapter_are_not_read(moe):
-    for offsets in ([2, 4, 6, 8], [10, 300, 700, 900]):
+    for offsets, plan in (([2, 4, 6, 8], "few"), ([10, 300, 700, 20000], "long")):
         c = Case(offsets[-1] + 10, 136, 136, 16, 3, offsets, [0, -1, 1], seed=6)
         ids = torch.from_numpy(oracle.row_adapters(c.M, offsets, c.adapter)).cuda()
         c.x[ids < 0] = float("nan")
-        c.run(moe)
+        c.run(moe, plan=plan)
         c.check()
 
 
@@ -187,12 +202,12 @@ def test_rows_without_an_adapter_are_not_read(moe):
     ([-4, 2, 4, 6], [0, 1, 1], -3, {0: -2, 1: -2, 2: 1, 3: 1, 4: 1, 5: 1}),
     ([0, 4, 2, 3], [0, 1, 1], -3, {0: 0, 1: 0}),  # the last one overlaps the first
 ])
-@pytest.mark.parametrize("M", [6, 900])
-def test_data_errors_are_reported(moe, offsets, adapter, status, rows, M):
+@pytest.mark.parametrize("M,plan", [(6, "few"), (900, "few"), (60000, "long")])
+def test_data_errors_are_reported(moe, offsets, adapter, status, rows, M, plan):
     if M > 6:
-        offsets = [o * 150 for o in offsets]
+        offsets = [o * (M // 6) for o in offsets]
     c = Case(M, 64, 64, 8, 2, offsets, adapter, seed=7)
-    assert c.run(moe) == status
+    assert c.run(moe, plan=plan) == status
     got = np64(c.out)
     for m, l in rows.items():
         m = m * (M // 6)
@@ -206,8 +221,9 @@ def test_data_errors_are_reported(moe, offsets, adapter, status, rows, M):
 def test_captured_calls_follow_the_tables(moe):
     """A graph's replays take the offsets and adapters that memory holds by then; another stream."""
     for M, plans in ((40, [([0, 1, 20, 40], [0, 1, 2]), ([0, 20, 20, 33], [2, 0, 0])]),
-                     (1000, [([0, 1, 200, 400], [0, 1, 2]), ([0, 520, 520, 933], [2, 0, 0])])):
+                     (9000, [([0, 1, 2000, 4000], [0, 1, 2]), ([0, 5200, 5200, 8933], [2, 0, 0])])):
         c = Case(M, 264, 264, 16, 3, *plans[0], seed=8)
+        assert moe.moe_adapter_gemm_plan(M, 264, 264, 16, 3, 3) == ("few" if M < 100 else "long")
         off, ad = i32(plans[0][0]), i32(plans[0][1])
         s = torch.cuda.Stream()
         ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
@@ -244,8 +260,9 @@ def test_offsets_past_32_bits(moe):
     a[L - 1], b[L - 1] = w, u
     out = torch.empty((600, N), dtype=torch.bfloat16, device="cuda")
     ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
-    for off, ad in (([0, 2, 5], [L - 1, 0]), ([0, 300, 600], [L - 1, 0])):
-        moe.moe_adapter_gemm(x, a, b, None, i32(off), i32(ad), None, 600, N, K, r, L, 2, out, moe.Ctx(workspace=ws))
+    assert moe.moe_adapter_gemm_plan(600, N, K, r, L, 2) == "long" and moe.moe_adapter_gemm_plan(5, N, K, r, L, 2) == "few"
+    for M, off, ad in ((5, [0, 2, 5], [L - 1, 0]), (600, [0, 300, 600], [L - 1, 0])):
+        moe.moe_adapter_gemm(x, a, b, None, i32(off), i32(ad), None, M, N, K, r, L, 2, out, moe.Ctx(workspace=ws))
         torch.cuda.synchronize()
         want = (xv[:off[1]] @ wv.T) @ uv.T
         assert np.all(np.abs(np64(out[:off[1]]) - want) <= bf16_half_ulp(want) * 1.01 + 2.0 ** -9)
