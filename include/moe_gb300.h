@@ -555,8 +555,8 @@ size_t moe_adapter_gemm_workspace_size(int64_t M, int32_t R, int32_t r);
  * out's type or NULL (zeros), it may be out itself: the output of moe_dense_gemm with the shared weight,
  * say; out [M, N] bf16 (out_f32 == 0) or fp32.  Rows of no request (before row_offsets[0], or from
  * row_offsets[R] on) are neither read nor written, and of requests without an adapter x is not read.
- * Products and sums in fp32 -- x . a^T enters the second product as a sum of two bf16 numbers, within
- * 2^-17 of itself -- rounded once; out must not overlap x, a or b.  A row depends on its own request's
+ * Products and sums in fp32 -- x . a^T enters the second product as a sum of bf16 numbers, within 2^-17
+ * of itself (2^-25 for fp32 outputs) -- rounded once; out must not overlap x, a or b.  A row depends on its own request's
  * adapter alone, also where another's is not finite.  Sums run in one fixed order for given sizes, offsets
  * and adapters: repeated calls give identical bits.
  * Data errors in ctx->dev_status: offsets that decrease or leave [0, M] (MOE_ERR_CAPACITY; such a request

@@ -12,7 +12,7 @@
 // not wait for v.
 // The operands of an MMA are read from global memory in their own layout, 16 or 8 bytes a lane: the
 // order of K within the products is the lanes', for both operands alike.  v is fp32 and enters the
-// second product as two bf16 numbers, 2^-17 of itself off.  Rows are never in one accumulator with
+// second product as a sum of bf16 numbers: two, 2^-17 of itself off, or three for fp32 outputs.  Rows are never in one accumulator with
 // another adapter's: a request's weights that are not finite stay its own.
 #include <algorithm>
 
@@ -52,7 +52,7 @@ struct DownSmem {
 };
 struct UpSmem {
   Rows t;
-  alignas(16) uint32_t vb[2][kTile * (kRankMost + 8) / 2];  // v's high and low parts: [row][rank], rows 8 ranks apart
+  alignas(16) uint32_t vb[3][kTile * (kRankMost + 8) / 2];  // v's bf16 parts: [row][rank], rows 8 ranks apart
 };
 
 // Equal shares of the tiles' blocks for the CTAs of a chunk.  Up to as many tiles as CTAs: `parts` CTAs a
@@ -317,8 +317,9 @@ MOE_DEV float4 pieces_of(const Adapter& p, int64_t row, int k, int from, int ste
   return s;
 }
 
-// The tile's v times the scale as two bf16 numbers: four ranks to a lane, or to 2 or 4 lanes with every
+// The tile's v times the scale as PARTS bf16 numbers: four ranks to a lane, or to 2 or 4 lanes with every
 // second or fourth piece, as many as fill the block.  lr: log2 of the ranks, rounded up.
+template <int PARTS>
 __device__ __forceinline__ void sum_pieces(const Adapter& p, UpSmem& sm, int64_t row0, int pieces, int lr, float scale) {
   constexpr int vs = (kRankMost + 8) / 2;
   const int by = 128 >> lr, mine = threadIdx.x & (by - 1), i = threadIdx.x >> (7 - lr);
@@ -331,17 +332,19 @@ __device__ __forceinline__ void sum_pieces(const Adapter& p, UpSmem& sm, int64_t
     s.w += __shfl_xor_sync(kAll, s.w, o);
   }
   if (mine == 0) {
-    const float f[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
-    uint32_t w[2][2];
+    float f[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const __nv_bfloat162 hi = __floats2bfloat162_rn(f[2 * h], f[2 * h + 1]);
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(f[2 * h] - __low2float(hi), f[2 * h + 1] - __high2float(hi));
-      w[0][h] = *reinterpret_cast<const uint32_t*>(&hi);
-      w[1][h] = *reinterpret_cast<const uint32_t*>(&lo);
+    for (int h = 0; h < PARTS; ++h) {
+      uint32_t w[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const __nv_bfloat162 e = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&e);
+        f[2 * i] -= __low2float(e);
+        f[2 * i + 1] -= __high2float(e);
+      }
+      *reinterpret_cast<uint2*>(&sm.vb[h][j * vs + k / 2]) = make_uint2(w[0], w[1]);
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) *reinterpret_cast<uint2*>(&sm.vb[h][j * vs + k / 2]) = make_uint2(w[h][0], w[h][1]);
   }
 }
 
@@ -421,6 +424,7 @@ template <bool F32, int S, bool WHOLE>
 __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p, int ctas) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   UpSmem& sm = *reinterpret_cast<UpSmem*>(smem_raw);
+  constexpr int kParts = F32 ? 3 : 2;  // bf16 numbers that carry a value of v
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int chunk = blockIdx.x / ctas, cta = blockIdx.x - chunk * ctas;
   const int64_t row0 = (int64_t)chunk * kChunk;
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
       few_rows<F32>(p, sm, id, row0, b0 * 32, min(b1 * 32, p.N), pieces, lr, scale);
       continue;
     }
-    sum_pieces(p, sm, row0, pieces, lr, scale);
+    sum_pieces<kParts>(p, sm, row0, pieces, lr, scale);
     __syncthreads();
     // v B^T, 32 features at a time: feature 8 (c / 2) + 2 j + c % 2 is column c of product j, so that a
     // lane ends with eight neighbouring ones of its rows
@@ -508,7 +512,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
         for (int s = 0; s < S; ++s) {
           if (s0 + s >= steps) break;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < kParts; ++h) {
             const int at = (s0 + s) * 8 + q * 2;
             const uint2 va = *reinterpret_cast<const uint2*>(&sm.vb[h][g * vs + at]);
             const uint2 vc = *reinterpret_cast<const uint2*>(&sm.vb[h][(g + 8) * vs + at]);

@@ -8,9 +8,12 @@
 // is known on the device only; every block adds up the requests' tiles, and each takes an equal run of
 // all tiles' blocks of K (first kernel) or of N (second), however the runs cut the tiles.
 //   down: stages of 64 of K, 128 rows of x and the adapter's r rows by TMA; M = 128, N = r, K = 16 MMAs
-//         into one of two accumulators; the sum of a tile's piece goes to the workspace in fp32.
-//   up:   the builder warps add the pieces of a tile's v, scale it and leave it as two bf16 operands,
-//         high and low part (2^-17 of v itself), the rows of an MMA against 128 features of B at a time;
+//         into one of two accumulators; the sum of a tile's piece goes to the workspace in fp32.  The
+//         accumulator loses up to a unit in the last place with every MMA, always towards zero, which a
+//         bf16 output hides: for fp32 outputs it takes kChunk stages at most, which are added there.
+//   up:   the builder warps add the pieces of a tile's v, scale it and leave it as two bf16 operands whose
+//         sum it is to 2^-17 of itself (three for fp32 outputs), the rows of MMAs against 128 features of B
+//         at a time;
 //         base comes in boxes of 128 bytes x 128 rows, six ahead, in which the epilogue warps add the
 //         accumulator and from which they store whole lines of the request's rows.
 // Every wait is bounded; one that runs out sets MOE_ERR_TIMEOUT and all roles leave their loops.
@@ -156,6 +159,7 @@ __device__ __forceinline__ uint32_t rows_bytes(const Tile& tl) {
 // ------------------------------------------------------------------------------------------ down
 
 constexpr int kDownThreads = 256, kDownStages = 10;
+constexpr int kChunk = 12;  // stages of an accumulator for fp32 outputs
 
 __global__ void __launch_bounds__(kDownThreads, 1)
     adapter_down_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_x32,
@@ -237,36 +241,38 @@ __global__ void __launch_bounds__(kDownThreads, 1)
     int s = 0, acc_it = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (; ok && run.next(tile, k0, k1); ++acc_it) {
-      const int acc = acc_it & 1;
-      if (!tc::mbar_wait(&tempty[acc], ((acc_it >> 1) & 1) ^ 1, wb)) ok = false;
-      tc::tc_fence_after();
-      for (int k = k0; k < k1 && ok; ++k) {
-        if (abort_flag || !tc::mbar_wait(&full[s], ph, wb)) {
-          ok = false;
-          break;
-        }
+    while (ok && run.next(tile, k0, k1))
+      for (int from = k0, until; ok && from < k1; from = until, ++acc_it) {
+        until = p.out_f32 ? min(k1, from + kChunk) : k1;
+        const int acc = acc_it & 1;
+        ok = tc::mbar_wait(&tempty[acc], ((acc_it >> 1) & 1) ^ 1, wb);
         tc::tc_fence_after();
-        if (leader) {
-          const uint64_t xd = tc::sdesc_sw128(smem_s + s * slot), ad = tc::sdesc_sw128(smem_s + s * slot + kBox);
+        for (int k = from; k < until && ok; ++k) {
+          if (abort_flag || !tc::mbar_wait(&full[s], ph, wb)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          if (leader) {
+            const uint64_t xd = tc::sdesc_sw128(smem_s + s * slot), ad = tc::sdesc_sw128(smem_s + s * slot + kBox);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tc::mma_f16_ss(taddr + acc * 128, xd + 2 * j, ad + 2 * j, idesc, k > k0 || j > 0);
-          tc::mma_commit(&empty[s]);
+            for (int j = 0; j < 4; ++j) tc::mma_f16_ss(taddr + acc * 128, xd + 2 * j, ad + 2 * j, idesc, k > from || j > 0);
+            tc::mma_commit(&empty[s]);
+          }
+          __syncwarp();
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) {
+          if (!abort_flag) moe::set_status(p.status, MOE_ERR_TIMEOUT);
+          abort_flag = 1;
+        } else if (leader) {
+          tc::mma_commit(&tfull[acc]);
         }
         __syncwarp();
-        if (++s == stages) {
-          s = 0;
-          ph ^= 1;
-        }
       }
-      if (!ok) {
-        if (!abort_flag) moe::set_status(p.status, MOE_ERR_TIMEOUT);
-        abort_flag = 1;
-      } else if (leader) {
-        tc::mma_commit(&tfull[acc]);
-      }
-      __syncwarp();
-    }
     if (leader) {
       tc::mma_commit(&drain);
       if (!tc::mbar_wait(&drain, 0, wb)) moe::set_status(p.status, MOE_ERR_TIMEOUT);
@@ -275,28 +281,42 @@ __global__ void __launch_bounds__(kDownThreads, 1)
   } else if (warp >= 4) {
     const int quarter = warp & 3, row = quarter * 32 + lane;
     int acc_it = 0;
-    for (; run.next(tile, k0, k1); ++acc_it) {
+    bool ok = true;
+    while (ok && run.next(tile, k0, k1)) {
       const Tile tl = tile_of(t, tile);
-      const int acc = acc_it & 1;
-      if (abort_flag || !tc::mbar_wait(&tfull[acc], (acc_it >> 1) & 1, wb)) {
-        if (!abort_flag) moe::set_status(p.status, MOE_ERR_TIMEOUT);
-        abort_flag = 1;
-        break;
-      }
-      tc::tc_fence_after();
       float* at = p.v + ((int64_t)(tile + blockIdx.x) * kRows + row) * p.r;
-      for (int c = 0; c < rp; c += 16) {
-        uint32_t v[16];
-        dense::tmem_ld16(taddr + acc * 128 + ((uint32_t)(quarter * 32) << 16) + c, v);
-        tc::tmem_ld_wait();
-        if (row < tl.rows)
+      for (int from = k0, until; from < k1; from = until, ++acc_it) {
+        until = p.out_f32 ? min(k1, from + kChunk) : k1;
+        const int acc = acc_it & 1;
+        if (abort_flag || !tc::mbar_wait(&tfull[acc], (acc_it >> 1) & 1, wb)) {
+          if (!abort_flag) moe::set_status(p.status, MOE_ERR_TIMEOUT);
+          abort_flag = 1;
+          ok = false;
+          break;
+        }
+        tc::tc_fence_after();
+        for (int c = 0; c < rp; c += 16) {
+          uint32_t v[16];
+          dense::tmem_ld16(taddr + acc * 128 + ((uint32_t)(quarter * 32) << 16) + c, v);
+          tc::tmem_ld_wait();
+          if (row < tl.rows)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (c + 4 * j < p.r) reinterpret_cast<uint4*>(at + c)[j] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            for (int j = 0; j < 4; ++j)
+              if (c + 4 * j < p.r) {
+                float4* to = reinterpret_cast<float4*>(at + c) + j;
+                float4 e = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]), __uint_as_float(v[4 * j + 2]),
+                                       __uint_as_float(v[4 * j + 3]));
+                if (from > k0) {  // this thread's own, of the accumulator before
+                  const float4 b = *to;
+                  e = make_float4(b.x + e.x, b.y + e.y, b.z + e.z, b.w + e.w);
+                }
+                *to = e;
+              }
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&tempty[acc]);
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&tempty[acc]);
     }
   }
   __syncwarp();
@@ -350,6 +370,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
   __shared__ uint64_t afull[2], aempty[2], tfull[kAccs], tempty[kAccs], drain;
   __shared__ uint32_t taddr_s;
   __shared__ volatile int abort_flag;
+  constexpr int kParts = F32 ? 3 : 2;  // bf16 numbers that carry a value of v
   constexpr int kCols = F32 ? 32 : 64, kTurns = kFeat / kCols;  // columns of a base box, boxes of an accumulator
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t smem_s = tc::smem_addr(smem);
@@ -479,9 +500,9 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         }
         tc::tc_fence_after();
         if (leader) {
-          for (int h = 0; h < 2; ++h)  // the high part, the low part
+          for (int h = 0; h < kParts; ++h)
             for (int k = 0; k < steps; ++k) {
-              const uint64_t ad = tc::sdesc_sw128(smem_s + pl.a + ((buf * 2 + h) * pl.blocks + k / 4) * kBox) + 2 * (k & 3);
+              const uint64_t ad = tc::sdesc_sw128(smem_s + pl.a + ((buf * kParts + h) * pl.blocks + k / 4) * kBox) + 2 * (k & 3);
               const uint64_t bd = tc::sdesc_sw128(smem_s + pl.b + (s * pl.blocks + k / 4) * kBox) + 2 * (k & 3);
               tc::mma_f16_ss(taddr + acc * kFeat, ad, bd, idesc, h > 0 || k > 0);
             }
@@ -508,7 +529,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 8) {
-    // v of a tile: the pieces' sum times the adapter's scale, as two bf16 numbers
+    // v of a tile: the pieces' sum times the adapter's scale, as bf16 numbers
     const int row = tid - 128, nk = (p.K + 63) / 64, own = t.own[p.R], ctas = down_ctas(own, nk, down_grid, p.r);
     const int64_t total = (int64_t)own * nk;
     const int per = p.r / 4;
@@ -524,7 +545,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       const float scale = p.scale ? p.scale[tl.id] : 1.f;
       const int c0 = owner((int64_t)tl.own * nk, total, ctas), pieces = owner((int64_t)(tl.own + 1) * nk - 1, total, ctas) - c0 + 1;
       const float4* at = reinterpret_cast<const float4*>(p.v + (int64_t)(tl.own + c0) * kRows * p.r);
-      const uint32_t mem = smem_s + pl.a + buf * 2 * pl.blocks * kBox;
+      const uint32_t mem = smem_s + pl.a + buf * kParts * pl.blocks * kBox;
       const int quads = tl.rows * per, piece = kRows * per;  // four ranks each
       for (int i0 = tid - 128; i0 < quads; i0 += 4 * kRows) {
         float4 s[4];
@@ -548,24 +569,26 @@ __global__ void __launch_bounds__(kUpThreads, 1)
           const int i = i0 + u * kRows;
           if (i >= quads) break;
           const int m = i / per, k = (i - m * per) * 4;
-          const float f[4] = {s[u].x * scale, s[u].y * scale, s[u].z * scale, s[u].w * scale};
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const __nv_bfloat162 a = __floats2bfloat162_rn(f[2 * h], f[2 * h + 1]);
-            const __nv_bfloat162 l = __floats2bfloat162_rn(f[2 * h] - __low2float(a), f[2 * h + 1] - __high2float(a));
-            hi[h] = *reinterpret_cast<const uint32_t*>(&a);
-            lo[h] = *reinterpret_cast<const uint32_t*>(&l);
-          }
+          float f[4] = {s[u].x * scale, s[u].y * scale, s[u].z * scale, s[u].w * scale};
           const uint32_t to = mem + (k >> 6) * kBox + tc::sw128_offset(m, (k & 63) >> 3) + (k & 4) * 2;
-          sts8(to, hi[0], hi[1]);
-          sts8(to + pl.blocks * kBox, lo[0], lo[1]);
+#pragma unroll
+          for (int h = 0; h < kParts; ++h) {
+            uint32_t w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+              w[e] = *reinterpret_cast<const uint32_t*>(&b);
+              f[2 * e] -= __low2float(b);
+              f[2 * e + 1] -= __high2float(b);
+            }
+            sts8(to + h * pl.blocks * kBox, w[0], w[1]);
+          }
         }
       }
       if (p.r & 8) {  // the MMA's last ranks, past the adapters'
         const uint32_t to = mem + (p.r >> 6) * kBox + tc::sw128_offset(row, (p.r & 63) >> 3);
-        sts16(to, make_uint4(0, 0, 0, 0));
-        sts16(to + pl.blocks * kBox, make_uint4(0, 0, 0, 0));
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) sts16(to + h * pl.blocks * kBox, make_uint4(0, 0, 0, 0));
       }
       tc::fence_proxy_async_smem();
       __syncwarp();
@@ -724,7 +747,7 @@ cudaError_t adapter_many(const Adapter& p, cudaStream_t stream) {
   pl.bufs = pl.blocks == 1 ? 2 : 1;
   pl.weight_slots = pl.blocks == 1 ? 3 : 2;
   pl.a = 0;
-  pl.b = pl.bufs * 2 * pl.blocks * kBox;
+  pl.b = pl.bufs * (p.out_f32 ? 3 : 2) * pl.blocks * kBox;
   pl.base = pl.b + pl.weight_slots * pl.blocks * kBox;
   pl.base_slots = std::min(kBaseSlots, (kSmemMost - 1024 - tables - pl.base) / kBox);
   pl.tab = pl.base + pl.base_slots * kBox;

@@ -195,23 +195,30 @@ MOE_DEV uint2 quant8(const float (&v)[8], uint32_t& scale) {
 // The smallest scale of a row: zero rows have it, and 1 / scale stays finite.
 constexpr float kRowScaleMin = 0x1p-120f;
 
-// The scale of a row whose largest magnitude is `most`, and what its values are multiplied by.  `most`
-// is taken as |s w| r: it may be two roundings off the largest |s r w|, which then saturates at 448.
-MOE_DEV float row_scale(float most, float& by) {
-  if (!(most <= 3.4028235e38f)) {  // an infinity, too, leaves NaN in its row
-    by = __uint_as_float(0x7fc00000u);
-    return by;
-  }
-  const bool small = most / 448.f < kRowScaleMin;
-  by = small ? 1.f / kRowScaleMin : 448.f / most;
-  return small ? kRowScaleMin : most / 448.f;
+// How a row becomes codes: of s `first` w `by`.
+struct RowCodes {
+  float scale, first, by;
+};
+// The scale of a row whose largest |s w| is `top`.  Its codes are those of s w 448 / top, which is
+// n 448 / max |n| without r's rounding, or of n 2^120 where the scale is the smallest.
+MOE_DEV RowCodes row_codes(float top, float r) {
+  const float most = top * r, nan = __uint_as_float(0x7fc00000u);
+  if (!(most <= 3.4028235e38f)) return RowCodes{nan, 1.f, nan};  // an infinity, too, leaves NaN in its row
+  if (most / 448.f < kRowScaleMin) return RowCodes{kRowScaleMin, r, 1.f / kRowScaleMin};
+  return RowCodes{most / 448.f, 1.f, 448.f / top};
 }
 
 // The outputs of eight values s of unit u (c: its unit in the row); every lane calls.
 template <int QUANT>
-MOE_DEV void finish(const ResidualNorm& p, const float (&s)[8], const uint4& w, float r, float by, int64_t u, int c, bool on) {
+MOE_DEV void finish(const ResidualNorm& p, const float (&s)[8], const uint4& w, float r, const RowCodes& rc, int64_t u, int c, bool on) {
   float f[8];
   unpack8(w, f);
+  if (QUANT == 2) {
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = s[i] * rc.first * f[i];
+    if (on) __stcs(reinterpret_cast<uint2*>(p.codes) + u, codes8(q, rc.by));
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = s[i] * r * f[i];  // zeros where a row does not count: its s are
   if (on && p.out) __stcs(static_cast<uint4*>(p.out) + u, pack8(f));
@@ -223,7 +230,6 @@ MOE_DEV void finish(const ResidualNorm& p, const float (&s)[8], const uint4& w, 
       if ((c & 3) == 0) static_cast<uint8_t*>(p.scales)[u >> 2] = (uint8_t)e;
     }
   }
-  if (QUANT == 2 && on) __stcs(reinterpret_cast<uint2*>(p.codes) + u, codes8(f, by));
 }
 
 // QUANT: 0 no codes, 1 a power of two per 32 values, 2 a scale per row.
@@ -275,15 +281,15 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_kernel(ResidualNorm p)
   }
   reduce_pair<M, QUANT == 2>(sum, top, red);
   const float r = inverse_rms(sum, 1.f / (float)p.K, p.eps);
-  float by = 0.f;
+  RowCodes rc{};
   if (QUANT == 2) {
-    const float scale = row_scale(top * r, by);
-    if (in && M::col() == 0) static_cast<float*>(p.scales)[row] = scale;
+    rc = row_codes(top, r);
+    if (in && M::col() == 0) static_cast<float*>(p.scales)[row] = rc.scale;
   }
 #pragma unroll
   for (int t = 0; t < V; ++t) {
     const int c = M::col() + t * M::step();
-    finish<QUANT>(p, s[t], w[t], r, by, u0 + c, c, in && c < units);
+    finish<QUANT>(p, s[t], w[t], r, rc, u0 + c, c, in && c < units);
   }
 }
 
@@ -573,15 +579,15 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_walk_kernel(ResidualNo
     }
     reduce_pair<M, QUANT == 2>(sum, top, red[turn]);  // two sets in turn: one barrier a row is enough
     const float r = inverse_rms(sum, inv_k, p.eps);
-    float by = 0.f;
+    RowCodes rc{};
     if (QUANT == 2) {
-      const float scale = row_scale(top * r, by);
-      if (in && M::col() == 0) static_cast<float*>(p.scales)[row] = scale;
+      rc = row_codes(top, r);
+      if (in && M::col() == 0) static_cast<float*>(p.scales)[row] = rc.scale;
     }
 #pragma unroll
     for (int t = 0; t < V; ++t) {
       const int c = M::col() + t * M::step();
-      finish<QUANT>(p, s[t], w[t], r, by, row * units + c, c, in && c < units);
+      finish<QUANT>(p, s[t], w[t], r, rc, row * units + c, c, in && c < units);
     }
   }
 }
