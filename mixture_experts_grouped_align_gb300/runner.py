@@ -10,13 +10,17 @@ loop never captures or sets up kernels on the hot path; ``step_bucketed`` pads a
 its bucket and replays that bucket's graph ("Bound Triton MoE JIT specializations via
 token-dim bucketing and warmup", TensorRT-LLM PR 15311, Description: bucketing bounds the
 set of specializations and a prewarm builds all of them up front).
+
+``ServeBlock`` is the layer in a residual stream: the norm before it in the operands' own format, the
+router, and a dense shared expert with the low-rank adapters of the requests in a batch.
 """
 from __future__ import annotations
 
 import torch
 
-from . import (Ctx, moe_align, moe_align_capacity, moe_bucket, moe_bucket_pad, moe_forward,
-               moe_forward_workspace_size)
+from . import (Ctx, MoeError, moe_act_checkpoint, moe_adapter_gemm, moe_adapter_gemm_workspace_size, moe_align,
+               moe_align_capacity, moe_bucket, moe_bucket_pad, moe_dense_gemm, moe_forward, moe_forward_workspace_size,
+               moe_residual_norm)
 
 BLOCK_M = 128
 
@@ -147,3 +151,88 @@ class DeviceLayer:
             g.replay()
         torch.cuda.current_stream().wait_stream(s)
         return self._y_graph[:T]
+
+
+class ServeBlock:
+    """A DeviceLayer behind its norm, in a residual stream, with its router and a shared expert:
+
+        s = residual + branch;  n = rmsnorm(s) * norm_w      (an MXFP8 layer reads n in MXFP8)
+        y = experts(n, router n) + swiglu(n ws1^T + bs1) ws2^T + bs2
+
+    norm_w [K], wr [E, K], ws1 [2Is, K], bs1 [2Is], ws2 [K, Is], bs2 [K]: bf16; ``shared`` = (ws1, bs1, ws2,
+    bs2) or None.  ``adapters``: a pair (for ws1 and for ws2; either may be None) of (a [L, r, in], b [L, out, r]
+    bf16, scale [L] fp32 or None): low-rank adapters, of which each request of a batch names one.  The stream is
+    bf16, or fp32 (``stream_f32``).  Up to ``max_requests`` requests a batch."""
+
+    def __init__(self, layer, norm_w, wr, shared=None, adapters=(None, None), eps=1e-5, stream_f32=False, max_requests=512):
+        bf, dev = torch.bfloat16, norm_w.device
+        self.layer, self.norm_w, self.wr, self.shared, self.adapters, self.eps = layer, norm_w, wr, shared, adapters, eps
+        T, K, E = layer.max_rows, layer.K, layer.E
+        if tuple(norm_w.shape) != (K,) or tuple(wr.shape) != (E, K):
+            raise MoeError(-1, f"need norm_w [{K}] and wr [{E}, {K}], got {tuple(norm_w.shape)} and {tuple(wr.shape)}")
+        if any(adapters) and shared is None:
+            raise MoeError(-1, "adapters need a shared expert")
+        new = lambda *s, dtype=bf: torch.empty(s, dtype=dtype, device=dev)  # noqa: E731
+        self.stream, self.normed = new(T, K, dtype=torch.float32 if stream_f32 else bf), new(T, K)
+        self.logits = new(T, E, dtype=torch.float32)
+        mx = layer.quant == "mxfp8"
+        self.codes = new(T, K, dtype=torch.uint8) if mx else None
+        self.scales = new(T, K // 32, dtype=torch.uint8) if mx else None
+        self.max_requests, ranks = max_requests, [0]
+        if shared is not None:
+            ws1, bs1, ws2, bs2 = shared
+            Is = self.Is = ws2.shape[1]
+            if tuple(ws1.shape) != (2 * Is, K) or ws2.shape[0] != K:
+                raise MoeError(-1, f"need ws1 [{2 * Is}, {K}] and ws2 [{K}, {Is}], got {tuple(ws1.shape)} and {tuple(ws2.shape)}")
+            for pair, (n_in, n_out) in zip(adapters, ((K, 2 * Is), (Is, K))):
+                if pair is None:
+                    continue
+                a, b = pair[:2]
+                if a.dim() != 3 or a.shape[2] != n_in or tuple(b.shape) != (a.shape[0], n_out, a.shape[1]):
+                    raise MoeError(-1, f"adapters: need a [L, r, {n_in}] and b [L, {n_out}, r], got {tuple(a.shape)} and {tuple(b.shape)}")
+                ranks.append(a.shape[1])
+            self.hs = new(T, Is)
+            if adapters[0] is not None:  # added before the activation, so the pre-activations are kept
+                self.gs = new(T, 2 * Is)
+                self.held = new(T, 2 * Is, dtype=torch.uint8), new(T, 2 * Is // 32, dtype=torch.uint8)
+        # the adapters' workspace is no smaller for more requests, and largest at whole 256s of rows, or at all
+        need = max([256] + [moe_adapter_gemm_workspace_size(t, min(t, max_requests), max(ranks))
+                            for t in {T, *range(256, T, 256)} if max(ranks)])
+        self.workspace = new(need, dtype=torch.uint8)
+        self.status = torch.zeros(4, dtype=torch.int32, device=dev)
+
+    def _adapt(self, which, x, T, n_out, n_in, row_offsets, adapter, out, ctx):
+        a, b, scale = (*self.adapters[which], None)[:3]
+        moe_adapter_gemm(x, a, b, scale, row_offsets, adapter, out, T, n_out, n_in, a.shape[1], a.shape[0], adapter.shape[0], out,
+                         ctx)
+
+    def step(self, branch, residual, T, y, row_offsets=None, adapter=None):
+        """branch [T, K] bf16 or None, residual [T, K] in the stream's type -> y [T, K] bf16 and the stream
+        [T, K] (the block's own, until its next step).  With adapters: row_offsets [R + 1] and adapter [R] int32 on
+        the device (-1: none), rows of no request having none."""
+        K, E, L = self.layer.K, self.layer.E, self.layer
+        if T > L.max_rows:
+            raise MoeError(-3, f"{T} rows, the layer was made for up to {L.max_rows}")
+        adapt = adapter is not None and adapter.shape[0] > 0
+        if adapt and adapter.shape[0] > self.max_requests:
+            raise MoeError(-3, f"{adapter.shape[0]} requests, the block was made for up to {self.max_requests}")
+        ctx = Ctx(workspace=self.workspace, dev_status=self.status)
+        moe_residual_norm(branch, residual, None, self.norm_w, T, K, self.eps, 0.0, None, 0, self.stream, self.normed, self.codes,
+                          self.scales, ctx)
+        if T == 0:
+            return y, self.stream[:0]
+        moe_dense_gemm(self.normed, self.wr, "nk", None, None, 1.0, T, E, K, "none", self.logits, ctx)
+        L.step(self.normed if self.codes is None else self.codes, self.logits, T, y, stream=torch.cuda.current_stream(),
+               x_scale=self.scales)
+        if self.shared is not None:
+            ws1, bs1, ws2, bs2 = self.shared
+            if adapt and self.adapters[0] is not None:
+                moe_dense_gemm(self.normed, ws1, "nk", bs1, None, 1.0, T, 2 * self.Is, K, "none", self.gs, ctx)
+                self._adapt(0, self.normed, T, 2 * self.Is, K, row_offsets, adapter, self.gs, ctx)
+                moe_act_checkpoint(self.gs, None, T, self.Is, "swiglu", self.hs, *self.held, ctx)
+            else:
+                moe_dense_gemm(self.normed, ws1, "nk", bs1, None, 1.0, T, self.Is, K, "swiglu", self.hs, ctx)
+            moe_dense_gemm(self.hs, ws2, "nk", bs2, y, 1.0, T, K, self.Is, "none", y, ctx)
+            if adapt and self.adapters[1] is not None:
+                self._adapt(1, self.hs, T, K, self.Is, row_offsets, adapter, y, ctx)
+        return y, self.stream[:T]

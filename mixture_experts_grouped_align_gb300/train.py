@@ -20,6 +20,9 @@ caller who wants more of the router's gradient has it there.
 a forward and its backward), and holds what lives from a forward to its backward: the routing, and
 the pre-activations as MXFP8 checkpoints (33/64 of their bf16 bytes).  Everything else is scratch,
 which layers can share.
+
+``TrainBlock`` puts the norm before a layer: the residual's addition of what the block before it left,
+with dropout, and the RMS norm, forward and back.
 """
 from __future__ import annotations
 
@@ -28,8 +31,9 @@ import math
 import torch
 
 from . import (Ctx, MoeError, moe_act_backward, moe_act_checkpoint, moe_align, moe_align_capacity, moe_dense_bias_grad,
-               moe_dense_gemm, moe_grouped_gemm, moe_pair_sum, moe_router_loss, moe_router_loss_workspace_size,
-               moe_wgrad, moe_wgrad_workspace_size)
+               moe_dense_gemm, moe_grouped_gemm, moe_pair_sum, moe_residual_norm, moe_residual_norm_backward,
+               moe_residual_norm_workspace_size, moe_router_loss, moe_router_loss_workspace_size, moe_wgrad,
+               moe_wgrad_workspace_size)
 
 BLOCK_M = 128
 
@@ -253,3 +257,93 @@ class TrainLayer:
         moe_wgrad(self.d_logits16, x, 0, T, 1, 1, self.Ep, K, *one, self.grad_wr, 0, c)
         moe_dense_gemm(self.dgs, self.ws1, "kn", None, dx, 1.0, T, K, 2 * Is, "none", dx, c)
         return dx
+
+
+class TrainBlock:
+    """A TrainLayer behind its norm, in a residual stream:
+
+        s = residual + dropout(branch)      branch: the layer's output of the block before this one
+        y = layer(rmsnorm(s) * norm_w)      the next block takes (y, s) as (branch, residual)
+
+    norm_w [K] bf16; ``dropout`` the probability, by the numbers of ``rng`` (int64 [2] on the device: seed
+    and step, which the program advances between steps, not between a forward and its backward) and
+    ``rng_stream``, which differs from block to block.  The stream is bf16, or fp32 (``stream_f32``).
+
+    Holds s, from which the backward pass has the norm again, and the norm's output, which the layer's
+    weight gradients read: 4 (or 6) bytes a value."""
+
+    def __init__(self, layer, norm_w, eps=1e-5, dropout=0.0, rng=None, rng_stream=0, stream_f32=False):
+        if not isinstance(layer, TrainLayer):
+            raise MoeError(-1, f"layer: need a TrainLayer, got {type(layer).__name__}")
+        self.layer, self.norm_w, self.eps, self.dropout, self.rng, self.rng_stream = layer, norm_w, eps, dropout, rng, rng_stream
+        dev = layer.wr.device
+        self._check_own()
+        self.stream = torch.empty((layer.max_rows, layer.K), dtype=torch.float32 if stream_f32 else torch.bfloat16, device=dev)
+        self.normed = torch.empty((layer.max_rows, layer.K), dtype=torch.bfloat16, device=dev)
+        self.grad_norm = torch.empty(layer.K, dtype=torch.float32, device=dev)
+        layer.scratch.reserve("workspace", moe_residual_norm_workspace_size(layer.K))
+        layer.scratch.reserve("d_normed", 2 * layer.max_rows * layer.K)
+        self.T = None
+
+    def _check_own(self):
+        dev = self.layer.wr.device
+        _check(self.norm_w, "norm_w", torch.bfloat16, dev, (self.layer.K,))
+        if self.dropout != 0.0:
+            _check(self.rng, "rng", torch.int64, dev, (2,))
+
+    def _rows(self, t, what, dtype, T):
+        _check(t, what, dtype, self.layer.wr.device, numel=T * self.layer.K)
+
+    def _ctx(self):
+        ws = self.layer.scratch.view("workspace", torch.uint8, moe_residual_norm_workspace_size(self.layer.K))
+        return Ctx(workspace=ws)
+
+    def forward(self, branch, residual, y, token_mask=None):
+        """branch [T, K] bf16 or None (the first block), residual [T, K] in the stream's type -> y [T, K]
+        bf16 and the stream [T, K] (the block's own, until its next forward).  Rows with a mask of 0 enter
+        the layer as zeros."""
+        K, bf = self.layer.K, torch.bfloat16
+        self._check_own()
+        if not isinstance(residual, torch.Tensor) or residual.dim() != 2:
+            raise MoeError(-1, "residual: need a torch tensor of 2 dimensions")
+        T = residual.shape[0]
+        if T > self.layer.max_rows:
+            raise MoeError(-3, f"residual: {T} rows, the layer was made for up to {self.layer.max_rows}")
+        _check(residual, "residual", self.stream.dtype, self.layer.wr.device, (T, K))
+        if branch is not None:
+            self._rows(branch, "branch", bf, T)
+            _apart(branch, self.normed, "branch and the block's rows")
+        if token_mask is not None:
+            _check(token_mask, "token_mask", torch.uint8, self.layer.wr.device, numel=T)
+        self._rows(y, "y", bf, T)
+        _apart(y, self.normed, "y and the block's rows")
+        stream, normed = self.stream[:T], self.normed[:T]
+        moe_residual_norm(branch, residual, token_mask, self.norm_w, T, K, self.eps, self.dropout if branch is not None else 0.0,
+                          self.rng, self.rng_stream, stream, normed, None, None, self._ctx())
+        self.layer.forward(normed, y)
+        self.T, self.mask, self.dropped = T, token_mask, branch is not None
+        return y, stream
+
+    def backward(self, dy, d_stream, d_residual, d_branch=None):
+        """dy [T, K] bf16: the gradient of y; d_stream [T, K] in the stream's type: that of the stream from
+        the blocks behind, or None -> d_residual [T, K] (it may be d_stream) and d_branch [T, K] bf16 (with
+        a branch; it may be dy), the layer's gradients in ``layer.grads`` and the norm's weight's in
+        ``grad_norm`` (fp32).  The token_mask of the forward holds here too."""
+        if self.T is None:
+            raise MoeError(-1, "backward needs a forward before it")
+        T, K, bf = self.T, self.layer.K, torch.bfloat16
+        self._check_own()
+        if d_stream is not None:
+            self._rows(d_stream, "d_stream", self.stream.dtype, T)
+        self._rows(d_residual, "d_residual", self.stream.dtype, T)
+        if d_branch is None and self.dropped:
+            raise MoeError(-1, "d_branch: the forward had a branch")
+        if d_branch is not None:
+            self._rows(d_branch, "d_branch", bf, T)
+            _apart(d_branch, d_residual, "d_branch and d_residual")
+        d_normed = self.layer.scratch.view("d_normed", bf, T, K) if T else torch.empty((0, K), dtype=bf, device=dy.device)
+        self.layer.backward(dy, d_normed, self.mask)
+        moe_residual_norm_backward(d_normed, d_stream, self.stream[:T], self.mask, self.norm_w, T, K, self.eps,
+                                   self.dropout if self.dropped else 0.0, self.rng, self.rng_stream, d_residual,
+                                   d_branch, self.grad_norm, self._ctx())
+        return d_residual, d_branch
