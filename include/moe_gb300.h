@@ -510,8 +510,8 @@ typedef struct {
  * of the two at least; token_mask [T] bytes or NULL; weight [K] bf16; stream [T, K] bf16
  * (stream_f32 == 0) or fp32, or NULL; out [T, K] bf16 or NULL; codes [T, K] and scales as the scale
  * mode says (MOE_SCALES_NONE: both NULL).  dropout may be NULL (none).
- *  - Rows that do not count are not read; their rows of stream, out and codes are zeros and their
- *    scales those of a row of zeros (bytes 0, or 2^-120).
+ *  - Rows that do not count may hold anything (they may be fetched, nothing of them is used); their rows
+ *    of stream, out and codes are zeros and their scales those of a row of zeros (bytes 0, or 2^-120).
  *  - A NaN or an infinity in s leaves NaN in its row: row scales NaN with codes 0x7F, MX NaN in the
  *    blocks that hold a NaN n.  Sums of squares above fp32's range (|s| near 10^18) give n = 0.
  *  - stream may be residual, and out may be x; other overlaps are not allowed.
@@ -531,9 +531,9 @@ size_t moe_residual_norm_workspace_size(int32_t K);
  * d_out [T, K] bf16: the gradient of out (and of the values that codes stand for); d_stream [T, K] in
  * the stream's type: what reaches the stream from behind, or NULL; d_residual [T, K] in the stream's
  * type, d_x [T, K] bf16 and d_weight [K] fp32 may each be NULL.  In fp32, rounded once; d_weight is
- * summed in a fixed order: repeated calls on a device give identical bits.  Rows that do not count are
- * not read, add nothing to d_weight, and their rows of d_residual and d_x are zeros.  d_residual may be
- * d_stream, and d_x may be d_out; other overlaps are not allowed.  Limits as above; d_weight needs
+ * summed in a fixed order: repeated calls on a device give identical bits.  Rows that do not count may
+ * hold anything, add nothing to d_weight, and their rows of d_residual and d_x are zeros.  d_residual may
+ * be d_stream, and d_x may be d_out; other overlaps are not allowed.  Limits as above; d_weight needs
  * moe_residual_norm_workspace_size(K) bytes of workspace (T = 0 gives zeros). */
 moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, const void* stream,
                                       const uint8_t* token_mask, const void* weight, int64_t T, int32_t K, float eps,
@@ -554,11 +554,11 @@ size_t moe_adapter_gemm_workspace_size(int64_t M, int32_t R, int32_t r);
  * scale [L] fp32 or NULL (1); row_offsets [R+1] and adapter [R] int32 in device memory; base [M, N] in
  * out's type or NULL (zeros), it may be out itself: the output of moe_dense_gemm with the shared weight,
  * say; out [M, N] bf16 (out_f32 == 0) or fp32.  Rows of no request (before row_offsets[0], or from
- * row_offsets[R] on) are neither read nor written, and of requests without an adapter x is not read.
+ * row_offsets[R] on) are not written, and may hold anything, as x may in requests without an adapter.
  * Products and sums in fp32 -- x . a^T enters the second product as a sum of bf16 numbers, within 2^-17
- * of itself (2^-25 for fp32 outputs) -- rounded once; out must not overlap x, a or b.  A row depends on its own request's
- * adapter alone, also where another's is not finite.  Sums run in one fixed order for given sizes, offsets
- * and adapters: repeated calls give identical bits.
+ * of itself (2^-25 for fp32 outputs) -- rounded once; out must not overlap x, a or b.  A row depends on
+ * its own request's adapter alone, also where another's is not finite.  Sums run in one fixed order for
+ * given sizes, offsets and adapters: repeated calls give identical bits.
  * Data errors in ctx->dev_status: offsets that decrease or leave [0, M] (MOE_ERR_CAPACITY; such a request
  * has no rows; where requests overlap, their rows are undefined), adapters outside [-1, L)
  * (MOE_ERR_INVALID_EXPERT; read as -1).
@@ -575,7 +575,8 @@ moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const f
 /* Self-test switch of the tensor-memory kernels' failure detection (their waits on
  * mbarriers are bounded and report MOE_ERR_TIMEOUT instead of hanging).  With stall_ns > 0,
  * every later launch of the W4A16 and MXFP8 tensor-memory grouped GEMMs in this process
- * (moe_forward above 256 rows, moe_grouped_gemm in MXFP8) and of moe_dense_gemm runs with its copy and MMA roles
+ * (moe_forward above 256 rows, moe_grouped_gemm in MXFP8), of moe_dense_gemm and of moe_adapter_gemm's
+ * kernels for long requests runs with its copy and MMA roles
  * switched off: the other roles wait on barriers that nothing arrives on, give up after
  * stall_ns nanoseconds, write MOE_ERR_TIMEOUT to ctx->dev_status, free their tensor memory
  * and return; no copy or MMA is in flight when they give up, and the context stays usable.

@@ -333,12 +333,15 @@ __global__ void __launch_bounds__(kDownThreads, 1)
 constexpr int kUpThreads = 512;
 constexpr int kFeat = 128;      // features of an accumulator
 constexpr int kAccs = 4;
-constexpr int kBaseSlots = 6;   // at most
+constexpr int kBaseSlots = 6;   // at most, and always even: see UpPlan
 constexpr int kWeightSlots = 3;
 
 struct UpPlan {
   int blocks;                   // of 64 ranks
   int bufs;                     // operands of v
+  // Base's slots are even in number, so that a slot's boxes are always the same drain group's: a wait by
+  // parity holds for the phase at hand or the next only, and a group that passed over the other's use of a
+  // slot would take that use's end for its own.
   int base_slots, weight_slots;
   int a, b, base, tab;          // offsets in shared memory
   int smem;
@@ -745,11 +748,11 @@ cudaError_t adapter_many(const Adapter& p, cudaStream_t stream) {
   UpPlan pl{};
   pl.blocks = (p.r + 63) / 64;
   pl.bufs = pl.blocks == 1 ? 2 : 1;
-  pl.weight_slots = pl.blocks == 1 ? 3 : 2;
+  pl.weight_slots = pl.blocks == 1 && !p.out_f32 ? kWeightSlots : 2;  // six boxes of base fit beside them
   pl.a = 0;
   pl.b = pl.bufs * (p.out_f32 ? 3 : 2) * pl.blocks * kBox;
   pl.base = pl.b + pl.weight_slots * pl.blocks * kBox;
-  pl.base_slots = std::min(kBaseSlots, (kSmemMost - 1024 - tables - pl.base) / kBox);
+  pl.base_slots = std::min(kBaseSlots, (kSmemMost - 1024 - tables - pl.base) / kBox) & ~1;
   pl.tab = pl.base + pl.base_slots * kBox;
   pl.smem = pl.tab + tables + 1024;
   const auto kern = p.out_f32 ? adapter_up_kernel<true> : adapter_up_kernel<false>;

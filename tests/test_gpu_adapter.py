@@ -267,3 +267,34 @@ def test_offsets_past_32_bits(moe):
         want = (xv[:off[1]] @ wv.T) @ uv.T
         assert np.all(np.abs(np64(out[:off[1]]) - want) <= bf16_half_ulp(want) * 1.01 + 2.0 ** -9)
         assert (out[off[1]:off[2]] == 0).all()
+
+
+@pytest.mark.parametrize("R,r,f32", [(16, 16, True), (16, 64, True), (3, 128, True), (16, 16, False), (1000, 64, False),
+                                     (1000, 64, True)])
+def test_long_prompts_under_load(moe, R, r, f32):
+    """Twenty calls in a graph, replayed, each with many boxes of base in flight on every SM: the same
+    bits as the first call alone, which are right.  (1000 requests: their tables leave less room for boxes.)"""
+    M, N, K = 20000, 1024, 512
+    offsets = np.linspace(0, M, R + 1).astype(int).tolist()
+    c = Case(M, N, K, r, 4, offsets, [(i * 3) % 4 for i in range(R)], f32=f32)
+    assert c.run(moe, plan="long") == 0
+    c.check()
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    size = moe.moe_adapter_gemm_workspace_size(M, R, r)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [torch.empty_like(c.out) for _ in range(20)]
+    off, ids = i32(offsets), i32(c.adapter)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        for i, o in enumerate(outs):
+            moe.moe_adapter_gemm(c.x, c.a, c.b, c.scale, off, ids, c.base, M, N, K, r, 4, R, o,
+                                 moe.Ctx(stream=stream, workspace=ws[i % 2], dev_status=status))
+    for _ in range(3):
+        for o in outs:
+            o.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(status[0]) == 0
+        for o in outs:
+            assert torch.equal(o, c.out)
