@@ -7,16 +7,23 @@
 // occurrence among the rows of its adapter, and every sixteenth is the first of a tile of up to
 // sixteen rows of one adapter, the rows of an m16n8k16 MMA.  (250 rows over five adapters are 20
 // tiles, and not 250 readings of an adapter.)  Two kernels, v = x A^T and out = base + v B^T; in each
-// the CTAs share the tiles' blocks of K, or of features, so that one tile and 200 alike use many SMs.  A tile's pieces of v are added in order by those who read them.  The second
-// kernel starts under the first one: its tables, the rows without an adapter and B's way into L2 do
-// not wait for v.
+// the CTAs share the tiles' blocks of K, or of features, so that one tile and 200 alike use many SMs.
+// A tile's pieces of v are added in order by those who read them.  The second kernel starts under the
+// first one: its tables, the rows without an adapter and the way of B and base into shared memory and
+// L2 do not wait for v.
 // The operands of an MMA are read from global memory in their own layout, 16 or 8 bytes a lane: the
 // order of K within the products is the lanes', for both operands alike.  v is fp32 and enters the
-// second product as a sum of bf16 numbers: two, 2^-17 of itself off, or three for fp32 outputs.  Rows are never in one accumulator with
-// another adapter's: a request's weights that are not finite stay its own.
+// second product as a sum of bf16 numbers: two, 2^-17 of itself off, or three for fp32 outputs.  Rows
+// are never in one accumulator with another adapter's: a request's weights that are not finite stay its
+// own.
+// Measured (replayed graphs, us): one token of rank 16, 2880 -> 2880: 6.2; 64 tokens over 100 adapters of
+// rank 16, 2880 -> 5760: 10.5 (19.5 MB; 11.7 from HBM); 250 rows over five adapters of rank 64, 7168 ->
+// 4096: 13.1 (14.5).  Not the bytes bound these but the chain: the launch, the tables (1.3), the first loads
+// of A (2.5), the pieces' sum and its way to the second kernel (1.7), the products and stores.  In one
+// kernel of clusters, which wait for the slowest piece in place of the launch, they took 7.4, 31 and 29.
 #include <algorithm>
 
-#include "moe_common.cuh"
+#include "cp_async.cuh"
 #include "moe_launch.h"
 
 namespace {
@@ -37,7 +44,8 @@ struct Rows {
   int16_t occ[kChunk];       // rows of its adapter before it
   int16_t leader[kChunk];    // first rows of the tiles
   int32_t slot_id[kSlots];   // adapters of the chunk's rows, hashed; -1: free
-  uint32_t slot_rows[kSlots][kChunk / 32];  // an adapter's rows
+  // an adapter's rows; later the first kernel's shares of v, and the second's operands
+  alignas(16) uint32_t slot_rows[kSlots][kChunk / 32];
   int32_t start[kChunk];     // the last request that starts at a row, -1: none
   int32_t start_id[kChunk];  // its adapter and its end
   int32_t start_end[kChunk];
@@ -45,14 +53,26 @@ struct Rows {
   int32_t tiles;
   int32_t rows[kTile];       // of the tile at hand
 };
-// Read and written 8 or 16 bytes at a time.
+// Read and written 8 or 16 bytes at a time, after the tables are made.
+constexpr int kVs = (kRankMost + 8) / 2;  // words of a row of v's bf16 parts
 struct DownSmem {
   Rows t;
-  alignas(16) float part[kWarps * kTile * 32];              // shares of v: [slice][row][rank]
+  MOE_DEV float* part() { return reinterpret_cast<float*>(t.slot_rows); }  // shares of v: [slice][row][rank]
 };
+static_assert(sizeof(Rows::slot_rows) >= kWarps * kTile * 32 * 4 && sizeof(Rows::slot_rows) >= 3 * kTile * kVs * 4, "");
+// What a thread of the second kernel reads first of B and of base is copied into shared memory while the
+// first kernel still runs, in places of its own, so that no thread waits for another's copies: 64 bytes of
+// B (32 for fp32 outputs), and of base what it adds to in its first block of features.
+template <bool F32>
 struct UpSmem {
   Rows t;
-  alignas(16) uint32_t vb[3][kTile * (kRankMost + 8) / 2];  // v's bf16 parts: [row][rank], rows 8 ranks apart
+  static constexpr int kAhead = F32 ? 2 : 4;  // of 16 bytes
+  alignas(16) uint8_t b[kAhead * kUpThreads * 16];
+  alignas(16) uint8_t base[(F32 ? 4 : 2) * kUpThreads * 16];
+  // v's h-th bf16 parts: [row][rank], rows 8 ranks apart
+  MOE_DEV uint32_t* vb(int h) { return &t.slot_rows[0][0] + h * kTile * kVs; }
+  // the i-th place of n bytes of this thread
+  static MOE_DEV uint8_t* place(uint8_t* mem, int i, int n) { return mem + (i * kUpThreads + (int)threadIdx.x) * n; }
 };
 
 // Equal shares of the tiles' blocks for the CTAs of a chunk.  Up to as many tiles as CTAs: `parts` CTAs a
@@ -182,6 +202,18 @@ struct Out8 {
     for (int i = 0; i < (F32 ? 2 : 1); ++i)
       v[i] = on && base ? static_cast<const uint4*>(base)[at / 8 * (F32 ? 2 : 1) + i] : make_uint4(0, 0, 0, 0);
   }
+  // The same by way of shared memory, piece i of its places.
+  static MOE_DEV void fetch(UpSmem<F32>& sm, int i, const void* base, int64_t at) {
+#pragma unroll
+    for (int j = 0; j < (F32 ? 2 : 1); ++j)
+      cpa::cp_async16(tc::smem_addr(sm.place(sm.base, i * (F32 ? 2 : 1) + j, 16)),
+                      static_cast<const uint4*>(base) + at / 8 * (F32 ? 2 : 1) + j);
+  }
+  MOE_DEV void take(UpSmem<F32>& sm, int i, bool on) {
+#pragma unroll
+    for (int j = 0; j < (F32 ? 2 : 1); ++j)
+      v[j] = on ? *reinterpret_cast<const uint4*>(sm.place(sm.base, i * (F32 ? 2 : 1) + j, 16)) : make_uint4(0, 0, 0, 0);
+  }
   MOE_DEV void add_and_store(void* out, int64_t at, const float (&f)[8]) const {
     uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[F32].x, v[F32].y, v[F32].z, v[F32].w};
     uint4* o = static_cast<uint4*>(out) + at / 8 * (F32 ? 2 : 1);
@@ -274,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_down_kernel(Adapter p
       }
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        float* at = sm.part + (slice * kTile + g) * rp + (rg * NJ + j) * 8 + q * 2;
+        float* at = sm.part() + (slice * kTile + g) * rp + (rg * NJ + j) * 8 + q * 2;
         *reinterpret_cast<float2*>(at) = make_float2(d[j][0], d[j][1]);
         *reinterpret_cast<float2*>(at + 8 * rp) = make_float2(d[j][2], d[j][3]);
       }
@@ -286,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_down_kernel(Adapter p
       const int m = sm.t.rows[2 * i / rp], k = 2 * i % rp;
       float2 s = make_float2(0.f, 0.f);
       for (int c = 0; c < slices; ++c) {
-        const float2 u = *reinterpret_cast<const float2*>(sm.part + c * kTile * rp + 2 * i);
+        const float2 u = *reinterpret_cast<const float2*>(sm.part() + c * kTile * rp + 2 * i);
         s.x += u.x;
         s.y += u.y;
       }
@@ -319,9 +351,8 @@ MOE_DEV float4 pieces_of(const Adapter& p, int64_t row, int k, int from, int ste
 
 // The tile's v times the scale as PARTS bf16 numbers: four ranks to a lane, or to 2 or 4 lanes with every
 // second or fourth piece, as many as fill the block.  lr: log2 of the ranks, rounded up.
-template <int PARTS>
-__device__ __forceinline__ void sum_pieces(const Adapter& p, UpSmem& sm, int64_t row0, int pieces, int lr, float scale) {
-  constexpr int vs = (kRankMost + 8) / 2;
+template <int PARTS, bool F32>
+__device__ __forceinline__ void sum_pieces(const Adapter& p, UpSmem<F32>& sm, int64_t row0, int pieces, int lr, float scale) {
   const int by = 128 >> lr, mine = threadIdx.x & (by - 1), i = threadIdx.x >> (7 - lr);
   const int j = 4 * i >> lr, m = sm.t.rows[j], k = 4 * i & ((1 << lr) - 1);
   float4 s = m >= 0 && k < p.r ? pieces_of(p, row0 + m, k, mine, by, pieces) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -343,20 +374,48 @@ __device__ __forceinline__ void sum_pieces(const Adapter& p, UpSmem& sm, int64_t
         f[2 * i] -= __low2float(e);
         f[2 * i + 1] -= __high2float(e);
       }
-      *reinterpret_cast<uint2*>(&sm.vb[h][j * vs + k / 2]) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(sm.vb(h) + j * kVs + k / 2) = make_uint2(w[0], w[1]);
     }
   }
 }
 
-// A tile of up to kFewest rows, without the tensor cores: a lane has a feature, whose weights it reads
-// whole, and multiplies them with v in fp32.  Most of a tile of sixteen rows would be empty, and what an
-// MMA wants around it is five times the instructions (64 tokens over 100 adapters: 0.9 us for 32 features
-// of each warp).
+// A tile of up to kFewest rows, without the tensor cores: a lane has two neighbouring features at a time,
+// whose weights it reads whole, and multiplies them with v in fp32.  Most of a tile of sixteen rows would
+// be empty, and what an MMA wants around it is five times the instructions (64 tokens over 100 adapters:
+// 0.9 us for 32 features of each warp).  16 bytes of B are number 2 (pair * rank / 8 + rank) + feature of
+// the thread's.
 template <bool F32>
-__device__ __forceinline__ void few_rows(const Adapter& p, UpSmem& sm, int id, int64_t row0, int n0, int n1, int pieces, int lr,
+__device__ __forceinline__ void fetch_few(const Adapter& p, UpSmem<F32>& sm, int id, int64_t row0, int n0, int n1) {
+  constexpr int kSize = F32 ? 8 : 4, kAhead = UpSmem<F32>::kAhead;  // bytes of a pair of base
+  const uint16_t* B = static_cast<const uint16_t*>(p.b) + (int64_t)id * p.N * p.r;
+  int n = n0 + 2 * (int)threadIdx.x;
+  for (int i = 0, k = 0; i < kAhead && n < n1; i += 2) {
+    cpa::cp_async16(tc::smem_addr(sm.place(sm.b, i, 16)), B + (int64_t)n * p.r + k);
+    cpa::cp_async16(tc::smem_addr(sm.place(sm.b, i + 1, 16)), B + (int64_t)(n + 1) * p.r + k);
+    if ((k += 8) == p.r) {
+      k = 0;
+      n += 2 * kUpThreads;
+    }
+  }
+  if (!p.base) return;
+  n = n0 + 2 * (int)threadIdx.x;
+  for (int u = 0; u < 2 && n < n1; ++u, n += 2 * kUpThreads)
+    for (int j = 0; j < kFewest; ++j) {
+      const int m = sm.t.rows[j];
+      if (m < 0) break;
+      const char* from = static_cast<const char*>(p.base) + ((row0 + m) * p.N + n) * (kSize / 2);
+      const uint32_t to = tc::smem_addr(sm.place(sm.base, u * kFewest + j, kSize));
+      if (F32) cpa::cp_async8(to, from);
+      else cpa::cp_async4(to, from);
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void few_rows(const Adapter& p, UpSmem<F32>& sm, int id, int64_t row0, int n0, int n1, int pieces, int lr,
                                          float scale) {
+  constexpr int kAhead = UpSmem<F32>::kAhead;
   const int tid = threadIdx.x;
-  float* v = reinterpret_cast<float*>(sm.vb);  // [row][rank] in fp32
+  float* v = reinterpret_cast<float*>(sm.vb(0));  // [row][rank] in fp32
   {
     const int i = tid >> 2, j = 4 * i >> lr, k = 4 * i & ((1 << lr) - 1);  // four lanes a sum
     const int m = j < kFewest ? sm.t.rows[j] : -1;
@@ -371,50 +430,54 @@ __device__ __forceinline__ void few_rows(const Adapter& p, UpSmem& sm, int id, i
     if ((tid & 3) == 0 && j < kFewest)
       reinterpret_cast<float4*>(v)[i] = make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
   }
+  cpa::cp_async_wait_all();
   __syncthreads();
   int rows = 0;
-  int64_t at[kFewest];
 #pragma unroll
-  for (int j = 0; j < kFewest; ++j) {
-    rows += sm.t.rows[j] >= 0;
-    at[j] = (row0 + sm.t.rows[j]) * p.N;
-  }
+  for (int j = 0; j < kFewest; ++j) rows += sm.t.rows[j] >= 0;
   const uint16_t* B = static_cast<const uint16_t*>(p.b) + (int64_t)id * p.N * p.r;
-  for (int n = n0 + tid; n < n1; n += kUpThreads) {
-    float base[kFewest], d[kFewest];
+  for (int n = n0 + 2 * tid, u = 0, i = 0; n < n1; n += 2 * kUpThreads, ++u) {
+    float d[kFewest][2];
 #pragma unroll
-    for (int j = 0; j < kFewest; ++j) {
-      d[j] = 0.f;
-      base[j] = 0.f;
-      if (j < rows && p.base)
-        base[j] = F32 ? static_cast<const float*>(p.base)[at[j] + n]
-                      : moe::bf16_bits_to_f32(static_cast<const uint16_t*>(p.base)[at[j] + n]);
-    }
-    const uint4* w = reinterpret_cast<const uint4*>(B + (int64_t)n * p.r);
-    for (int k = 0; k < p.r; k += 16) {
-      const bool two = k + 8 < p.r;
-      const uint4 a = moe::ldg_nc_u128(w + k / 8), b = two ? moe::ldg_nc_u128(w + k / 8 + 1) : make_uint4(0, 0, 0, 0);
-      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    for (int j = 0; j < kFewest; ++j) d[j][0] = d[j][1] = 0.f;
+    for (int k = 0; k < p.r; k += 8, i += 2) {
+      uint4 w[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        w[h] = i < kAhead ? *reinterpret_cast<const uint4*>(sm.place(sm.b, i + h, 16)) : moe::ldg_nc_u128(B + (int64_t)(n + h) * p.r + k);
 #pragma unroll
       for (int j = 0; j < kFewest; ++j) {
         if (j >= rows) break;
-        const float* f = v + (j << lr) + k;
+        const float4 e = *reinterpret_cast<const float4*>(v + (j << lr) + k);
+        const float4 f = *reinterpret_cast<const float4*>(v + (j << lr) + k + 4);
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {  // what v has past the rank is 0
-          const float4 e = *reinterpret_cast<const float4*>(f + 2 * i);
-          d[j] = __fmaf_rn(e.x, __uint_as_float(u[i] << 16), d[j]);
-          d[j] = __fmaf_rn(e.y, __uint_as_float(u[i] & 0xffff0000u), d[j]);
-          d[j] = __fmaf_rn(e.z, __uint_as_float(u[i + 1] << 16), d[j]);
-          d[j] = __fmaf_rn(e.w, __uint_as_float(u[i + 1] & 0xffff0000u), d[j]);
+        for (int h = 0; h < 2; ++h) {
+          d[j][h] = __fmaf_rn(e.x, __uint_as_float(w[h].x << 16), d[j][h]);
+          d[j][h] = __fmaf_rn(e.y, __uint_as_float(w[h].x & 0xffff0000u), d[j][h]);
+          d[j][h] = __fmaf_rn(e.z, __uint_as_float(w[h].y << 16), d[j][h]);
+          d[j][h] = __fmaf_rn(e.w, __uint_as_float(w[h].y & 0xffff0000u), d[j][h]);
+          d[j][h] = __fmaf_rn(f.x, __uint_as_float(w[h].z << 16), d[j][h]);
+          d[j][h] = __fmaf_rn(f.y, __uint_as_float(w[h].z & 0xffff0000u), d[j][h]);
+          d[j][h] = __fmaf_rn(f.z, __uint_as_float(w[h].w << 16), d[j][h]);
+          d[j][h] = __fmaf_rn(f.w, __uint_as_float(w[h].w & 0xffff0000u), d[j][h]);
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < kFewest; ++j)
-      if (j < rows) {
-        if (F32) static_cast<float*>(p.out)[at[j] + n] = base[j] + d[j];
-        else static_cast<uint16_t*>(p.out)[at[j] + n] = moe::f32_to_bf16_bits(base[j] + d[j]);
+    for (int j = 0; j < kFewest; ++j) {
+      if (j >= rows) break;
+      const int64_t at = ((row0 + sm.t.rows[j]) * p.N + n) / 2;
+      if (F32) {
+        float2 e = make_float2(0.f, 0.f);
+        if (p.base) e = u < 2 ? *reinterpret_cast<const float2*>(sm.place(sm.base, u * kFewest + j, 8)) : static_cast<const float2*>(p.base)[at];
+        static_cast<float2*>(p.out)[at] = make_float2(e.x + d[j][0], e.y + d[j][1]);
+      } else {
+        uint32_t e = 0;
+        if (p.base) e = u < 2 ? *reinterpret_cast<const uint32_t*>(sm.place(sm.base, u * kFewest + j, 4)) : static_cast<const uint32_t*>(p.base)[at];
+        const __nv_bfloat162 o = __floats2bfloat162_rn(__uint_as_float(e << 16) + d[j][0], __uint_as_float(e & 0xffff0000u) + d[j][1]);
+        static_cast<uint32_t*>(p.out)[at] = *reinterpret_cast<const uint32_t*>(&o);
       }
+    }
   }
 }
 
@@ -423,8 +486,9 @@ __device__ __forceinline__ void few_rows(const Adapter& p, UpSmem& sm, int id, i
 template <bool F32, int S, bool WHOLE>
 __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p, int ctas) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  UpSmem& sm = *reinterpret_cast<UpSmem*>(smem_raw);
+  UpSmem<F32>& sm = *reinterpret_cast<UpSmem<F32>*>(smem_raw);
   constexpr int kParts = F32 ? 3 : 2;  // bf16 numbers that carry a value of v
+  constexpr int kAhead = UpSmem<F32>::kAhead;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
   const int chunk = blockIdx.x / ctas, cta = blockIdx.x - chunk * ctas;
   const int64_t row0 = (int64_t)chunk * kChunk;
@@ -435,21 +499,44 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
   // written already.
   make_tables(p, sm.t, row0, rows, false);
   const int nk = (p.K + 31) / 32, nb = (p.N + 31) / 32, pieces = Share(sm.t.tiles, nk, kPieces, 0, ctas).parts;
-  const int lr = p.r <= 32 ? 5 : p.r <= 64 ? 6 : 7, vs = (kRankMost + 8) / 2, steps = (p.r + 15) / 16;
+  const int lr = p.r <= 32 ? 5 : p.r <= 64 ? 6 : 7, steps = (p.r + 15) / 16;
   const Share share(sm.t.tiles, nb, nb, cta, ctas);
   float scale = 1.f;
   int t, b0, b1;
-  // A tile's rows; its scale, and its part of B and of its rows of base on their way into L2.
+  // A tile's rows; its scale, and its part of B and of its rows of base on their way: what each thread
+  // reads first into shared memory, the rest into L2.
   const auto begin = [&] {
     const int id = tile_rows(sm.t, t), wide = min(b1 * 32, p.N) - b0 * 32;
     if (p.scale) scale = p.scale[id];
-    const char* B = reinterpret_cast<const char*>(static_cast<const uint16_t*>(p.b) + ((int64_t)id * p.N + b0 * 32) * p.r);
-    for (int64_t i = (int64_t)tid * 128; i < (int64_t)wide * p.r * 2; i += kUpThreads * 128) prefetch_l2(B + i);
+    if (sm.t.rows[kFewest] < 0) {
+      fetch_few<F32>(p, sm, id, row0, b0 * 32, min(b1 * 32, p.N));
+    } else {
+      // a step of 16 ranks of a block of 32 features is number (block * steps + step) of the warp's
+      const uint16_t* B = static_cast<const uint16_t*>(p.b) + ((int64_t)id * p.N + 8 * (g >> 1) + (g & 1)) * p.r + q * 4;
+      int b = b0 + warp;
+      for (int i = 0, s = 0; i < kAhead / 2 && b < b1; ++i) {
+        if (b * 32 + 8 * (g >> 1) < p.N && s * 16 + q * 4 < p.r)
+          for (int j = 0; j < 4; ++j)
+            cpa::cp_async8(tc::smem_addr(sm.place(sm.b, i * 4 + j, 8)), B + (int64_t)b * 32 * p.r + 2 * j * p.r + s * 16);
+        if (++s == steps) {
+          s = 0;
+          b += kUpWarps;
+        }
+      }
+      b = b0 + warp;
+      if (p.base && b < b1 && b * 32 + 8 * q < p.N) {
+        const int ra = sm.t.rows[g], rb = sm.t.rows[g + 8];
+        if (ra >= 0) Out8<F32>::fetch(sm, 0, p.base, (row0 + ra) * p.N + 8 * q + b * 32);
+        if (rb >= 0) Out8<F32>::fetch(sm, 1, p.base, (row0 + rb) * p.N + 8 * q + b * 32);
+      }
+    }
+    const char* from = reinterpret_cast<const char*>(static_cast<const uint16_t*>(p.b) + ((int64_t)id * p.N + b0 * 32) * p.r);
+    for (int64_t i = kAhead * kUpThreads * 16 + (int64_t)tid * 128; i < (int64_t)wide * p.r * 2; i += kUpThreads * 128) prefetch_l2(from + i);
     constexpr int kSize = F32 ? 4 : 2;
     const int m = sm.t.rows[warp];
     if (p.base && m >= 0) {
       const char* at = static_cast<const char*>(p.base) + ((row0 + m) * p.N + b0 * 32) * kSize;
-      for (int i = lane * 128; i < wide * kSize; i += 32 * 128) prefetch_l2(at + i);
+      for (int i = 32 * kUpWarps * kSize + lane * 128; i < wide * kSize; i += 32 * 128) prefetch_l2(at + i);
     }
     return id;
   };
@@ -473,6 +560,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
       continue;
     }
     sum_pieces<kParts>(p, sm, row0, pieces, lr, scale);
+    cpa::cp_async_wait_all();
     __syncthreads();
     // v B^T, 32 features at a time: feature 8 (c / 2) + 2 j + c % 2 is column c of product j, so that a
     // lane ends with eight neighbouring ones of its rows
@@ -484,16 +572,24 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
     const auto load_w = [&](int b, int s0) {  // eight features are all within N, or none
       const bool on = b < b1 && b * 32 + 8 * (g >> 1) < p.N;
       const uint16_t* at = B + (int64_t)b * 32 * p.r + s0 * 16;
+      const int n = (b - b0) / kUpWarps * steps + s0;
 #pragma unroll
       for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          w[s][j] = on && (s0 + s) * 16 + q * 4 < p.r ? moe::ldg_nc_u64(at + 2 * j * p.r + s * 16) : make_uint2(0, 0);
+          w[s][j] = !on || (s0 + s) * 16 + q * 4 >= p.r ? make_uint2(0, 0)
+                    : n + s < kAhead / 2 ? *reinterpret_cast<const uint2*>(sm.place(sm.b, (n + s) * 4 + j, 8))
+                                         : moe::ldg_nc_u64(at + 2 * j * p.r + s * 16);
     };
     const auto load_o = [&](int b) {
       const bool on = b < b1 && b * 32 + 8 * q < p.N;
-      oa.load(p.base, at_a + b * 32, on && ra >= 0);
-      ob.load(p.base, at_b + b * 32, on && rb >= 0);
+      if (b == b0 + warp) {
+        oa.take(sm, 0, on && p.base && ra >= 0);
+        ob.take(sm, 1, on && p.base && rb >= 0);
+      } else {
+        oa.load(p.base, at_a + b * 32, on && ra >= 0);
+        ob.load(p.base, at_b + b * 32, on && rb >= 0);
+      }
     };
     if (WHOLE) {
       load_w(b0 + warp, 0);
@@ -514,8 +610,8 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
 #pragma unroll
           for (int h = 0; h < kParts; ++h) {
             const int at = (s0 + s) * 8 + q * 2;
-            const uint2 va = *reinterpret_cast<const uint2*>(&sm.vb[h][g * vs + at]);
-            const uint2 vc = *reinterpret_cast<const uint2*>(&sm.vb[h][(g + 8) * vs + at]);
+            const uint2 va = *reinterpret_cast<const uint2*>(sm.vb(h) + g * kVs + at);
+            const uint2 vc = *reinterpret_cast<const uint2*>(sm.vb(h) + (g + 8) * kVs + at);
             const uint32_t a[4] = {va.x, vc.x, va.y, vc.y};
 #pragma unroll
             for (int j = 0; j < 4; ++j) moe::mma_bf16(d[j], a, w[s][j].x, w[s][j].y, d[j]);
@@ -539,6 +635,18 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
 
 constexpr int kCtasMost = 160;  // of a call, where its chunks are fewer
 
+constexpr int kCarveout = 44;  // per cent of 228 KB
+static_assert(sizeof(DownSmem) + std::max(sizeof(UpSmem<false>), sizeof(UpSmem<true>)) + 2 * 1024 <= 100 * 1024, "");
+
+cudaError_t share_sm(const void* kernel, std::atomic<uint64_t>& done) {
+  int dev = -1;
+  const bool known = cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64;
+  if (known && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveout);
+  if (err == cudaSuccess && known) done.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
+  return err;
+}
+
 int64_t chunks_of(int64_t M) { return (M + kChunk - 1) / kChunk; }
 int ctas_of(int64_t M, int sms) { return (int)std::max<int64_t>(1, std::min(sms, kCtasMost) / chunks_of(M)); }
 
@@ -556,12 +664,24 @@ cudaError_t adapter_few(const Adapter& p, cudaStream_t stream) {
   const int ctas = ctas_of(p.M, sm_count_current());
   const dim3 grid((unsigned)(chunks_of(p.M) * ctas));
   const auto down = p.r <= 16 ? adapter_few_down_kernel<2, 4> : adapter_few_down_kernel<4, 3>;
-  cudaError_t e = launch_staged(down, grid, dim3(kThreads), sizeof(DownSmem), stream, 1, p, ctas);
+  // An SM that is set up for the shared memory of the first kernel's blocks alone would take the second's
+  // only when it is empty; and what is not shared memory is L1, which the first kernel's loads need.  So both
+  // ask for 100 KB, a block of each (250 rows of rank 64 over five adapters: 13.2 us; with nothing asked for
+  // 14.6, with 164 KB and twice as much copied ahead 13.5, with all of it 14.4).
+  static std::atomic<uint64_t> set[2] = {};
+  cudaError_t e = share_sm((const void*)down, set[p.r > 16]);
+  if (e != cudaSuccess) return e;
+  e = launch_staged(down, grid, dim3(kThreads), sizeof(DownSmem), stream, 1, p, ctas);
   if (e != cudaSuccess) return e;
   const auto up = p.r <= 16   ? (p.out_f32 ? adapter_few_up_kernel<true, 1, true> : adapter_few_up_kernel<false, 1, true>)
                   : p.r <= 32 ? (p.out_f32 ? adapter_few_up_kernel<true, 2, true> : adapter_few_up_kernel<false, 2, true>)
                               : (p.out_f32 ? adapter_few_up_kernel<true, 2, false> : adapter_few_up_kernel<false, 2, false>);
-  return launch_staged(up, grid, dim3(kUpThreads), sizeof(UpSmem), stream, 1, p, ctas);
+  const int smem = p.out_f32 ? sizeof(UpSmem<true>) : sizeof(UpSmem<false>);
+  static std::atomic<uint64_t> done[6] = {}, set_up[6] = {};
+  e = allow_smem((const void*)up, smem, done[(p.out_f32 ? 3 : 0) + (p.r <= 16 ? 0 : p.r <= 32 ? 1 : 2)]);
+  if (e == cudaSuccess) e = share_sm((const void*)up, set_up[(p.out_f32 ? 3 : 0) + (p.r <= 16 ? 0 : p.r <= 32 ? 1 : 2)]);
+  if (e != cudaSuccess) return e;
+  return launch_staged(up, grid, dim3(kUpThreads), smem, stream, 1, p, ctas);
 }
 
 }  // namespace moe_launch

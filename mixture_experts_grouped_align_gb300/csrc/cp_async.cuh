@@ -21,6 +21,10 @@ MOE_DEV void cp_async16z(uint32_t dst, const void* src, bool valid) {
 MOE_DEV void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
+// 8 bytes (.ca); both addresses 8-byte aligned.
+MOE_DEV void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src) : "memory");
+}
 // 4 bytes, or 4 zero bytes when !valid (source size 0: nothing is read).
 MOE_DEV void cp_async4z(uint32_t dst, const void* src, bool valid) {
   const int sz = valid ? 4 : 0;
