@@ -14,6 +14,15 @@
 // numbers, one for each of the eight values that a thread moves as 16 bytes: 20 wide multiplications
 // for eight values instead of the 40 that 32-bit numbers would take, at the price of a probability in
 // steps of 2^-16.
+//
+// Both passes are bound by memory: every tensor is read or written once, and a row stays in registers from
+// its sums to its outputs.  Measured (replayed graphs): 8192 x 7168 to bf16, stream and MX codes 81 us, 6.56
+// TB/s (a copy moves 6.78); 61440 x 2880 with an fp32 stream and dropout, forward and back, 743 us, 6.5 TB/s;
+// 8192 x 7168 in bf16 the same 178 us, 5.9 TB/s: what the generator computes (25 instructions a value, both
+// passes) is not all hidden there.  Few rows are bound by the launch and two latencies: 64 x 2880 1.5 us.
+// The backward pass in blocks that walk over rows, loads into registers, took 283 us where the rings of
+// asynchronous copies take 100 (no room for loads ahead beside the sums of d_w); rings of bulk copies, which
+// need a barrier and a thread that issues them, 238 where these took 178.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -139,13 +148,19 @@ struct Map {
 // in a fixed order.  `red`: shared memory for WIDE; the caller separates two uses of it by a barrier.
 template <typename M, bool MAX = false>
 MOE_DEV void reduce_pair(float& a, float& b, float2* red) {
-  const auto add = [&](int o) {
-    a += __shfl_xor_sync(kAll, a, o);
-    const float c = __shfl_xor_sync(kAll, b, o);
-    b = MAX ? __uint_as_float(max(__float_as_uint(b), __float_as_uint(c))) : b + c;
-  };
+  const auto lanes = [&](int n) {
+    const bool whole = MAX && n == 32;  // shuffles bound row scales: 8192 x 7168 to codes alone 64 us without this, 58
+    if (whole) b = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(b)));
 #pragma unroll
-  for (int o = M::kLanes / 2; o > 0; o >>= 1) add(o);
+    for (int o = 16; o > 0; o >>= 1) {
+      if (o >= n) continue;
+      a += __shfl_xor_sync(kAll, a, o);
+      if (whole) continue;
+      const float c = __shfl_xor_sync(kAll, b, o);
+      b = MAX ? __uint_as_float(max(__float_as_uint(b), __float_as_uint(c))) : b + c;
+    }
+  };
+  lanes(M::kLanes);
   if (M::kWide) {
     const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) red[threadIdx.x >> 5] = make_float2(a, b);
@@ -153,8 +168,7 @@ MOE_DEV void reduce_pair(float& a, float& b, float2* red) {
     const float2 v = lane < warps ? red[lane] : make_float2(0.f, 0.f);
     a = v.x;
     b = v.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) add(o);
+    lanes(32);
   }
 }
 
@@ -504,6 +518,10 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(Residu
 template <bool F32, int QUANT, typename M, int kAhead>
 __global__ void __launch_bounds__(M::kMost) residual_norm_walk_kernel(ResidualNorm p) {
   constexpr int V = M::kV, kS = F32 ? 2 : 1, kPer = 1 + kS, kChunks = V * kPer;  // a stage's: x, residual
+  // With codes, a row's outputs all leave at once and two rows are read ahead (8192 x 7168 MX: 80 us; the
+  // stream before the sums 86, and with four rows ahead 91: memory that turns between reads and writes less
+  // often moves more); dropout spreads them well enough (forward and back 178 us, otherwise 184).
+  constexpr bool kLate = QUANT != 0;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][32];
   moe::wait_for_stream();
@@ -569,7 +587,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_walk_kernel(ResidualNo
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[t][i] = __fadd_rn(s[t][i], f[i]);
       }
-      if (p.stream && in && c < units) Eight<F32>::store(p.stream, u, s[t]);
+      if (!kLate && p.stream && in && c < units) Eight<F32>::store(p.stream, u, s[t]);
       if (QUANT == 2) unpack8(w[t], f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -587,6 +605,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_walk_kernel(ResidualNo
 #pragma unroll
     for (int t = 0; t < V; ++t) {
       const int c = M::col() + t * M::step();
+      if (kLate && p.stream && in && c < units) Eight<F32>::store(p.stream, row * units + c, s[t]);
       finish<QUANT>(p, s[t], w[t], r, rc, row * units + c, c, in && c < units);
     }
   }
@@ -627,17 +646,19 @@ constexpr int64_t kFew = 200000;  // eights of columns in all
 
 // A block or a part of a warp for each row: as many threads as there are eights in wide rows and in few
 // narrow ones, which leaves registers for most threads an SM has (8192 x 7168 80 us as four eights a
-// thread, 78 as one; 20388 x 2880 MX 105 and 84), up to four eights a lane in many narrow ones, so that
-// a row stays within a warp.
+// thread, 78 as one), up to four eights a lane in many narrow ones, so that a row stays within a warp.
+// With codes or dropout, what every thread does for the row counts beside its eights: two of them a thread
+// (20000 x 2880: MX 81 us as one, 78 as two; row scales 82 and 75, to codes alone 74 and 66, with four 67;
+// dropout, forward and back, 189 and 182).
 template <typename F>
-cudaError_t pick_once(int64_t T, int K, F launch) {
+cudaError_t pick_once(int64_t T, int K, bool more, F launch) {
   const int units = K / 8;
   if (units <= 8) return launch(Map<8, false, 1>{});
   const bool few = T * units < kFew;
   if (units <= 32) return few ? launch(Map<32, false, 1>{}) : launch(Map<8, false, 4>{});
   if (units <= 64 && !few) return launch(Map<16, false, 4>{});
   if (units <= 128 && !few) return launch(Map<32, false, 4>{});
-  if (units <= 1024) return launch(Map<32, true, 1>{});
+  if (units <= 1024 && (few || !more)) return launch(Map<32, true, 1>{});
   return launch(Map<32, true, 2>{});
 }
 
@@ -681,9 +702,11 @@ template <bool F32, int QUANT>
 cudaError_t forward(const ResidualNorm& p, cudaStream_t stream) {
   // Blocks that walk over rows pay where a block of its own leaves a row too few neighbours beside it to
   // hide what it computes: wide rows with dropout or codes, and those above 1024 eights, in bf16
-  // (8192 x 7168: dropout 79 us and 88 as blocks of their own, row scales 85 and 94, MX 91 and 92, the
+  // (8192 x 7168: dropout 79 us and 88 as blocks of their own, row scales 82 and 84, MX 80 and 92, the
   // norm alone 82 and 78; 4778 x 12288: 80 and 86, dropout 78 and 103; 14336 x 4096 MX 95 and 81; fp32
-  // streams 121 and 101 and more).
+  // streams 121 and 101 and more).  A thread has two eights where a row becomes codes of its own scale alone
+  // (66 us as one and as two; without x and the stream, 58 and 50), otherwise one (with the bf16 rows beside
+  // the codes 82 as one and 94 as two).
   if constexpr (!F32) {
     if (p.K > 8192 ? p.T * (p.K / 8) >= kFew : p.K > 4096 && p.T * (p.K / 8) >= 4 * kFew && (p.drop_below || QUANT)) {
       const auto walk = [&](auto m) {
@@ -691,7 +714,7 @@ cudaError_t forward(const ResidualNorm& p, cudaStream_t stream) {
         static std::atomic<uint64_t> done[2] = {};
         static moe_host::PerDevice<33> known[2];
         const int threads = threads_of<M>(p.K), stage = threads * 16 * M::kV * 2;
-        const bool deep = 4 * stage <= kRingMost;  // rows ahead: four, or two where they do not fit
+        const bool deep = QUANT == 0 && 4 * stage <= kRingMost;  // rows ahead: four, or two with codes and where they do not fit
         const auto kern = deep ? residual_norm_walk_kernel<F32, QUANT, M, 4> : residual_norm_walk_kernel<F32, QUANT, M, 2>;
         const int smem = (deep ? 4 : 2) * stage;
         const cudaError_t e = moe_launch::allow_smem((const void*)kern, kRingMost, done[deep]);
@@ -699,10 +722,10 @@ cudaError_t forward(const ResidualNorm& p, cudaStream_t stream) {
         const int64_t blocks = walkers<M>(p.T, kern, threads, smem, known[deep]);
         return moe_launch::launch_staged(kern, dim3((unsigned)blocks), dim3((unsigned)threads), smem, stream, 1, p);
       };
-      return p.K <= 8192 ? walk(Map<32, true, 1>{}) : walk(Map<32, true, 2>{});
+      return p.K <= 8192 && (QUANT != 2 || p.out) ? walk(Map<32, true, 1>{}) : walk(Map<32, true, 2>{});
     }
   }
-  return pick_once(p.T, p.K, [&](auto m) {
+  return pick_once(p.T, p.K, QUANT != 0 || p.drop_below != 0, [&](auto m) {
     using M = decltype(m);
     return moe_launch::launch_staged(residual_norm_kernel<F32, QUANT, M>, dim3((unsigned)blocks_of<M>(p.T)),
                                      dim3((unsigned)threads_of<M>(p.K)), 0, stream, 1, p);
