@@ -18,11 +18,10 @@
 // Both passes are bound by memory: every tensor is read or written once, and a row stays in registers from
 // its sums to its outputs.  Measured (replayed graphs): 8192 x 7168 to bf16, stream and MX codes 81 us, 6.56
 // TB/s (a copy moves 6.78); 61440 x 2880 with an fp32 stream and dropout, forward and back, 743 us, 6.5 TB/s;
-// 8192 x 7168 in bf16 the same 178 us, 5.9 TB/s: what the generator computes (25 instructions a value, both
-// passes) is not all hidden there.  Few rows are bound by the launch and two latencies: 64 x 2880 1.5 us.
-// The backward pass in blocks that walk over rows, loads into registers, took 283 us where the rings of
-// asynchronous copies take 100 (no room for loads ahead beside the sums of d_w); rings of bulk copies, which
-// need a barrier and a thread that issues them, 238 where these took 178.
+// 8192 x 7168 in bf16 the same 177 us, 6.0 TB/s (171 without dropout: what the generator computes is not all
+// hidden).  Few rows are bound by the launch and two latencies: 64 x 2880 1.5 us.
+// With the backward pass's loads into registers these were 283 us (no room for loads ahead beside the sums
+// of d_w), with rings of bulk copies, which need a barrier and a thread that issues them, 238.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -657,7 +656,7 @@ cudaError_t pick_once(int64_t T, int K, bool more, F launch) {
   const bool few = T * units < kFew;
   if (units <= 32) return few ? launch(Map<32, false, 1>{}) : launch(Map<8, false, 4>{});
   if (units <= 64 && !few) return launch(Map<16, false, 4>{});
-  if (units <= 128 && !few) return launch(Map<32, false, 4>{});
+  if (units <= 128 && !few && !more) return launch(Map<32, false, 4>{});
   if (units <= 1024 && (few || !more)) return launch(Map<32, true, 1>{});
   return launch(Map<32, true, 2>{});
 }
@@ -672,7 +671,14 @@ int64_t blocks_of(int64_t T) {
   return (T + rows - 1) / rows;
 }
 
-constexpr int kPartsMost = 608;      // blocks that leave a part of d_w
+// Blocks of an SM that walk over rows: as many small ones as hold 1024 threads (40000 x 1024, dropout, forward
+// and back: 187 us with four, 131 with eight).
+constexpr int walkers_most(int threads) { return std::max(4, std::min(8, 1024 / threads)); }
+// Blocks that leave a part of d_w.
+int parts_most(int K) {
+  const int units = K / 8;
+  return 152 * walkers_most(units <= 64 ? kThreads : (units + 31) / 32 * 32);  // 1024 eights and more: four
+}
 constexpr int kRingMost = 224 * 1024;  // shared memory of an SM for the rings of its blocks
 
 // Columns of a thread where blocks walk over rows: narrow rows share warps; wide ones have a block.
@@ -695,7 +701,7 @@ int64_t walkers(int64_t T, K kern, int threads, int smem, moe_host::PerDevice<33
     int n = 0;
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) == cudaSuccess ? n : 0;
   });
-  return std::min<int64_t>(blocks_of<M>(T), (int64_t)std::min(fit, 4) * moe_launch::sm_count_current());
+  return std::min<int64_t>(blocks_of<M>(T), (int64_t)std::min(fit, walkers_most(threads)) * moe_launch::sm_count_current());
 }
 
 template <bool F32, int QUANT>
@@ -737,19 +743,18 @@ cudaError_t backward(ResidualNormBackward p, float* d_weight, cudaStream_t strea
   int64_t parts = 0;
   cudaError_t err = pick_walk(p.K, [&](auto m) {
     using M = decltype(m);
-    static std::atomic<uint64_t> done[3] = {};
-    static moe_host::PerDevice<33> known[3];
+    static std::atomic<uint64_t> done[2] = {};
+    static moe_host::PerDevice<33> known[2];
     const int threads = threads_of<M>(p.K), chunk = threads * 16 * M::kV, chunks = F32 ? 5 : 3;
-    // three rows ahead where one block has the SM to itself; the weights of a row that is not held
-    const int stage = chunks * chunk, weights = M::kWide && M::kV > 1 ? chunk : 0, fit = (kRingMost - weights) / stage;
-    const int ahead = threads > 512 && fit >= 3 ? 3 : std::min(2, fit), which = ahead - 1;
-    const auto kern = ahead == 3   ? residual_norm_backward_kernel<F32, M, 3>
-                      : ahead == 2 ? residual_norm_backward_kernel<F32, M, 2>
-                                   : residual_norm_backward_kernel<F32, M, 1>;
+    // two rows ahead (three: 8192 x 7168 forward and back 178 us in place of 177, without dropout 176 and
+    // 171), one where they do not fit; the weights of a row that is not held
+    const int stage = chunks * chunk, weights = M::kWide && M::kV > 1 ? chunk : 0;
+    const int ahead = std::min(2, (kRingMost - weights) / stage), which = ahead - 1;
+    const auto kern = ahead == 2 ? residual_norm_backward_kernel<F32, M, 2> : residual_norm_backward_kernel<F32, M, 1>;
     const int smem = std::max(ahead * stage + weights, M::kWide ? 0 : kThreads * 8 * M::kV * 4);
     const cudaError_t e = moe_launch::allow_smem((const void*)kern, kRingMost, done[which]);
     if (e != cudaSuccess) return e;
-    parts = std::min<int64_t>(walkers<M>(p.T, kern, threads, smem, known[which]), kPartsMost);
+    parts = std::min<int64_t>(walkers<M>(p.T, kern, threads, smem, known[which]), parts_most(p.K));
     return moe_launch::launch_staged(kern, dim3((unsigned)parts), dim3((unsigned)threads), smem, stream, 1, p);
   });
   if (err != cudaSuccess || d_weight == nullptr) return err;
@@ -761,7 +766,7 @@ cudaError_t backward(ResidualNormBackward p, float* d_weight, cudaStream_t strea
 
 namespace moe_launch {
 
-size_t residual_norm_workspace_bytes(int K) { return (size_t)kPartsMost * K * 4; }
+size_t residual_norm_workspace_bytes(int K) { return (size_t)parts_most(K) * K * 4; }
 
 cudaError_t residual_norm(const ResidualNorm& p, cudaStream_t stream) {
   if (p.T == 0) return cudaSuccess;
