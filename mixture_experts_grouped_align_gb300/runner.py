@@ -195,8 +195,9 @@ class ServeBlock:
             if adapters[0] is not None:  # added before the activation, so the pre-activations are kept
                 self.gs = new(T, 2 * Is)
                 self.held = new(T, 2 * Is, dtype=torch.uint8), new(T, 2 * Is // 32, dtype=torch.uint8)
-        # the adapters' workspace is no smaller for more requests, and largest at whole 256s of rows, or at all
-        need = max([256] + [moe_adapter_gemm_workspace_size(t, min(t, max_requests), max(ranks))
+        # the adapters' workspace is no smaller for more requests up to 1024 (beyond, other kernels run), and
+        # largest at whole 256s of rows, or at all; requests may be more than rows
+        need = max([256] + [moe_adapter_gemm_workspace_size(t, min(1024, max_requests), max(ranks))
                             for t in {T, *range(256, T, 256)} if max(ranks)])
         self.workspace = new(need, dtype=torch.uint8)
         self.status = torch.zeros(4, dtype=torch.int32, device=dev)

@@ -247,3 +247,19 @@ def test_serving_block_refusals(moe):
         B.step(None, z(5, K), 5, z(5, K), i, i[:5])
     with pytest.raises(MoeError, match="rows"):
         B.step(None, z(17, K), 17, z(17, K))
+
+
+@pytest.mark.parametrize("max_requests", [4, 512, 2000])
+def test_serving_block_workspace_holds_every_batch(moe, max_requests):
+    """Whatever the rows and requests of a batch, also more requests than rows and more than 1024."""
+    from mixture_experts_grouped_align_gb300 import moe_adapter_gemm_workspace_size
+    from mixture_experts_grouped_align_gb300.runner import DeviceLayer, ServeBlock
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    E, K, I, Is, r = 8, 64, 64, 32, 16
+    L = DeviceLayer("bf16", E, K, I, 2, z(E, 2 * I, K), None, None, z(E, K, I), None, None, 2050, device="cpu")
+    B = ServeBlock(L, z(K), z(E, K), (z(2 * Is, K), z(2 * Is), z(K, Is), z(K)), (None, (z(3, r, Is), z(3, K, r), None)),
+                   max_requests=max_requests)
+    for T in (1, 100, 255, 256, 257, 300, 511, 512, 1000, 1792, 2048, 2050):
+        for R in {1, 3, 300, 1000, 1024, 1025, 2000}:
+            if R <= max_requests:
+                assert B.workspace.numel() >= moe_adapter_gemm_workspace_size(T, R, r), (T, R)
