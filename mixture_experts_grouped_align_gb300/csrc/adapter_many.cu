@@ -13,10 +13,13 @@
 //         bf16 output hides: for fp32 outputs it takes kChunk stages at most, which are added there.
 //   up:   the builder warps add the pieces of a tile's v, scale it and leave it as two bf16 operands whose
 //         sum it is to 2^-17 of itself (three for fp32 outputs), the rows of MMAs against 128 features of B
-//         at a time;
-//         base comes in boxes of 128 bytes x 128 rows, six ahead, in which the epilogue warps add the
-//         accumulator and from which they store whole lines of the request's rows.
+//         at a time; base comes in boxes of 128 bytes x 128 rows, six ahead, in which the epilogue warps add
+//         the accumulator and from which they store whole lines of the request's rows.
 // Every wait is bounded; one that runs out sets MOE_ERR_TIMEOUT and all roles leave their loops.
+// Measured (replayed graphs): 58879 rows of 16 requests of rank 64, 2880 -> 2880, 190 us for 1022 MB: down 62 (5.6
+// TB/s), up 121 (6.0 TB/s; a copy moves 6.8); 8192 rows of rank 32, 7168 -> 4096, 56 us: 25 (4.7 TB/s) and 33, of
+// which 8 are the kernel's start, the first v and the last stores.  The kernels follow one another, as each
+// fills an SM's shared memory; the next launch is set up meanwhile.
 #include <algorithm>
 
 #include "dense_common.cuh"
