@@ -140,6 +140,18 @@ def test_row_codes_of_other_widths(moe):
         c.check(*c.run(moe))
 
 
+@pytest.mark.parametrize("T,K,quant,f32", [(700, 2880, "mx", False), (700, 2880, "row", True), (1700, 1024, "row", False),
+                                           (3100, 520, "row", False), (900, 7168, "row", False), (900, 7168, "mx", False),
+                                           (901, 4104, "row", True), (140, 12288, "row", False), (140, 12288, "mx", False)])
+@pytest.mark.parametrize("out", [False, True])
+def test_codes_of_many_rows(moe, T, K, quant, f32, out):
+    """Two eights a thread, blocks that walk over rows, stores after the sums: with and without the bf16 rows."""
+    c = Case(T, K, f32, p=0.1 if out else 0.0, quant=quant, masked=True, seed=13)
+    c.check(*c.run(moe, out=out))
+    c = Case(T, K, f32, branch=False, quant=quant, seed=14)
+    c.check(*c.run(moe, stream=False, out=out))
+
+
 @pytest.mark.parametrize("branch,stream,out,quant", [(False, False, True, None), (False, True, True, "mx"),
                                                      (True, True, False, None), (True, False, False, "row")])
 def test_parts_of_the_call(moe, branch, stream, out, quant):
@@ -247,6 +259,12 @@ def backward(moe, c, use=("d_stream", "d_residual", "d_x", "d_weight"), in_place
 @pytest.mark.parametrize("f32", [False, True])
 def test_backward(moe, T, K, f32):
     backward(moe, Case(T, K, f32, p=0.1, masked=T > 2, seed=6))
+
+
+@pytest.mark.parametrize("T,K,f32", [(3000, 1024, False), (4000, 768, True), (2500, 1536, False)])
+def test_backward_of_many_narrow_rows(moe, T, K, f32):
+    """More than four blocks on an SM."""
+    backward(moe, Case(T, K, f32, p=0.1, masked=True, seed=15))
 
 
 @pytest.mark.parametrize("use", [("d_residual",), ("d_x",), ("d_weight",), ("d_stream", "d_x"), ("d_stream", "d_residual")])
