@@ -77,17 +77,38 @@ struct UpSmem {
 
 // Equal shares of the tiles' blocks for the CTAs of a chunk.  Up to as many tiles as CTAs: `parts` CTAs a
 // tile, a piece of one tile each, as every further piece costs a CTA the latency of its first loads (64
-// tokens over 100 adapters: 3.2 us of loads for two pieces, 1.6 for one).  More tiles: whole ones in turn.
+// tokens over 100 adapters: 3.2 us of loads for two pieces, 1.6 for one).  More tiles: whole ones in turn, or
+// up to four pieces of each where that fills the last turn better; a block of 32 takes a CTA about 2.3 ns a
+// rank, and a piece 1500 ns more (500 rows over 150 adapters of rank 64, 4096 -> 4096: 102 us in whole tiles,
+// 86; 2000 rows of 100 requests over 8 of rank 16 39 and 35).
 constexpr int kPieces = 32;
 struct Share {
   int tiles, blocks, parts, cta, ctas;
-  MOE_DEV Share(int tiles, int blocks, int most, int cta, int ctas)
-      : tiles(tiles), blocks(blocks), parts(tiles ? max(1, min(min(most, blocks), ctas / tiles)) : 1), cta(cta), ctas(ctas) {}
-  // The n-th tile of this CTA, and its blocks of it.
-  MOE_DEV bool get(int n, int& tile, int& b0, int& b1) const {
-    const int part = parts > 1 ? cta % parts : 0;
-    tile = parts > 1 ? cta / parts : cta + n * ctas;
-    if (tile >= tiles || (parts > 1 && n > 0)) return false;
+  MOE_DEV Share(int tiles, int blocks, int most, int r, int cta, int ctas) : tiles(tiles), blocks(blocks), parts(1), cta(cta), ctas(ctas) {
+    if (tiles <= ctas) {
+      if (tiles) parts = max(1, min(min(most, blocks), ctas / tiles));
+      return;
+    }
+    // in integers, as both kernels have to find the same; `parts` pieces where they save 4 per cent
+    const int tile = 23 * min(blocks, 4096) / 10 * r, whole = tiles / ctas, rest = tiles - whole * ctas;
+    int least = (whole + (rest > 0)) * ((tile + 1500) / 25 * 24);
+#pragma unroll
+    for (int n = 2; n <= 4; ++n) {
+      if (n > most || n > blocks || n > ctas) break;
+      const int turns = n * whole + (n * rest > 0) + (n * rest > ctas) + (n * rest > 2 * ctas) + (n * rest > 3 * ctas);
+      const int time = turns * (tile / n + 1500);
+      if (time < least) {
+        least = time;
+        parts = n;
+      }
+    }
+  }
+  // The n-th piece of this CTA: its tile, its number among the tile's, and its blocks.
+  MOE_DEV bool get(int n, int& tile, int& part, int& b0, int& b1) const {
+    const int i = cta + n * ctas;
+    if (i >= tiles * parts) return false;
+    tile = parts > 1 ? i / parts : i;
+    part = i - tile * parts;
     b0 = (int)((int64_t)blocks * part / parts);
     b1 = (int)((int64_t)blocks * (part + 1) / parts);
     return true;
@@ -263,16 +284,17 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_down_kernel(Adapter p
   make_tables(p, sm.t, row0, rows, blockIdx.x == 0);
 
   const int nk = (p.K + 31) / 32;
-  const Share share(sm.t.tiles, nk, kPieces, cta, ctas);
+  const Share share(sm.t.tiles, nk, kPieces, p.r, cta, ctas);
   const int groups = (p.r + 8 * NJ - 1) / (8 * NJ);
   const int slices = kWarps / groups, rg = warp % groups, slice = warp / groups, rp = groups * 8 * NJ;
   const uint16_t* x = static_cast<const uint16_t*>(p.x);
-  int t, k0, k1;
-  for (int turn = 0; share.get(turn, t, k0, k1); ++turn) {
-    int t1, l0, l1;
-    if (share.get(turn + 1, t1, l0, l1)) {  // the next tile's A on its way into L2 meanwhile
+  int t, part, k0, k1;
+  for (int turn = 0; share.get(turn, t, part, k0, k1); ++turn) {
+    int t1, part1, l0, l1;
+    if (share.get(turn + 1, t1, part1, l0, l1)) {  // the next piece's A on its way into L2 meanwhile
       const char* A = reinterpret_cast<const char*>(static_cast<const uint16_t*>(p.a) + (int64_t)sm.t.id[sm.t.leader[t1]] * p.r * p.K);
-      for (int64_t i = (int64_t)tid * 128; i < (int64_t)p.r * p.K * 2; i += kThreads * 128) prefetch_l2(A + i);
+      const int first = l0 * 64, bytes = min(l1 * 64, p.K * 2) - first, lines = (bytes + 127) / 128;
+      for (int i = tid; i < p.r * lines; i += kThreads) prefetch_l2(A + (int64_t)(i / lines) * p.K * 2 + first + i % lines * 128);
     }
     const int id = tile_rows(sm.t, t);
     const uint16_t* A = static_cast<const uint16_t*>(p.a) + (int64_t)id * p.r * p.K;
@@ -312,8 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_few_down_kernel(Adapter p
       }
     }
     __syncthreads();
-    const int piece = share.parts > 1 ? cta % share.parts : 0;
-    float* v = p.v + ((int64_t)piece * p.M + row0) * p.r;
+    float* v = p.v + ((int64_t)part * p.M + row0) * p.r;
     for (int i = tid; i < kTile * rp / 2; i += kThreads) {  // two ranks each
       const int m = sm.t.rows[2 * i / rp], k = 2 * i % rp;
       float2 s = make_float2(0.f, 0.f);
@@ -498,11 +519,11 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
   // The first kernel lets this one start when all before it is complete: what is not v can be read and
   // written already.
   make_tables(p, sm.t, row0, rows, false);
-  const int nk = (p.K + 31) / 32, nb = (p.N + 31) / 32, pieces = Share(sm.t.tiles, nk, kPieces, 0, ctas).parts;
+  const int nk = (p.K + 31) / 32, nb = (p.N + 31) / 32, pieces = Share(sm.t.tiles, nk, kPieces, p.r, 0, ctas).parts;
   const int lr = p.r <= 32 ? 5 : p.r <= 64 ? 6 : 7, steps = (p.r + 15) / 16;
-  const Share share(sm.t.tiles, nb, nb, cta, ctas);
+  const Share share(sm.t.tiles, nb, nb, p.r, cta, ctas);
   float scale = 1.f;
-  int t, b0, b1;
+  int t, part, b0, b1;
   // A tile's rows; its scale, and its part of B and of its rows of base on their way: what each thread
   // reads first into shared memory, the rest into L2.
   const auto begin = [&] {
@@ -540,7 +561,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
     }
     return id;
   };
-  int id = share.get(0, t, b0, b1) ? begin() : 0;
+  int id = share.get(0, t, part, b0, b1) ? begin() : 0;
   // rows of requests without an adapter: base as it is
   if (p.base != p.out) {
     const int units = p.N / 8 * (F32 ? 2 : 1);
@@ -553,7 +574,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
   }
   moe::wait_for_stream();
   moe::let_next_start();
-  for (int turn = 0; share.get(turn, t, b0, b1); ++turn) {
+  for (int turn = 0; share.get(turn, t, part, b0, b1); ++turn) {
     if (turn > 0) id = begin();
     if (sm.t.rows[kFewest] < 0) {
       few_rows<F32>(p, sm, id, row0, b0 * 32, min(b1 * 32, p.N), pieces, lr, scale);

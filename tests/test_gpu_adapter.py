@@ -172,6 +172,16 @@ def test_same_bits_twice(moe):
         assert torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
 
 
+@pytest.mark.parametrize("M,L,r,N,K", [(256, 256, 16, 264, 4104), (500, 150, 64, 520, 2056), (700, 30, 32, 4096, 4096)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_more_tiles_than_ctas(moe, M, L, r, N, K, f32):
+    """Whole tiles in turn, and pieces of them; the rows of the first case have an adapter each."""
+    offsets, ad = decode(M, L)
+    c = Case(M, N, K, r, L, offsets, ad if L < M else list(range(L)), f32=f32, seed=21)
+    c.run(moe, plan="few")
+    c.check()
+
+
 def test_adapters_that_are_not_finite_stay_with_their_requests(moe):
     for offsets, ad, plan in (([0, 1, 2, 3, 4], [0, 1, 0, 2], "few"), ([0, 3, 4, 130, 140], [0, 1, 2, 1], "few"),
                               ([0, 100, 230, 20000, 20070], [0, 1, 0, 2], "long")):
