@@ -403,24 +403,39 @@ __device__ __forceinline__ void sum_pieces(const Adapter& p, UpSmem<F32>& sm, in
 // A tile of up to kFewest rows, without the tensor cores: a lane has two neighbouring features at a time,
 // whose weights it reads whole, and multiplies them with v in fp32.  Most of a tile of sixteen rows would
 // be empty, and what an MMA wants around it is five times the instructions (64 tokens over 100 adapters:
-// 0.9 us for 32 features of each warp).  16 bytes of B are number 2 (pair * rank / 8 + rank) + feature of
-// the thread's.
-template <bool F32>
+// 0.9 us for 32 features of each warp).  Where the features leave most threads without any, four or eight lanes
+// share two of them, every eight ranks another lane (one row of rank 128, 928 -> 4104: 9.9 us without, 7.5; with
+// ranks below 64, or two lanes a pair, no gain: 6.2 and 6.4 for rank 16, 10.3 and 11.4 for 8 rows of rank 64).  16 bytes of B are number 2 (pair * eights + eight) +
+// feature of the thread's.
+template <bool SHARED>
+struct Lanes {
+  int log, first, step;  // of a pair of features; this thread's first feature, and how far its next one is
+  MOE_DEV Lanes(int n0, int n1, int r) {
+    const int pairs = (n1 - n0) / 2;
+    log = !SHARED || r < 64 ? 0 : pairs <= kUpThreads / 8 ? 3 : pairs <= kUpThreads / 4 ? 2 : 0;
+    first = n0 + 2 * ((int)threadIdx.x >> log);
+    step = 2 * (kUpThreads >> log);
+  }
+  MOE_DEV int rank() const { return SHARED ? ((int)threadIdx.x & ((1 << log) - 1)) * 8 : 0; }
+};
+
+template <bool F32, bool SHARED>
 __device__ __forceinline__ void fetch_few(const Adapter& p, UpSmem<F32>& sm, int id, int64_t row0, int n0, int n1) {
   constexpr int kSize = F32 ? 8 : 4, kAhead = UpSmem<F32>::kAhead;  // bytes of a pair of base
   const uint16_t* B = static_cast<const uint16_t*>(p.b) + (int64_t)id * p.N * p.r;
-  int n = n0 + 2 * (int)threadIdx.x;
-  for (int i = 0, k = 0; i < kAhead && n < n1; i += 2) {
-    cpa::cp_async16(tc::smem_addr(sm.place(sm.b, i, 16)), B + (int64_t)n * p.r + k);
-    cpa::cp_async16(tc::smem_addr(sm.place(sm.b, i + 1, 16)), B + (int64_t)(n + 1) * p.r + k);
-    if ((k += 8) == p.r) {
-      k = 0;
-      n += 2 * kUpThreads;
+  const Lanes<SHARED> lanes(n0, n1, p.r);
+  for (int i = 0, k = lanes.rank(), n = lanes.first; i < kAhead && n < n1; i += 2) {
+    if (k < p.r) {
+      cpa::cp_async16(tc::smem_addr(sm.place(sm.b, i, 16)), B + (int64_t)n * p.r + k);
+      cpa::cp_async16(tc::smem_addr(sm.place(sm.b, i + 1, 16)), B + (int64_t)(n + 1) * p.r + k);
+    }
+    if ((k += 8 << lanes.log) >= p.r) {
+      k = lanes.rank();
+      n += lanes.step;
     }
   }
-  if (!p.base) return;
-  n = n0 + 2 * (int)threadIdx.x;
-  for (int u = 0; u < 2 && n < n1; ++u, n += 2 * kUpThreads)
+  if (!p.base || lanes.rank() > 0) return;  // the first lane stores the sums
+  for (int u = 0, n = lanes.first; u < 2 && n < n1; ++u, n += lanes.step)
     for (int j = 0; j < kFewest; ++j) {
       const int m = sm.t.rows[j];
       if (m < 0) break;
@@ -431,7 +446,7 @@ __device__ __forceinline__ void fetch_few(const Adapter& p, UpSmem<F32>& sm, int
     }
 }
 
-template <bool F32>
+template <bool F32, bool SHARED>
 __device__ __forceinline__ void few_rows(const Adapter& p, UpSmem<F32>& sm, int id, int64_t row0, int n0, int n1, int pieces, int lr,
                                          float scale) {
   constexpr int kAhead = UpSmem<F32>::kAhead;
@@ -457,11 +472,13 @@ __device__ __forceinline__ void few_rows(const Adapter& p, UpSmem<F32>& sm, int 
 #pragma unroll
   for (int j = 0; j < kFewest; ++j) rows += sm.t.rows[j] >= 0;
   const uint16_t* B = static_cast<const uint16_t*>(p.b) + (int64_t)id * p.N * p.r;
-  for (int n = n0 + 2 * tid, u = 0, i = 0; n < n1; n += 2 * kUpThreads, ++u) {
+  const Lanes<SHARED> lanes(n0, n1, p.r);
+  const unsigned together = ((1u << (1 << lanes.log)) - 1) << (tid & 31 & -(1 << lanes.log));
+  for (int n = lanes.first, u = 0, i = 0; n < n1; n += lanes.step, ++u) {
     float d[kFewest][2];
 #pragma unroll
     for (int j = 0; j < kFewest; ++j) d[j][0] = d[j][1] = 0.f;
-    for (int k = 0; k < p.r; k += 8, i += 2) {
+    for (int k = lanes.rank(); k < p.r; k += 8 << lanes.log, i += 2) {
       uint4 w[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -484,6 +501,14 @@ __device__ __forceinline__ void few_rows(const Adapter& p, UpSmem<F32>& sm, int 
         }
       }
     }
+    for (int o = 1; SHARED && o < 1 << lanes.log; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < kFewest; ++j) {
+        if (j >= rows) break;
+        d[j][0] += __shfl_xor_sync(together, d[j][0], o);
+        d[j][1] += __shfl_xor_sync(together, d[j][1], o);
+      }
+    if (lanes.rank() > 0) continue;
 #pragma unroll
     for (int j = 0; j < kFewest; ++j) {
       if (j >= rows) break;
@@ -530,7 +555,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
     const int id = tile_rows(sm.t, t), wide = min(b1 * 32, p.N) - b0 * 32;
     if (p.scale) scale = p.scale[id];
     if (sm.t.rows[kFewest] < 0) {
-      fetch_few<F32>(p, sm, id, row0, b0 * 32, min(b1 * 32, p.N));
+      fetch_few<F32, !WHOLE>(p, sm, id, row0, b0 * 32, min(b1 * 32, p.N));
     } else {
       // a step of 16 ranks of a block of 32 features is number (block * steps + step) of the warp's
       const uint16_t* B = static_cast<const uint16_t*>(p.b) + ((int64_t)id * p.N + 8 * (g >> 1) + (g & 1)) * p.r + q * 4;
@@ -577,7 +602,7 @@ __global__ void __launch_bounds__(kUpThreads, 2) adapter_few_up_kernel(Adapter p
   for (int turn = 0; share.get(turn, t, part, b0, b1); ++turn) {
     if (turn > 0) id = begin();
     if (sm.t.rows[kFewest] < 0) {
-      few_rows<F32>(p, sm, id, row0, b0 * 32, min(b1 * 32, p.N), pieces, lr, scale);
+      few_rows<F32, !WHOLE>(p, sm, id, row0, b0 * 32, min(b1 * 32, p.N), pieces, lr, scale);
       continue;
     }
     sum_pieces<kParts>(p, sm, row0, pieces, lr, scale);
