@@ -16,10 +16,10 @@
 //         at a time; base comes in boxes of 128 bytes x 128 rows, six ahead, in which the epilogue warps add
 //         the accumulator and from which they store whole lines of the request's rows.
 // Every wait is bounded; one that runs out sets MOE_ERR_TIMEOUT and all roles leave their loops.
-// Measured (replayed graphs): 58879 rows of 16 requests of rank 64, 2880 -> 2880, 190 us for 1022 MB: down 62 (5.6
-// TB/s), up 121 (6.0 TB/s; a copy moves 6.8); 8192 rows of rank 32, 7168 -> 4096, 56 us: 25 (4.7 TB/s) and 33, of
-// which 8 are the kernel's start, the first v and the last stores.  The kernels follow one another, as each
-// fills an SM's shared memory; the next launch is set up meanwhile.
+// Measured (replayed graphs): 58879 rows of 16 requests of rank 64, 2880 -> 2880, 187 us for 1022 MB: down 62 (5.6
+// TB/s), up 119 (6.1 TB/s; a copy moves 6.8); 8192 rows of rank 32, 7168 -> 4096, 54 us: 25 (4.7 TB/s) and 31, of
+// which 6 are the first v and the last stores.  The kernels follow one another on an SM, as each fills its
+// shared memory; what is not v of the second one starts where the first has left (56 us with a wait for all).
 #include <algorithm>
 
 #include "dense_common.cuh"
@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     tc::tmem_alloc(&taddr_s, kAccs * kFeat);
     tc::tmem_relinquish();
   }
-  moe::wait_for_stream();
+  // The first kernel lets this one start when all before it is complete: only v is waited for, by the
+  // warps that read it (of every CTA, so that this kernel never ends before the first).
   moe::let_next_start();
   if (warp == 2) make_tables(p, tab, p.base != p.out, false);
   tc::tc_fence_before();
@@ -536,6 +537,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     __syncwarp();
   } else if (warp >= 4 && warp < 8) {
     // v of a tile: the pieces' sum times the adapter's scale, as bf16 numbers
+    moe::wait_for_stream();
     const int row = tid - 128, nk = (p.K + 63) / 64, own = t.own[p.R], ctas = down_ctas(own, nk, down_grid, p.r);
     const int64_t total = (int64_t)own * nk;
     const int per = p.r / 4;
