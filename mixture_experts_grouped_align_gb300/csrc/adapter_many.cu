@@ -714,14 +714,15 @@ bool adapter_many_can(int64_t M, int R) { return M >= 256 && R <= kRequestsMost;
 
 // The estimated time against that of the kernels for few rows, in ns: a tile costs about the same whatever
 // it has of rows, since its adapter's B comes once for it, and a request ends with a tile that is not full
-// (0.8 of a tile a request in the fit); the others' time goes by the rows and the rank.  Times measured at
-// both (us, tiles of 128 rows first): 4096 -> 4096 of rank 16: 1000 rows of 16 requests 18.0 and 18.0, of
-// 100 48.6 and 21.8, 2000 of 60 35.3 and 32.7, 512 of 8 15.6 and 12.6; 2880 -> 2880 of rank 64: 1000 of 16
-// 21.3 and 29.0, 4096 of 128 53.8 and 102, of 400 125 and 107.
+// (0.62 of a tile a request in the fit, over 21 sizes: the slower was chosen in four, by 5% at most); the
+// others' time goes by the rows and the rank.  Times measured at both (us, tiles of 128 rows first): 4096 -> 4096
+// of rank 16: 1000 rows of 16 requests 17.1 and 15.6, of 100 46.7 and 18.1, 2000 of 60 33.1 and 29.2, 512 of 8
+// 14.1 and 11.6; 2880 -> 2880 of rank 64: 1000 of 16 19.7 and 23.9, 4096 of 128 51 and 101, of 400 123 and 103;
+// 520 -> 256 of rank 16: 8000 of 100 17 and 26.
 bool adapter_many_takes(int64_t M, int R, int r, int N, int K) {
   if (!adapter_many_can(M, R)) return false;
   const double size = ((double)N + K) / 8192;
-  const double many = 12000 + 70.0 * r + 360 * (M / 128.0 + 0.8 * R) * size, few = 8500 + M * (6 + 0.375 * r) * size;
+  const double many = 9300 + 92.0 * r + 480 * (M / 128.0 + 0.62 * R) * size, few = 5100 + M * (1.1 + (6.2 + 0.38 * r) * size);
   return many < few;
 }
 
