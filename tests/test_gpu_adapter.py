@@ -308,3 +308,26 @@ def test_long_prompts_under_load(moe, R, r, f32):
         assert int(status[0]) == 0
         for o in outs:
             assert torch.equal(o, c.out)
+
+
+def test_calls_at_once(moe):
+    """Calls of both kinds on two streams at once, each with a workspace of its own: the bits of a call alone."""
+    cases = [Case(6000, 1032, 520, 32, 4, lengths(2500, 0, 1500, 2000), [2, 1, -1, 0], seed=31),
+             Case(6000, 520, 1032, 64, 4, lengths(3000, 3000), [1, 3], f32=True, seed=32),
+             Case(300, 4096, 2056, 16, 40, *decode(300, 40), seed=33), Case(64, 2880, 2880, 128, 9, *decode(64, 9), f32=True, seed=34)]
+    for c, plan in zip(cases, ("long", "long", "few", "few")):
+        assert c.run(moe, plan=plan) == 0
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    calls, status = [], torch.zeros(4, dtype=torch.int32, device="cuda")
+    for i in range(24):
+        c, s = cases[(i // 2 + (i % 2) * 2) % 4], streams[i % 2]  # another case on the other stream
+        ws = torch.empty(moe.moe_adapter_gemm_workspace_size(c.M, c.R, c.r), dtype=torch.uint8, device="cuda")
+        calls.append((c, torch.full_like(c.out, float("nan")), i32(c.offsets), i32(c.adapter),
+                      moe.Ctx(stream=s, workspace=ws, dev_status=status)))
+    torch.cuda.synchronize()
+    for c, out, off, ids, ctx in calls:
+        moe.moe_adapter_gemm(c.x, c.a, c.b, c.scale, off, ids, c.base, c.M, c.N, c.K, c.r, c.L, c.R, out, ctx)
+    torch.cuda.synchronize()
+    assert int(status[0]) == 0
+    for c, out, *_ in calls:
+        assert torch.equal(out, c.out)

@@ -352,3 +352,38 @@ def test_captured_calls_draw_by_the_state_in_memory(moe):
         step(moe.Ctx(workspace=ws))
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (st, o, dr, dx, dw)))
+
+
+def test_calls_at_once(moe):
+    """Forward and backward passes on two streams at once, each with a workspace of its own."""
+    cases = [Case(900, 7168, p=0.1, masked=True, quant="mx", seed=41), Case(2500, 1536, True, p=0.25, quant="row", seed=42)]
+    alone = []
+
+    def outputs(c):
+        T, K = c.T, c.K
+        st, dr = (nans((T, K), c.res.dtype) for _ in range(2))
+        o, dx = (nans((T, K), torch.bfloat16) for _ in range(2))
+        codes = torch.empty((T, K), dtype=torch.uint8, device="cuda")
+        scales = torch.empty((T, K // 32), dtype=torch.uint8, device="cuda") if c.quant == "mx" else nans((T,), torch.float32)
+        ws = torch.full((moe.moe_residual_norm_workspace_size(K),), 0xFF, dtype=torch.uint8, device="cuda")
+        return st, o, codes, scales, dr, dx, nans((K,), torch.float32), ws
+
+    def run(c, b, stream):
+        st, o, codes, scales, dr, dx, dw, ws = b
+        ctx = moe.Ctx(stream=stream, workspace=ws)
+        moe.moe_residual_norm(c.x, c.res, c.mask, c.w, c.T, c.K, EPS, c.p, c.rng, STREAM_ID, st, o, codes, scales, ctx)
+        moe.moe_residual_norm_backward(c.x, None, st, c.mask, c.w, c.T, c.K, EPS, c.p, c.rng, STREAM_ID, dr, dx, dw, ctx)
+
+    for c in cases:
+        alone.append(outputs(c))
+        run(c, alone[-1], torch.cuda.current_stream())
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    many = [(i % 2, outputs(cases[i % 2])) for i in range(12)]
+    torch.cuda.synchronize()
+    for i, b in many:
+        run(cases[i], b, streams[i])
+    torch.cuda.synchronize()
+    for i, b in many:
+        for got, want in zip(b[:-1], alone[i][:-1]):
+            assert torch.equal(got, want)
