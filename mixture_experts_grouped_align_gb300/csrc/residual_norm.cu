@@ -212,13 +212,38 @@ constexpr float kRowScaleMin = 0x1p-120f;
 struct RowCodes {
   float scale, first, by;
 };
-// The scale of a row whose largest |s w| is `top`.  Its codes are those of s w 448 / top, which is
-// n 448 / max |n| without r's rounding, or of n 2^120 where the scale is the smallest.
+// Below this 448 / max |s w| may be infinite, and the products s w lose bits (or all of them).
+constexpr float kTopMin = 0x1p-119f;
+// The scale of a row whose largest |s w| is `top`, kTopMin at least.  Its codes are those of s w 448 / top,
+// which is n 448 / max |n| without r's rounding, or of n 2^120 where the scale is the smallest.
 MOE_DEV RowCodes row_codes(float top, float r) {
   const float most = top * r, nan = __uint_as_float(0x7fc00000u);
   if (!(most <= 3.4028235e38f)) return RowCodes{nan, 1.f, nan};  // an infinity, too, leaves NaN in its row
   if (most / 448.f < kRowScaleMin) return RowCodes{kRowScaleMin, r, 1.f / kRowScaleMin};
   return RowCodes{most / 448.f, 1.f, 448.f / top};
+}
+// The same from the largest |n|, for smaller rows: of n 448 / most, at most n 2^120.
+MOE_DEV RowCodes small_row_codes(float most, float r) {
+  if (most / 448.f < kRowScaleMin) return RowCodes{kRowScaleMin, r, 1.f / kRowScaleMin};
+  return RowCodes{most / 448.f, r, 448.f / most};
+}
+// How the row of s becomes codes.  Small rows (those of zeros among them) go over their products again, so all
+// threads of a row call, and of a warp; `red`: as reduce_pair's, this thread's last use of it is over.
+template <typename M>
+MOE_DEV RowCodes codes_of(const float (&s)[M::kV][8], const uint4 (&w)[M::kV], float top, float r, float2* red) {
+  const bool small = top < kTopMin;
+  if (!(M::kWide ? small : __any_sync(kAll, small))) return row_codes(top, r);
+  float none = 0.f, most = 0.f;
+#pragma unroll
+  for (int t = 0; t < M::kV; ++t) {
+    float f[8];
+    unpack8(w[t], f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = __uint_as_float(max(__float_as_uint(most), __float_as_uint(s[t][i] * r * f[i]) & 0x7fffffffu));
+  }
+  if (M::kWide) __syncthreads();  // the first sums have been read
+  reduce_pair<M, true>(none, most, red);
+  return small ? small_row_codes(most, r) : row_codes(top, r);
 }
 
 // The outputs of eight values s of unit u (c: its unit in the row); every lane calls.
@@ -296,7 +321,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_kernel(ResidualNorm p)
   const float r = inverse_rms(sum, 1.f / (float)p.K, p.eps);
   RowCodes rc{};
   if (QUANT == 2) {
-    rc = row_codes(top, r);
+    rc = codes_of<M>(s, w, top, r, red);
     if (in && M::col() == 0) static_cast<float*>(p.scales)[row] = rc.scale;
   }
 #pragma unroll
@@ -598,7 +623,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_walk_kernel(ResidualNo
     const float r = inverse_rms(sum, inv_k, p.eps);
     RowCodes rc{};
     if (QUANT == 2) {
-      rc = row_codes(top, r);
+      rc = codes_of<M>(s, w, top, r, red[turn]);
       if (in && M::col() == 0) static_cast<float*>(p.scales)[row] = rc.scale;
     }
 #pragma unroll
