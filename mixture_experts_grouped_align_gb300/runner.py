@@ -21,6 +21,7 @@ import torch
 from . import (Ctx, MoeError, moe_act_checkpoint, moe_adapter_gemm, moe_adapter_gemm_workspace_size, moe_align,
                moe_align_capacity, moe_bucket, moe_bucket_pad, moe_dense_gemm, moe_forward, moe_forward_workspace_size,
                moe_residual_norm)
+from .train import _apart, _check
 
 BLOCK_M = 128
 
@@ -162,7 +163,10 @@ class ServeBlock:
     norm_w [K], wr [E, K], ws1 [2Is, K], bs1 [2Is], ws2 [K, Is], bs2 [K]: bf16; ``shared`` = (ws1, bs1, ws2,
     bs2) or None.  ``adapters``: a pair (for ws1 and for ws2; either may be None) of (a [L, r, in], b [L, out, r]
     bf16, scale [L] fp32 or None): low-rank adapters, of which each request of a batch names one.  The stream is
-    bf16, or fp32 (``stream_f32``).  Up to ``max_requests`` requests a batch."""
+    bf16, or fp32 (``stream_f32``).  Up to ``max_requests`` requests a batch.
+
+    Weights are checked when the block is made, and a step's operands before anything is launched (MoeError):
+    type, size, density, alignment and device, and that what is written lies apart from what is still read."""
 
     def __init__(self, layer, norm_w, wr, shared=None, adapters=(None, None), eps=1e-5, stream_f32=False, max_requests=512):
         bf, dev = torch.bfloat16, norm_w.device
@@ -170,6 +174,8 @@ class ServeBlock:
         T, K, E = layer.max_rows, layer.K, layer.E
         if tuple(norm_w.shape) != (K,) or tuple(wr.shape) != (E, K):
             raise MoeError(-1, f"need norm_w [{K}] and wr [{E}, {K}], got {tuple(norm_w.shape)} and {tuple(wr.shape)}")
+        for what, t in (("norm_w", norm_w), ("wr", wr)):
+            _check(t, what, bf, layer.status.device, t.shape)
         if any(adapters) and shared is None:
             raise MoeError(-1, "adapters need a shared expert")
         new = lambda *s, dtype=bf: torch.empty(s, dtype=dtype, device=dev)  # noqa: E731
@@ -184,12 +190,18 @@ class ServeBlock:
             Is = self.Is = ws2.shape[1]
             if tuple(ws1.shape) != (2 * Is, K) or ws2.shape[0] != K:
                 raise MoeError(-1, f"need ws1 [{2 * Is}, {K}] and ws2 [{K}, {Is}], got {tuple(ws1.shape)} and {tuple(ws2.shape)}")
+            for what, t, n in (("ws1", ws1, 2 * Is * K), ("bs1", bs1, 2 * Is), ("ws2", ws2, K * Is), ("bs2", bs2, K)):
+                _check(t, what, bf, dev, numel=n)
             for pair, (n_in, n_out) in zip(adapters, ((K, 2 * Is), (Is, K))):
                 if pair is None:
                     continue
                 a, b = pair[:2]
                 if a.dim() != 3 or a.shape[2] != n_in or tuple(b.shape) != (a.shape[0], n_out, a.shape[1]):
                     raise MoeError(-1, f"adapters: need a [L, r, {n_in}] and b [L, {n_out}, r], got {tuple(a.shape)} and {tuple(b.shape)}")
+                _check(a, "adapters' a", bf, dev, a.shape)
+                _check(b, "adapters' b", bf, dev, b.shape)
+                if len(pair) > 2 and pair[2] is not None:
+                    _check(pair[2], "adapters' scale", torch.float32, dev, numel=a.shape[0])
                 ranks.append(a.shape[1])
             self.hs = new(T, Is)
             if adapters[0] is not None:  # added before the activation, so the pre-activations are kept
@@ -207,6 +219,23 @@ class ServeBlock:
         moe_adapter_gemm(x, a, b, scale, row_offsets, adapter, out, T, n_out, n_in, a.shape[1], a.shape[0], adapter.shape[0], out,
                          ctx)
 
+    def _check_step(self, branch, residual, T, y, row_offsets, adapter):
+        dev, n, i32 = self.norm_w.device, T * self.layer.K, torch.int32
+        _check(y, "y", torch.bfloat16, dev, numel=n)
+        if branch is not None:
+            _check(branch, "branch", torch.bfloat16, dev, numel=n)
+        if residual is not None:
+            _check(residual, "residual", self.stream.dtype, dev, numel=n)
+        if adapter is not None:
+            _check(adapter, "adapter", i32, dev, (adapter.shape[0],))
+            _check(row_offsets, "row_offsets", i32, dev, numel=adapter.shape[0] + 1)
+        # the norm may write its rows over the branch's and the stream over the residual, at the same place
+        for t, what, own, same in ((y, "y", self.stream, False), (y, "y", self.normed, False), (branch, "branch", self.stream, False),
+                                   (branch, "branch", self.normed, True), (residual, "residual", self.stream, True),
+                                   (residual, "residual", self.normed, False)):
+            if t is not None and not (same and t.data_ptr() == own.data_ptr()):
+                _apart(t, own, f"{what} and the block's rows")
+
     def step(self, branch, residual, T, y, row_offsets=None, adapter=None):
         """branch [T, K] bf16 or None, residual [T, K] in the stream's type -> y [T, K] bf16 and the stream
         [T, K] (the block's own, until its next step).  With adapters: row_offsets [R + 1] and adapter [R] int32 on
@@ -217,6 +246,8 @@ class ServeBlock:
         adapt = adapter is not None and adapter.shape[0] > 0
         if adapt and adapter.shape[0] > self.max_requests:
             raise MoeError(-3, f"{adapter.shape[0]} requests, the block was made for up to {self.max_requests}")
+        if T > 0:
+            self._check_step(branch, residual, T, y, row_offsets, adapter if adapt and any(self.adapters) else None)
         ctx = Ctx(workspace=self.workspace, dev_status=self.status)
         moe_residual_norm(branch, residual, None, self.norm_w, T, K, self.eps, 0.0, None, 0, self.stream, self.normed, self.codes,
                           self.scales, ctx)
