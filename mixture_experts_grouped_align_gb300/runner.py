@@ -162,8 +162,9 @@ class ServeBlock:
 
     norm_w [K], wr [E, K], ws1 [2Is, K], bs1 [2Is], ws2 [K, Is], bs2 [K]: bf16; ``shared`` = (ws1, bs1, ws2,
     bs2) or None.  ``adapters``: a pair (for ws1 and for ws2; either may be None) of (a [L, r, in], b [L, out, r]
-    bf16, scale [L] fp32 or None): low-rank adapters, of which each request of a batch names one.  The stream is
-    bf16, or fp32 (``stream_f32``).  Up to ``max_requests`` requests a batch.
+    bf16, scale [L] fp32 or None): low-rank adapters, of which each request of a batch names one.  Is is a
+    multiple of 8, with adapters for ws1 of 32.  The stream is bf16, or fp32 (``stream_f32``).  Up to
+    ``max_requests`` requests a batch.
 
     Weights are checked when the block is made, and a step's operands before anything is launched (MoeError):
     type, size, density, alignment and device, and that what is written lies apart from what is still read."""
@@ -203,6 +204,8 @@ class ServeBlock:
                 if len(pair) > 2 and pair[2] is not None:
                     _check(pair[2], "adapters' scale", torch.float32, dev, numel=a.shape[0])
                 ranks.append(a.shape[1])
+            if adapters[0] is not None and Is % 32:  # refused by moe_act_checkpoint, at the first batch with an adapter
+                raise MoeError(-2, f"adapters for ws1 need a shared width that is a multiple of 32, got {Is}")
             self.hs = new(T, Is)
             if adapters[0] is not None:  # added before the activation, so the pre-activations are kept
                 self.gs = new(T, 2 * Is)

@@ -81,3 +81,14 @@ def test_shared_weights_and_adapters_that_do_not_fit():
     for what, pair in (("a: need", (a.float(), b, scale)), ("b: need", (a, b.to("meta"), scale)), ("scale: need", (a, b, scale[:2])),
                        ("scale: need", (a, b, scale.double()))):
         refused(what, ServeBlock, **{**p, "adapters": (pair, None)})
+
+
+def test_shared_width_with_adapters_before_the_activation():
+    """The pre-activations with adapters in them pass through moe_act_checkpoint, whose rows are multiples of 32."""
+    from mixture_experts_grouped_align_gb300.runner import ServeBlock
+    p = parts()
+    n = 40
+    shared = (z(2 * n, K), z(2 * n), z(K, n), z(K))
+    refused("multiple of 32", ServeBlock, **{**p, "shared": shared, "adapters": ((z(3, 8, K), z(3, 2 * n, 8), None), None)})
+    for adapters in ((None, None), (None, (z(3, 8, n), z(3, K, 8), None))):  # neither needs it
+        assert ServeBlock(**{**p, "shared": shared, "adapters": adapters}).Is == n
