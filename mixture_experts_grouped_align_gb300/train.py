@@ -300,8 +300,8 @@ class TrainBlock:
 
     def forward(self, branch, residual, y, token_mask=None):
         """branch [T, K] bf16 or None (the first block), residual [T, K] in the stream's type -> y [T, K]
-        bf16 and the stream [T, K] (the block's own, until its next forward).  Rows with a mask of 0 enter
-        the layer as zeros."""
+        bf16 (it may be branch) and the stream [T, K] (the block's own, until its next forward; residual may
+        be the one of the last).  Rows with a mask of 0 enter the layer as zeros."""
         K, bf = self.layer.K, torch.bfloat16
         self._check_own()
         if not isinstance(residual, torch.Tensor) or residual.dim() != 2:
@@ -313,10 +313,15 @@ class TrainBlock:
         if branch is not None:
             self._rows(branch, "branch", bf, T)
             _apart(branch, self.normed, "branch and the block's rows")
+            _apart(branch, self.stream, "branch and the block's stream")
+        _apart(residual, self.normed, "residual and the block's rows")
+        if residual.data_ptr() != self.stream.data_ptr():
+            _apart(residual, self.stream, "residual and the block's stream")
         if token_mask is not None:
             _check(token_mask, "token_mask", torch.uint8, self.layer.wr.device, numel=T)
         self._rows(y, "y", bf, T)
         _apart(y, self.normed, "y and the block's rows")
+        _apart(y, self.stream, "y and the block's stream")  # backward has the norm from it again
         stream, normed = self.stream[:T], self.normed[:T]
         moe_residual_norm(branch, residual, token_mask, self.norm_w, T, K, self.eps, self.dropout if branch is not None else 0.0,
                           self.rng, self.rng_stream, stream, normed, None, None, self._ctx())
@@ -336,11 +341,17 @@ class TrainBlock:
         if d_stream is not None:
             self._rows(d_stream, "d_stream", self.stream.dtype, T)
         self._rows(d_residual, "d_residual", self.stream.dtype, T)
+        _apart(d_residual, self.stream, "d_residual and the block's stream")
+        if d_stream is not None and d_residual.data_ptr() != d_stream.data_ptr():
+            _apart(d_residual, d_stream, "d_residual and d_stream")
         if d_branch is None and self.dropped:
             raise MoeError(-1, "d_branch: the forward had a branch")
         if d_branch is not None:
             self._rows(d_branch, "d_branch", bf, T)
             _apart(d_branch, d_residual, "d_branch and d_residual")
+            _apart(d_branch, self.stream, "d_branch and the block's stream")
+            if d_stream is not None:
+                _apart(d_branch, d_stream, "d_branch and d_stream")
         d_normed = self.layer.scratch.view("d_normed", bf, T, K) if T else torch.empty((0, K), dtype=bf, device=dy.device)
         self.layer.backward(dy, d_normed, self.mask)
         moe_residual_norm_backward(d_normed, d_stream, self.stream[:T], self.mask, self.norm_w, T, K, self.eps,
