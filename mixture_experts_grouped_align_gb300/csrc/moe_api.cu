@@ -892,7 +892,8 @@ moe_status moe_residual_norm_backward(const void* d_out, const void* d_stream, c
 }
 
 size_t moe_adapter_gemm_workspace_size(int64_t M, int32_t R, int32_t r) {
-  if (M < 1 || M >= (int64_t)1 << 30 || R < 1 || r < 1 || r > 128) return 0;
+  const int64_t most = (int64_t)1 << 30;
+  if (M < 1 || M >= most || R < 1 || R >= most || r < 1 || r > 128 || r % 8 != 0) return 0;
   const size_t few = moe_launch::adapter_few_workspace_bytes(M, r);
   return moe_launch::adapter_many_can(M, R) ? std::max(few, moe_launch::adapter_many_workspace_bytes(M, R, r)) : few;
 }
