@@ -258,7 +258,7 @@ MOE_DEV void finish(const ResidualNorm& p, const float (&s)[8], const uint4& w, 
     if (on) __stcs(reinterpret_cast<uint2*>(p.codes) + u, codes8(q, rc.by));
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = s[i] * r * f[i];  // zeros where a row does not count: its s are
+  for (int i = 0; i < 8; ++i) f[i] = s[i] * r * f[i];  // zeros where a row does not count: its s and w are
   if (on && p.out) __stcs(static_cast<uint4*>(p.out) + u, pack8(f));
   if (QUANT == 1) {
     uint32_t e;
@@ -268,6 +268,16 @@ MOE_DEV void finish(const ResidualNorm& p, const float (&s)[8], const uint4& w, 
       if ((c & 3) == 0) static_cast<uint8_t*>(p.scales)[u >> 2] = (uint8_t)e;
     }
   }
+}
+
+// The outputs of eight values of a row that does not count, but for a row's scale.
+template <bool F32, int QUANT>
+MOE_DEV void store_zeros(const ResidualNorm& p, int64_t u, int c) {
+  const float z[8] = {};
+  if (p.stream) Eight<F32>::store(p.stream, u, z);
+  if (p.out) __stcs(static_cast<uint4*>(p.out) + u, make_uint4(0, 0, 0, 0));
+  if (QUANT) __stcs(reinterpret_cast<uint2*>(p.codes) + u, make_uint2(0, 0));
+  if (QUANT == 1 && (c & 3) == 0) static_cast<uint8_t*>(p.scales)[u >> 2] = 0;
 }
 
 // QUANT: 0 no codes, 1 a power of two per 32 values, 2 a scale per row.
@@ -295,6 +305,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_kernel(ResidualNorm p)
     else res[t].zero();
     x[t] = on && p.x ? __ldcs(static_cast<const uint4*>(p.x) + u0 + c) : make_uint4(0, 0, 0, 0);
     w[t] = c < units ? static_cast<const uint4*>(p.weight)[c] : make_uint4(0, 0, 0, 0);
+    if (!live) w[t] = make_uint4(0, 0, 0, 0);  // its outputs are zeros, whatever the weight holds
   }
   float s[V][8], sum = 0.f, top = 0.f;
 #pragma unroll
@@ -400,6 +411,11 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(Residu
   constexpr int V = M::kV, kS = F32 ? 2 : 1, kPer = 1 + 2 * kS, kChunks = V * kPer;  // a stage's: d_out, stream, d_stream
   constexpr bool kHold = !M::kWide || V == 1;
   constexpr int kHeld = kHold ? V : 1;
+  // A row that does not count is zeros, whatever the weight holds: as products with a weight of zeros for fp32
+  // streams (61440 x 2880 forward and back 737 us, as a branch 752), as a branch otherwise (8192 x 7168 177, as
+  // products 184).
+  constexpr bool kBranch = !F32;
+  const auto weight = [](bool live, const uint4& z) { return kBranch || live ? z : make_uint4(0, 0, 0, 0); };
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][32];
   moe::wait_for_stream();
@@ -462,7 +478,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(Residu
       float v[8], g[8], f[8];
       st[h].get(v);
       unpack8(d[h], g);
-      unpack8(w[h], f);
+      unpack8(weight(live, w[h]), f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         sum += v[i] * v[i];
@@ -482,6 +498,12 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(Residu
       const int c = M::col() + t * M::step(), h = kHold ? t : 0, k = stage * kChunks + t * kPer;
       if (!in || c >= units) continue;
       const int64_t u = row * units + c;
+      if (kBranch && !live) {
+        const float z[8] = {};
+        if (p.d_residual) Eight<F32>::store(p.d_residual, u, z);
+        if (p.d_x) __stcs(static_cast<uint4*>(p.d_x) + u, make_uint4(0, 0, 0, 0));
+        continue;
+      }
       if (!kHold && live) {
         d[0] = ring.read(ring.at(k));
         st[0] = ring.template stream<F32>(k + 1);
@@ -491,10 +513,10 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(Residu
       float v[8], g[8], f[8], o[8];
       st[h].get(v);
       unpack8(d[h], g);
-      unpack8(w[h], f);
+      unpack8(weight(live, w[h]), f);
       ds[h].get(o);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {  // a row that does not count: zeros all along (r is finite, as eps > 0)
+      for (int i = 0; i < 8; ++i) {
         o[i] = r * (g[i] * f[i] - v[i] * q) + o[i];
         dw[t][i] += g[i] * (v[i] * r);
       }
@@ -546,6 +568,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_walk_kernel(ResidualNo
   // stream before the sums 86, and with four rows ahead 91: memory that turns between reads and writes less
   // often moves more); dropout spreads them well enough (forward and back 178 us, otherwise 184).
   constexpr bool kLate = QUANT != 0;
+  static_assert(M::kWide, "whether a row counts is the same for the whole block");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[2][32];
   moe::wait_for_stream();
@@ -579,7 +602,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_walk_kernel(ResidualNo
   for (int s = 0; s < kAhead; ++s) fetch(row + s * stride, s);
   uint32_t counts = p.mask == nullptr || (row < p.T && p.mask[row] != 0);
   int stage = 0, turn = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * rows; row0 < p.T; row0 += stride, row += stride, turn ^= 1) {
+  for (int64_t row0 = (int64_t)blockIdx.x * rows; row0 < p.T; row0 += stride, row += stride) {
     const bool in = row < p.T, live = in && counts;
     if (p.mask) counts = row + stride < p.T ? p.mask[row + stride] : 0;  // the next row's, a turn ahead
     cpa::cp_async_wait<kAhead - 1>();
@@ -598,6 +621,15 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_walk_kernel(ResidualNo
     if (F32) __syncwarp();
     fetch(row + kAhead * stride, stage);
     stage = stage + 1 == kAhead ? 0 : stage + 1;
+    if (!live) {  // all zeros, whatever the weight holds
+#pragma unroll
+      for (int t = 0; t < V; ++t) {
+        const int c = M::col() + t * M::step();
+        if (c < units) store_zeros<F32, QUANT>(p, row * units + c, c);
+      }
+      if (QUANT == 2 && M::col() == 0) static_cast<float*>(p.scales)[row] = kRowScaleMin;
+      continue;
+    }
     float s[V][8], sum = 0.f, top = 0.f;
 #pragma unroll
     for (int t = 0; t < V; ++t) {
@@ -632,6 +664,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_walk_kernel(ResidualNo
       if (kLate && p.stream && in && c < units) Eight<F32>::store(p.stream, row * units + c, s[t]);
       finish<QUANT>(p, s[t], w[t], r, rc, row * units + c, c, in && c < units);
     }
+    turn ^= 1;
   }
 }
 
