@@ -385,18 +385,10 @@ __device__ __forceinline__ void sum_pieces(const Adapter& p, UpSmem<F32>& sm, in
   }
   if (mine == 0) {
     float f[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
+    uint32_t w[PARTS][2];
+    moe::split_bf16_any<PARTS>(f, w);
 #pragma unroll
-    for (int h = 0; h < PARTS; ++h) {
-      uint32_t w[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const __nv_bfloat162 e = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&e);
-        f[2 * i] -= __low2float(e);
-        f[2 * i + 1] -= __high2float(e);
-      }
-      *reinterpret_cast<uint2*>(sm.vb(h) + j * kVs + k / 2) = make_uint2(w[0], w[1]);
-    }
+    for (int h = 0; h < PARTS; ++h) *reinterpret_cast<uint2*>(sm.vb(h) + j * kVs + k / 2) = make_uint2(w[h][0], w[h][1]);
   }
 }
 

@@ -26,6 +26,45 @@ MOE_DEV void set_status(int32_t* status, int32_t code) {
   if (status) atomicCAS(status, 0, code);
 }
 
+// Four numbers as sums of PARTS bf16 numbers each, a pair to a word (the first in its lower half): within 2^-8
+// of themselves with one part, 2^-8 of that with the next.  Not for numbers whose first part is an infinity:
+// what is left of them is one too, or NaN.
+template <int PARTS>
+MOE_DEV void split_bf16(float (&f)[4], uint32_t (&w)[PARTS][2], int from = 0) {
+#pragma unroll
+  for (int p = 0; p < PARTS; ++p) {
+    if (p < from) continue;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __nv_bfloat162 e = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[p][i] = *reinterpret_cast<const uint32_t*>(&e);
+      f[2 * i] -= __uint_as_float(w[p][i] << 16);
+      f[2 * i + 1] -= __uint_as_float(w[p][i] & 0xffff0000u);
+    }
+  }
+}
+// The same for any numbers: one that would round to an infinity begins with the largest bf16 number, and
+// infinities and NaN are their first part alone.
+constexpr float kBf16Most = 3.3895314e38f;
+MOE_DEV float largest4(const float (&f)[4]) {  // passes over NaN, which stay NaN in every part
+  return fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
+}
+template <int PARTS>
+MOE_DEV void split_bf16_any(float (&f)[4], uint32_t (&w)[PARTS][2]) {
+  if (largest4(f) <= kBf16Most) return split_bf16<PARTS>(f, w);
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool finite = fabsf(f[i]) <= 3.4028235e38f;
+    const float first = __bfloat162float(__float2bfloat16_rn(finite ? fminf(fmaxf(f[i], -kBf16Most), kBf16Most) : f[i]));
+    f[i] = finite ? f[i] - first : 0.f;
+    h[i] = __float_as_uint(first);
+  }
+  w[0][0] = h[0] >> 16 | (h[1] & 0xffff0000u);
+  w[0][1] = h[2] >> 16 | (h[3] & 0xffff0000u);
+  split_bf16<PARTS>(f, w, 1);
+}
+
 // E8M0 scale byte -> float: 2^(e-127); 0x00 is 2^-127 (a float32 subnormal, bits
 // 0x00400000), 0xFF is NaN.  A plain (e << 23) would give 0 and +inf for those two.
 MOE_DEV float e8m0_to_f32(uint32_t e) {
