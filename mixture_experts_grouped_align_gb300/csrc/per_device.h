@@ -5,6 +5,14 @@
 
 namespace moe_host {
 
+// Whether this process sees one GPU alone; count(&n): the query, true on success.  Loads that a cluster shares
+// (TMA multicast) are for such runs only: where there are several GPUs every block loads its own tiles.
+template <typename Query>
+bool sole_device(Query count) {
+  int n = 0;
+  return count(&n) && n == 1;
+}
+
 template <int N>
 class PerDevice {
  public:

@@ -56,17 +56,6 @@ MOE_DEV void load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
       : "memory");
 }
 
-// load_2d into the same shared-memory offset of every CTA of the cluster in cta_mask; each
-// destination's mbarrier at the offset of `bar` receives the box's bytes.
-MOE_DEV void load_2d_multicast(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint64_t* bar,
-                               uint16_t cta_mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_addr(bar)), "h"(cta_mask)
-      : "memory");
-}
-
 // L2 cache policies for the copies below: lines that should leave L2 first (data written
 // once and not read again soon) or last (data read again by other tiles).
 MOE_DEV uint64_t policy_evict_first() {
@@ -89,7 +78,8 @@ MOE_DEV void load_2d_hint(uint32_t dst, const CUtensorMap* map, int32_t x, int32
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_addr(bar)), "l"(policy)
       : "memory");
 }
-// load_2d_multicast with an L2 cache policy.
+// load_2d_hint into the same shared-memory offset of every CTA of the cluster in cta_mask; each destination's
+// mbarrier at the offset of `bar` receives the box's bytes.  For runs on one GPU alone (moe_host::sole_device).
 MOE_DEV void load_2d_multicast_hint(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint64_t* bar,
                                     uint16_t cta_mask, uint64_t policy) {
   asm volatile(

@@ -23,7 +23,9 @@
 //     Launched in clusters of C CTAs that take the C N tiles of one (expert, Kin tile): the
 //     input boxes, the same for all of them, are loaded once per cluster and multicast
 //     (each CTA issues its share), and every CTA's MMA commit frees the stage in all of
-//     them, which halves (C = 4) the operand bytes the L2 serves per output.
+//     them, which halves (C = 4) the operand bytes the L2 serves per output (dW1 of 256
+//     experts 7.45 ms, 8.18 with C = 1).  A process that sees several GPUs runs C = 1, the
+//     same MMAs in the same order.
 // Warp 0 owns TMEM (two 128 x 256 fp32 accumulators) and issues the MMAs.  Both feeds run
 // the same MMAs on the same stages in the same order, so they give identical bits.
 // Every mbarrier wait is bounded; a wait that runs out sets MOE_ERR_TIMEOUT and every
@@ -31,6 +33,7 @@
 #include "moe_common.cuh"
 #include "cp_async.cuh"
 #include "moe_launch.h"
+#include "per_device.h"
 #include "tcgen05.cuh"
 #include "tma.cuh"
 
@@ -597,13 +600,14 @@ cudaError_t wgrad_tc(const Wgrad& g, cudaStream_t stream) {
     cudaError_t rerr = expert_ranges(g, stream);
     if (rerr != cudaSuccess) return rerr;
     // the largest cluster that divides the N tiles and fits
+    const bool alone = moe_host::sole_device([](int* n) { return cudaGetDeviceCount(n) == cudaSuccess; });
     bool no_fit = false;
-    if (wa.n_tiles % 4 == 0) {
+    if (alone && wa.n_tiles % 4 == 0) {
       cudaError_t err = launch_slot<4>(mg, mi, wa, L.total, stream, &no_fit);
       if (err != cudaSuccess || !no_fit) return err == cudaSuccess ? cudaGetLastError() : err;
     }
     no_fit = false;
-    if (wa.n_tiles % 2 == 0) {
+    if (alone && wa.n_tiles % 2 == 0) {
       cudaError_t err = launch_slot<2>(mg, mi, wa, L.total, stream, &no_fit);
       if (err != cudaSuccess || !no_fit) return err == cudaSuccess ? cudaGetLastError() : err;
     }
