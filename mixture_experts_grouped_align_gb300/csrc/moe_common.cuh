@@ -27,8 +27,8 @@ MOE_DEV void set_status(int32_t* status, int32_t code) {
 }
 
 // Four numbers as sums of PARTS bf16 numbers each, a pair to a word (the first in its lower half): within 2^-8
-// of themselves with one part, 2^-8 of that with the next.  Not for numbers whose first part is an infinity:
-// what is left of them is one too, or NaN.
+// of themselves with one part, 2^-17 with two, 2^-26 with three.  Not for numbers whose first part is an
+// infinity: what is left of them is one too, or NaN.
 template <int PARTS>
 MOE_DEV void split_bf16(float (&f)[4], uint32_t (&w)[PARTS][2], int from = 0) {
 #pragma unroll
