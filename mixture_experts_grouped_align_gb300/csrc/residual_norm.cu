@@ -214,25 +214,26 @@ struct RowCodes {
 };
 // Below this 448 / max |s w| may be infinite, and the products s w lose bits (or all of them).
 constexpr float kTopMin = 0x1p-119f;
-// The scale of a row whose largest |s w| is `top`, kTopMin at least.  Its codes are those of s w 448 / top,
-// which is n 448 / max |n| without r's rounding, or of n 2^120 where the scale is the smallest.
+// The scale of a row whose largest |s w| is `top`, finite and kTopMin at least.  Its codes are those of s w 448 /
+// top, which is n 448 / max |n| without r's rounding, or of n 2^120 where the scale is the smallest.
 MOE_DEV RowCodes row_codes(float top, float r) {
   const float most = top * r, nan = __uint_as_float(0x7fc00000u);
   if (!(most <= 3.4028235e38f)) return RowCodes{nan, 1.f, nan};  // an infinity, too, leaves NaN in its row
   if (most / 448.f < kRowScaleMin) return RowCodes{kRowScaleMin, r, 1.f / kRowScaleMin};
   return RowCodes{most / 448.f, 1.f, 448.f / top};
 }
-// The same from the largest |n|, for smaller rows: of n 448 / most, at most n 2^120.
-MOE_DEV RowCodes small_row_codes(float most, float r) {
-  if (most / 448.f < kRowScaleMin) return RowCodes{kRowScaleMin, r, 1.f / kRowScaleMin};
-  return RowCodes{most / 448.f, r, 448.f / most};
+// The same from the largest |n|, for other rows: of n 448 / most, at most n 2^120.
+MOE_DEV RowCodes row_codes_of_n(float most, float r) {
+  const RowCodes rc = row_codes(most, 1.f);
+  return RowCodes{rc.scale, r, rc.by};
 }
-// How the row of s becomes codes.  Small rows (those of zeros among them) go over their products again, so all
-// threads of a row call, and of a warp; `red`: as reduce_pair's, this thread's last use of it is over.
+// How the row of s becomes codes.  Small rows (those of zeros among them) and those in which s w overflows (n is 0
+// where the sum of squares did) go over their products again, so all threads of a row call, and of a warp; `red`:
+// as reduce_pair's, this thread's last use of it is over.
 template <typename M>
 MOE_DEV RowCodes codes_of(const float (&s)[M::kV][8], const uint4 (&w)[M::kV], float top, float r, float2* red) {
-  const bool small = top < kTopMin;
-  if (!(M::kWide ? small : __any_sync(kAll, small))) return row_codes(top, r);
+  const bool other = !(top >= kTopMin && top <= 3.4028235e38f);
+  if (!(M::kWide ? other : __any_sync(kAll, other))) return row_codes(top, r);
   float none = 0.f, most = 0.f;
 #pragma unroll
   for (int t = 0; t < M::kV; ++t) {
@@ -243,7 +244,7 @@ MOE_DEV RowCodes codes_of(const float (&s)[M::kV][8], const uint4 (&w)[M::kV], f
   }
   if (M::kWide) __syncthreads();  // the first sums have been read
   reduce_pair<M, true>(none, most, red);
-  return small ? small_row_codes(most, r) : row_codes(top, r);
+  return other ? row_codes_of_n(most, r) : row_codes(top, r);
 }
 
 // The outputs of eight values s of unit u (c: its unit in the row); every lane calls.
