@@ -531,7 +531,8 @@ size_t moe_residual_norm_workspace_size(int32_t K);
  * d_out [T, K] bf16: the gradient of out (and of the values that codes stand for); d_stream [T, K] in
  * the stream's type: what reaches the stream from behind, or NULL; d_residual [T, K] in the stream's
  * type, d_x [T, K] bf16 and d_weight [K] fp32 may each be NULL.  In fp32, rounded once; d_weight is
- * summed in a fixed order: repeated calls on a device give identical bits.  Rows that do not count may
+ * summed in a fixed order: repeated calls on a device give identical bits.  Rows whose sum of squares is
+ * above fp32's range have ds = d_stream and add nothing to d_weight.  Rows that do not count may
  * hold anything, add nothing to d_weight, and their rows of d_residual and d_x are zeros.  d_residual may
  * be d_stream, and d_x may be d_out; other overlaps are not allowed.  Limits as above; d_weight needs
  * moe_residual_norm_workspace_size(K) bytes of workspace (T = 0 gives zeros). */

@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(Residu
       fetch(row + kAhead * stride, stage);
     }
     reduce_pair<M>(sum, dot, red[turn]);  // two sets in turn: one barrier a row is enough
-    const float r = inverse_rms(sum, inv_k, p.eps), q = r * r * (dot * inv_k);
+    const float r = inverse_rms(sum, inv_k, p.eps);
+    const float q = r == 0.f ? 0.f : r * r * (dot * inv_k);  // the norm of such a row is 0, whatever overflows in dot
 #pragma unroll
     for (int t = 0; t < V; ++t) {
       const int c = M::col() + t * M::step(), h = kHold ? t : 0, k = stage * kChunks + t * kPer;

@@ -1,5 +1,6 @@
-"""Rows whose sum of squares is above fp32's range: their norm is 0, in every format, also where s times the
-weight overflows.  A row with an infinity is NaN in its scale.  No tolerances: zeros.
+"""Rows whose sum of squares is above fp32's range: their norm is 0, in every format, and so is what passes
+through it backward, also where s times the weight overflows.  A row with an infinity is NaN in its scale.
+No tolerances: zeros, and d_stream as it is.
 """
 import numpy as np
 import pytest
@@ -53,3 +54,22 @@ def test_forward(moe, T, K, f32, quant):
         assert (sc[zero] == 0).all() and sc[2, 0] == 255
     if quant == "row":
         assert (sc[zero] == 2.0 ** -120).all() and torch.isnan(sc[2]) and (codes[2] & 0x7F == 0x7F).all()
+
+
+@pytest.mark.parametrize("T,K", SIZES)
+@pytest.mark.parametrize("f32", [False, True])
+def test_backward(moe, T, K, f32):
+    s, w, large = inputs(T, K, f32)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    do = torch.randn((T, K), generator=g, device="cuda").bfloat16()
+    ds = torch.randn((T, K), generator=g, device="cuda").to(s.dtype)
+    dr, dx = torch.full_like(s, 7.0), torch.full((T, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    dw, dw_rest = (torch.full((K,), 7.0, device="cuda") for _ in range(2))
+    ws = torch.full((moe.moe_residual_norm_workspace_size(K),), 0xFF, dtype=torch.uint8, device="cuda")
+    ctx = moe.Ctx(workspace=ws)
+    moe.moe_residual_norm_backward(do, ds, s, None, w, T, K, 1e-5, 0.0, None, 0, dr, dx, dw, ctx)
+    # the weight's gradient is that of the other rows alone
+    moe.moe_residual_norm_backward(do, ds, s, (~large).to(torch.uint8), w, T, K, 1e-5, 0.0, None, 0, None, None, dw_rest, ctx)
+    torch.cuda.synchronize()
+    assert torch.equal(dr[large], ds[large]) and torch.equal(dx[large], ds[large].bfloat16())
+    assert torch.isfinite(dr).all() and torch.equal(dw, dw_rest)
