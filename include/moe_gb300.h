@@ -561,8 +561,11 @@ size_t moe_adapter_gemm_workspace_size(int64_t M, int32_t R, int32_t r);
  * its own request's adapter alone, also where another's is not finite.  Sums run in one fixed order for
  * given sizes, offsets and adapters: repeated calls give identical bits.
  * Data errors in ctx->dev_status: offsets that decrease or leave [0, M] (MOE_ERR_CAPACITY; such a request
- * has no rows; where requests overlap, their rows are undefined), adapters outside [-1, L)
- * (MOE_ERR_INVALID_EXPERT; read as -1).
+ * has no rows, and the rows of requests that overlap, or that start below an offset before theirs, are
+ * undefined), adapters outside [-1, L) (MOE_ERR_INVALID_EXPERT; read as -1).
+ * More than 1024 requests, and adapters of 2^31 rows and more, run on the kernels for few rows a request,
+ * however long they are (moe_adapter_gemm_plan): 131072 rows of 1025 requests of rank 16, 4096 -> 4096, take
+ * 1.12 ms, of 1024 requests 0.69 ms, so a batch of many long requests is better given in several calls.
  * Limits: K and N multiples of 8, r a multiple of 8 up to 128, M, N, K, R < 2^30, L >= 1.  M = 0 or R = 0:
  * nothing is done.  Needs moe_adapter_gemm_workspace_size() bytes of workspace. */
 moe_status moe_adapter_gemm(const void* x, const void* a, const void* b, const float* scale, const int32_t* row_offsets,

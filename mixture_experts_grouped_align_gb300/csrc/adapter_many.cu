@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(kUpThreads, 1)
     tc::tmem_relinquish();
   }
   // The first kernel lets this one start when all before it is complete: only v is waited for, by the
-  // warps that read it (of every CTA, so that this kernel never ends before the first).
+  // warps that read it (of every CTA, so that this kernel never ends before the first).  What follows this
+  // kernel waits for its end before it touches memory (launch_staged).
   moe::let_next_start();
   if (warp == 2) make_tables(p, tab, p.base != p.out, false);
   tc::tc_fence_before();

@@ -7,7 +7,7 @@
  * type, density, place and size, and calls the library.  It returns the status; a tensor that
  * fails the checks is handed to the error function, which raises.
  *
- * setup(error, f32, i32, bf16, u8, addresses): the error function (tensor, name, type, elements),
+ * setup(error, f32, i32, bf16, u8, i64, addresses): the error function (tensor, name, type, elements),
  * the torch types and the addresses of the library's functions, in the order of `enum`.
  */
 #define PY_SSIZE_T_CLEAN

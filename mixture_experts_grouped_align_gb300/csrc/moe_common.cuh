@@ -13,12 +13,14 @@
 namespace moe {
 
 // In a kernel launched by launch_staged: returns once the work before it in the stream has
-// completed and its writes are visible.  Every thread calls it before it touches memory.
+// completed and its writes are visible.  Every thread calls it before it touches memory, but for
+// kernels that always follow one of their own call (launch_staged says which and when).
 MOE_DEV void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Lets the next kernel of the stream, if it was launched by launch_staged too, begin its setup
 // once every block of this one has called this (or ended).  Called after wait_for_stream(), so
-// that the work before this kernel is complete for whatever starts then.
+// that the work before this kernel is complete for whatever starts then; a kernel that calls it
+// earlier must wait itself before it ends, and its successor before it touches memory.
 MOE_DEV void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // First data-dependent error wins; nothing traps.

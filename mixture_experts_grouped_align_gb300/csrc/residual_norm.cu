@@ -17,7 +17,7 @@
 //
 // Both passes are bound by memory: every tensor is read or written once, and a row stays in registers from
 // its sums to its outputs.  Measured (replayed graphs): 8192 x 7168 to bf16, stream and MX codes 81 us, 6.56
-// TB/s (a copy moves 6.78); 61440 x 2880 with an fp32 stream and dropout, forward and back, 743 us, 6.5 TB/s;
+// TB/s (a copy moves 6.78); 61440 x 2880 with an fp32 stream and dropout, forward and back, 735 us, 6.6 TB/s;
 // 8192 x 7168 in bf16 the same 177 us, 6.0 TB/s (171 without dropout: what the generator computes is not all
 // hidden).  Few rows are bound by the launch and two latencies: 64 x 2880 1.5 us.
 // With the backward pass's loads into registers these were 283 us (no room for loads ahead beside the sums
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(M::kMost) residual_norm_backward_kernel(Residu
   constexpr bool kHold = !M::kWide || V == 1;
   constexpr int kHeld = kHold ? V : 1;
   // A row that does not count is zeros, whatever the weight holds: as products with a weight of zeros for fp32
-  // streams (61440 x 2880 forward and back 737 us, as a branch 752), as a branch otherwise (8192 x 7168 177, as
+  // streams (61440 x 2880 forward and back 735 us, as a branch 752), as a branch otherwise (8192 x 7168 177, as
   // products 184).
   constexpr bool kBranch = !F32;
   const auto weight = [](bool live, const uint4& z) { return kBranch || live ? z : make_uint4(0, 0, 0, 0); };
