@@ -21,7 +21,7 @@ import torch
 from . import (Ctx, MoeError, moe_act_checkpoint, moe_adapter_gemm, moe_adapter_gemm_workspace_size, moe_align,
                moe_align_capacity, moe_bucket, moe_bucket_pad, moe_dense_gemm, moe_forward, moe_forward_workspace_size,
                moe_residual_norm)
-from .train import _apart, _check
+from .train import _check
 
 BLOCK_M = 128
 
@@ -181,6 +181,7 @@ class ServeBlock:
             raise MoeError(-1, "adapters need a shared expert")
         new = lambda *s, dtype=bf: torch.empty(s, dtype=dtype, device=dev)  # noqa: E731
         self.stream, self.normed = new(T, K, dtype=torch.float32 if stream_f32 else bf), new(T, K)
+        self._own = [(t, t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in (self.stream, self.normed)]
         self.logits = new(T, E, dtype=torch.float32)
         mx = layer.quant == "mxfp8"
         self.codes = new(T, K, dtype=torch.uint8) if mx else None
@@ -223,21 +224,23 @@ class ServeBlock:
                          ctx)
 
     def _check_step(self, branch, residual, T, y, row_offsets, adapter):
-        dev, n, i32 = self.norm_w.device, T * self.layer.K, torch.int32
-        _check(y, "y", torch.bfloat16, dev, numel=n)
+        dev, n, bf = self.norm_w.device, T * self.layer.K, torch.bfloat16
+        # rows, and whether they may begin where the block's stream or its norm does: the stream may be written over
+        # the residual and the norm over the branch
+        rows = [(y, "y", bf, None)]
         if branch is not None:
-            _check(branch, "branch", torch.bfloat16, dev, numel=n)
+            rows.append((branch, "branch", bf, self.normed))
         if residual is not None:
-            _check(residual, "residual", self.stream.dtype, dev, numel=n)
+            rows.append((residual, "residual", self.stream.dtype, self.stream))
+        for t, what, dtype, same in rows:
+            _check(t, what, dtype, dev, numel=n)
+            at, size = t.data_ptr(), n * dtype.itemsize
+            for own, start, end in self._own:
+                if at < end and start < at + size and not (own is same and at == start):
+                    raise MoeError(-1, f"{what} and the block's rows must not overlap")
         if adapter is not None:
-            _check(adapter, "adapter", i32, dev, (adapter.shape[0],))
-            _check(row_offsets, "row_offsets", i32, dev, numel=adapter.shape[0] + 1)
-        # the norm may write its rows over the branch's and the stream over the residual, at the same place
-        for t, what, own, same in ((y, "y", self.stream, False), (y, "y", self.normed, False), (branch, "branch", self.stream, False),
-                                   (branch, "branch", self.normed, True), (residual, "residual", self.stream, True),
-                                   (residual, "residual", self.normed, False)):
-            if t is not None and not (same and t.data_ptr() == own.data_ptr()):
-                _apart(t, own, f"{what} and the block's rows")
+            _check(adapter, "adapter", torch.int32, dev, (adapter.shape[0],))
+            _check(row_offsets, "row_offsets", torch.int32, dev, numel=adapter.shape[0] + 1)
 
     def step(self, branch, residual, T, y, row_offsets=None, adapter=None):
         """branch [T, K] bf16 or None, residual [T, K] in the stream's type -> y [T, K] bf16 and the stream
